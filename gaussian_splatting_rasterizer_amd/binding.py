@@ -31,6 +31,8 @@ GS_EXPORT_DEPTH_KEYS = 2
 GS_EXPORT_SORTED_IDS = 3
 GS_EXPORT_RANGES = 4
 GS_EXPORT_PIXEL_STATS = 5
+GS_F32, GS_BF16, GS_F16 = 0, 1, 2
+GS_ACT_SILU, GS_ACT_GELU = 0, 1
 STAGES = ("project", "depth_sort", "scan", "emit", "tile_sort", "ranges", "render", "replay", "finalize",
           "backward", "backward_finalize", "features", "attribute")
 
@@ -38,7 +40,9 @@ ABI_SYMBOLS = ("gs_default_params", "gs_workspace_size", "gs_context_create", "g
                "gs_project", "gs_bin_sort", "gs_render", "gs_score_replay", "gs_backward", "gs_render_features",
                "gs_attribute", "gs_status_string",
                "gs_last_error", "gs_debug_exp2", "gs_debug_export", "gs_debug_topk", "gs_profile_enable",
-               "gs_profile_stages", "gs_profile_read", "gs_render_score_noalloc")
+               "gs_profile_stages", "gs_profile_read", "gs_render_score_noalloc",
+               "gs_ffn_sizes", "gs_ffn_forward", "gs_ffn_backward", "gs_scan_sizes", "gs_scan_forward",
+               "gs_scan_backward", "gs_default_ortho_dims", "gs_ortho_size", "gs_orthogonalize")
 
 
 class gs_gaussians(ctypes.Structure):
@@ -66,6 +70,41 @@ class gs_params(ctypes.Structure):
     _fields_ = [("eps", ctypes.c_float), ("den_min", ctypes.c_float), ("lam", ctypes.c_float),
                 ("near_plane", ctypes.c_float), ("far_plane", ctypes.c_float),
                 ("background", ctypes.c_float * 3), ("antialiased", ctypes.c_int32)]
+
+
+class gs_ffn_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d_in", ctypes.c_int32), ("d_hidden", ctypes.c_int32),
+                ("d_out", ctypes.c_int32), ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class gs_ffn_weights(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("down", ctypes.c_void_p)]
+
+
+class gs_ffn_grads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("gate", ctypes.c_void_p),
+                ("up", ctypes.c_void_p), ("down", ctypes.c_void_p)]
+
+
+class gs_scan_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n_seq", ctypes.c_int64), ("channels", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class gs_scan_inputs(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("x", ctypes.c_void_p), ("h0", ctypes.c_void_p),
+                ("ld_gate", ctypes.c_int64), ("ld_x", ctypes.c_int64)]
+
+
+class gs_scan_grads(ctypes.Structure):
+    _fields_ = [("gate", ctypes.c_void_p), ("x", ctypes.c_void_p), ("h0", ctypes.c_void_p),
+                ("ld_gate", ctypes.c_int64), ("ld_x", ctypes.c_int64)]
+
+
+class gs_ortho_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("batch", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("steps", ctypes.c_int32),
+                ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class GsrError(RuntimeError):
@@ -129,6 +168,25 @@ def load_library(path: str = LIB_PATH):
     lib.gs_render_score_noalloc.argtypes = [ctypes.POINTER(gs_gaussians), ctypes.POINTER(gs_camera), ctypes.c_int32,
                                             ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(gs_params), P, P, P, P,
                                             P, P]
+    Z, I64, R = ctypes.c_size_t, ctypes.c_int64, ctypes.POINTER
+    lib.gs_ffn_sizes.restype = St
+    lib.gs_ffn_sizes.argtypes = [R(gs_ffn_dims), R(Z), R(Z), R(Z)]
+    lib.gs_ffn_forward.restype = St
+    lib.gs_ffn_forward.argtypes = [R(gs_ffn_dims), P, I64, R(gs_ffn_weights), P, I64, P, P, Z, P]
+    lib.gs_ffn_backward.restype = St
+    lib.gs_ffn_backward.argtypes = [R(gs_ffn_dims), P, I64, R(gs_ffn_weights), P, P, I64, R(gs_ffn_grads), P, Z, P]
+    lib.gs_scan_sizes.restype = St
+    lib.gs_scan_sizes.argtypes = [R(gs_scan_dims), R(Z), R(Z)]
+    lib.gs_scan_forward.restype = St
+    lib.gs_scan_forward.argtypes = [R(gs_scan_dims), P, R(gs_scan_inputs), P, I64, P, P, P, Z, P]
+    lib.gs_scan_backward.restype = St
+    lib.gs_scan_backward.argtypes = [R(gs_scan_dims), P, R(gs_scan_inputs), P, P, I64, P, R(gs_scan_grads), P, Z, P]
+    lib.gs_default_ortho_dims.restype = St
+    lib.gs_default_ortho_dims.argtypes = [R(gs_ortho_dims)]
+    lib.gs_ortho_size.restype = St
+    lib.gs_ortho_size.argtypes = [R(gs_ortho_dims), R(Z)]
+    lib.gs_orthogonalize.restype = St
+    lib.gs_orthogonalize.argtypes = [R(gs_ortho_dims), P, P, P, Z, P]
     _lib = lib
     return lib
 
@@ -154,6 +212,10 @@ def _stream_handle(stream=None) -> ctypes.c_void_p:
 
 def _dev_ptr(t) -> ctypes.c_void_p:
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(None)
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size() if t is not None else 0
 
 
 # ---- the ABI calls, same names as in C -------------------------------------------------------------
@@ -264,6 +326,65 @@ def gs_profile_read(ctx) -> dict:
     calls = (ctypes.c_int64 * len(STAGES))()
     _check(load_library().gs_profile_read(ctx, ms, calls, len(STAGES)), "gs_profile_read")
     return {name: (float(ms[i]), int(calls[i])) for i, name in enumerate(STAGES)}
+
+
+def gs_ffn_sizes(dims: gs_ffn_dims) -> tuple:
+    """(saved bytes, forward workspace bytes, backward workspace bytes)"""
+    out = [ctypes.c_size_t(0) for _ in range(3)]
+    _check(load_library().gs_ffn_sizes(ctypes.byref(dims), *[ctypes.byref(o) for o in out]), "gs_ffn_sizes")
+    return tuple(int(o.value) for o in out)
+
+
+def gs_ffn_forward(dims, x, ld_x, weights: gs_ffn_weights, y, ld_y, saved, workspace, stream=None) -> None:
+    _check(load_library().gs_ffn_forward(ctypes.byref(dims), _dev_ptr(x), ld_x, ctypes.byref(weights), _dev_ptr(y),
+                                         ld_y, _dev_ptr(saved), _dev_ptr(workspace), _nbytes(workspace),
+                                         _stream_handle(stream)), "gs_ffn_forward")
+
+
+def gs_ffn_backward(dims, x, ld_x, weights: gs_ffn_weights, saved, dy, ld_dy, grads: gs_ffn_grads, workspace,
+                    stream=None) -> None:
+    _check(load_library().gs_ffn_backward(ctypes.byref(dims), _dev_ptr(x), ld_x, ctypes.byref(weights),
+                                          _dev_ptr(saved), _dev_ptr(dy), ld_dy, ctypes.byref(grads),
+                                          _dev_ptr(workspace), _nbytes(workspace), _stream_handle(stream)),
+           "gs_ffn_backward")
+
+
+def gs_scan_sizes(dims: gs_scan_dims) -> tuple:
+    """(saved bytes, workspace bytes)"""
+    s, w = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load_library().gs_scan_sizes(ctypes.byref(dims), ctypes.byref(s), ctypes.byref(w)), "gs_scan_sizes")
+    return int(s.value), int(w.value)
+
+
+def gs_scan_forward(dims, offsets, inputs: gs_scan_inputs, y, ld_y, h_last, saved, workspace, stream=None) -> None:
+    _check(load_library().gs_scan_forward(ctypes.byref(dims), _dev_ptr(offsets), ctypes.byref(inputs), _dev_ptr(y),
+                                          ld_y, _dev_ptr(h_last), _dev_ptr(saved), _dev_ptr(workspace),
+                                          _nbytes(workspace), _stream_handle(stream)), "gs_scan_forward")
+
+
+def gs_scan_backward(dims, offsets, inputs: gs_scan_inputs, saved, dy, ld_dy, dh_last, grads: gs_scan_grads,
+                     workspace, stream=None) -> None:
+    _check(load_library().gs_scan_backward(ctypes.byref(dims), _dev_ptr(offsets), ctypes.byref(inputs),
+                                           _dev_ptr(saved), _dev_ptr(dy), ld_dy, _dev_ptr(dh_last),
+                                           ctypes.byref(grads), _dev_ptr(workspace), _nbytes(workspace),
+                                           _stream_handle(stream)), "gs_scan_backward")
+
+
+def gs_default_ortho_dims() -> gs_ortho_dims:
+    d = gs_ortho_dims()
+    _check(load_library().gs_default_ortho_dims(ctypes.byref(d)), "gs_default_ortho_dims")
+    return d
+
+
+def gs_ortho_size(dims: gs_ortho_dims) -> int:
+    w = ctypes.c_size_t(0)
+    _check(load_library().gs_ortho_size(ctypes.byref(dims), ctypes.byref(w)), "gs_ortho_size")
+    return int(w.value)
+
+
+def gs_orthogonalize(dims: gs_ortho_dims, g, out, workspace, stream=None) -> None:
+    _check(load_library().gs_orthogonalize(ctypes.byref(dims), _dev_ptr(g), _dev_ptr(out), _dev_ptr(workspace),
+                                           _nbytes(workspace), _stream_handle(stream)), "gs_orthogonalize")
 
 
 # ---- convenience wrapper ----------------------------------------------------------------------------

@@ -22,13 +22,17 @@ namespace {
 
 thread_local char g_err[512] = "";
 
-gs_status fail(gs_status s, const char* fmt, ...) {
+}  // namespace
+
+gs_status gsr::fail(gs_status s, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(g_err, sizeof g_err, fmt, ap);
     va_end(ap);
     return s;
 }
+
+namespace {
 
 gs_status hip_fail(hipError_t e, const char* where) {
     return fail(GS_ERR_HIP, "%s: %s", where, hipGetErrorString(e));

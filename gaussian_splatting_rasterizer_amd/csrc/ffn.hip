@@ -1,0 +1,414 @@
+// ffn.hip -- gated feed-forward block of the learned updater and its gradients.
+//
+//   g = x Wg^T, u = x Wu^T, h = act(g) u, y = h Wd^T                                  (forward)
+//   dh = dy Wd, dg = dh u act'(g), du = dh act(g),
+//   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dy^T h                      (backward)
+//
+// Every product runs on k_gemm16: both projections share one pass over x, the activation and the gating are in the
+// first product's epilogue, their derivatives in the epilogue of dh, and dx sums its two products in one
+// accumulator.  float32 operands are split into three bfloat16 parts and multiplied with six partial products,
+// which keeps 24 bits (the parts left out are below 2^-24) at the bfloat16 matrix rate / 6.
+//
+// Rows that are not 16-byte aligned, or whose length is not a multiple of 8 elements, are copied once into a
+// zero-padded layout in the workspace (k_pack); other operands are read in place.
+#include "gsr_internal.hpp"
+#include "gemm16.hpp"
+
+namespace gsr {
+
+namespace {
+
+// ---- packing -------------------------------------------------------------------------------------------
+
+struct PackJob {
+    const void* src;
+    uint16_t* dst;
+    int64_t rows, cols, ld, plane;  // dst rows are round8(cols) long, planes `plane` elements apart
+};
+struct PackJobs {
+    PackJob j[5];
+};
+
+// [rows][cols] -> planes of [rows][round8(cols)], zero padded; one thread per 8 destination elements.
+template <class F>
+__global__ __launch_bounds__(256) void k_pack(const PackJobs jobs) {
+    const PackJob& jb = jobs.j[blockIdx.y];
+    const int64_t c8 = (jb.cols + 7) / 8, n = jb.rows * c8;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / c8, c = (i - r * c8) * 8;
+        const typename F::Elem* s = (const typename F::Elem*)jb.src + r * jb.ld + c;
+        uint16_t* d = jb.dst + i * 8;
+        const int64_t left = jb.cols - c;
+        if constexpr (F::kPlanes == 1) {
+            uint16_t v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = e < left ? s[e] : (uint16_t)0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = v[e];
+        } else {
+            f32x4 v[2];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] = e < left ? s[e] : 0.f;
+            put_operand<F>(d, jb.plane, v[0]);
+            put_operand<F>(d + 4, jb.plane, v[1]);
+        }
+    }
+}
+
+// ---- activations ---------------------------------------------------------------------------------------
+
+// act(g) and its derivative (silu: exp overflows to inf for g < -88 and the sigmoid is then 0)
+template <int ACT>
+__device__ __forceinline__ void activation(float g, float& a, float& da) {
+    if constexpr (ACT == GS_ACT_SILU) {
+        const float s = 1.f / (1.f + __expf(-g));
+        a = g * s;
+        da = s * (1.f + g * (1.f - s));
+    } else {
+        const float cdf = 0.5f * (1.f + erff(g * 0.70710678118654752f));
+        a = g * cdf;
+        da = cdf + g * 0.39894228040143268f * __expf(-0.5f * g * g);
+    }
+}
+
+// ---- epilogues -----------------------------------------------------------------------------------------
+
+// h = act(g) u, with g and u kept for the backward pass when asked for
+template <class F, int ACT>
+struct EpiGate {
+    static constexpr bool kDual = true, kSymmetric = false;
+    uint16_t* h;
+    int64_t h_plane;
+    typename F::Elem* gu;  // [M][2 F8] or null
+    int64_t f8;
+    int M;
+    __device__ __forceinline__ void pair(int m, int n, f32x4 g, f32x4 u) const {
+        if (m >= M || n >= f8) return;
+        if (gu) {
+            F::put(gu + (int64_t)m * 2 * f8 + n, g);
+            F::put(gu + (int64_t)m * 2 * f8 + f8 + n, u);
+        }
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float a, da;
+            activation<ACT>(g[e], a, da);
+            v[e] = a * u[e];
+        }
+        put_operand<F>(h + (int64_t)m * f8 + n, h_plane, v);
+    }
+};
+
+// dg and du from dh and the saved g and u
+template <class F, int ACT>
+struct EpiGateGrad {
+    static constexpr bool kDual = false, kSymmetric = false;
+    const typename F::Elem* gu;
+    uint16_t* dgu;  // [M][2 F8]
+    int64_t plane;
+    int64_t f8;
+    int M;
+    __device__ __forceinline__ void one(int, int, int m, int n, f32x4 dh) const {
+        if (m >= M || n >= f8) return;
+        const int64_t at = (int64_t)m * 2 * f8 + n;
+        const f32x4 g = F::get(gu + at), u = F::get(gu + at + f8);
+        f32x4 dg, du;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float a, da;
+            activation<ACT>(g[e], a, da);
+            du[e] = dh[e] * a;
+            dg[e] = dh[e] * u[e] * da;
+        }
+        put_operand<F>(dgu + at, plane, dg);
+        put_operand<F>(dgu + at + f8, plane, du);
+    }
+};
+
+// Plain store.  Rows [0, rows0) go to c0; rows [off1, off1 + rows0) to c1 (the two halves of a joint gradient).
+template <class F>
+struct EpiStore {
+    static constexpr bool kDual = false, kSymmetric = false;
+    typename F::Elem* c0;
+    typename F::Elem* c1;
+    int64_t ld;
+    int rows0, off1, N;
+    bool vec;  // rows allow 4-element stores
+    __device__ __forceinline__ void one(int, int, int m, int n, f32x4 v) const {
+        typename F::Elem* c = c0;
+        int r = m;
+        if (m >= rows0) {
+            r = m - off1;
+            c = c1;
+            if (r < 0 || r >= rows0) return;
+        }
+        if (!c || n >= N) return;
+        c += (int64_t)r * ld + n;
+        if (vec && n + 4 <= N) {
+            F::put(c, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < N) F::put1(c + e, v[e]);
+        }
+    }
+};
+
+// float32 partial sums of a product split along k: part[split][M][n4]
+struct EpiPartial {
+    static constexpr bool kDual = false, kSymmetric = false;
+    float* part;
+    int64_t n4;
+    int M;
+    __device__ __forceinline__ void one(int, int split, int m, int n, f32x4 v) const {
+        if (m >= M || n >= n4) return;
+        *(f32x4*)(part + ((int64_t)split * M + m) * n4 + n) = v;
+    }
+};
+
+// Sum of the partials in split order (the result does not depend on scheduling), stored like EpiStore.
+template <class F>
+__global__ __launch_bounds__(256) void k_reduce(const float* part, int splits, int M, int64_t n4, EpiStore<F> st) {
+    const int64_t q4 = n4 / 4, n = (int64_t)M * q4;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        f32x4 s = *(const f32x4*)(part + i * 4);
+        for (int k = 1; k < splits; ++k) s += *(const f32x4*)(part + ((int64_t)k * M * n4) + i * 4);
+        const int64_t m = i / q4;
+        st.one(0, 0, (int)m, (int)(i - m * q4) * 4, s);
+    }
+}
+
+// ---- launchers -----------------------------------------------------------------------------------------
+
+// Segments of one product: one, or the six partial products of split operands, the smallest first.
+template <class F>
+void add_segments(GemmArgs& g, const Operand& a, const Operand& b, const Operand* b2, int64_t a_off = 0) {
+    static const int pa[6] = {2, 0, 1, 1, 0, 0}, pb[6] = {0, 2, 1, 0, 1, 0};
+    const int n = F::kPlanes == 1 ? 1 : 6;
+    for (int i = 0; i < n; ++i) {
+        const int ia = F::kPlanes == 1 ? 0 : pa[i], ib = F::kPlanes == 1 ? 0 : pb[i];
+        g.a[g.nseg] = a.p + ia * a.plane + a_off;
+        g.b[g.nseg] = b.p + ib * b.plane;
+        g.b2[g.nseg] = b2 ? b2->p + ib * b2->plane : nullptr;
+        ++g.nseg;
+    }
+    g.lda = a.ld;
+    g.ldb = b.ld;
+}
+
+// Splits of a weight gradient along its rows: enough workgroups to fill the GPU, at least 8 k tiles each.
+int grad_splits(int64_t M, int64_t N, int64_t K, int nseg) {
+    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+    const int64_t kt = (K + kGemmBK - 1) / kGemmBK * nseg;
+    int64_t s = 512 / (tiles > 0 ? tiles : 1);
+    if (s > kt / 8) s = kt / 8;
+    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+
+// ---- workspace -----------------------------------------------------------------------------------------
+
+template <class F>
+struct Layout {
+    int64_t M, D, H, O, D8, H8, O8;
+    explicit Layout(const gs_ffn_dims& d)
+        : M(d.rows), D(d.d_in), H(d.d_hidden), O(d.d_out), D8(round8(D)), H8(round8(H)), O8(round8(O)) {}
+    int64_t saved_gu_bytes() const { return round_up(M * 2 * H8 * (int64_t)sizeof(typename F::Elem), kAlign); }
+    int64_t h_elems() const { return M * H8 * F::kPlanes; }
+};
+
+// An operand is read in place when its rows are 16-byte aligned and a multiple of 8 elements long.
+template <class F>
+bool direct(const void* p, int64_t cols, int64_t ld) {
+    return F::kPlanes == 1 && cols % 8 == 0 && ld % 8 == 0 && ((uintptr_t)p % 16) == 0;
+}
+
+struct Packer {
+    PackJobs jobs{};
+    int n = 0;
+    int64_t most = 0;
+    template <class F>
+    Operand add(Carver& cv, const void* src, int64_t rows, int64_t cols, int64_t ld,
+                bool always = false) {
+        if (!always && direct<F>(src, cols, ld)) return {(const uint16_t*)src, 0, ld};
+        const int64_t c8 = round8(cols);
+        uint16_t* d = cv.take<uint16_t>(rows * c8 * F::kPlanes);
+        jobs.j[n++] = {src, d, rows, cols, ld, rows * c8};
+        if (rows * c8 / 8 > most) most = rows * c8 / 8;
+        return {d, rows * c8, c8};
+    }
+    template <class F>
+    hipError_t launch(hipStream_t st) const {
+        if (!n || !most) return hipSuccess;
+        int64_t bx = (most + 255) / 256;
+        if (bx > 4096) bx = 4096;
+        k_pack<F><<<dim3((unsigned)bx, (unsigned)n), 256, 0, st>>>(jobs);
+        return hipGetLastError();
+    }
+};
+
+template <class F, int ACT>
+hipError_t forward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const gs_ffn_weights& w, void* y,
+                        int64_t ldy, void* saved, char* ws, hipStream_t st) {
+    using E = typename F::Elem;
+    const Layout<F> L(d);
+    Carver cv{ws};
+    Packer pk;
+    const Operand ox = pk.add<F>(cv, x, L.M, L.D, ldx);
+    const bool wdir = direct<F>(w.gate, L.D, L.D) && direct<F>(w.up, L.D, L.D);
+    Operand og, ou;
+    if (wdir) {
+        og = {(const uint16_t*)w.gate, 0, L.D};
+        ou = {(const uint16_t*)w.up, 0, L.D};
+    } else {  // the dual product reads both with one row length
+        og = pk.add<F>(cv, w.gate, L.H, L.D, L.D, true);
+        ou = pk.add<F>(cv, w.up, L.H, L.D, L.D, true);
+    }
+    const Operand od = pk.add<F>(cv, w.down, L.O, L.H, L.H);
+    GSR_TRY(pk.launch<F>(st));
+    uint16_t* h;
+    E* gu = nullptr;
+    if (saved) {
+        gu = (E*)saved;
+        h = (uint16_t*)((char*)saved + L.saved_gu_bytes());
+    } else {
+        h = cv.take<uint16_t>(L.h_elems());
+    }
+    const int64_t h_plane = L.M * L.H8;
+    GemmArgs g1 = make_args(L.M, L.H, L.D);
+    add_segments<F>(g1, ox, og, &ou);
+    one_split(g1);
+    EpiGate<F, ACT> e1{h, h_plane, gu, L.H8, (int)L.M};
+    GSR_TRY((launch_gemm<typename F::Mma, true, true>(g1, e1, st)));
+    GemmArgs g2 = make_args(L.M, L.O, L.H8);
+    add_segments<F>(g2, Operand{h, h_plane, L.H8}, od, nullptr);
+    g2.K = (int)L.H;
+    one_split(g2);
+    EpiStore<F> e2{(E*)y, nullptr, ldy, (int)L.M, 0, (int)L.O, vec_ok(y, ldy, sizeof(E))};
+    return launch_gemm<typename F::Mma, true, true>(g2, e2, st);
+}
+
+template <class F>
+hipError_t weight_grad(const Operand& a, int64_t a_cols, const Operand& b, int64_t b_cols, int64_t rows,
+                       EpiStore<F> store, float* part, hipStream_t st) {
+    GemmArgs g = make_args(a_cols, b_cols, rows);
+    add_segments<F>(g, a, b, nullptr);
+    const int64_t n4 = (store.N + 3) / 4 * 4;
+    g.splits = grad_splits(a_cols, b_cols, rows, g.nseg);
+    const int total = g.nseg * ((g.K + kGemmBK - 1) / kGemmBK);
+    g.tiles_per_split = (total + g.splits - 1) / g.splits;
+    if (g.splits == 1) return launch_gemm<typename F::Mma, false, false>(g, store, st);
+    EpiPartial ep{part, n4, (int)a_cols};
+    GSR_TRY((launch_gemm<typename F::Mma, false, false>(g, ep, st)));
+    const int64_t n = a_cols * n4 / 4;
+    int64_t bx = (n + 255) / 256;
+    if (bx > 8192) bx = 8192;
+    k_reduce<F><<<dim3((unsigned)bx), 256, 0, st>>>(part, g.splits, (int)a_cols, n4, store);
+    return hipGetLastError();
+}
+
+template <class F>
+int64_t part_elems(const Layout<F>& L) {
+    const int nseg = F::kPlanes == 1 ? 1 : 6;
+    const int64_t s1 = grad_splits(2 * L.H8, L.D8, L.M, nseg), s2 = grad_splits(L.O8, L.H8, L.M, nseg);
+    const int64_t p1 = s1 > 1 ? s1 * 2 * L.H8 * L.D8 : 0, p2 = s2 > 1 ? s2 * L.O8 * L.H8 : 0;
+    return p1 > p2 ? p1 : p2;
+}
+
+template <class F, int ACT>
+hipError_t backward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const gs_ffn_weights& w,
+                         const void* saved, const void* dy, int64_t lddy, const gs_ffn_grads& out, int64_t lddx,
+                         char* ws, hipStream_t st) {
+    using E = typename F::Elem;
+    using T = typename F::Mma;
+    const Layout<F> L(d);
+    Carver cv{ws};
+    float* part = cv.take<float>(part_elems<F>(L));
+    const int64_t plane = L.M * 2 * L.H8;
+    uint16_t* dgu = cv.take<uint16_t>(plane * F::kPlanes);
+    const E* gu = (const E*)saved;
+    const uint16_t* h = (const uint16_t*)((const char*)saved + L.saved_gu_bytes());
+    const int64_t h_plane = L.M * L.H8;
+    Packer pk;
+    const Operand ody = pk.add<F>(cv, dy, L.M, L.O, lddy);
+    const Operand od = pk.add<F>(cv, w.down, L.O, L.H, L.H);
+    const Operand ox = pk.add<F>(cv, x, L.M, L.D, ldx);
+    // one row length for both weight matrices of dx
+    const bool wpack = !(direct<F>(w.gate, L.D, L.D) && direct<F>(w.up, L.D, L.D));
+    const Operand og = pk.add<F>(cv, w.gate, L.H, L.D, L.D, wpack);
+    const Operand ou = pk.add<F>(cv, w.up, L.H, L.D, L.D, wpack);
+    GSR_TRY(pk.launch<F>(st));
+
+    GemmArgs g1 = make_args(L.M, L.H8, L.O);
+    add_segments<F>(g1, ody, od, nullptr);
+    one_split(g1);
+    EpiGateGrad<F, ACT> e1{gu, dgu, plane, L.H8, (int)L.M};
+    GSR_TRY((launch_gemm<T, true, false>(g1, e1, st)));
+    const Operand odgu{dgu, plane, 2 * L.H8};
+    if (out.x) {
+        GemmArgs g2 = make_args(L.M, L.D8, L.H);
+        add_segments<F>(g2, odgu, og, nullptr, 0);
+        add_segments<F>(g2, odgu, ou, nullptr, L.H8);
+        one_split(g2);
+        EpiStore<F> e2{(E*)out.x, nullptr, lddx, (int)L.M, 0, (int)L.D, vec_ok(out.x, lddx, sizeof(E))};
+        GSR_TRY((launch_gemm<T, true, false>(g2, e2, st)));
+    }
+    if (out.gate || out.up) {
+        EpiStore<F> e3{(E*)out.gate, (E*)out.up, L.D, (int)L.H, (int)L.H8, (int)L.D,
+                       vec_ok(out.gate, L.D, sizeof(E)) && vec_ok(out.up, L.D, sizeof(E))};
+        GSR_TRY(weight_grad<F>(odgu, 2 * L.H8, ox, L.D8, L.M, e3, part, st));
+    }
+    if (out.down) {
+        EpiStore<F> e4{(E*)out.down, nullptr, L.H, (int)L.O, 0, (int)L.H, vec_ok(out.down, L.H, sizeof(E))};
+        GSR_TRY(weight_grad<F>(ody, L.O8, Operand{h, h_plane, L.H8}, L.H8, L.M, e4, part, st));
+    }
+    return hipSuccess;
+}
+
+template <class F>
+void sizes_impl(const gs_ffn_dims& d, size_t* saved, size_t* fwd, size_t* bwd) {
+    const Layout<F> L(d);
+    auto pad = [](int64_t rows, int64_t c8) { return round_up(rows * c8 * F::kPlanes * 2, kAlign); };
+    *saved = (size_t)(L.saved_gu_bytes() + round_up(L.h_elems() * 2, kAlign));
+    // every operand counted as copied: whether one is depends on its address and stride
+    const int64_t weights = 2 * pad(L.H, L.D8) + pad(L.O, L.H8) + pad(L.M, L.D8);
+    *fwd = (size_t)(weights + round_up(L.h_elems() * 2, kAlign));
+    *bwd = (size_t)(weights + pad(L.M, L.O8) + pad(L.M, 2 * L.H8) + round_up(part_elems<F>(L) * 4, kAlign));
+}
+
+}  // namespace
+
+void ffn_sizes(const gs_ffn_dims& d, size_t* saved, size_t* fwd, size_t* bwd) {
+    if (d.dtype == GS_F32) return sizes_impl<FmtF32>(d, saved, fwd, bwd);
+    return sizes_impl<FmtBf16>(d, saved, fwd, bwd);
+}
+
+hipError_t launch_ffn_forward(const gs_ffn_dims& d, const void* x, int64_t ldx, const gs_ffn_weights& w, void* y,
+                              int64_t ldy, void* saved, void* ws, hipStream_t st) {
+    char* b = (char*)ws;
+    const bool silu = d.activation == GS_ACT_SILU;
+    if (d.dtype == GS_BF16)
+        return silu ? forward_impl<FmtBf16, GS_ACT_SILU>(d, x, ldx, w, y, ldy, saved, b, st)
+                    : forward_impl<FmtBf16, GS_ACT_GELU>(d, x, ldx, w, y, ldy, saved, b, st);
+    if (d.dtype == GS_F16)
+        return silu ? forward_impl<FmtF16, GS_ACT_SILU>(d, x, ldx, w, y, ldy, saved, b, st)
+                    : forward_impl<FmtF16, GS_ACT_GELU>(d, x, ldx, w, y, ldy, saved, b, st);
+    return silu ? forward_impl<FmtF32, GS_ACT_SILU>(d, x, ldx, w, y, ldy, saved, b, st)
+                : forward_impl<FmtF32, GS_ACT_GELU>(d, x, ldx, w, y, ldy, saved, b, st);
+}
+
+hipError_t launch_ffn_backward(const gs_ffn_dims& d, const void* x, int64_t ldx, const gs_ffn_weights& w,
+                               const void* saved, const void* dy, int64_t lddy, const gs_ffn_grads& out,
+                               int64_t lddx, void* ws, hipStream_t st) {
+    char* b = (char*)ws;
+    const bool silu = d.activation == GS_ACT_SILU;
+    if (d.dtype == GS_BF16)
+        return silu ? backward_impl<FmtBf16, GS_ACT_SILU>(d, x, ldx, w, saved, dy, lddy, out, lddx, b, st)
+                    : backward_impl<FmtBf16, GS_ACT_GELU>(d, x, ldx, w, saved, dy, lddy, out, lddx, b, st);
+    if (d.dtype == GS_F16)
+        return silu ? backward_impl<FmtF16, GS_ACT_SILU>(d, x, ldx, w, saved, dy, lddy, out, lddx, b, st)
+                    : backward_impl<FmtF16, GS_ACT_GELU>(d, x, ldx, w, saved, dy, lddy, out, lddx, b, st);
+    return silu ? backward_impl<FmtF32, GS_ACT_SILU>(d, x, ldx, w, saved, dy, lddy, out, lddx, b, st)
+                : backward_impl<FmtF32, GS_ACT_GELU>(d, x, ldx, w, saved, dy, lddy, out, lddx, b, st);
+}
+
+}  // namespace gsr

@@ -207,6 +207,25 @@ hipError_t launch_render_features(const Sizes& s, const Workspace& ws, const uin
                                   int C, const float* bg_host, float* out, hipStream_t st);
 hipError_t launch_attribute(const Sizes& s, const Workspace& ws, const uint32_t* sorted_g, const float* map, int C,
                             float* out, hipStream_t st);
+// ---- the updater's operators (ffn.hip, scan.hip, ortho.hip); arguments are checked by the ABI calls --------
+void ffn_sizes(const gs_ffn_dims& d, size_t* saved, size_t* fwd, size_t* bwd);
+hipError_t launch_ffn_forward(const gs_ffn_dims& d, const void* x, int64_t ldx, const gs_ffn_weights& w, void* y,
+                              int64_t ldy, void* saved, void* ws, hipStream_t st);
+hipError_t launch_ffn_backward(const gs_ffn_dims& d, const void* x, int64_t ldx, const gs_ffn_weights& w,
+                               const void* saved, const void* dy, int64_t lddy, const gs_ffn_grads& out,
+                               int64_t lddx, void* ws, hipStream_t st);
+void scan_sizes(const gs_scan_dims& d, size_t* saved, size_t* ws);
+hipError_t launch_scan_forward(const gs_scan_dims& d, const int64_t* offsets, const gs_scan_inputs& in, void* y,
+                               int64_t ldy, float* h_last, float* saved, void* ws, hipStream_t st);
+hipError_t launch_scan_backward(const gs_scan_dims& d, const int64_t* offsets, const gs_scan_inputs& in,
+                                const float* saved, const void* dy, int64_t lddy, const float* dh_last,
+                                const gs_scan_grads& out, void* ws, hipStream_t st);
+size_t ortho_workspace(const gs_ortho_dims& d);
+hipError_t launch_ortho(const gs_ortho_dims& d, const void* g, void* out, void* ws, hipStream_t st);
+
+// the calling thread's last error message (gs_last_error) and the status to return with it
+gs_status fail(gs_status s, const char* fmt, ...);
+
 hipError_t launch_topk(const Sizes& s, const Workspace& ws, const uint32_t* sorted_g, int k, int32_t* ids, float* w,
                        hipStream_t st);
 

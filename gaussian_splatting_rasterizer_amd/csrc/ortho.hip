@@ -1,0 +1,256 @@
+// ortho.hip -- orthogonalisation of an update by Newton-Schulz products.
+//
+//   X = G / max(|G|_F, eps);  repeat: P = X X^T, Q = b P + c P P, X = a X + Q X        (rows <= cols)
+//   and with P = X^T X, X = a X + X Q for rows > cols, so that P is the smaller square.
+//
+// All products run on k_gemm16 in float16 with float32 accumulation.  P and Q are symmetric: only tiles on and above
+// the diagonal are computed and each writes its mirror image.  Every singular value of X stays below 1.2 after the
+// normalisation, so X is held as 2^12 X and P, Q as 2^13 P, 2^13 Q: far from float16's overflow (|Q| <= 5) and, for
+// the entries that matter, above its subnormals.  float16 keeps 11 bits; in bfloat16 the same steps lose 8 times as
+// much.  For a float32 result each of X, P, Q is a pair hi + lo of float16 (22 bits) and a product is
+// lo hi + hi lo + hi hi.
+#include "gsr_internal.hpp"
+#include "gemm16.hpp"
+
+namespace gsr {
+
+namespace {
+
+constexpr float kXScale = 4096.f;     // X is stored as 2^12 X
+constexpr float kPScale = 8192.f;     // P and Q as 2^13 P, 2^13 Q
+constexpr int kNormBlocks = 64;       // partial sums of squares per matrix
+
+template <int PL>
+__device__ __forceinline__ void put_planes(uint16_t* p, int64_t plane, f32x4 v) {
+    const u16x4 hi = to16<_Float16>(v);
+    *(u16x4*)p = hi;
+    if constexpr (PL == 2) *(u16x4*)(p + plane) = to16<_Float16>(v - from16<_Float16>(hi));
+}
+template <int PL>
+__device__ __forceinline__ f32x4 get_planes(const uint16_t* p, int64_t plane) {
+    f32x4 v = from16<_Float16>(*(const u16x4*)p);
+    if constexpr (PL == 2) v += from16<_Float16>(*(const u16x4*)(p + plane));
+    return v;
+}
+
+template <class E>
+__device__ __forceinline__ float load_value(const E* p);
+template <>
+__device__ __forceinline__ float load_value<float>(const float* p) {
+    return *p;
+}
+template <>
+__device__ __forceinline__ float load_value<__bf16>(const __bf16* p) {
+    return (float)*p;
+}
+
+// Partial sums of squares in float64: block j of matrix b sums the elements j, j + kNormBlocks, ... (256 at a time).
+template <class E>
+__global__ __launch_bounds__(256) void k_norm(const E* g, int64_t n, double* part) {
+    const E* p = g + blockIdx.y * n;
+    double s = 0.0;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += 256 * kNormBlocks) {
+        const double v = load_value(p + i);
+        s += v * v;
+    }
+    __shared__ double red[256];
+    red[threadIdx.x] = s;
+    __syncthreads();
+    for (int w = 128; w > 0; w >>= 1) {
+        if ((int)threadIdx.x < w) red[threadIdx.x] += red[threadIdx.x + w];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) part[blockIdx.y * kNormBlocks + blockIdx.x] = red[0];
+}
+
+// X = 2^12 G / max(|G|, eps) into padded float16 planes
+template <class E, int PL>
+__global__ __launch_bounds__(256) void k_normalise(const E* g, int64_t rows, int64_t cols, const double* part,
+                                                   float eps, uint16_t* x, int64_t plane) {
+    const int64_t c8 = (cols + 7) / 8 * 8, n = rows * c8 / 4;
+    const int64_t b = blockIdx.y;
+    double s = 0.0;
+    for (int j = 0; j < kNormBlocks; ++j) s += part[b * kNormBlocks + j];
+    const double norm = sqrt(s);
+    const double inv = (double)kXScale / (norm < (double)eps ? (double)eps : norm);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i * 4 / c8, c = i * 4 - r * c8;
+        const E* p = g + (b * rows + r) * cols + c;
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = c + e < cols ? (float)((double)load_value(p + e) * inv) : 0.f;
+        put_planes<PL>(x + b * rows * c8 + i * 4, plane, v);
+    }
+}
+
+// C = alpha acc + beta S on and above the diagonal, mirrored below (S: null for P, the stored P for Q)
+template <int PL>
+struct EpiSymmetric {
+    static constexpr bool kDual = false, kSymmetric = true;
+    uint16_t* c;
+    const uint16_t* s;
+    int64_t plane, ld, batch_stride;
+    int n;
+    float alpha, beta;
+    int bm;  // tile size, to tell diagonal tiles
+    __device__ __forceinline__ void one(int batch, int, int m, int col, f32x4 v) const {
+        if (m >= n || col >= ld) return;
+        const int64_t base = batch * batch_stride;
+        v *= alpha;
+        if (s) v += beta * get_planes<PL>(s + base + m * ld + col, plane);
+        put_planes<PL>(c + base + m * ld + col, plane, v);
+        if (m / bm == col / bm) return;  // a diagonal tile holds both halves already
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (col + e >= n) break;
+            uint16_t* d = c + base + (int64_t)(col + e) * ld + m;
+            const _Float16 hi = (_Float16)v[e];
+            *d = __builtin_bit_cast(uint16_t, hi);
+            if constexpr (PL == 2) d[plane] = __builtin_bit_cast(uint16_t, (_Float16)(v[e] - (float)hi));
+        }
+    }
+};
+
+// X' = a X + alpha acc, stored again in float16 planes, or in the result's type after the last step
+template <int PL, class Out>
+struct EpiUpdate {
+    static constexpr bool kDual = false, kSymmetric = false;
+    const uint16_t* x;
+    uint16_t* xn;
+    int64_t plane, ld, batch_stride;
+    Out* out;  // null: another step follows
+    int M, N;  // rows, columns of the matrix
+    float a, alpha;
+    bool vec;
+    __device__ __forceinline__ void one(int batch, int, int m, int n, f32x4 v) const {
+        if (m >= M || n >= ld) return;
+        const int64_t at = batch * batch_stride + (int64_t)m * ld + n;
+        v = a * get_planes<PL>(x + at, plane) + alpha * v;
+        if (!out) {
+            put_planes<PL>(xn + at, plane, v);
+            return;
+        }
+        v *= 1.f / kXScale;
+        Out* d = out + ((int64_t)batch * M + m) * N + n;
+        if (vec && n + 4 <= N) {
+            if constexpr (sizeof(Out) == 4)
+                *(f32x4*)d = v;
+            else
+                *(u16x4*)d = to16<Out>(v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < N) d[e] = (Out)v[e];
+        }
+    }
+};
+
+template <int PL>
+void ortho_segments(GemmArgs& g, const uint16_t* a, int64_t pa, const uint16_t* b, int64_t pb) {
+    if (PL == 2) {
+        g.a[g.nseg] = a + pa, g.b[g.nseg] = b, ++g.nseg;
+        g.a[g.nseg] = a, g.b[g.nseg] = b + pb, ++g.nseg;
+    }
+    g.a[g.nseg] = a, g.b[g.nseg] = b, ++g.nseg;
+    one_split(g);
+}
+
+// tile counts of a symmetric product leave half of the workgroups without work
+template <bool KC, class Epi>
+hipError_t launch_symmetric(const GemmArgs& p, Epi epi, hipStream_t st) {
+    if (tile_count(p, 256, 256) >= 2 * kBigTiles) {
+        epi.bm = 256;
+        return launch_tiles<_Float16, KC, KC, 256, 256, 2, 4, Epi>(p, epi, st);
+    }
+    epi.bm = 128;
+    return launch_tiles<_Float16, KC, KC, 128, 128, 2, 2, Epi>(p, epi, st);
+}
+
+struct OrthoLayout {
+    int64_t B, R, C, lo, C8, lo8, x_plane, p_plane;
+    int planes;
+    explicit OrthoLayout(const gs_ortho_dims& d)
+        : B(d.batch), R(d.rows), C(d.cols), lo(d.rows < d.cols ? d.rows : d.cols), C8(round8(C)), lo8(round8(lo)),
+          x_plane(B * R * C8), p_plane(B * lo * lo8), planes(d.out_dtype == GS_F32 ? 2 : 1) {}
+};
+
+template <class In, class Out, int PL>
+hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* ws, hipStream_t st) {
+    const OrthoLayout L(d);
+    Carver cv{ws};
+    double* part = cv.take<double>(L.B * kNormBlocks);
+    uint16_t* x = cv.take<uint16_t>(L.x_plane * PL);
+    uint16_t* xn = cv.take<uint16_t>(L.x_plane * PL);
+    uint16_t* P = cv.take<uint16_t>(L.p_plane * PL);
+    uint16_t* Q = cv.take<uint16_t>(L.p_plane * PL);
+    const In* g = (const In*)gin;
+    k_norm<In><<<dim3(kNormBlocks, (unsigned)L.B), 256, 0, st>>>(g, L.R * L.C, part);
+    GSR_TRY(hipGetLastError());
+    int64_t bx = (L.R * L.C8 / 4 + 255) / 256;
+    if (bx > 2048) bx = 2048;
+    k_normalise<In, PL><<<dim3((unsigned)bx, (unsigned)L.B), 256, 0, st>>>(g, L.R, L.C, part, d.eps, x, L.x_plane);
+    GSR_TRY(hipGetLastError());
+    const bool tall = d.rows > d.cols;
+    for (int step = 0; step < d.steps; ++step) {
+        EpiSymmetric<PL> es{P, nullptr, L.p_plane, L.lo8, L.lo * L.lo8, (int)L.lo, kPScale / (kXScale * kXScale), 0.f,
+                            128};
+        GemmArgs gp = make_args(L.lo, L.lo, tall ? L.R : L.C);
+        gp.batch = (int)L.B;
+        gp.lda = gp.ldb = L.C8;
+        gp.batch_a = gp.batch_b = L.R * L.C8;
+        ortho_segments<PL>(gp, x, L.x_plane, x, L.x_plane);
+        if (tall) {
+            gp.M = gp.N = (int)L.lo8;  // columns of X: the padded ones are zero
+            GSR_TRY((launch_symmetric<false>(gp, es, st)));
+        } else {
+            GSR_TRY((launch_symmetric<true>(gp, es, st)));
+        }
+        EpiSymmetric<PL> eq{Q, P, L.p_plane, L.lo8, L.lo * L.lo8, (int)L.lo, d.c / kPScale, d.b, 128};
+        GemmArgs gq = make_args(L.lo, L.lo, L.lo);
+        gq.batch = (int)L.B;
+        gq.lda = gq.ldb = L.lo8;
+        gq.batch_a = gq.batch_b = L.lo * L.lo8;
+        ortho_segments<PL>(gq, P, L.p_plane, P, L.p_plane);
+        GSR_TRY((launch_symmetric<true>(gq, eq, st)));
+        const bool last = step + 1 == d.steps;
+        EpiUpdate<PL, Out> eu{x, xn, L.x_plane, L.C8, L.R * L.C8, last ? (Out*)out : nullptr, (int)L.R, (int)L.C,
+                              d.a, 1.f / kPScale, vec_ok(out, L.C, sizeof(Out))};
+        GemmArgs gu = make_args(L.R, L.C8, L.lo);
+        gu.batch = (int)L.B;
+        if (tall) {  // X Q, Q symmetric
+            gu.N = (int)L.C;
+            gu.lda = L.C8, gu.ldb = L.lo8;
+            gu.batch_a = L.R * L.C8, gu.batch_b = L.lo * L.lo8;
+            ortho_segments<PL>(gu, x, L.x_plane, Q, L.p_plane);
+            GSR_TRY((launch_gemm<_Float16, true, true>(gu, eu, st)));
+        } else {  // Q X
+            gu.lda = L.lo8, gu.ldb = L.C8;
+            gu.batch_a = L.lo * L.lo8, gu.batch_b = L.R * L.C8;
+            ortho_segments<PL>(gu, Q, L.p_plane, x, L.x_plane);
+            GSR_TRY((launch_gemm<_Float16, true, false>(gu, eu, st)));
+        }
+        uint16_t* t = x;
+        x = xn;
+        xn = t;
+    }
+    return hipSuccess;
+}
+
+}  // namespace
+
+size_t ortho_workspace(const gs_ortho_dims& d) {
+    const OrthoLayout L(d);
+    return (size_t)(round_up(L.B * kNormBlocks * 8, kAlign) + 2 * round_up(L.x_plane * L.planes * 2, kAlign) +
+                    2 * round_up(L.p_plane * L.planes * 2, kAlign));
+}
+
+hipError_t launch_ortho(const gs_ortho_dims& d, const void* g, void* out, void* ws, hipStream_t st) {
+    char* b = (char*)ws;
+    if (d.dtype == GS_F32)
+        return d.out_dtype == GS_F32 ? ortho_impl<float, float, 2>(d, g, out, b, st)
+                                     : ortho_impl<float, __bf16, 1>(d, g, out, b, st);
+    return d.out_dtype == GS_F32 ? ortho_impl<__bf16, float, 2>(d, g, out, b, st)
+                                 : ortho_impl<__bf16, __bf16, 1>(d, g, out, b, st);
+}
+
+}  // namespace gsr

@@ -294,6 +294,128 @@ GSR_API gs_status gs_render_features(gs_context* ctx, const float* features, int
 GSR_API gs_status gs_attribute(gs_context* ctx, const float* pixel_map, int32_t n_channels, float* out,
                                hipStream_t stream);
 
+/* ---- operators of the learned updater -------------------------------------
+ *
+ * The score tokens feed a learned recurrent updater ("Final Token and Updater"
+ * of the Renderer Score Tokens proposal: a projection of the token, a hidden
+ * state carried from update to update), which trains on the gradients that
+ * gs_backward returns.  These calls are its building blocks.  They need no
+ * context: sizes come in a host struct, every array is a caller-owned device
+ * array, nothing is allocated, and all work is asynchronous on `stream`.  A
+ * workspace must not be used by two overlapping calls; its contents need not
+ * be kept or cleared between calls.
+ *
+ * Arithmetic: sums, activations, recurrent states and norms are float32 (or
+ * wider); results are rounded to the array's type once when stored.  Results
+ * do not depend on scheduling: the same call gives the same bits. */
+typedef enum { GS_F32 = 0, GS_BF16 = 1, GS_F16 = 2 } gs_dtype;
+typedef enum { GS_ACT_SILU = 0, GS_ACT_GELU = 1 } gs_activation;  /* GELU: the exact form, g Phi(g) */
+
+/* Gated feed-forward block on `rows` rows:
+ *   h = act(x Wg^T) * (x Wu^T),  y = h Wd^T
+ * x [rows, d_in], Wg and Wu [d_hidden, d_in], Wd [d_out, d_hidden], y [rows, d_out],
+ * all of one type, weights contiguous, row strides of x and y in elements.
+ * Widths are 1 .. 2^20, rows 0 .. 2^31 - 512, row strides up to 2^21. */
+typedef struct {
+    int64_t rows;
+    int32_t d_in, d_hidden, d_out;
+    int32_t dtype;       /* gs_dtype */
+    int32_t activation;  /* gs_activation */
+} gs_ffn_dims;
+typedef struct {
+    const void* gate;
+    const void* up;
+    const void* down;
+} gs_ffn_weights;
+/* Gradients, contiguous, written (not accumulated); null members are skipped. */
+typedef struct {
+    void* x;     /* row stride ld_x */
+    int64_t ld_x;
+    void* gate;
+    void* up;
+    void* down;
+} gs_ffn_grads;
+/* Bytes of the saved activations and of the two calls' workspaces (any pointer may be null). */
+GSR_API gs_status gs_ffn_sizes(const gs_ffn_dims* dims, size_t* saved_bytes, size_t* forward_bytes,
+                               size_t* backward_bytes);
+/* Forward pass.  saved (may be null: inference) receives the pre-activations and h in the block's type, which
+ * gs_ffn_backward reads.  saved and workspace are 256-byte aligned.  Errors: GS_ERR_INVALID_ARGUMENT (null or
+ * misaligned arrays, bad sizes or enums), GS_ERR_UNSUPPORTED (beyond the limits above),
+ * GS_ERR_WORKSPACE_TOO_SMALL, GS_ERR_HIP; nothing is launched for the first three. */
+GSR_API gs_status gs_ffn_forward(const gs_ffn_dims* dims, const void* x, int64_t ld_x, const gs_ffn_weights* weights,
+                                 void* y, int64_t ld_y, void* saved, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+/* Gradients of a scalar loss for dy = dL/dy [rows, d_out]; x and weights as given to the forward pass. */
+GSR_API gs_status gs_ffn_backward(const gs_ffn_dims* dims, const void* x, int64_t ld_x,
+                                  const gs_ffn_weights* weights, const void* saved, const void* dy, int64_t ld_dy,
+                                  const gs_ffn_grads* grads, void* workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+
+/* Gated linear recurrence, per channel:
+ *   a_t = sigma(gate_t),  h_t = a_t h_{t-1} + (1 - a_t) x_t
+ * over n_seq sequences that lie one after another in `rows` rows.  offsets
+ * (device, [n_seq + 1], non-decreasing, first 0, last rows) gives the first row
+ * of each sequence; null means n_seq sequences of equal length.  Sequences may
+ * be empty.  Offsets outside [0, rows] are not followed; other values that are
+ * not non-decreasing give unspecified results but no access out of range.
+ * gate, x and y [rows, channels] in the type of dims, row strides in elements;
+ * h0 (state before the first row, null: zero) and h_last (state after the last
+ * row, null: not wanted) float32 [n_seq, channels].  h_last may be h0.
+ * rows and n_seq are 0 .. 2^31 - 512, channels 1 .. 2^20. */
+typedef struct {
+    int64_t rows;
+    int64_t n_seq;
+    int32_t channels;
+    int32_t dtype;  /* gs_dtype */
+} gs_scan_dims;
+typedef struct {
+    const void* gate;
+    const void* x;
+    const float* h0;
+    int64_t ld_gate, ld_x;
+} gs_scan_inputs;
+typedef struct {
+    void* gate;
+    void* x;
+    float* h0;
+    int64_t ld_gate, ld_x;
+} gs_scan_grads;
+GSR_API gs_status gs_scan_sizes(const gs_scan_dims* dims, size_t* saved_bytes, size_t* workspace_bytes);
+/* saved (may be null) receives the float32 states that gs_scan_backward starts from. */
+GSR_API gs_status gs_scan_forward(const gs_scan_dims* dims, const int64_t* offsets, const gs_scan_inputs* in, void* y,
+                                  int64_t ld_y, float* h_last, void* saved, void* workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+/* Gradients for dy [rows, channels] and dh_last (float32 [n_seq, channels], null: zero); null members of grads are
+ * skipped.  in and offsets as given to the forward pass. */
+GSR_API gs_status gs_scan_backward(const gs_scan_dims* dims, const int64_t* offsets, const gs_scan_inputs* in,
+                                   const void* saved, const void* dy, int64_t ld_dy, const float* dh_last,
+                                   const gs_scan_grads* grads, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+
+/* Orthogonalisation of `batch` matrices [rows, cols] (contiguous) by `steps`
+ * Newton-Schulz steps, X = G / max(|G|_F, eps), then
+ *   P = X X^T, Q = b P + c P P, X = a X + Q X
+ * (from the other side when rows > cols), as used on a momentum matrix before
+ * it is taken off a weight.  dtype and out_dtype: GS_F32 or GS_BF16.  A bfloat16 result
+ * is computed from float16 operands (11 bits), a float32 result from pairs of
+ * them (22 bits).  The coefficients have to keep singular values in [0, 1]
+ * below 8, or float16 overflows.  smaller side 1 .. 2^15, larger 1 .. 2^20,
+ * steps 1 .. 64, batch 0 .. 2^16 - 1.
+ * A matrix with an infinite or NaN entry gives NaN (that matrix only). */
+typedef struct {
+    int64_t rows, cols;
+    int32_t batch;
+    int32_t dtype, out_dtype; /* gs_dtype */
+    int32_t steps;
+    float a, b, c;
+    float eps;
+} gs_ortho_dims;
+/* steps 5, coefficients 3.4445, -4.7750, 2.0315, eps 1e-7; everything else 0. */
+GSR_API gs_status gs_default_ortho_dims(gs_ortho_dims* out);
+GSR_API gs_status gs_ortho_size(const gs_ortho_dims* dims, size_t* workspace_bytes);
+GSR_API gs_status gs_orthogonalize(const gs_ortho_dims* dims, const void* g, void* out, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
 GSR_API const char* gs_status_string(gs_status s);
 GSR_API const char* gs_last_error(void);
 
