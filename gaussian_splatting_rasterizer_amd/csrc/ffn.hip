@@ -11,6 +11,8 @@
 //
 // Rows that are not 16-byte aligned, or whose length is not a multiple of 8 elements, are copied once into a
 // zero-padded layout in the workspace (k_pack); other operands are read in place.
+#include <algorithm>
+
 #include "gsr_internal.hpp"
 #include "gemm16.hpp"
 
@@ -40,17 +42,15 @@ __global__ __launch_bounds__(256) void k_pack(const PackJobs jobs) {
         uint16_t* d = jb.dst + i * 8;
         const int64_t left = jb.cols - c;
         if constexpr (F::kPlanes == 1) {
-            uint16_t v[8];
+            u16x8 v;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = e < left ? s[e] : (uint16_t)0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = v[e];
+            *(u16x8*)d = v;
         } else {
             f32x4 v[2];
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] = e < left ? s[e] : 0.f;
-            put_operand<F>(d, jb.plane, v[0]);
-            put_operand<F>(d + 4, jb.plane, v[1]);
+            put_operand8<F>(d, jb.plane, v[0], v[1]);
         }
     }
 }
@@ -77,51 +77,75 @@ __device__ __forceinline__ void activation(float g, float& a, float& da) {
 template <class F, int ACT>
 struct EpiGate {
     static constexpr bool kDual = true, kSymmetric = false;
+    static constexpr int kAhead = 0;
     uint16_t* h;
     int64_t h_plane;
     typename F::Elem* gu;  // [M][2 F8] or null
     int64_t f8;
     int M;
-    __device__ __forceinline__ void pair(int m, int n, f32x4 g, f32x4 u) const {
+    __device__ __forceinline__ void row(int m, int n, f32x4 g0, f32x4 g1, f32x4 u0, f32x4 u1) const {
         if (m >= M || n >= f8) return;
         if (gu) {
-            F::put(gu + (int64_t)m * 2 * f8 + n, g);
-            F::put(gu + (int64_t)m * 2 * f8 + f8 + n, u);
+            F::put8(gu + (int64_t)m * 2 * f8 + n, g0, g1);
+            F::put8(gu + (int64_t)m * 2 * f8 + f8 + n, u0, u1);
         }
-        f32x4 v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float a, da;
-            activation<ACT>(g[e], a, da);
-            v[e] = a * u[e];
+            activation<ACT>(g0[e], a, da);
+            u0[e] *= a;
+            activation<ACT>(g1[e], a, da);
+            u1[e] *= a;
         }
-        put_operand<F>(h + (int64_t)m * f8 + n, h_plane, v);
+        put_operand8<F>(h + (int64_t)m * f8 + n, h_plane, u0, u1);
     }
 };
 
-// dg and du from dh and the saved g and u
+// dg and du from dh and the saved g and u.  The saved values are fetched ahead: read where they are used, each row of
+// products waited for its own (131072 x 2048 x 512: 1050 us).
 template <class F, int ACT>
 struct EpiGateGrad {
     static constexpr bool kDual = false, kSymmetric = false;
+    static constexpr int kAhead = F::kPlanes == 1 ? 3 : 1;
     const typename F::Elem* gu;
     uint16_t* dgu;  // [M][2 F8]
     int64_t plane;
     int64_t f8;
     int M;
-    __device__ __forceinline__ void one(int, int, int m, int n, f32x4 dh) const {
-        if (m >= M || n >= f8) return;
+    struct Pre {
+        typename F::Raw8 g[2], u[2];
+    };
+    __device__ __forceinline__ Pre fetch(int, int m, int n) const {
+        Pre r;
         const int64_t at = (int64_t)m * 2 * f8 + n;
-        const f32x4 g = F::get(gu + at), u = F::get(gu + at + f8);
-        f32x4 dg, du;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float a, da;
-            activation<ACT>(g[e], a, da);
-            du[e] = dh[e] * a;
-            dg[e] = dh[e] * u[e] * da;
+        for (int h = 0; h < 2; ++h)
+            if (m < M && n + h * 8 < f8) {
+                r.g[h] = *(const typename F::Raw8*)(gu + at + h * 8);
+                r.u[h] = *(const typename F::Raw8*)(gu + at + f8 + h * 8);
+            }
+        return r;
+    }
+    __device__ __forceinline__ void row(int, int, int m, int n, const f32x4 (&dh)[4], const Pre& pre) const {
+        const int64_t at = (int64_t)m * 2 * f8 + n;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (m >= M || n + h * 8 >= f8) continue;
+            f32x4 dg[2], du[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const f32x4 g = F::unpack(pre.g[h], q), u = F::unpack(pre.u[h], q), d = dh[h * 2 + q];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float a, da;
+                    activation<ACT>(g[e], a, da);
+                    du[q][e] = d[e] * a;
+                    dg[q][e] = d[e] * u[e] * da;
+                }
+            }
+            put_operand8<F>(dgu + at + h * 8, plane, dg[0], dg[1]);
+            put_operand8<F>(dgu + at + f8 + h * 8, plane, du[0], du[1]);
         }
-        put_operand<F>(dgu + at, plane, dg);
-        put_operand<F>(dgu + at + f8, plane, du);
     }
 };
 
@@ -129,27 +153,40 @@ struct EpiGateGrad {
 template <class F>
 struct EpiStore {
     static constexpr bool kDual = false, kSymmetric = false;
+    static constexpr int kAhead = 0;
+    using Pre = NoPre;
     typename F::Elem* c0;
     typename F::Elem* c1;
     int64_t ld;
     int rows0, off1, N;
-    bool vec;  // rows allow 4-element stores
-    __device__ __forceinline__ void one(int, int, int m, int n, f32x4 v) const {
-        typename F::Elem* c = c0;
-        int r = m;
-        if (m >= rows0) {
-            r = m - off1;
-            c = c1;
-            if (r < 0 || r >= rows0) return;
-        }
-        if (!c || n >= N) return;
-        c += (int64_t)r * ld + n;
-        if (vec && n + 4 <= N) {
-            F::put(c, v);
+    int vec;  // elements a store may take: 8, 4 or 1
+    __device__ __forceinline__ Pre fetch(int, int, int) const { return {}; }
+    __device__ __forceinline__ typename F::Elem* row_of(int m) const {
+        if (m < rows0) return c0 ? c0 + (int64_t)m * ld : nullptr;
+        const int r = m - off1;
+        return c1 && r >= 0 && r < rows0 ? c1 + (int64_t)r * ld : nullptr;
+    }
+    __device__ __forceinline__ void put4(typename F::Elem* c, int n, f32x4 v) const {
+        if (vec >= 4 && n + 4 <= N) {
+            F::put(c + n, v);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (n + e < N) F::put1(c + e, v[e]);
+                if (n + e < N) F::put1(c + n + e, v[e]);
+        }
+    }
+    __device__ __forceinline__ void row(int, int, int m, int n, const f32x4 (&v)[4], const Pre&) const {
+        typename F::Elem* c = row_of(m);
+        if (!c) return;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = n + h * 8;
+            if (vec == 8 && k + 8 <= N) {
+                F::put8(c + k, v[h * 2], v[h * 2 + 1]);
+            } else {
+                put4(c, k, v[h * 2]);
+                put4(c, k + 4, v[h * 2 + 1]);
+            }
         }
     }
 };
@@ -157,12 +194,18 @@ struct EpiStore {
 // float32 partial sums of a product split along k: part[split][M][n4]
 struct EpiPartial {
     static constexpr bool kDual = false, kSymmetric = false;
+    static constexpr int kAhead = 0;
+    using Pre = NoPre;
     float* part;
     int64_t n4;
     int M;
-    __device__ __forceinline__ void one(int, int split, int m, int n, f32x4 v) const {
-        if (m >= M || n >= n4) return;
-        *(f32x4*)(part + ((int64_t)split * M + m) * n4 + n) = v;
+    __device__ __forceinline__ Pre fetch(int, int, int) const { return {}; }
+    __device__ __forceinline__ void row(int, int split, int m, int n, const f32x4 (&v)[4], const Pre&) const {
+        if (m >= M) return;
+        float* p = part + ((int64_t)split * M + m) * n4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (n + q * 4 < n4) *(f32x4*)(p + n + q * 4) = v[q];
     }
 };
 
@@ -174,7 +217,8 @@ __global__ __launch_bounds__(256) void k_reduce(const float* part, int splits, i
         f32x4 s = *(const f32x4*)(part + i * 4);
         for (int k = 1; k < splits; ++k) s += *(const f32x4*)(part + ((int64_t)k * M * n4) + i * 4);
         const int64_t m = i / q4;
-        st.one(0, 0, (int)m, (int)(i - m * q4) * 4, s);
+        typename F::Elem* c = st.row_of((int)m);
+        if (c) st.put4(c, (int)(i - m * q4) * 4, s);
     }
 }
 
@@ -283,7 +327,7 @@ hipError_t forward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const 
     add_segments<F>(g2, Operand{h, h_plane, L.H8}, od, nullptr);
     g2.K = (int)L.H;
     one_split(g2);
-    EpiStore<F> e2{(E*)y, nullptr, ldy, (int)L.M, 0, (int)L.O, vec_ok(y, ldy, sizeof(E))};
+    EpiStore<F> e2{(E*)y, nullptr, ldy, (int)L.M, 0, (int)L.O, vec_width(y, ldy, sizeof(E))};
     return launch_gemm<typename F::Mma, true, true>(g2, e2, st);
 }
 
@@ -349,16 +393,16 @@ hipError_t backward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const
         add_segments<F>(g2, odgu, og, nullptr, 0);
         add_segments<F>(g2, odgu, ou, nullptr, L.H8);
         one_split(g2);
-        EpiStore<F> e2{(E*)out.x, nullptr, lddx, (int)L.M, 0, (int)L.D, vec_ok(out.x, lddx, sizeof(E))};
+        EpiStore<F> e2{(E*)out.x, nullptr, lddx, (int)L.M, 0, (int)L.D, vec_width(out.x, lddx, sizeof(E))};
         GSR_TRY((launch_gemm<T, true, false>(g2, e2, st)));
     }
     if (out.gate || out.up) {
         EpiStore<F> e3{(E*)out.gate, (E*)out.up, L.D, (int)L.H, (int)L.H8, (int)L.D,
-                       vec_ok(out.gate, L.D, sizeof(E)) && vec_ok(out.up, L.D, sizeof(E))};
+                       std::min(vec_width(out.gate, L.D, sizeof(E)), vec_width(out.up, L.D, sizeof(E)))};
         GSR_TRY(weight_grad<F>(odgu, 2 * L.H8, ox, L.D8, L.M, e3, part, st));
     }
     if (out.down) {
-        EpiStore<F> e4{(E*)out.down, nullptr, L.H, (int)L.O, 0, (int)L.H, vec_ok(out.down, L.H, sizeof(E))};
+        EpiStore<F> e4{(E*)out.down, nullptr, L.H, (int)L.O, 0, (int)L.H, vec_width(out.down, L.H, sizeof(E))};
         GSR_TRY(weight_grad<F>(ody, L.O8, Operand{h, h_plane, L.H8}, L.H8, L.M, e4, part, st));
     }
     return hipSuccess;

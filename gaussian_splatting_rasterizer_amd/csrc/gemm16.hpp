@@ -9,10 +9,22 @@
 //
 // Tile BM x BN x 64 per workgroup, split over WM x WN waves of 16x16x32 matrix instructions.  Tiles go from global
 // memory to LDS directly (16 bytes per lane, no registers), double buffered.  A row of a KC tile is 128 bytes = 8
-// chunks; chunk c of row r lies at chunk position c ^ (r & 7), so the 16-byte fragment reads of 8 consecutive rows
-// cover all banks.  A tile with rows contiguous keeps its [k][row] order and is read with the LDS transpose read
-// (4 k x 16 rows per 16 lanes); chunk position c ^ f(k) spreads the four k rows over the banks.
+// chunks; chunk c of row r lies at chunk position c ^ f(r), so the 16-byte fragment reads of 8 lanes cover all 32
+// banks (no conflicts measured).  A tile with rows contiguous keeps its [k][row] order and is read with the LDS
+// transpose read (4 k x 16 rows per 16 lanes); chunk position c ^ f(k) spreads the four k rows over the banks.
 // Out-of-range rows and k read as zero through the buffer descriptor's range check.
+//
+// The loop keeps one half of a tile (32 k) in registers while it multiplies the other: the second half is read
+// during the first half's products, the next tile's first half during the second's, and the tile after it is fetched
+// there too, one 16-byte load per few products.  There is one barrier per tile, in front of which the wave already
+// holds the operands of its next 32 products.  Issuing all fetches at the top of a tile instead stalled the waves
+// behind the load queue: 8192^3 in bfloat16 took 1005 (both KC), 1209 (one KC), 1214 us (none) that way and 978,
+// 1005, 1022 us as it is, 1125, 1095, 1076 TFLOP/s.  The matrix pipes are then busy in 65 % of the cycles, at the
+// 1.9 GHz the card holds under this load.  32x32x16 instructions, 32-k tiles in a ring of four, and waves taking
+// turns between reading and multiplying were measured slower (1040, 1080, 1090 us).
+//
+// Fragments of the column operand take their 16 rows four apart, so that a lane ends up with 16 (dual: 8 + 8)
+// consecutive columns of a row and the epilogue reads and writes 16 bytes at a time.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -71,36 +83,47 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t gemm_rsrc(const void* p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, 0x7fffffff, 0x00020000);
 }
 
-// Loader of one operand's tiles: R rows x 64 k by NT threads.
-template <bool KC, int R, int NT, bool DUAL, int WROWS>
+// Loader of one operand's tiles: R rows x 64 k by NT threads.  SPREAD: 0, fragment j holds rows 16 j + i; otherwise
+// rows 4 SPREAD (i >> 2) + 4 (j % SPREAD) + (i & 3) of its group of 16 SPREAD rows (i: the lane's row, 0..15).
+// DUAL: each group of 64 rows is 32 rows of the first matrix and the same 32 of the second.
+template <bool KC, int R, int NT, int SPREAD, bool DUAL>
 struct TileLoader {
     static constexpr int kLoads = R * 8 / NT;
     static constexpr int kBytes = R * 128;
     uint32_t off[kLoads];  // byte offset within the tile, kOobOffset for rows out of range
     int kk[kLoads];        // k within the tile of the chunk (its first k for KC)
 
+    static __device__ __forceinline__ int row_swizzle(int r) {
+        if (SPREAD == 4) return (r & 3) | ((r >> 2) & 4);
+        if (SPREAD == 2) return (r & 3) | ((r >> 1) & 4);
+        return r & 7;
+    }
+    static __device__ __forceinline__ int k_swizzle(int k) {
+        return SPREAD ? (k & 1) | ((k & 2) << 2) : 2 * ((k & 3) | ((k >> 1) & 4));
+    }
+    static __device__ __forceinline__ int frag_row(int j, int i) {
+        if (SPREAD) return (j / SPREAD) * 16 * SPREAD + (i >> 2) * 4 * SPREAD + (j % SPREAD) * 4 + (i & 3);
+        return j * 16 + i;
+    }
     __device__ __forceinline__ void init(int tid, int row0, int rows, int64_t ld) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int q = i * NT + tid;
             if (KC) {
                 int r = q >> 3;
-                const int c = (q & 7) ^ (r & 7);
-                // dual: the wave's WROWS rows are WROWS/2 of the first matrix, then the same rows of the second
-                if (DUAL) r = (r / WROWS) * (WROWS / 2) + (r % (WROWS / 2));
+                const int c = (q & 7) ^ row_swizzle(r);
+                if (DUAL) r = (r / 64) * 32 + (r % 32);
                 kk[i] = c * 8;
                 off[i] = row0 + r < rows ? (uint32_t)(r * (uint32_t)ld * 2u + c * 16u) : kOobOffset;
             } else {
                 constexpr int CH = R / 8;
                 const int k = q / CH;
-                const int c = (q % CH) ^ swz(k);
+                const int c = (q % CH) ^ k_swizzle(k);
                 kk[i] = k;
                 off[i] = row0 + c * 8 < rows ? (uint32_t)(k * (uint32_t)ld * 2u + c * 16u) : kOobOffset;
             }
         }
     }
-    static __device__ __forceinline__ int swz(int k) { return 2 * ((k & 3) | ((k >> 1) & 4)); }
-
     // first / second: the tile's first element in the (two) matrices; krem: k left from the tile's start
     __device__ __forceinline__ void load(const uint16_t* first, const uint16_t* second, int krem, char* lds,
                                          int tid) const {
@@ -111,24 +134,24 @@ struct TileLoader {
         for (int i = 0; i < kLoads; ++i) {
             const uint32_t o = kk[i] < krem ? off[i] : kOobOffset;
             // dual: the 8 rows of one instruction belong to one matrix
-            const bool up = DUAL && (((i * NT + wave * 64) >> 3) % WROWS) >= WROWS / 2;
+            const bool up = DUAL && (((i * NT + wave * 64) >> 3) % 64) >= 32;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? rb : ra, (lds_void*)(lds + (i * NT + wave * 64) * 16), 16, o,
                                                      0, 0, 0);
         }
     }
-    // fragment of 16 rows from row r0, k from kk0 (0 or 32): lane l holds row l % 16, k (l / 16) * 8 .. + 8
-    static __device__ __forceinline__ s16x8 frag(const char* lds, int r0, int kk0, int lane) {
+    // fragment j of the wave's rows from r0, k from kk0 (0 or 32): lane l holds row i = l % 16, k (l / 16) * 8 .. + 8
+    static __device__ __forceinline__ s16x8 frag(const char* lds, int r0, int j, int kk0, int lane) {
         if (KC) {
-            const int r = r0 + (lane & 15);
-            const int c = ((kk0 >> 3) + (lane >> 4)) ^ (r & 7);
+            const int r = r0 + frag_row(j, lane & 15);
+            const int c = ((kk0 >> 3) + (lane >> 4)) ^ row_swizzle(r);
             return *reinterpret_cast<const s16x8*>(lds + r * 128 + c * 16);
         } else {
             s16x8 v;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k = kk0 + (lane >> 4) * 8 + h * 4 + ((lane & 15) >> 2);
-                const int col = r0 + (lane & 3) * 4;
-                const char* p = lds + k * (R * 2) + (((col >> 3) ^ swz(k)) << 4) + (col & 4) * 2;
+                const int col = r0 + frag_row(j, (lane & 3) * 4);
+                const char* p = lds + k * (R * 2) + (((col >> 3) ^ k_swizzle(k)) << 4) + (col & 4) * 2;
                 const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[h * 4 + e] = t[e];
@@ -157,13 +180,14 @@ __device__ __forceinline__ int xcd_order(int bid, int n) {
 }
 
 template <class T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, class Epi>
-__global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p,
-                                                                                         const Epi epi) {
+__global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p, const Epi epi) {
     constexpr int NT = WM * WN * 64;
     constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
-    using LA = TileLoader<AKC, BM, NT, false, BM>;
-    using LB = TileLoader<BKC, BN, NT, Epi::kDual, BN / WN>;
+    static_assert(NI == 4, "a wave covers 64 columns");
+    using LA = TileLoader<AKC, BM, NT, 0, false>;
+    using LB = TileLoader<BKC, BN, NT, Epi::kDual ? 2 : 4, Epi::kDual>;
     constexpr int kStage = LA::kBytes + LB::kBytes;
+    constexpr int kLoads = LA::kLoads + LB::kLoads;
     __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -186,9 +210,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p,
     lb.init(tid, n0, p.N, p.ldb);
 
     const int ktiles = (p.K + kGemmBK - 1) / kGemmBK;
-    const int total = ktiles * p.nseg;
     const int t_begin = split * p.tiles_per_split;
-    const int t_end = min(total, t_begin + p.tiles_per_split);
+    const int t_end = min(ktiles * p.nseg, t_begin + p.tiles_per_split);
     const int64_t a0 = batch * p.batch_a + (AKC ? (int64_t)m0 * p.lda : m0);
     const int64_t b0 = batch * p.batch_b + (BKC ? (int64_t)n0 * p.ldb : n0);
     const int64_t astep = AKC ? kGemmBK : kGemmBK * p.lda;
@@ -200,53 +223,101 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p,
 #pragma unroll
         for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    auto issue = [&](int t, char* buf) {
-        const int s = t / ktiles, kt = t - s * ktiles;
-        const int krem = p.K - kt * kGemmBK;
-        la.load(p.a[s] + a0 + kt * astep, nullptr, krem, buf, tid);
-        lb.load(p.b[s] + b0 + kt * bstep, Epi::kDual ? p.b2[s] + b0 + kt * bstep : nullptr, krem, buf + LA::kBytes,
-                tid);
-    };
-    if (t_begin < t_end) issue(t_begin, smem);
-    for (int t = t_begin; t < t_end; ++t) {
-        char* cur = smem + ((t - t_begin) & 1) * kStage;
-        char* nxt = smem + ((t - t_begin + 1) & 1) * kStage;
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (t + 1 < t_end) issue(t + 1, nxt);
+    if (t_begin < t_end) {
+        // next tile to fetch; past the last one nothing is read (krem 0: every lane is out of range)
+        int s = t_begin / ktiles, kt = t_begin - s * ktiles, left = t_end - t_begin, krem = 0;
+        const uint16_t *pa = nullptr, *pb = nullptr, *pb2 = nullptr;
+        auto next = [&]() {
+            krem = left > 0 ? p.K - kt * kGemmBK : 0;
+            pa = p.a[s] + a0 + kt * astep;
+            pb = p.b[s] + b0 + kt * bstep;
+            if (Epi::kDual) pb2 = p.b2[s] + b0 + kt * bstep;
+            --left;
+            if (++kt == ktiles) {
+                kt = 0;
+                if (s + 1 < p.nseg) ++s;
+            }
+        };
+        auto fetch = [&](char* buf) {
+            la.load(pa, nullptr, krem, buf, tid);
+            lb.load(pb, pb2, krem, buf + LA::kBytes, tid);
+        };
+        s16x8 fa[2][MI], fb[2][NI];
+        auto read = [&](int half, const char* buf) {
 #pragma unroll
-        for (int kk = 0; kk < kGemmBK; kk += 32) {
-            s16x8 fa[MI], fb[NI];
+            for (int j = 0; j < NI; ++j)
+                fb[half][j] = LB::frag(buf + LA::kBytes, wn * (BN / WN), j, half * 32, lane);
 #pragma unroll
-            for (int j = 0; j < NI; ++j) fb[j] = LB::frag(cur + LA::kBytes, wn * (BN / WN) + j * 16, kk, lane);
-#pragma unroll
-            for (int i = 0; i < MI; ++i) fa[i] = LA::frag(cur, wm * (BM / WM) + i * 16, kk, lane);
+            for (int i = 0; i < MI; ++i) fa[half][i] = LA::frag(buf, wm * (BM / WM), i, half * 32, lane);
+        };
+        auto multiply = [&](int half) {
 #pragma unroll
             for (int i = 0; i < MI; ++i)
 #pragma unroll
-                for (int j = 0; j < NI; ++j) acc[i][j] = Mfma<T>::run(fb[j], fa[i], acc[i][j]);
+                for (int j = 0; j < NI; ++j) acc[i][j] = Mfma<T>::run(fb[half][j], fa[half][i], acc[i][j]);
+        };
+        // LDS reads per row of products, so that the last rows have none left to wait for
+        constexpr int kReads = (MI * (AKC ? 1 : 2) + NI * (BKC ? 1 : 2) + MI - 3) / (MI - 2);
+        next();
+        fetch(smem);
+        next();
+        fetch(smem + kStage);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        read(0, smem);
+        for (int t = t_begin; t < t_end; ++t) {
+            char* cur = smem + ((t - t_begin) & 1) * kStage;
+            char* nxt = smem + ((t - t_begin + 1) & 1) * kStage;
+            read(1, cur);
+            multiply(0);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);  // LDS reads
+                __builtin_amdgcn_sched_group_barrier(0x8, NI, 0);        // matrix instructions
+            }
+            // the wave has read all of cur, and its share of nxt has landed; after the barrier everyone's has
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            next();
+            read(0, nxt);
+            fetch(cur);
+            multiply(1);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+                __builtin_amdgcn_sched_group_barrier(0x20, (kLoads + MI - 1) / MI, 0);  // fetches
+                __builtin_amdgcn_sched_group_barrier(0x8, NI, 0);
+            }
         }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no fetch outlives the workgroup's LDS
     }
-    // lane: row m, four consecutive columns
+
+    // lane: row m, 16 consecutive columns (dual: 8 of each product); what the epilogue reads is fetched ahead
     const int mb = m0 + wm * (BM / WM) + (lane & 15);
-    const int nb = n0 + wn * (BNR / WN) + (lane >> 4) * 4;
+    constexpr int kAhead = Epi::kAhead;
     if constexpr (Epi::kDual) {
+        const int nb = n0 + wn * (BNR / WN) + (lane >> 4) * 8;
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NI / 2; ++j) epi.pair(mb + i * 16, nb + j * 16, acc[i][j], acc[i][j + NI / 2]);
+        for (int i = 0; i < MI; ++i) epi.row(mb + i * 16, nb, acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
     } else {
+        const int nb = n0 + wn * (BN / WN) + (lane >> 4) * 16;
+        typename Epi::Pre pre[kAhead + 1];
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < kAhead && i < MI; ++i) pre[i] = epi.fetch(batch, mb + i * 16, nb);
 #pragma unroll
-            for (int j = 0; j < NI; ++j) epi.one(batch, split, mb + i * 16, nb + j * 16, acc[i][j]);
+        for (int i = 0; i < MI; ++i) {
+            if (i + kAhead < MI) pre[(i + kAhead) % (kAhead + 1)] = epi.fetch(batch, mb + (i + kAhead) * 16, nb);
+            epi.row(batch, split, mb + i * 16, nb, acc[i], pre[i % (kAhead + 1)]);
+        }
     }
 }
 
 // ---- values in and out -------------------------------------------------------------------------------
 
 typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
 
 template <class T>
 __device__ __forceinline__ u16x4 to16(f32x4 v) {
@@ -261,6 +332,11 @@ __device__ __forceinline__ f32x4 from16(u16x4 v) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = (float)__builtin_bit_cast(T, (uint16_t)v[e]);
     return o;
+}
+
+__device__ __forceinline__ u16x8 pack8(u16x4 a, u16x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
+__device__ __forceinline__ u16x4 half8(u16x8 v, int h) {
+    return h ? __builtin_shufflevector(v, v, 4, 5, 6, 7) : __builtin_shufflevector(v, v, 0, 1, 2, 3);
 }
 
 // float32 as the sum of three bfloat16: hi + mid + lo carries 24 bits, each part rounded to nearest.  A value whose
@@ -284,6 +360,9 @@ struct FmtBf16 {
     static constexpr int kPlanes = 1;
     static __device__ __forceinline__ f32x4 get(const Elem* p) { return from16<__bf16>(*(const u16x4*)p); }
     static __device__ __forceinline__ void put(Elem* p, f32x4 v) { *(u16x4*)p = to16<__bf16>(v); }
+    typedef u16x8 Raw8;  // eight values, 16-byte aligned
+    static __device__ __forceinline__ f32x4 unpack(Raw8 v, int h) { return from16<__bf16>(half8(v, h)); }
+    static __device__ __forceinline__ void put8(Elem* p, f32x4 a, f32x4 b) { *(u16x8*)p = pack8(to16<__bf16>(a), to16<__bf16>(b)); }
     static __device__ __forceinline__ float get1(const Elem* p) { return (float)__builtin_bit_cast(__bf16, *p); }
     static __device__ __forceinline__ void put1(Elem* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
 };
@@ -293,6 +372,9 @@ struct FmtF16 {
     static constexpr int kPlanes = 1;
     static __device__ __forceinline__ f32x4 get(const Elem* p) { return from16<_Float16>(*(const u16x4*)p); }
     static __device__ __forceinline__ void put(Elem* p, f32x4 v) { *(u16x4*)p = to16<_Float16>(v); }
+    typedef u16x8 Raw8;  // eight values, 16-byte aligned
+    static __device__ __forceinline__ f32x4 unpack(Raw8 v, int h) { return from16<_Float16>(half8(v, h)); }
+    static __device__ __forceinline__ void put8(Elem* p, f32x4 a, f32x4 b) { *(u16x8*)p = pack8(to16<_Float16>(a), to16<_Float16>(b)); }
     static __device__ __forceinline__ float get1(const Elem* p) { return (float)__builtin_bit_cast(_Float16, *p); }
     static __device__ __forceinline__ void put1(Elem* p, float v) { *p = __builtin_bit_cast(uint16_t, (_Float16)v); }
 };
@@ -302,28 +384,39 @@ struct FmtF32 {
     static constexpr int kPlanes = 3;  // matrix operands are split into three bfloat16 planes
     static __device__ __forceinline__ f32x4 get(const Elem* p) { return *(const f32x4*)p; }
     static __device__ __forceinline__ void put(Elem* p, f32x4 v) { *(f32x4*)p = v; }
+    struct Raw8 {
+        f32x4 v[2];
+    };
+    static __device__ __forceinline__ f32x4 unpack(Raw8 v, int h) { return v.v[h]; }
+    static __device__ __forceinline__ void put8(Elem* p, f32x4 a, f32x4 b) {
+        *(f32x4*)p = a;
+        *(f32x4*)(p + 4) = b;
+    }
     static __device__ __forceinline__ float get1(const Elem* p) { return *p; }
     static __device__ __forceinline__ void put1(Elem* p, float v) { *p = v; }
 };
 
-// Four consecutive values of a matrix operand (one or three planes).
+// Eight consecutive values of a matrix operand (one or three planes), 16-byte aligned.
 template <class F>
-__device__ __forceinline__ void put_operand(uint16_t* p, int64_t plane, f32x4 v) {
+__device__ __forceinline__ void put_operand8(uint16_t* p, int64_t plane, f32x4 v0, f32x4 v1) {
     if constexpr (F::kPlanes == 1) {
-        *(u16x4*)p = to16<typename F::Mma>(v);
+        *(u16x8*)p = pack8(to16<typename F::Mma>(v0), to16<typename F::Mma>(v1));
     } else {
-        u16x4 h, m, l;
+        u16x8 h, m, l;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 8; ++e) {
             uint16_t a, b, c;
-            split3(v[e], a, b, c);
+            split3(e < 4 ? v0[e & 3] : v1[e & 3], a, b, c);
             h[e] = a, m[e] = b, l[e] = c;
         }
-        *(u16x4*)p = h;
-        *(u16x4*)(p + plane) = m;
-        *(u16x4*)(p + 2 * plane) = l;
+        *(u16x8*)p = h;
+        *(u16x8*)(p + plane) = m;
+        *(u16x8*)(p + 2 * plane) = l;
     }
 }
+
+// What an epilogue fetches ahead when it needs nothing.
+struct NoPre {};
 
 // ---- launchers -----------------------------------------------------------------------------------------
 
@@ -392,7 +485,11 @@ struct Carver {
     }
 };
 
-inline bool vec_ok(const void* p, int64_t ld, size_t elem) { return ld % 4 == 0 && ((uintptr_t)p % (4 * elem)) == 0; }
+// widest store the rows of an output allow: 8, 4 or 1 elements
+inline int vec_width(const void* p, int64_t ld, size_t elem) {
+    if (ld % 8 == 0 && (uintptr_t)p % 16 == 0) return 8;
+    return ld % 4 == 0 && (uintptr_t)p % (4 * elem) == 0 ? 4 : 1;
+}
 
 #define GSR_TRY(x)                          \
     do {                                    \

@@ -18,20 +18,33 @@ namespace {
 
 constexpr float kXScale = 4096.f;     // X is stored as 2^12 X
 constexpr float kPScale = 8192.f;     // P and Q as 2^13 P, 2^13 Q
-constexpr int kNormBlocks = 64;       // partial sums of squares per matrix
+constexpr int kNormBlocks = 256;      // partial sums of squares per matrix
 
 template <int PL>
-__device__ __forceinline__ void put_planes(uint16_t* p, int64_t plane, f32x4 v) {
-    const u16x4 hi = to16<_Float16>(v);
-    *(u16x4*)p = hi;
-    if constexpr (PL == 2) *(u16x4*)(p + plane) = to16<_Float16>(v - from16<_Float16>(hi));
+__device__ __forceinline__ void put_planes(uint16_t* p, int64_t plane, f32x4 v0, f32x4 v1) {
+    const u16x4 h0 = to16<_Float16>(v0), h1 = to16<_Float16>(v1);
+    *(u16x8*)p = pack8(h0, h1);
+    if constexpr (PL == 2)
+        *(u16x8*)(p + plane) =
+            pack8(to16<_Float16>(v0 - from16<_Float16>(h0)), to16<_Float16>(v1 - from16<_Float16>(h1)));
 }
+// 16 stored values, fetched ahead
 template <int PL>
-__device__ __forceinline__ f32x4 get_planes(const uint16_t* p, int64_t plane) {
-    f32x4 v = from16<_Float16>(*(const u16x4*)p);
-    if constexpr (PL == 2) v += from16<_Float16>(*(const u16x4*)(p + plane));
-    return v;
-}
+struct Planes16 {
+    u16x8 v[PL][2];
+    __device__ __forceinline__ void fetch(const uint16_t* p, int64_t plane, int n, int64_t ld) {
+#pragma unroll
+        for (int k = 0; k < PL; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (n + h * 8 < ld) v[k][h] = *(const u16x8*)(p + k * plane + h * 8);
+    }
+    __device__ __forceinline__ f32x4 get(int q) const {
+        f32x4 r = from16<_Float16>(half8(v[0][q >> 1], q & 1));
+        if constexpr (PL == 2) r += from16<_Float16>(half8(v[1][q >> 1], q & 1));
+        return r;
+    }
+};
 
 template <class E>
 __device__ __forceinline__ float load_value(const E* p);
@@ -67,19 +80,19 @@ __global__ __launch_bounds__(256) void k_norm(const E* g, int64_t n, double* par
 template <class E, int PL>
 __global__ __launch_bounds__(256) void k_normalise(const E* g, int64_t rows, int64_t cols, const double* part,
                                                    float eps, uint16_t* x, int64_t plane) {
-    const int64_t c8 = (cols + 7) / 8 * 8, n = rows * c8 / 4;
+    const int64_t c8 = (cols + 7) / 8 * 8, n = rows * c8 / 8;
     const int64_t b = blockIdx.y;
     double s = 0.0;
     for (int j = 0; j < kNormBlocks; ++j) s += part[b * kNormBlocks + j];
     const double norm = sqrt(s);
     const double inv = (double)kXScale / (norm < (double)eps ? (double)eps : norm);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i * 4 / c8, c = i * 4 - r * c8;
+        const int64_t r = i * 8 / c8, c = i * 8 - r * c8;
         const E* p = g + (b * rows + r) * cols + c;
-        f32x4 v;
+        f32x4 v[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = c + e < cols ? (float)((double)load_value(p + e) * inv) : 0.f;
-        put_planes<PL>(x + b * rows * c8 + i * 4, plane, v);
+        for (int e = 0; e < 8; ++e) v[e >> 2][e & 3] = c + e < cols ? (float)((double)load_value(p + e) * inv) : 0.f;
+        put_planes<PL>(x + b * rows * c8 + i * 8, plane, v[0], v[1]);
     }
 }
 
@@ -87,26 +100,41 @@ __global__ __launch_bounds__(256) void k_normalise(const E* g, int64_t rows, int
 template <int PL>
 struct EpiSymmetric {
     static constexpr bool kDual = false, kSymmetric = true;
+    static constexpr int kAhead = 2;
+    using Pre = Planes16<PL>;
     uint16_t* c;
     const uint16_t* s;
     int64_t plane, ld, batch_stride;
     int n;
     float alpha, beta;
     int bm;  // tile size, to tell diagonal tiles
-    __device__ __forceinline__ void one(int batch, int, int m, int col, f32x4 v) const {
-        if (m >= n || col >= ld) return;
+    __device__ __forceinline__ Pre fetch(int batch, int m, int col) const {
+        Pre r;
+        if (s && m < n) r.fetch(s + batch * batch_stride + m * ld + col, plane, col, ld);
+        return r;
+    }
+    __device__ __forceinline__ void row(int batch, int, int m, int col, const f32x4 (&acc)[4], const Pre& pre) const {
+        if (m >= n) return;
         const int64_t base = batch * batch_stride;
-        v *= alpha;
-        if (s) v += beta * get_planes<PL>(s + base + m * ld + col, plane);
-        put_planes<PL>(c + base + m * ld + col, plane, v);
-        if (m / bm == col / bm) return;  // a diagonal tile holds both halves already
+        const bool mirror = m / bm != col / bm;  // a diagonal tile holds both halves already
+        f32x4 v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (col + e >= n) break;
+        for (int q = 0; q < 4; ++q) {
+            v[q] = acc[q] * alpha;
+            if (s) v[q] += beta * pre.get(q);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (col + h * 8 < ld) put_planes<PL>(c + base + m * ld + col + h * 8, plane, v[h * 2], v[h * 2 + 1]);
+        if (!mirror) return;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            if (col + e >= n) continue;
             uint16_t* d = c + base + (int64_t)(col + e) * ld + m;
-            const _Float16 hi = (_Float16)v[e];
+            const float x = v[e >> 2][e & 3];
+            const _Float16 hi = (_Float16)x;
             *d = __builtin_bit_cast(uint16_t, hi);
-            if constexpr (PL == 2) d[plane] = __builtin_bit_cast(uint16_t, (_Float16)(v[e] - (float)hi));
+            if constexpr (PL == 2) d[plane] = __builtin_bit_cast(uint16_t, (_Float16)(x - (float)hi));
         }
     }
 };
@@ -115,32 +143,46 @@ struct EpiSymmetric {
 template <int PL, class Out>
 struct EpiUpdate {
     static constexpr bool kDual = false, kSymmetric = false;
+    static constexpr int kAhead = 2;
+    using Pre = Planes16<PL>;
     const uint16_t* x;
     uint16_t* xn;
     int64_t plane, ld, batch_stride;
     Out* out;  // null: another step follows
     int M, N;  // rows, columns of the matrix
     float a, alpha;
-    bool vec;
-    __device__ __forceinline__ void one(int batch, int, int m, int n, f32x4 v) const {
-        if (m >= M || n >= ld) return;
-        const int64_t at = batch * batch_stride + (int64_t)m * ld + n;
-        v = a * get_planes<PL>(x + at, plane) + alpha * v;
+    int vec;
+    __device__ __forceinline__ Pre fetch(int batch, int m, int n) const {
+        Pre r;
+        if (m < M) r.fetch(x + batch * batch_stride + (int64_t)m * ld + n, plane, n, ld);
+        return r;
+    }
+    __device__ __forceinline__ void row(int batch, int, int m, int n, const f32x4 (&acc)[4], const Pre& pre) const {
+        if (m >= M) return;
+        f32x4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = a * pre.get(q) + alpha * acc[q];
         if (!out) {
-            put_planes<PL>(xn + at, plane, v);
+            uint16_t* d = xn + batch * batch_stride + (int64_t)m * ld + n;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (n + h * 8 < ld) put_planes<PL>(d + h * 8, plane, v[h * 2], v[h * 2 + 1]);
             return;
         }
-        v *= 1.f / kXScale;
         Out* d = out + ((int64_t)batch * M + m) * N + n;
-        if (vec && n + 4 <= N) {
-            if constexpr (sizeof(Out) == 4)
-                *(f32x4*)d = v;
-            else
-                *(u16x4*)d = to16<Out>(v);
-        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (n + e < N) d[e] = (Out)v[e];
+        for (int q = 0; q < 4; ++q) {
+            v[q] *= 1.f / kXScale;
+            if (vec >= 4 && n + q * 4 + 4 <= N) {
+                if constexpr (sizeof(Out) == 4)
+                    *(f32x4*)(d + q * 4) = v[q];
+                else
+                    *(u16x4*)(d + q * 4) = to16<Out>(v[q]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + q * 4 + e < N) d[q * 4 + e] = (Out)v[q][e];
+            }
         }
     }
 };
@@ -186,7 +228,7 @@ hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* 
     const In* g = (const In*)gin;
     k_norm<In><<<dim3(kNormBlocks, (unsigned)L.B), 256, 0, st>>>(g, L.R * L.C, part);
     GSR_TRY(hipGetLastError());
-    int64_t bx = (L.R * L.C8 / 4 + 255) / 256;
+    int64_t bx = (L.R * L.C8 / 8 + 255) / 256;
     if (bx > 2048) bx = 2048;
     k_normalise<In, PL><<<dim3((unsigned)bx, (unsigned)L.B), 256, 0, st>>>(g, L.R, L.C, part, d.eps, x, L.x_plane);
     GSR_TRY(hipGetLastError());
@@ -214,7 +256,7 @@ hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* 
         GSR_TRY((launch_symmetric<true>(gq, eq, st)));
         const bool last = step + 1 == d.steps;
         EpiUpdate<PL, Out> eu{x, xn, L.x_plane, L.C8, L.R * L.C8, last ? (Out*)out : nullptr, (int)L.R, (int)L.C,
-                              d.a, 1.f / kPScale, vec_ok(out, L.C, sizeof(Out))};
+                              d.a, 1.f / kPScale, vec_width(out, L.C, sizeof(Out))};
         GemmArgs gu = make_args(L.R, L.C8, L.lo);
         gu.batch = (int)L.B;
         if (tall) {  // X Q, Q symmetric
