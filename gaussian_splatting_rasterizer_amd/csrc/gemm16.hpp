@@ -363,8 +363,10 @@ struct FmtBf16 {
     typedef u16x8 Raw8;  // eight values, 16-byte aligned
     static __device__ __forceinline__ f32x4 unpack(Raw8 v, int h) { return from16<__bf16>(half8(v, h)); }
     static __device__ __forceinline__ void put8(Elem* p, f32x4 a, f32x4 b) { *(u16x8*)p = pack8(to16<__bf16>(a), to16<__bf16>(b)); }
-    static __device__ __forceinline__ float get1(const Elem* p) { return (float)__builtin_bit_cast(__bf16, *p); }
-    static __device__ __forceinline__ void put1(Elem* p, float v) { *p = __builtin_bit_cast(uint16_t, (__bf16)v); }
+    static __device__ __forceinline__ float to_float(uint16_t v) { return (float)__builtin_bit_cast(__bf16, v); }
+    static __device__ __forceinline__ uint16_t from_float(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+    static __device__ __forceinline__ float get1(const Elem* p) { return to_float(*p); }
+    static __device__ __forceinline__ void put1(Elem* p, float v) { *p = from_float(v); }
 };
 struct FmtF16 {
     using Mma = _Float16;
@@ -375,8 +377,10 @@ struct FmtF16 {
     typedef u16x8 Raw8;  // eight values, 16-byte aligned
     static __device__ __forceinline__ f32x4 unpack(Raw8 v, int h) { return from16<_Float16>(half8(v, h)); }
     static __device__ __forceinline__ void put8(Elem* p, f32x4 a, f32x4 b) { *(u16x8*)p = pack8(to16<_Float16>(a), to16<_Float16>(b)); }
-    static __device__ __forceinline__ float get1(const Elem* p) { return (float)__builtin_bit_cast(_Float16, *p); }
-    static __device__ __forceinline__ void put1(Elem* p, float v) { *p = __builtin_bit_cast(uint16_t, (_Float16)v); }
+    static __device__ __forceinline__ float to_float(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
+    static __device__ __forceinline__ uint16_t from_float(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+    static __device__ __forceinline__ float get1(const Elem* p) { return to_float(*p); }
+    static __device__ __forceinline__ void put1(Elem* p, float v) { *p = from_float(v); }
 };
 struct FmtF32 {
     using Mma = __bf16;

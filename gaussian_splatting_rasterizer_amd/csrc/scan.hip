@@ -4,20 +4,18 @@
 //   e_t = a_t G_t,    G_t = dy_t + e_{t+1}                           e past the last row = dh_last
 //   dx = (1 - a) G,   dz = a (1 - a) (h_{t-1} - x) G,   dh0 = e_0
 //
-// Sequences of any length lie one after another in the rows.  One pass over the data: a workgroup takes a chunk of
-// rows of some channels into registers, row groups of R rows reduce to (A, H) -- h_out = A h_in + H -- and are joined
-// in LDS, the chunk's (A, H) is published, the state that enters the chunk is gathered from the chunks before it,
-// and the rows are then run once more from their registers with the true state.  A row that starts a sequence
-// replaces the state instead of multiplying it by zero, so nothing of one sequence, NaN included, reaches the next.
+// Sequences of any length lie one after another in the rows.  Rows are cut into spans (one wave's rows) and chunks of
+// 8 spans (one workgroup's).  Three kernels: k_scan_spans reduces every span to (A, H) with h_out = A h_in + H, and
+// every chunk; k_scan_join runs through the chunks and leaves the state that enters each; k_scan_forward (or
+// k_scan_backward) joins the spans before it in the chunk and runs the recurrence.  The second reading of the inputs
+// goes backwards through the chunks, so most of it comes from the 256 MB last-level cache.  A span that starts a
+// sequence needs no state: where all do (short equal sequences, single steps) the last kernel runs alone.
 //
-// The state entering chunk k is joined in a fixed order whatever the timing, so results are reproducible: first the
-// (A, H) of the chunks before it in its group of 8, then those of the whole groups before it in its group of 64,
-// then the running state of the group of 64 before that, which alone forms a chain along the sequence.  Published
-// values are 64-bit words {value, tag} written and read atomically, so a word is either absent or whole.  Chunks are
-// taken by ticket, so a workgroup only ever waits for one that has already started.
+// A row that starts a sequence replaces the state instead of multiplying it by zero, so nothing of one sequence, NaN
+// included, reaches the next.  All orders are fixed: results are reproducible.
 //
-// The forward pass keeps the state entering every chunk in float32; the backward pass reruns the states
-// from there, instead of reading back rounded ones, and scans e from the other end in the same way.
+// The forward pass keeps the state in front of every 8 rows in float32; the backward pass reruns the states from
+// there, instead of reading back rounded ones.
 #include "gsr_internal.hpp"
 #include "gemm16.hpp"
 
@@ -25,11 +23,10 @@ namespace gsr {
 
 namespace {
 
-constexpr int kChunk = 128;     // rows of a chunk
-constexpr int kGroupRows = 16;  // rows of a row group (one thread's)
-constexpr int kGroups = kChunk / kGroupRows;
-constexpr int kFan = 8;         // chunks per level-1 group, level-1 groups per level-2 group
-constexpr uint32_t kTagValid = 1u, kTagReset = 2u;
+constexpr int kBatch = 8;   // rows held in registers at a time; the forward pass saves the state in front of each
+constexpr int kSpans = 8;   // spans of a chunk
+constexpr int kMaxSpan = 128;
+constexpr int kJoinLanes = 16, kJoinRuns = 64, kJoinChunks = 16;  // k_scan_join: channels, runs, chunks of a run
 
 struct ScanArgs {
     const void* z;
@@ -40,20 +37,19 @@ struct ScanArgs {
     const float* dh_last;
     void* y;
     float* h_last;
-    float* saved;
+    float* saved;      // [rows / 8][C]
     void* dz;
     void* dx;
     float* dh0;
     const int64_t* offsets;
-    int64_t n_seq, seq_len, rows;
-    int C, ncb;
-    int64_t nchunks;
-    uint64_t* agg1;    // [chunk][2][C]
-    uint64_t* agg2;    // [chunk / 8][2][C]
-    uint64_t* run;     // [chunk / 64][C]
-    uint32_t* ticket;
+    int64_t n_seq, seq_len, rows, nchunks;
+    int C, ncb, span;  // span: rows of a span
+    float* agg1;       // [chunk * 8 + span][2][C], null: no state passes between spans
+    float* agg2;       // [chunk][2][C]
+    float* state;      // [chunk][C] state entering the chunk
 };
 
+// a = sigma(z) and 1 - a, each to its own relative precision
 __device__ __forceinline__ void gate(float z, float& a, float& na) {
     const float e = __expf(-__builtin_fabsf(z));
     const float r = __builtin_amdgcn_rcpf(1.f + e);
@@ -62,104 +58,35 @@ __device__ __forceinline__ void gate(float z, float& a, float& na) {
     na = z >= 0.f ? er : r;
 }
 
-__device__ __forceinline__ uint64_t word(float v, uint32_t tag) {
-    return ((uint64_t)tag << 32) | __builtin_bit_cast(uint32_t, v);
-}
-__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ void post(uint64_t* p, uint64_t v) {
-    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// waits for a word; v holds what a first look found
-__device__ __forceinline__ uint64_t await(const uint64_t* p, uint64_t v) {
-    while (!(uint32_t)(v >> 32)) {
-        __builtin_amdgcn_s_sleep(1);
-        v = peek(p);
-    }
-    return v;
-}
-__device__ __forceinline__ float value(uint64_t w) { return __builtin_bit_cast(float, (uint32_t)w); }
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-struct Span {  // h_out = reset ? H : A h_in + H
+// What a run of rows does to the state: h_out = A h_in + H, or h_out = H where a sequence starts (backward: ends) in
+// it, which a negative A says (a product of gates never is negative).
+struct Span {
     float A, H;
-    bool reset;
+    __device__ __forceinline__ bool reset() const { return A < 0.f; }
 };
 __device__ __forceinline__ Span join(const Span& first, const Span& then) {
-    if (then.reset) return then;
-    return {first.A * then.A, __builtin_fmaf(then.A, first.H, then.H), first.reset};
+    if (then.reset()) return then;
+    return {first.reset() ? first.A : first.A * then.A, __builtin_fmaf(then.A, first.H, then.H)};
 }
 __device__ __forceinline__ float apply(const Span& s, float h) {
-    return s.reset ? s.H : __builtin_fmaf(s.A, h, s.H);
-}
-
-// State entering chunk k (counted in scan direction) of one channel; publishes the chunk's own span.
-__device__ float exchange(const ScanArgs& p, int64_t k, int c, const Span& own) {
-    const uint32_t tag = kTagValid | (own.reset ? kTagReset : 0u);
-    uint64_t* mine = p.agg1 + k * 2 * p.C + c;
-    post(mine, word(own.A, tag));
-    post(mine + p.C, word(own.H, tag));
-    const int64_t k1 = k / kFan, k2 = k1 / kFan;
-    const int n1 = (int)(k - k1 * kFan), n2 = (int)(k1 - k2 * kFan);
-    // one look at everything that is needed, so that the latencies overlap
-    uint64_t wa[kFan - 1], wh[kFan - 1], va[kFan - 1], vh[kFan - 1], wr = 0;
-    const uint64_t* b1 = p.agg1 + k1 * kFan * 2 * p.C + c;
-    const uint64_t* b2 = p.agg2 + k2 * kFan * 2 * p.C + c;
-    const uint64_t* br = p.run + (k2 - 1) * p.C + c;
-#pragma unroll
-    for (int j = 0; j < kFan - 1; ++j) {
-        wa[j] = j < n1 ? peek(b1 + (int64_t)j * 2 * p.C) : 0;
-        wh[j] = j < n1 ? peek(b1 + ((int64_t)j * 2 + 1) * p.C) : 0;
-        va[j] = j < n2 ? peek(b2 + (int64_t)j * 2 * p.C) : 0;
-        vh[j] = j < n2 ? peek(b2 + ((int64_t)j * 2 + 1) * p.C) : 0;
-    }
-    if (k2 > 0) wr = peek(br);
-    Span s1{1.f, 0.f, false};
-#pragma unroll
-    for (int j = 0; j < kFan - 1; ++j) {
-        if (j < n1) {
-            const uint64_t a = await(b1 + (int64_t)j * 2 * p.C, wa[j]);
-            const uint64_t h = await(b1 + ((int64_t)j * 2 + 1) * p.C, wh[j]);
-            s1 = join(s1, Span{value(a), value(h), ((uint32_t)(a >> 32) & kTagReset) != 0});
-        }
-    }
-    if (n1 == kFan - 1) {
-        const Span g = join(s1, own);
-        const uint32_t t = kTagValid | (g.reset ? kTagReset : 0u);
-        uint64_t* d = p.agg2 + k1 * 2 * p.C + c;
-        post(d, word(g.A, t));
-        post(d + p.C, word(g.H, t));
-    }
-    float h = 0.f;
-    if (!s1.reset) {
-        Span s2{1.f, 0.f, false};
-#pragma unroll
-        for (int j = 0; j < kFan - 1; ++j) {
-            if (j < n2) {
-                const uint64_t a = await(b2 + (int64_t)j * 2 * p.C, va[j]);
-                const uint64_t v = await(b2 + ((int64_t)j * 2 + 1) * p.C, vh[j]);
-                s2 = join(s2, Span{value(a), value(v), ((uint32_t)(a >> 32) & kTagReset) != 0});
-            }
-        }
-        if (!s2.reset && k2 > 0) h = value(await(br, wr));
-        h = apply(s2, h);
-    }
-    h = apply(s1, h);
-    if (n1 == kFan - 1 && n2 == kFan - 1) post(p.run + k2 * p.C + c, word(apply(own, h), kTagValid));
-    return h;
+    return s.reset() ? s.H : __builtin_fmaf(s.A, h, s.H);
 }
 
 // Sequence starts of a chunk: s_start[i] is the sequence that starts at row row0 + i (the last one, where empty
 // sequences share the row), -1 where none does, and the row past the last one counts as a start.  Returns the
 // sequence that holds row row0 - 1 or starts at row0.
 __device__ int64_t sequence_starts(const ScanArgs& p, int64_t row0, int* s_start, int tid, int nt) {
+    const int rows = p.span * kSpans;
     if (!p.offsets) {
-        for (int i = tid; i <= kChunk; i += nt) {
-            const int64_t r = row0 + i;
-            s_start[i] = r >= p.rows || r % p.seq_len == 0 ? (int)(r / p.seq_len) : -1;
+        const uint32_t len = (uint32_t)p.seq_len, first = (uint32_t)row0 / len;  // rows stay below 2^31
+        for (int i = tid; i <= rows; i += nt) {
+            const uint32_t r = (uint32_t)row0 + i, q = r / len;
+            s_start[i] = r >= (uint32_t)p.rows || q * len == r ? (int)q : -1;
         }
         __syncthreads();
-        return row0 / p.seq_len;
+        return first;
     }
     // first sequence with offsets[s] >= row0
     int64_t lo = 0, hi = p.n_seq;
@@ -170,386 +97,514 @@ __device__ int64_t sequence_starts(const ScanArgs& p, int64_t row0, int* s_start
         else
             hi = mid;
     }
-    for (int i = tid; i <= kChunk; i += nt) s_start[i] = row0 + i >= p.rows ? (int)p.n_seq : -1;
+    for (int i = tid; i <= rows; i += nt) s_start[i] = row0 + i >= p.rows ? (int)p.n_seq : -1;
     __syncthreads();
     for (int64_t s = lo + tid; s <= p.n_seq; s += nt) {
         const int64_t at = p.offsets[s] - row0;
-        if (at > kChunk) break;
+        if (at > rows) break;
         if (at >= 0 && row0 + at < p.rows) atomicMax(&s_start[at], (int)s);
     }
     __syncthreads();
     return lo - 1;
 }
 
-// sequence that holds row i of the chunk
-__device__ __forceinline__ int64_t sequence_of(const int* s_start, int i, int64_t before) {
-    for (; i >= 0; --i)
-        if (s_start[i] >= 0) return s_start[i];
-    return before;
+// sequence that starts at / that holds row i of the chunk (i is uniform over the wave)
+__device__ __forceinline__ int start_of(const int* st, int i) { return __builtin_amdgcn_readfirstlane(st[i]); }
+__device__ __forceinline__ int sequence_of(const int* s_start, int i, int64_t before) {
+    for (; i >= 0; --i) {
+        const int s = start_of(s_start, i);
+        if (s >= 0) return s;
+    }
+    return (int)before;
 }
 
+// One lane's channels of a row in a register: a pair of 16-bit values stays one word, or the compiler splits it.
 template <class F, int VC>
-struct Vec;
-template <int VC>
-struct Vec<FmtF32, VC> {
-    typedef float V __attribute__((ext_vector_type(VC)));
-};
-template <int VC>
-struct Vec<FmtBf16, VC> {
-    typedef uint16_t V __attribute__((ext_vector_type(VC)));
-};
-template <int VC>
-struct Vec<FmtF16, VC> {
-    typedef uint16_t V __attribute__((ext_vector_type(VC)));
-};
-
-// LPR lanes x VC channels hold a row; kGroups row groups of kGroupRows rows.
-template <class F, int VC, int LPR, bool CARRY>
-__global__ __launch_bounds__(LPR* kGroups) void k_scan_forward(const ScanArgs p) {
+struct Cell {
     using E = typename F::Elem;
-    using V = typename Vec<F, VC>::V;
-    constexpr int CB = LPR * VC, NT = LPR * kGroups;
-    __shared__ int s_start[kChunk + 1];
-    __shared__ float s_a[kGroups][CB], s_h[kGroups][CB];
-    __shared__ int s_reset[kGroups];
-    __shared__ uint32_t s_ticket;
-    const int tid = threadIdx.x;
-    uint32_t t = blockIdx.x;
-    if (CARRY) {
-        if (tid == 0) s_ticket = atomicAdd(p.ticket, 1u);
-        __syncthreads();
-        t = s_ticket;
+    E v[VC];
+    __device__ __forceinline__ float get(int e) const { return F::get1(v + e); }
+    __device__ __forceinline__ void set(int e, float x) { F::put1(v + e, x); }
+};
+template <class F>
+struct Pair16 {
+    uint32_t v;
+    __device__ __forceinline__ float get(int e) const {
+        return F::to_float((uint16_t)(e ? v >> 16 : v & 0xffffu));
     }
-    const int64_t chunk = t / (uint32_t)p.ncb;
-    const int cb = (int)(t - (uint32_t)chunk * (uint32_t)p.ncb);
-    const int g = tid / LPR, li = tid % LPR;
-    const int c = cb * CB + li * VC;
-    const bool live = c < p.C;
-    const int64_t row0 = chunk * kChunk, base = row0 + g * kGroupRows;
-    const int n = (int)(p.rows - base < kGroupRows ? (p.rows - base < 0 ? 0 : p.rows - base) : kGroupRows);
+    __device__ __forceinline__ void set(int e, float x) {
+        const uint32_t h = F::from_float(x);
+        v = e ? (v & 0xffffu) | (h << 16) : h;  // element 0 is set first
+    }
+};
+template <>
+struct Cell<FmtBf16, 2> : Pair16<FmtBf16> {};
+template <>
+struct Cell<FmtF16, 2> : Pair16<FmtF16> {};
 
-    V z[kGroupRows], x[kGroupRows];
-    const E* pz = (const E*)p.z + base * p.ldz + c;
-    const E* px = (const E*)p.x + base * p.ldx + c;
+// Element c of a row that starts at a uniform address: a scalar base and a 32-bit lane offset.
+template <class T, class E>
+__device__ __forceinline__ T* lane_at(E* row, int c) {
+    return (T*)((char*)row + (uint32_t)c * (uint32_t)sizeof(E));
+}
+
+// Rows of one array seen from a span: descriptor at the span's first row, this lane's column as the offset.  Rows past
+// the end and lanes past the channels go out of the descriptor's range: they read zero and are not written.
+struct RowPtr {
+    __amdgpu_buffer_rsrc_t rs;
+    uint32_t step, col;  // bytes of a row; the lane's column, kOobOffset for a lane without channels
+    template <class E>
+    static __device__ __forceinline__ RowPtr make(const void* p, int64_t row, int64_t ld, int c, bool live) {
+        return {gemm_rsrc((const E*)p + row * ld), (uint32_t)(ld * sizeof(E)),
+                live ? (uint32_t)c * (uint32_t)sizeof(E) : kOobOffset};
+    }
+    __device__ __forceinline__ uint32_t at(int r, int n) const { return r < n ? col : kOobOffset; }
+};
+
+// One batch of rows of one lane's channels.
+template <class F, int VC>
+struct Rows {
+    using V = Cell<F, VC>;
+    V v[kBatch];
+    __device__ __forceinline__ void load(const RowPtr& p, int r0, int n) {
 #pragma unroll
-    for (int r = 0; r < kGroupRows; ++r) {
-        if (live && r < n) {
-            z[r] = *(const V*)(pz + r * p.ldz);
-            x[r] = *(const V*)(px + r * p.ldx);
+        for (int r = 0; r < kBatch; ++r) {
+            const uint32_t off = p.at(r0 + r, n), row = (uint32_t)(r0 + r) * p.step;
+            if constexpr (sizeof(V) == 8)
+                v[r] = __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b64(p.rs, off, row, 0));
+            else if constexpr (sizeof(V) == 4)
+                v[r] = __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b32(p.rs, off, row, 0));
+            else
+                v[r] = __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b16(p.rs, off, row, 0));
         }
     }
-    const int64_t before = sequence_starts(p, row0, s_start, tid, NT);
-    const int* st = s_start + g * kGroupRows;
+    __device__ __forceinline__ float get(int r, int e) const { return v[r].get(e); }
+};
+template <class V>
+__device__ __forceinline__ void store_row(const RowPtr& p, int r, int n, const V& v) {
+    const uint32_t off = p.at(r, n), row = (uint32_t)r * p.step;
+    if constexpr (sizeof(V) == 8)
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, v), p.rs, off, row, 0);
+    else if constexpr (sizeof(V) == 4)
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), p.rs, off, row, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, v), p.rs, off, row, 0);
+}
 
+// What a wave of the row kernels works on: 64 lanes x VC channels, span g of a chunk.  All but c and live are uniform
+// over the wave and kept in scalar registers, so that rows are addressed by a scalar base and a lane offset.
+template <int VC>
+struct Place {
+    int g, li, c0, c, n;
+    int64_t chunk, row0, base;
+    bool live;
+    __device__ __forceinline__ Place(const ScanArgs& p, uint32_t id) {
+        const uint32_t k = id / (uint32_t)p.ncb;
+        chunk = k;
+        c0 = (int)(id - k * (uint32_t)p.ncb) * (64 * VC);
+        g = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        li = threadIdx.x & 63;
+        c = c0 + li * VC;
+        live = c < p.C;
+        row0 = chunk * (p.span * kSpans);
+        base = row0 + g * p.span;
+        const int64_t left = p.rows - base;
+        n = (int)(left < 0 ? 0 : left < p.span ? left : p.span);
+    }
+};
+
+// bit r: a sequence starts at row r of the batch, one of the first n
+__device__ __forceinline__ uint32_t start_bits(const int* st, int n) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int r = 0; r < kBatch; ++r) m |= st[r] >= 0 ? 1u << r : 0u;
+    m = __builtin_amdgcn_readfirstlane(m);
+    return n < kBatch ? m & ((1u << n) - 1u) : m;
+}
+
+template <class F, int VC, bool BWD>
+__global__ __launch_bounds__(64 * kSpans) void k_scan_spans(const ScanArgs p) {
+    using E = typename F::Elem;
+    constexpr int CB = 64 * VC, NT = 64 * kSpans;
+    __shared__ int s_start[kMaxSpan * kSpans + 1];
+    __shared__ float s_a[kSpans][CB], s_h[kSpans][CB];
+    const Place<VC> at(p, blockIdx.x);
+    const int tid = threadIdx.x;
+    const int* st = s_start + at.g * p.span;
+    const RowPtr pz = RowPtr::make<E>(p.z, at.base, p.ldz, at.c, at.live);
+    const RowPtr px = BWD ? RowPtr::make<E>(p.dy, at.base, p.lddy, at.c, at.live)
+                          : RowPtr::make<E>(p.x, at.base, p.ldx, at.c, at.live);
     float A[VC], H[VC];
     bool reset = false;
 #pragma unroll
     for (int e = 0; e < VC; ++e) A[e] = 1.f, H[e] = 0.f;
-    if (live) {
+    const int nb = (at.n + kBatch - 1) / kBatch;
+    Rows<F, VC> z[2], x[2];
+    auto fetch = [&](int k, int b) {
+        const int r0 = (BWD ? nb - 1 - k : k) * kBatch;
+        z[b].load(pz, r0, at.n);
+        x[b].load(px, r0, at.n);
+    };
+    if (nb > 0) fetch(0, 0);
+    const int64_t before = sequence_starts(p, at.row0, s_start, tid, NT);
+    auto run = [&](int k, int b) {
+        const int r0 = (BWD ? nb - 1 - k : k) * kBatch;
+        const uint32_t marks = start_bits(st + r0 + (BWD ? 1 : 0), at.n - r0);
+        if (marks) reset = true;
+        // rows past the end, which read zero, come last (backward: first, and leave the zero gradient zero)
 #pragma unroll
-        for (int r = 0; r < kGroupRows; ++r) {
-            if (r < n) {
-                const int s = st[r];
-                float h0[VC];
-    #pragma unroll
-                for (int e = 0; e < VC; ++e) h0[e] = 0.f;
-                if (s >= 0) {
-                    reset = true;
-                    if (p.h0 && s < p.n_seq) {
-    #pragma unroll
-                        for (int e = 0; e < VC; ++e) h0[e] = p.h0[(int64_t)s * p.C + c + e];
-                    }
-                }
-    #pragma unroll
-                for (int e = 0; e < VC; ++e) {
-                    float a, na;
-                    gate(F::get1((const E*)&z[r] + e), a, na);
-                    const float b = na * F::get1((const E*)&x[r] + e);
-                    H[e] = __builtin_fmaf(a, s >= 0 ? h0[e] : H[e], b);
-                    A[e] *= a;
-                }
+        for (int i = 0; i < kBatch; ++i) {
+            const int r = BWD ? kBatch - 1 - i : i;
+            if ((marks >> r) & 1) {
+                const float* src = BWD ? p.dh_last : p.h0;
+                const int64_t q = BWD ? sequence_of(s_start, at.g * p.span + r0 + r, before) : start_of(st, r0 + r);
+                const bool given = src && q >= 0 && q < p.n_seq && at.live;
+#pragma unroll
+                for (int e = 0; e < VC; ++e) H[e] = given ? lane_at<const float>(src + q * p.C, at.c)[e] : 0.f;
             }
-        }
-    }
 #pragma unroll
-    for (int e = 0; e < VC; ++e) {
-        s_a[g][li * VC + e] = A[e];
-        s_h[g][li * VC + e] = H[e];
-    }
-    if (li == 0) s_reset[g] = reset;
-    __syncthreads();
-    // the chunk's span, the state entering it, and the state entering each row group (left in s_h)
-    for (int i = tid; i < CB; i += NT) {
-        const int cc = cb * CB + i;
-        if (cc >= p.C) break;
-        float h = 0.f;
-        if (CARRY) {
-            Span own{1.f, 0.f, false};
-#pragma unroll
-            for (int k = 0; k < kGroups; ++k) own = join(own, Span{s_a[k][i], s_h[k][i], s_reset[k] != 0});
-            h = exchange(p, chunk, cc, own);
-        }
-        if (p.saved) p.saved[chunk * p.C + cc] = h;
-#pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-            const Span s{s_a[k][i], s_h[k][i], s_reset[k] != 0};
-            s_h[k][i] = h;
-            h = apply(s, h);
-        }
-    }
-    __syncthreads();
-    if (!live) return;
-    float h[VC];
-#pragma unroll
-    for (int e = 0; e < VC; ++e) h[e] = s_h[g][li * VC + e];
-    E* py = (E*)p.y + base * p.ldy + c;
-#pragma unroll
-    for (int r = 0; r < kGroupRows; ++r) {
-        if (r < n) {
-            const int s = st[r];
-            if (s >= 0) {
-    #pragma unroll
-                for (int e = 0; e < VC; ++e) h[e] = p.h0 && s < p.n_seq ? p.h0[(int64_t)s * p.C + c + e] : 0.f;
-            }
-            V o;
-    #pragma unroll
             for (int e = 0; e < VC; ++e) {
                 float a, na;
-                gate(F::get1((const E*)&z[r] + e), a, na);
-                const float b = na * F::get1((const E*)&x[r] + e);
-                h[e] = __builtin_fmaf(a, h[e], b);
-                F::put1((E*)&o + e, h[e]);
-            }
-            *(V*)(py + r * p.ldy) = o;
-            if (p.h_last && st[r + 1] >= 0) {
-                const int64_t q = sequence_of(s_start, g * kGroupRows + r, before);
-                if (q >= 0 && q < p.n_seq) {
-    #pragma unroll
-                    for (int e = 0; e < VC; ++e) p.h_last[q * p.C + c + e] = h[e];
-                }
+                gate(z[b].get(r, e), a, na);
+                H[e] = BWD ? a * (x[b].get(r, e) + H[e]) : __builtin_fmaf(a, H[e], na * x[b].get(r, e));
+                A[e] *= a;
             }
         }
+    };
+    for (int k = 0; k < nb; k += 2) {
+        if (k + 1 < nb) fetch(k + 1, 1);
+        run(k, 0);
+        if (k + 2 < nb) fetch(k + 2, 0);
+        if (k + 1 < nb) run(k + 1, 1);
+    }
+    if (reset) {
+#pragma unroll
+        for (int e = 0; e < VC; ++e) A[e] = -1.f;
+    }
+    if (at.live && nb > 0) {
+        float* d = lane_at<float>(p.agg1 + (at.chunk * kSpans + at.g) * 2 * p.C, at.c);
+#pragma unroll
+        for (int e = 0; e < VC; ++e) d[e] = A[e], d[p.C + e] = H[e];
+    }
+#pragma unroll
+    for (int e = 0; e < VC; ++e) s_a[at.g][at.li * VC + e] = A[e], s_h[at.g][at.li * VC + e] = H[e];
+    __syncthreads();
+    if (tid < CB && at.c0 + tid < p.C) {
+        Span own{1.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kSpans; ++i) {
+            const int k = BWD ? kSpans - 1 - i : i;
+            own = join(own, Span{s_a[k][tid], s_h[k][tid]});
+        }
+        float* d = p.agg2 + at.chunk * 2 * p.C + at.c0 + tid;
+        d[0] = own.A;
+        d[p.C] = own.H;
+    }
+    // an empty sequence passes its state through
+    if (p.offsets) {
+        const float* from = BWD ? p.dh_last : p.h0;
+        float* to = BWD ? p.dh0 : p.h_last;
+        if (to)
+            for (int64_t i = (int64_t)blockIdx.x * NT + tid; i < p.n_seq * p.C; i += (int64_t)gridDim.x * NT) {
+                const int64_t s = i / p.C;
+                if (p.offsets[s] == p.offsets[s + 1]) to[i] = from ? from[i] : 0.f;
+            }
     }
 }
 
-template <class F, int VC, int LPR, bool CARRY>
-__global__ __launch_bounds__(LPR* kGroups) void k_scan_backward(const ScanArgs p) {
-    using E = typename F::Elem;
-    using V = typename Vec<F, VC>::V;
-    constexpr int CB = LPR * VC, NT = LPR * kGroups;
-    __shared__ int s_start[kChunk + 1];
-    // A is the same product in both directions; s_h: states, s_e: the gradient's
-    __shared__ float s_a[kGroups][CB], s_h[kGroups][CB], s_e[kGroups][CB];
-    __shared__ int s_reset[kGroups], s_end[kGroups];
-    __shared__ uint32_t s_ticket;
-    const int tid = threadIdx.x;
-    uint32_t t = blockIdx.x;
-    if (CARRY) {
-        if (tid == 0) s_ticket = atomicAdd(p.ticket, 1u);
-        __syncthreads();
-        t = s_ticket;
-    }
-    const int64_t order = t / (uint32_t)p.ncb;  // chunks from the last to the first
-    const int cb = (int)(t - (uint32_t)order * (uint32_t)p.ncb);
-    const int64_t chunk = p.nchunks - 1 - order;
-    const int g = tid / LPR, li = tid % LPR;
-    const int c = cb * CB + li * VC;
+// The same for a call without rows.
+__global__ __launch_bounds__(256) void k_scan_empty(const float* from, float* to, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        to[i] = from ? from[i] : 0.f;
+}
+
+// State entering every chunk.  A workgroup takes 16 channels and splits the chunks into 64 runs of 16: each thread
+// reduces its run in registers, all runs are joined through LDS, and the thread walks its run again.  64 channels and
+// 16 runs of 32 took 14 us for 512 chunks, nearly all of it waiting for the loads of one wave's run.
+template <bool BWD>
+__global__ __launch_bounds__(kJoinLanes* kJoinRuns) void k_scan_join(const ScanArgs p) {
+    __shared__ float s_a[kJoinRuns][kJoinLanes], s_h[kJoinRuns][kJoinLanes];
+    const int lane = threadIdx.x % kJoinLanes, w = threadIdx.x / kJoinLanes;
+    const int c = blockIdx.x * kJoinLanes + lane;
     const bool live = c < p.C;
-    const int64_t row0 = chunk * kChunk, base = row0 + g * kGroupRows;
-    const int n = (int)(p.rows - base < kGroupRows ? (p.rows - base < 0 ? 0 : p.rows - base) : kGroupRows);
-
-    V z[kGroupRows], x[kGroupRows], dy[kGroupRows];
-    const E* pz = (const E*)p.z + base * p.ldz + c;
-    const E* px = (const E*)p.x + base * p.ldx + c;
-    const E* pd = (const E*)p.dy + base * p.lddy + c;
+    float run = 0.f;  // state in front of the block of runs
+    for (int64_t o = 0; o < p.nchunks; o += kJoinRuns * kJoinChunks) {
+        Span v[kJoinChunks];
+        const int64_t o0 = o + w * kJoinChunks;
 #pragma unroll
-    for (int r = 0; r < kGroupRows; ++r) {
-        if (live && r < n) {
-            z[r] = *(const V*)(pz + r * p.ldz);
-            x[r] = *(const V*)(px + r * p.ldx);
-            dy[r] = *(const V*)(pd + r * p.lddy);
-        }
-    }
-    const int64_t before = sequence_starts(p, row0, s_start, tid, NT);
-    const int* st = s_start + g * kGroupRows;
-
-    float A[VC], H[VC], Ee[VC];
-    bool reset = false, end = false;
-#pragma unroll
-    for (int e = 0; e < VC; ++e) A[e] = 1.f, H[e] = 0.f, Ee[e] = 0.f;
-    if (live) {
-#pragma unroll
-        for (int r = 0; r < kGroupRows; ++r) {
-            if (r < n) {
-                const int s = st[r];
-                if (s >= 0) {
-                    reset = true;
-    #pragma unroll
-                    for (int e = 0; e < VC; ++e) H[e] = p.h0 && s < p.n_seq ? p.h0[(int64_t)s * p.C + c + e] : 0.f;
-                }
-    #pragma unroll
-                for (int e = 0; e < VC; ++e) {
-                    float a, na;
-                    gate(F::get1((const E*)&z[r] + e), a, na);
-                    H[e] = __builtin_fmaf(a, H[e], na * F::get1((const E*)&x[r] + e));
-                    A[e] *= a;
-                }
+        for (int i = 0; i < kJoinChunks; ++i) {
+            v[i] = {1.f, 0.f};
+            if (live && o0 + i < p.nchunks) {
+                const float* a = p.agg2 + (BWD ? p.nchunks - 1 - o0 - i : o0 + i) * 2 * p.C + c;
+                v[i] = {a[0], a[p.C]};
             }
         }
+        Span own{1.f, 0.f};
 #pragma unroll
-        for (int r = kGroupRows - 1; r >= 0; --r) {
-            if (r < n) {
-                if (st[r + 1] >= 0) {
-                    end = true;
-                    const int64_t q = sequence_of(s_start, g * kGroupRows + r, before);
-    #pragma unroll
-                    for (int e = 0; e < VC; ++e)
-                        Ee[e] = p.dh_last && q >= 0 && q < p.n_seq ? p.dh_last[q * p.C + c + e] : 0.f;
-                }
-    #pragma unroll
-                for (int e = 0; e < VC; ++e) {
-                    float a, na;
-                    gate(F::get1((const E*)&z[r] + e), a, na);
-                    Ee[e] = a * (F::get1((const E*)&dy[r] + e) + Ee[e]);
-                }
-            }
+        for (int i = 0; i < kJoinChunks; ++i) own = join(own, v[i]);
+        s_a[w][lane] = own.A, s_h[w][lane] = own.H;
+        __syncthreads();
+        float h = run;
+#pragma unroll 8
+        for (int j = 0; j < kJoinRuns; ++j) {
+            if (j == w) h = run;
+            run = apply(Span{s_a[j][lane], s_h[j][lane]}, run);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kJoinChunks; ++i) {
+            if (live && o0 + i < p.nchunks) p.state[(BWD ? p.nchunks - 1 - o0 - i : o0 + i) * p.C + c] = h;
+            h = apply(v[i], h);
         }
     }
+}
+
+// State entering the lane's span: the chunk's, then the spans in front of it.
+template <int VC, bool BWD>
+__device__ __forceinline__ void span_state(const ScanArgs& p, const Place<VC>& at, float (*s_a)[64 * VC],
+                                           float (*s_h)[64 * VC], float (&h)[VC]) {
+#pragma unroll
+    for (int e = 0; e < VC; ++e) h[e] = 0.f;
+    if (!p.agg1) return;
+    const bool mine = at.live && at.n > 0;
+    const float* d = lane_at<const float>(p.agg1 + (at.chunk * kSpans + at.g) * 2 * p.C, at.c);
+    const float* s = lane_at<const float>(p.state + at.chunk * p.C, at.c);
 #pragma unroll
     for (int e = 0; e < VC; ++e) {
-        s_a[g][li * VC + e] = A[e];
-        s_h[g][li * VC + e] = H[e];
-        s_e[g][li * VC + e] = Ee[e];
-    }
-    if (li == 0) s_reset[g] = reset, s_end[g] = end;
-    __syncthreads();
-    for (int i = tid; i < CB; i += NT) {
-        const int cc = cb * CB + i;
-        if (cc >= p.C) break;
-        float h = p.saved[chunk * p.C + cc], e = 0.f;
-        if (CARRY) {
-            Span own{1.f, 0.f, false};
-#pragma unroll
-            for (int k = kGroups - 1; k >= 0; --k) own = join(own, Span{s_a[k][i], s_e[k][i], s_end[k] != 0});
-            e = exchange(p, order, cc, own);
-        }
-#pragma unroll
-        for (int k = kGroups - 1; k >= 0; --k) {
-            const Span s{s_a[k][i], s_e[k][i], s_end[k] != 0};
-            s_e[k][i] = e;
-            e = apply(s, e);
-        }
-#pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-            const Span s{s_a[k][i], s_h[k][i], s_reset[k] != 0};
-            s_h[k][i] = h;
-            h = apply(s, h);
-        }
+        s_a[at.g][at.li * VC + e] = mine ? d[e] : 1.f;
+        s_h[at.g][at.li * VC + e] = mine ? d[p.C + e] : 0.f;
+        if (at.live && p.state) h[e] = s[e];
     }
     __syncthreads();
-    if (!live) return;
-    float hp[kGroupRows][VC];  // h_{t-1} of every row
-    float h[VC], ev[VC];
 #pragma unroll
-    for (int e = 0; e < VC; ++e) h[e] = s_h[g][li * VC + e], ev[e] = s_e[g][li * VC + e];
+    for (int i = 0; i < kSpans - 1; ++i) {
+        const int j = BWD ? kSpans - 1 - i : i;
+        if (BWD ? j > at.g : j < at.g) {
 #pragma unroll
-    for (int r = 0; r < kGroupRows; ++r) {
-        if (r < n) {
-            const int s = st[r];
-            if (s >= 0) {
-    #pragma unroll
-                for (int e = 0; e < VC; ++e) h[e] = p.h0 && s < p.n_seq ? p.h0[(int64_t)s * p.C + c + e] : 0.f;
-            }
-    #pragma unroll
-            for (int e = 0; e < VC; ++e) {
-                hp[r][e] = h[e];
-                float a, na;
-                gate(F::get1((const E*)&z[r] + e), a, na);
-                h[e] = __builtin_fmaf(a, h[e], na * F::get1((const E*)&x[r] + e));
-            }
+            for (int e = 0; e < VC; ++e) h[e] = apply(Span{s_a[j][at.li * VC + e], s_h[j][at.li * VC + e]}, h[e]);
         }
     }
-    E* oz = (E*)p.dz + base * p.lddz + c;
-    E* ox = (E*)p.dx + base * p.lddx + c;
+}
+
+template <class F, int VC>
+__global__ __launch_bounds__(64 * kSpans) void k_scan_forward(const ScanArgs p) {
+    using E = typename F::Elem;
+    constexpr int CB = 64 * VC, NT = 64 * kSpans;
+    __shared__ int s_start[kMaxSpan * kSpans + 1];
+    __shared__ float s_a[kSpans][CB], s_h[kSpans][CB];
+    const Place<VC> at(p, gridDim.x - 1 - blockIdx.x);  // what was read last comes first
+    const int* st = s_start + at.g * p.span;
+    const RowPtr pz = RowPtr::make<E>(p.z, at.base, p.ldz, at.c, at.live);
+    const RowPtr px = RowPtr::make<E>(p.x, at.base, p.ldx, at.c, at.live);
+    const RowPtr py = RowPtr::make<E>(p.y, at.base, p.ldy, at.c, at.live);
+    const int nb = (at.n + kBatch - 1) / kBatch;
+    Rows<F, VC> z[2], x[2];
+    auto fetch = [&](int k, int b) {
+        z[b].load(pz, k * kBatch, at.n);
+        x[b].load(px, k * kBatch, at.n);
+    };
+    if (nb > 0) fetch(0, 0);
+    const int64_t before = sequence_starts(p, at.row0, s_start, threadIdx.x, NT);
+    float h[VC];
+    span_state<VC, false>(p, at, s_a, s_h, h);
+    auto run = [&](int k, int b) {
+        const int r0 = k * kBatch;
+        const uint32_t starts = start_bits(st + r0, at.n - r0);
+        const uint32_t ends = p.h_last ? start_bits(st + r0 + 1, at.n - r0) : 0u;
+        if (p.saved && at.live) {
+            float* d = lane_at<float>(p.saved + (at.base + r0) / kBatch * p.C, at.c);
 #pragma unroll
-    for (int r = kGroupRows - 1; r >= 0; --r) {
-        if (r < n) {
-            if (st[r + 1] >= 0) {
-                const int64_t q = sequence_of(s_start, g * kGroupRows + r, before);
-    #pragma unroll
+            for (int e = 0; e < VC; ++e) d[e] = h[e];
+        }
+        float first[kBatch][VC];
+        if (starts) {
+#pragma unroll
+            for (int r = 0; r < kBatch; ++r) {
+                const int s = (starts >> r) & 1 ? start_of(st, r0 + r) : -1;
+                const bool given = p.h0 && s >= 0 && s < p.n_seq && at.live;
+#pragma unroll
                 for (int e = 0; e < VC; ++e)
-                    ev[e] = p.dh_last && q >= 0 && q < p.n_seq ? p.dh_last[q * p.C + c + e] : 0.f;
+                    first[r][e] = given ? lane_at<const float>(p.h0 + (int64_t)s * p.C, at.c)[e] : 0.f;
             }
-            V vz, vx;
-    #pragma unroll
+        }
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+            Cell<F, VC> y;
+#pragma unroll
             for (int e = 0; e < VC; ++e) {
+                if ((starts >> r) & 1) h[e] = first[r][e];
                 float a, na;
-                gate(F::get1((const E*)&z[r] + e), a, na);
-                const float G = F::get1((const E*)&dy[r] + e) + ev[e];
-                const float gx = na * G;
-                F::put1((E*)&vx + e, gx);
-                F::put1((E*)&vz + e, a * gx * (hp[r][e] - F::get1((const E*)&x[r] + e)));
-                ev[e] = a * G;
+                gate(z[b].get(r, e), a, na);
+                h[e] = __builtin_fmaf(a, h[e], na * x[b].get(r, e));
+                y.set(e, h[e]);
             }
-            if (p.dz) *(V*)(oz + r * p.lddz) = vz;
-            if (p.dx) *(V*)(ox + r * p.lddx) = vx;
-            const int s = st[r];
-            if (p.dh0 && s >= 0 && s < p.n_seq) {
-    #pragma unroll
-                for (int e = 0; e < VC; ++e) p.dh0[(int64_t)s * p.C + c + e] = ev[e];
+            store_row(py, r0 + r, at.n, y);
+            if (((ends >> r) & 1) && at.live) {
+                const int64_t q = sequence_of(s_start, at.g * p.span + r0 + r, before);
+                if (q >= 0 && q < p.n_seq) {
+#pragma unroll
+                    for (int e = 0; e < VC; ++e) lane_at<float>(p.h_last + q * p.C, at.c)[e] = h[e];
+                }
+            }
+        }
+    };
+    for (int k = 0; k < nb; k += 2) {
+        if (k + 1 < nb) fetch(k + 1, 1);
+        run(k, 0);
+        if (k + 2 < nb) fetch(k + 2, 0);
+        if (k + 1 < nb) run(k + 1, 1);
+    }
+}
+
+template <class F, int VC>
+__global__ __launch_bounds__(64 * kSpans) void k_scan_backward(const ScanArgs p) {
+    using E = typename F::Elem;
+    constexpr int CB = 64 * VC, NT = 64 * kSpans;
+    __shared__ int s_start[kMaxSpan * kSpans + 1];
+    __shared__ float s_a[kSpans][CB], s_h[kSpans][CB];
+    const Place<VC> at(p, blockIdx.x);  // the spans were read from the last chunk to the first
+    const int* st = s_start + at.g * p.span;
+    const RowPtr pz = RowPtr::make<E>(p.z, at.base, p.ldz, at.c, at.live);
+    const RowPtr px = RowPtr::make<E>(p.x, at.base, p.ldx, at.c, at.live);
+    const RowPtr pd = RowPtr::make<E>(p.dy, at.base, p.lddy, at.c, at.live);
+    const RowPtr oz = RowPtr::make<E>(p.dz, at.base, p.lddz, at.c, at.live && p.dz);
+    const RowPtr ox = RowPtr::make<E>(p.dx, at.base, p.lddx, at.c, at.live && p.dx);
+    const int nb = (at.n + kBatch - 1) / kBatch;
+    Rows<F, VC> z, x, dy;
+    float hs[VC];
+    auto fetch = [&](int k) {
+        const int r0 = k * kBatch;
+        z.load(pz, r0, at.n);
+        x.load(px, r0, at.n);
+        dy.load(pd, r0, at.n);
+        const float* d = lane_at<const float>(p.saved + (at.base + r0) / kBatch * p.C, at.live ? at.c : 0);
+#pragma unroll
+        for (int e = 0; e < VC; ++e) hs[e] = d[e];
+    };
+    if (nb > 0) fetch(nb - 1);
+    const int64_t before = sequence_starts(p, at.row0, s_start, threadIdx.x, NT);
+    float ev[VC];
+    span_state<VC, true>(p, at, s_a, s_h, ev);
+    for (int k = nb - 1; k >= 0; --k) {
+        const int r0 = k * kBatch;
+        const uint32_t starts = start_bits(st + r0, at.n - r0), ends = start_bits(st + r0 + 1, at.n - r0);
+        // the smaller of a and 1 - a, negative when that is a; a (1 - a) (h_{t-1} - x)
+        float q[kBatch][VC], w[kBatch][VC];
+        float h[VC];
+#pragma unroll
+        for (int e = 0; e < VC; ++e) h[e] = hs[e];
+        // states in front of rows that start a sequence, then the gradients that leave those rows
+        float first[kBatch][VC];
+        if (starts) {
+#pragma unroll
+            for (int r = 0; r < kBatch; ++r) {
+                const int s = (starts >> r) & 1 ? start_of(st, r0 + r) : -1;
+                const bool given = p.h0 && s >= 0 && s < p.n_seq && at.live;
+#pragma unroll
+                for (int e = 0; e < VC; ++e)
+                    first[r][e] = given ? lane_at<const float>(p.h0 + (int64_t)s * p.C, at.c)[e] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kBatch; ++r) {
+#pragma unroll
+            for (int e = 0; e < VC; ++e) {
+                if ((starts >> r) & 1) h[e] = first[r][e];
+                float a, na;
+                gate(z.get(r, e), a, na);
+                const float xv = x.get(r, e);
+                q[r][e] = __builtin_bit_cast(int, z.get(r, e)) < 0 ? -a : na;
+                w[r][e] = a * na * (h[e] - xv);
+                h[e] = __builtin_fmaf(a, h[e], na * xv);
+            }
+        }
+        const Rows<F, VC> d = dy;
+        if (k > 0) fetch(k - 1);
+        float last[kBatch][VC];
+        if (ends) {
+#pragma unroll
+            for (int r = 0; r < kBatch; ++r) {
+                const int64_t s = (ends >> r) & 1 ? sequence_of(s_start, at.g * p.span + r0 + r, before) : -1;
+                const bool given = p.dh_last && s >= 0 && s < p.n_seq && at.live;
+#pragma unroll
+                for (int e = 0; e < VC; ++e)
+                    last[r][e] = given ? lane_at<const float>(p.dh_last + s * p.C, at.c)[e] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int r = kBatch - 1; r >= 0; --r) {
+            Cell<F, VC> vz, vx;
+#pragma unroll
+            for (int e = 0; e < VC; ++e) {
+                if ((ends >> r) & 1) ev[e] = last[r][e];
+                const float small = __builtin_fabsf(q[r][e]), large = 1.f - small;
+                const bool keeps = __builtin_bit_cast(int, q[r][e]) >= 0;
+                const float G = d.get(r, e) + ev[e];
+                vx.set(e, (keeps ? small : large) * G);
+                vz.set(e, w[r][e] * G);
+                ev[e] = (keeps ? large : small) * G;
+                first[r][e] = ev[e];
+            }
+            store_row(oz, r0 + r, at.n, vz);
+            store_row(ox, r0 + r, at.n, vx);
+        }
+        if (starts && p.dh0 && at.live) {
+#pragma unroll
+            for (int r = 0; r < kBatch; ++r) {
+                const int s = (starts >> r) & 1 ? start_of(st, r0 + r) : -1;
+                if (s >= 0 && s < p.n_seq) {
+#pragma unroll
+                    for (int e = 0; e < VC; ++e) lane_at<float>(p.dh0 + (int64_t)s * p.C, at.c)[e] = first[r][e];
+                }
             }
         }
     }
 }
 
-// Clears the exchange words and the ticket, and passes the state of empty sequences through.
-__global__ __launch_bounds__(256) void k_scan_prepare(uint64_t* words, int64_t n, const int64_t* offsets,
-                                                      int64_t n_seq, int C, const float* from, float* to) {
-    const int64_t step = (int64_t)gridDim.x * 256;
-    const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    for (int64_t i = i0; i < n; i += step) words[i] = 0;
-    if (!offsets || !to) return;
-    for (int64_t i = i0; i < n_seq * C; i += step) {
-        const int64_t s = i / C;
-        if (offsets[s] == offsets[s + 1]) to[i] = from ? from[i] : 0.f;
-    }
+// ---- host ----------------------------------------------------------------------------------------------
+
+// Rows of a span.  Longer spans leave fewer states to join, shorter ones more waves: 16 rows while that gives 4096
+// waves (16 a CU), longer ones only from 16384 waves on.  Forward + backward of one sequence of 311,296 rows x 256
+// bfloat16 channels took 464 us with spans of 32, 475 with 64, 586 with 128; 50,021 x 192 float32 140 us with spans of
+// 16, 145 with 8.
+int span_rows(const gs_scan_dims& d) {
+    const int64_t waves = d.rows * ((d.channels + 127) / 128);
+    int s = kBatch;
+    while (s < kMaxSpan && waves / (2 * s) >= (s == kBatch ? 4096 : 16384)) s *= 2;
+    return s;
+}
+int64_t chunks_of(const gs_scan_dims& d) {
+    const int64_t c = (int64_t)span_rows(d) * kSpans;
+    return (d.rows + c - 1) / c;
 }
 
-int64_t chunks_of(int64_t rows) { return (rows + kChunk - 1) / kChunk; }
-int64_t exchange_words(int64_t rows, int64_t C) {
-    const int64_t k = chunks_of(rows), k1 = (k + kFan - 1) / kFan, k2 = (k1 + kFan - 1) / kFan;
-    return 1 + (2 * k + 2 * k1 + k2) * C;
-}
-
-template <class F, int VC, int LPR, bool BWD>
-hipError_t launch_scan(ScanArgs p, bool carry, hipStream_t st) {
-    p.ncb = (p.C + LPR * VC - 1) / (LPR * VC);
+template <class F, int VC, bool BWD>
+hipError_t launch_scan(ScanArgs p, hipStream_t st) {
+    p.ncb = (p.C + 64 * VC - 1) / (64 * VC);
     const int64_t grid = p.nchunks * p.ncb;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    const dim3 gd((unsigned)grid), bd(LPR * kGroups);
-    if (BWD) {
-        if (carry)
-            k_scan_backward<F, VC, LPR, true><<<gd, bd, 0, st>>>(p);
-        else
-            k_scan_backward<F, VC, LPR, false><<<gd, bd, 0, st>>>(p);
-    } else {
-        if (carry)
-            k_scan_forward<F, VC, LPR, true><<<gd, bd, 0, st>>>(p);
-        else
-            k_scan_forward<F, VC, LPR, false><<<gd, bd, 0, st>>>(p);
+    const dim3 gd((unsigned)grid), bd(64 * kSpans);
+    if (p.agg1) {
+        k_scan_spans<F, VC, BWD><<<gd, bd, 0, st>>>(p);
+        GSR_TRY(hipGetLastError());
+        if (p.nchunks > 1) {
+            k_scan_join<BWD><<<dim3((unsigned)((p.C + kJoinLanes - 1) / kJoinLanes)), kJoinLanes * kJoinRuns, 0, st>>>(p);
+            GSR_TRY(hipGetLastError());
+        } else {
+            p.state = nullptr;
+        }
     }
+    if (BWD)
+        k_scan_backward<F, VC><<<gd, bd, 0, st>>>(p);
+    else
+        k_scan_forward<F, VC><<<gd, bd, 0, st>>>(p);
     return hipGetLastError();
 }
 
-// Widest vector the addresses and strides allow; narrow rows take 32 lanes so that no half wave idles.
+// Two channels a lane where addresses and strides allow and there are more than one for every lane.
 template <class F, bool BWD>
-hipError_t pick_scan(const ScanArgs& p, bool carry, bool pairs, hipStream_t st) {
-    if (pairs) {
-        if (p.C <= 64) return launch_scan<F, 2, 32, BWD>(p, carry, st);
-        return launch_scan<F, 2, 64, BWD>(p, carry, st);
-    }
-    if (p.C <= 32) return launch_scan<F, 1, 32, BWD>(p, carry, st);
-    return launch_scan<F, 1, 64, BWD>(p, carry, st);
+hipError_t pick_scan(const ScanArgs& p, bool pairs, hipStream_t st) {
+    return pairs && p.C > 64 ? launch_scan<F, 2, BWD>(p, st) : launch_scan<F, 1, BWD>(p, st);
 }
 
 size_t elem_size(int dtype) { return dtype == GS_F32 ? 4 : 2; }
@@ -563,78 +618,70 @@ bool pairs_ok(const gs_scan_dims& d, std::initializer_list<const void*> ptrs, st
     return true;
 }
 
-// A scan needs no exchange when every chunk starts a sequence, or is the only one.
-bool needs_carry(const gs_scan_dims& d, const int64_t* offsets, int64_t nchunks) {
-    if (nchunks <= 1) return false;
-    if (offsets) return true;
-    return kChunk % (d.rows / d.n_seq) != 0;
+int64_t carve_scan(const gs_scan_dims& d, char* ws, ScanArgs* p) {
+    Carver cv{ws};
+    const int64_t n = chunks_of(d), C = d.channels;
+    p->agg1 = cv.take<float>(n * kSpans * 2 * C);
+    p->agg2 = cv.take<float>(n * 2 * C);
+    p->state = cv.take<float>(n * C);
+    return cv.used;
 }
 
-void fill_common(ScanArgs& p, const gs_scan_dims& d, const int64_t* offsets, void* ws) {
+void fill_common(ScanArgs& p, const gs_scan_dims& d, const int64_t* offsets, const gs_scan_inputs& in, void* ws) {
+    carve_scan(d, (char*)ws, &p);
+    p.z = in.gate, p.x = in.x, p.h0 = in.h0, p.ldz = in.ld_gate, p.ldx = in.ld_x;
     p.offsets = offsets;
     p.n_seq = d.n_seq;
     p.rows = d.rows;
-    p.seq_len = !offsets && d.n_seq > 0 ? d.rows / d.n_seq : 1;
-    if (p.seq_len < 1) p.seq_len = 1;
+    p.seq_len = !offsets && d.n_seq > 0 && d.rows > 0 ? d.rows / d.n_seq : 1;
     p.C = d.channels;
-    p.nchunks = chunks_of(d.rows);
-    const int64_t k1 = (p.nchunks + kFan - 1) / kFan;
-    uint64_t* w = (uint64_t*)ws;
-    p.ticket = (uint32_t*)w;
-    p.agg1 = w + 1;
-    p.agg2 = p.agg1 + 2 * p.nchunks * p.C;
-    p.run = p.agg2 + 2 * k1 * p.C;
+    p.span = span_rows(d);
+    p.nchunks = chunks_of(d);
+    if (!offsets && p.span % p.seq_len == 0) p.agg1 = nullptr;  // every span starts a sequence
 }
 
-hipError_t prepare(const ScanArgs& p, bool carry, const float* from, float* to, hipStream_t st) {
-    const int64_t n = carry ? exchange_words(p.rows, p.C) : 0;
-    const int64_t work = n > p.n_seq * p.C ? n : (p.offsets && to ? p.n_seq * p.C : n);
-    if (work <= 0) return hipSuccess;
-    int64_t bx = (work + 255) / 256;
-    if (bx > 2048) bx = 2048;
-    k_scan_prepare<<<dim3((unsigned)bx), 256, 0, st>>>((uint64_t*)p.ticket, n, p.offsets, p.n_seq, p.C, from, to);
+hipError_t pass_through(const gs_scan_dims& d, const float* from, float* to, hipStream_t st) {
+    const int64_t n = d.n_seq * d.channels;
+    if (!to || n == 0) return hipSuccess;
+    const int64_t bx = (n + 255) / 256;
+    k_scan_empty<<<dim3((unsigned)(bx > 2048 ? 2048 : bx)), 256, 0, st>>>(from, to, n);
     return hipGetLastError();
 }
 
 }  // namespace
 
 void scan_sizes(const gs_scan_dims& d, size_t* saved, size_t* ws) {
-    *saved = (size_t)round_up(chunks_of(d.rows) * d.channels * 4, kAlign);
-    *ws = (size_t)round_up(exchange_words(d.rows, d.channels) * 8, kAlign);
+    ScanArgs p{};
+    *saved = (size_t)round_up((d.rows + kBatch - 1) / kBatch * d.channels * 4, kAlign);
+    *ws = (size_t)carve_scan(d, nullptr, &p);
 }
 
 hipError_t launch_scan_forward(const gs_scan_dims& d, const int64_t* offsets, const gs_scan_inputs& in, void* y,
                                int64_t ldy, float* h_last, float* saved, void* ws, hipStream_t st) {
+    if (d.rows == 0) return pass_through(d, in.h0, h_last, st);
     ScanArgs p{};
-    fill_common(p, d, offsets, ws);
-    p.z = in.gate, p.x = in.x, p.h0 = in.h0, p.ldz = in.ld_gate, p.ldx = in.ld_x;
+    fill_common(p, d, offsets, in, ws);
     p.y = y, p.ldy = ldy, p.h_last = h_last, p.saved = saved;
-    const bool carry = needs_carry(d, offsets, p.nchunks);
-    GSR_TRY(prepare(p, carry, in.h0, h_last, st));
-    if (d.rows == 0) return hipSuccess;
     const bool pairs = pairs_ok(d, {in.gate, in.x, y}, {in.ld_gate, in.ld_x, ldy});
-    if (d.dtype == GS_BF16) return pick_scan<FmtBf16, false>(p, carry, pairs, st);
-    if (d.dtype == GS_F16) return pick_scan<FmtF16, false>(p, carry, pairs, st);
-    return pick_scan<FmtF32, false>(p, carry, pairs, st);
+    if (d.dtype == GS_BF16) return pick_scan<FmtBf16, false>(p, pairs, st);
+    if (d.dtype == GS_F16) return pick_scan<FmtF16, false>(p, pairs, st);
+    return pick_scan<FmtF32, false>(p, pairs, st);
 }
 
 hipError_t launch_scan_backward(const gs_scan_dims& d, const int64_t* offsets, const gs_scan_inputs& in,
                                 const float* saved, const void* dy, int64_t lddy, const float* dh_last,
                                 const gs_scan_grads& out, void* ws, hipStream_t st) {
+    if (d.rows == 0) return pass_through(d, dh_last, out.h0, st);
     ScanArgs p{};
-    fill_common(p, d, offsets, ws);
-    p.z = in.gate, p.x = in.x, p.h0 = in.h0, p.ldz = in.ld_gate, p.ldx = in.ld_x;
+    fill_common(p, d, offsets, in, ws);
     p.saved = const_cast<float*>(saved);
     p.dy = dy, p.lddy = lddy, p.dh_last = dh_last;
     p.dz = out.gate, p.dx = out.x, p.dh0 = out.h0, p.lddz = out.ld_gate, p.lddx = out.ld_x;
-    const bool carry = needs_carry(d, offsets, p.nchunks);
-    GSR_TRY(prepare(p, carry, dh_last, out.h0, st));
-    if (d.rows == 0) return hipSuccess;
     const bool pairs = pairs_ok(d, {in.gate, in.x, dy, out.gate, out.x},
                                 {in.ld_gate, in.ld_x, lddy, out.ld_gate, out.ld_x});
-    if (d.dtype == GS_BF16) return pick_scan<FmtBf16, true>(p, carry, pairs, st);
-    if (d.dtype == GS_F16) return pick_scan<FmtF16, true>(p, carry, pairs, st);
-    return pick_scan<FmtF32, true>(p, carry, pairs, st);
+    if (d.dtype == GS_BF16) return pick_scan<FmtBf16, true>(p, pairs, st);
+    if (d.dtype == GS_F16) return pick_scan<FmtF16, true>(p, pairs, st);
+    return pick_scan<FmtF32, true>(p, pairs, st);
 }
 
 }  // namespace gsr
