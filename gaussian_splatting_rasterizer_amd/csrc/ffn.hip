@@ -117,6 +117,30 @@ struct EpiGate {
     }
 };
 
+// The same for few rows: h is also the next product's input, which takes the block's type as it is; split planes are
+// written only for the backward pass.
+template <class F, int ACT>
+struct EpiGateFew {
+    static constexpr bool kDual = true;
+    EpiGate<F, ACT> all;        // all.h null: nothing is kept
+    typename F::Elem* h;        // [M][f8]
+    __device__ __forceinline__ void row(int m, int n, f32x4 g0, f32x4 g1, f32x4 u0, f32x4 u1) const {
+        if (m >= all.M || n >= all.f8) return;
+        if (all.h) all.row(m, n, g0, g1, u0, u1);
+        if ((const void*)h == (const void*)all.h) return;
+        f32x4 a0, a1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float a, da;
+            activation<F, ACT>(g0[e], a, da);
+            a0[e] = a * u0[e];
+            activation<F, ACT>(g1[e], a, da);
+            a1[e] = a * u1[e];
+        }
+        F::put8(h + (int64_t)m * all.f8 + n, a0, a1);
+    }
+};
+
 // dg and du from dh and the saved g and u.  The saved values are fetched ahead: read where they are used, each row of
 // products waited for its own (131072 x 2048 x 512: 1050 us).
 template <class F, int ACT>
@@ -192,17 +216,17 @@ struct EpiStore {
         }
     }
     __device__ __forceinline__ void row(int, int, int m, int n, const f32x4 (&v)[4], const Pre&) const {
+        row8(m, n, v[0], v[1]);
+        row8(m, n + 8, v[2], v[3]);
+    }
+    __device__ __forceinline__ void row8(int m, int n, f32x4 v0, f32x4 v1) const {
         typename F::Elem* c = row_of(m);
         if (!c) return;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int k = n + h * 8;
-            if (vec == 8 && k + 8 <= N) {
-                F::put8(c + k, v[h * 2], v[h * 2 + 1]);
-            } else {
-                put4(c, k, v[h * 2]);
-                put4(c, k + 4, v[h * 2 + 1]);
-            }
+        if (vec == 8 && n + 8 <= N) {
+            F::put8(c + n, v0, v1);
+        } else {
+            put4(c, n, v0);
+            put4(c, n + 4, v1);
         }
     }
 };
@@ -235,6 +259,141 @@ __global__ __launch_bounds__(256) void k_reduce(const float* part, int splits, i
         const int64_t m = i / q4;
         typename F::Elem* c = st.row_of((int)m);
         if (c) st.put4(c, (int)(i - m * q4) * 4, s);
+    }
+}
+
+// ---- few rows ------------------------------------------------------------------------------------------
+
+// At most 64 rows: the weights are read once, straight into the matrix instructions' operands, and that is all the
+// work there is.  A workgroup takes 16 columns (of both projections) and splits k over its waves; the partial sums
+// meet in LDS.  Every wave's loads are independent, so the whole weight matrix is in flight at once.
+// 16-bit: lane l holds row l % 16, k (l / 16) * 8 .. + 8 of a 16x16x32 product.  float32: k (l / 16) * 4 + j for the
+// j-th of four 16x16x4 products (both operands permute k alike).  WIDE: rows allow 16-byte loads; otherwise
+// elements are read one by one.
+constexpr int kFewRows = 64;
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <class F>
+struct FewRows {
+    static constexpr int kStep = F::kPlanes == 1 ? 32 : 16;  // k of one set of fragments
+    static constexpr int kLane = kStep / 4;                  // elements of a lane
+    static constexpr uint32_t kElem = sizeof(typename F::Elem);
+
+    // the lane's elements of one row, k0 .. of K; `row` is the byte offset of the row or kOobOffset
+    template <bool WIDE>
+    static __device__ __forceinline__ u32x4 load(__amdgpu_buffer_rsrc_t rs, uint32_t row, int k0, int K) {
+        if constexpr (WIDE) {
+            const uint32_t off = k0 < K ? row + k0 * kElem : kOobOffset;
+            return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+        } else if constexpr (kElem == 4) {
+            u32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, k0 + e < K ? row + (k0 + e) * 4u : kOobOffset, 0, 0);
+            return v;
+        } else {
+            u32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int k = k0 + e * 2;
+                const uint32_t lo =
+                    (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, k < K ? row + k * 2u : kOobOffset, 0, 0);
+                const uint32_t hi =
+                    (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, k + 1 < K ? row + k * 2u + 2u : kOobOffset, 0, 0);
+                v[e] = lo | (hi << 16);
+            }
+            return v;
+        }
+    }
+    static __device__ __forceinline__ f32x4 multiply(u32x4 w, u32x4 x, f32x4 acc) {
+        if constexpr (F::kPlanes == 1) {
+            return Mfma<typename F::Mma>::run(__builtin_bit_cast(s16x8, w), __builtin_bit_cast(s16x8, x), acc);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, (uint32_t)w[j]),
+                                                           __builtin_bit_cast(float, (uint32_t)x[j]), acc, 0, 0, 0);
+            return acc;
+        }
+    }
+};
+
+struct FewArgs {
+    const void* x;
+    const void* w;
+    const void* w2;  // the second projection of a dual product
+    int M, N, K;
+    int64_t ldx, ldw;
+};
+
+// MT tiles of 16 rows, NW waves
+template <class F, int MT, int NW, bool WIDE, class Epi>
+__global__ __launch_bounds__(NW * 64) void k_few_rows(const FewArgs p, const Epi epi) {
+    using R = FewRows<F>;
+    using E = typename F::Elem;
+    constexpr int ND = Epi::kDual ? 2 : 1;
+    constexpr int kAhead = MT == 1 ? 8 : 4;  // steps whose loads are issued together
+    __shared__ __attribute__((aligned(16))) float red[NW][MT * 16][ND * 16 + 4];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * 16, li = lane & 15;
+    const int steps = (p.K + R::kStep - 1) / R::kStep, per = (steps + NW - 1) / NW;
+    const int s0 = wave * per, s1 = min(steps, s0 + per);
+    const E* w0 = (const E*)p.w + (int64_t)n0 * p.ldw;
+    const E* w1 = (const E*)(Epi::kDual ? p.w2 : p.w) + (int64_t)n0 * p.ldw;
+    const __amdgpu_buffer_rsrc_t rw[2] = {gemm_rsrc(w0), gemm_rsrc(w1)};
+    const __amdgpu_buffer_rsrc_t rx = gemm_rsrc(p.x);
+    const uint32_t wrow = n0 + li < p.N ? (uint32_t)li * (uint32_t)p.ldw * R::kElem : kOobOffset;
+    uint32_t xrow[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+        xrow[m] = m * 16 + li < p.M ? (uint32_t)(m * 16 + li) * (uint32_t)p.ldx * R::kElem : kOobOffset;
+    f32x4 acc[MT][ND];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[m][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = s0; s < s1; s += kAhead) {
+        u32x4 wf[kAhead][ND], xf[kAhead][MT];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            // past the wave's share: out of range, zero
+            const int k0 = s + i < s1 ? (s + i) * R::kStep + (lane >> 4) * R::kLane : p.K;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+                wf[i][d] = R::template load<WIDE>(rw[d], wrow, wrow == kOobOffset ? p.K : k0, p.K);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                xf[i][m] = R::template load<WIDE>(rx, xrow[m], xrow[m] == kOobOffset ? p.K : k0, p.K);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int d = 0; d < ND; ++d) acc[m][d] = R::multiply(wf[i][d], xf[i][m], acc[m][d]);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+            *(f32x4*)&red[wave][m * 16 + li][d * 16 + (lane >> 4) * 4] = acc[m][d];
+    __syncthreads();
+    // eight columns of one row (dual: of both products) a thread, the waves' sums in order
+    for (int t = threadIdx.x; t < MT * 32; t += NW * 64) {
+        const int m = t >> 1, c = (t & 1) * 8;
+        f32x4 v[2 * ND];
+#pragma unroll
+        for (int q = 0; q < 2 * ND; ++q) {
+            const int at = (q >> 1) * 16 + c + (q & 1) * 4;
+            v[q] = *(const f32x4*)&red[0][m][at];
+#pragma unroll 4
+            for (int w = 1; w < NW; ++w) v[q] += *(const f32x4*)&red[w][m][at];
+        }
+        if constexpr (Epi::kDual)
+            epi.row(m, n0 + c, v[0], v[1], v[2], v[3]);
+        else
+            epi.row8(m, n0 + c, v[0], v[1]);
     }
 }
 
@@ -306,11 +465,55 @@ struct Packer {
     }
 };
 
+template <class F, int NW, bool WIDE, class Epi>
+hipError_t launch_few(const FewArgs& p, const Epi& epi, hipStream_t st) {
+    const dim3 gd((unsigned)((p.N + 15) / 16)), bd(NW * 64);
+    if (p.M <= 16)
+        k_few_rows<F, 1, NW, WIDE, Epi><<<gd, bd, 0, st>>>(p, epi);
+    else if (p.M <= 32)
+        k_few_rows<F, 2, NW, WIDE, Epi><<<gd, bd, 0, st>>>(p, epi);
+    else
+        k_few_rows<F, 4, NW, WIDE, Epi><<<gd, bd, 0, st>>>(p, epi);
+    return hipGetLastError();
+}
+
+// 16-byte loads: rows of 16-byte multiples on 16-byte boundaries
+template <class F>
+bool wide_rows(const void* p, int64_t cols, int64_t ld) {
+    const int64_t e = 16 / (int64_t)sizeof(typename F::Elem);
+    return cols % e == 0 && ld % e == 0 && ((uintptr_t)p % 16) == 0;
+}
+
+template <class F, int ACT>
+hipError_t forward_few(const gs_ffn_dims& d, const void* x, int64_t ldx, const gs_ffn_weights& w, void* y,
+                       int64_t ldy, void* saved, char* ws, hipStream_t st) {
+    using E = typename F::Elem;
+    const Layout<F> L(d);
+    Carver cv{ws};
+    EpiGateFew<F, ACT> e1{{nullptr, L.M * L.H8, nullptr, L.H8, (int)L.M}, nullptr};
+    if (saved) {
+        e1.all.gu = (E*)saved;
+        e1.all.h = (uint16_t*)((char*)saved + L.saved_gu_bytes());
+    }
+    // the 16-bit h that is kept is the next product's input too
+    e1.h = saved && F::kPlanes == 1 ? (E*)e1.all.h : cv.take<E>(L.M * L.H8);
+    FewArgs a{x, w.gate, w.up, (int)L.M, (int)L.H, (int)L.D, ldx, L.D};
+    if (wide_rows<F>(x, L.D, ldx) && wide_rows<F>(w.gate, L.D, L.D) && wide_rows<F>(w.up, L.D, L.D))
+        GSR_TRY((launch_few<F, 8, true>(a, e1, st)));
+    else
+        GSR_TRY((launch_few<F, 8, false>(a, e1, st)));
+    FewArgs b{e1.h, w.down, nullptr, (int)L.M, (int)L.O, (int)L.H, L.H8, L.H};
+    EpiStore<F> e2{(E*)y, nullptr, ldy, (int)L.M, 0, (int)L.O, vec_width(y, ldy, sizeof(E))};
+    if (wide_rows<F>(w.down, L.H, L.H)) return launch_few<F, 16, true>(b, e2, st);
+    return launch_few<F, 16, false>(b, e2, st);
+}
+
 template <class F, int ACT>
 hipError_t forward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const gs_ffn_weights& w, void* y,
                         int64_t ldy, void* saved, char* ws, hipStream_t st) {
     using E = typename F::Elem;
     const Layout<F> L(d);
+    if (L.M <= kFewRows) return forward_few<F, ACT>(d, x, ldx, w, y, ldy, saved, ws, st);
     Carver cv{ws};
     Packer pk;
     const Operand ox = pk.add<F>(cv, x, L.M, L.D, ldx);
@@ -431,7 +634,7 @@ void sizes_impl(const gs_ffn_dims& d, size_t* saved, size_t* fwd, size_t* bwd) {
     *saved = (size_t)(L.saved_gu_bytes() + round_up(L.h_elems() * 2, kAlign));
     // every operand counted as copied: whether one is depends on its address and stride
     const int64_t weights = 2 * pad(L.H, L.D8) + pad(L.O, L.H8) + pad(L.M, L.D8);
-    *fwd = (size_t)(weights + round_up(L.h_elems() * 2, kAlign));
+    *fwd = (size_t)(weights + round_up(std::max(L.h_elems() * 2, L.M * L.H8 * (int64_t)sizeof(typename F::Elem)), kAlign));
     *bwd = (size_t)(weights + pad(L.M, L.O8) + pad(L.M, 2 * L.H8) + round_up(part_elems<F>(L) * 4, kAlign));
 }
 

@@ -22,18 +22,17 @@ def _dtype_code(dtype, allowed=("float32", "bfloat16", "float16")):
 
 
 def _matrix(t, name, rows, cols, dtype, device):
-    """Checks a [rows, cols] device tensor whose rows are contiguous; returns its row stride."""
-    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{'rows' if rows is None else rows}, {cols}]")
+    """Checks a [rows, cols] device tensor whose rows are contiguous and do not overlap; returns its row stride."""
+    if t.dim() != 2 or tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{rows}, {cols}]")
     if t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.shape[0] > 1 and t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < cols:
+    step, along = t.stride()
+    if (cols > 1 and along != 1) or (rows > 1 and step < cols):
         raise ValueError(f"{name} needs contiguous rows that do not overlap (strides {t.stride()})")
-    if t.shape[0] <= 1 and t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} needs contiguous rows (strides {t.stride()})")
-    return max(int(t.stride(0)), cols) if t.shape[0] > 1 else cols
+    return step if rows > 1 else cols
 
 
 def _exact(t, name, shape, dtype, device):
@@ -43,23 +42,10 @@ def _exact(t, name, shape, dtype, device):
     return t
 
 
-class _Workspace:
-    """Device scratch of one object.  It is replaced when a call needs more; the old one is released in the order of
-    the stream that used it last."""
-
-    def __init__(self, device):
-        self.device = device
-        self.buf = None
-
-    def get(self, nbytes, stream):
-        import torch
-        if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=self.device)
-        self.buf.record_stream(stream)
-        return self.buf
-
-
 class _Op:
+    """A device, and scratch memory that grows when a call needs more (released in the order of the streams that used
+    it)."""
+
     def __init__(self, device):
         import torch
         b.load_library()
@@ -69,12 +55,25 @@ class _Op:
             raise ValueError(f"the tensors must be on a GPU, got {self.device}")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
-        self.workspace = _Workspace(self.device)
+        self.workspace = None
+        self._home = None  # the stream the workspace was allocated on
 
-    def _scope(self, stream):
-        """The stream of a call, current (with its device) while outputs and scratch are allocated for it."""
-        s = self.torch.cuda.current_stream(self.device) if stream is None else stream
-        return s, self.torch.cuda.stream(s)
+    def _scratch(self, nbytes, stream):
+        if self.workspace is None or self.workspace.numel() < nbytes:
+            self.workspace = self.torch.empty(max(int(nbytes), 256), dtype=self.torch.uint8, device=self.device)
+            self._home = stream.cuda_stream
+        elif stream.cuda_stream != self._home:
+            self.workspace.record_stream(stream)
+        return self.workspace
+
+    def _on(self, stream, call, *args):
+        """call(stream, *args) with the stream and its device current, for allocations and the launch."""
+        t = self.torch
+        current = t.cuda.current_stream(self.device)
+        if (stream is None or stream == current) and t.cuda.current_device() == self.device.index:
+            return call(current, *args)
+        with t.cuda.stream(current if stream is None else stream) as _, t.cuda.device(self.device):
+            return call(current if stream is None else stream, *args)
 
 
 class GatedFFN(_Op):
@@ -100,29 +99,35 @@ class GatedFFN(_Op):
         self.w_down = _exact(w_down, "w_down", (self.d_out, self.d_hidden), self.dtype, self.device)
         self._sizes = {}
 
-    def _dims(self, rows):
-        d = b.gs_ffn_dims(rows, self.d_in, self.d_hidden, self.d_out, self.code, self.activation)
-        if rows not in self._sizes:
-            if len(self._sizes) > 64:
-                self._sizes.clear()
-            self._sizes[rows] = b.gs_ffn_sizes(d)
-        return d, self._sizes[rows]
-
+    @property
     def _weights(self):
         return b.gs_ffn_weights(self.w_gate.data_ptr(), self.w_up.data_ptr(), self.w_down.data_ptr())
 
+    def _dims(self, rows):
+        """(dims, sizes) for a number of rows."""
+        if rows not in self._sizes:
+            if len(self._sizes) > 64:
+                self._sizes.clear()
+            d = b.gs_ffn_dims(rows, self.d_in, self.d_hidden, self.d_out, self.code, self.activation)
+            self._sizes[rows] = (d, b.gs_ffn_sizes(d))
+        return self._sizes[rows]
+
     def forward(self, x, y=None, save=False, stream=None):
         """x [rows, d_in] -> y [rows, d_out]; with save, (y, saved) for backward."""
+        return self._on(stream, self._forward, x, y, save)
+
+    def _forward(self, stream, x, y, save):
         rows = int(x.shape[0])
         ldx = _matrix(x, "x", rows, self.d_in, self.dtype, self.device)
         dims, (n_saved, n_ws, _) = self._dims(rows)
-        s, scope = self._scope(stream)
-        with scope:
-            if y is None:
-                y = self.torch.empty((rows, self.d_out), dtype=self.dtype, device=self.device)
+        empty = self.torch.empty
+        if y is None:
+            y = empty((rows, self.d_out), dtype=self.dtype, device=self.device)
+            ldy = self.d_out
+        else:
             ldy = _matrix(y, "y", rows, self.d_out, self.dtype, self.device)
-            saved = self.torch.empty(max(n_saved, 256), dtype=self.torch.uint8, device=self.device) if save else None
-            b.gs_ffn_forward(dims, x, ldx, self._weights(), y, ldy, saved, self.workspace.get(n_ws, s), s)
+        saved = empty(max(n_saved, 256), dtype=self.torch.uint8, device=self.device) if save else None
+        b.gs_ffn_forward(dims, x, ldx, self._weights, y, ldy, saved, self._scratch(n_ws, stream), stream)
         return (y, saved) if save else y
 
     def new_grads(self, rows):
@@ -135,26 +140,27 @@ class GatedFFN(_Op):
     def backward(self, x, saved, dy, grads=None, stream=None):
         """Gradients for dL/dy = dy [rows, d_out]: a dict of x, w_gate, w_up, w_down (written; with a given dict, only
         the tensors it holds)."""
+        return self._on(stream, self._backward, x, saved, dy, grads)
+
+    def _backward(self, stream, x, saved, dy, grads):
         rows = int(x.shape[0])
         ldx = _matrix(x, "x", rows, self.d_in, self.dtype, self.device)
         lddy = _matrix(dy, "dy", rows, self.d_out, self.dtype, self.device)
         dims, (n_saved, _, n_ws) = self._dims(rows)
         if saved is None or saved.numel() < n_saved or saved.device != self.device:
             raise ValueError("saved is not what forward(x, save=True) returned for these rows")
-        s, scope = self._scope(stream)
-        with scope:
-            if grads is None:
-                grads = self.new_grads(rows)
-            ld_gx = self.d_in
+        ld_gx = self.d_in
+        if grads is None:
+            grads = self.new_grads(rows)
+        else:
             if grads.get("x") is not None:
                 ld_gx = _matrix(grads["x"], "grads['x']", rows, self.d_in, self.dtype, self.device)
             for name in ("w_gate", "w_up", "w_down"):
                 if grads.get(name) is not None:
                     _exact(grads[name], f"grads[{name!r}]", getattr(self, name).shape, self.dtype, self.device)
-            ptr = {k: grads[k].data_ptr() if grads.get(k) is not None else None
-                   for k in ("x", "w_gate", "w_up", "w_down")}
-            out = b.gs_ffn_grads(ptr["x"], ld_gx, ptr["w_gate"], ptr["w_up"], ptr["w_down"])
-            b.gs_ffn_backward(dims, x, ldx, self._weights(), saved, dy, lddy, out, self.workspace.get(n_ws, s), s)
+        ptr = {k: grads[k].data_ptr() if grads.get(k) is not None else None for k in ("x", "w_gate", "w_up", "w_down")}
+        out = b.gs_ffn_grads(ptr["x"], ld_gx, ptr["w_gate"], ptr["w_up"], ptr["w_down"])
+        b.gs_ffn_backward(dims, x, ldx, self._weights, saved, dy, lddy, out, self._scratch(n_ws, stream), stream)
         return grads
 
 
@@ -171,6 +177,7 @@ class GatedScan(_Op):
         self.channels = int(channels)
         self.dtype = dtype
         self.code = _dtype_code(dtype)
+        self._sizes = {}
 
     def _setup(self, gate, x, h0, offsets):
         t = self.torch
@@ -186,53 +193,62 @@ class GatedScan(_Op):
             n_seq = int(h0.shape[0]) if h0 is not None else 1
         if h0 is not None:
             _exact(h0, "h0", (n_seq, c), t.float32, self.device)
-        dims = b.gs_scan_dims(rows, n_seq, c, self.code)
+        key = (rows, n_seq)
+        if key not in self._sizes:
+            if len(self._sizes) > 64:
+                self._sizes.clear()
+            d = b.gs_scan_dims(rows, n_seq, c, self.code)
+            self._sizes[key] = (d, b.gs_scan_sizes(d))
+        dims, sizes = self._sizes[key]
         inputs = b.gs_scan_inputs(gate.data_ptr(), x.data_ptr(), h0.data_ptr() if h0 is not None else None, ldz, ldx)
-        return rows, n_seq, dims, inputs
+        return rows, n_seq, dims, sizes, inputs
 
     def forward(self, gate, x, h0=None, offsets=None, y=None, h_last=None, save=False, stream=None):
         """-> (y, h_last); with save, (y, h_last, saved) for backward.  h_last may be h0 (updated in place)."""
-        rows, n_seq, dims, inputs = self._setup(gate, x, h0, offsets)
-        n_saved, n_ws = b.gs_scan_sizes(dims)
-        s, scope = self._scope(stream)
-        t = self.torch
-        with scope:
-            if y is None:
-                y = t.empty((rows, self.channels), dtype=self.dtype, device=self.device)
-            ldy = _matrix(y, "y", rows, self.channels, self.dtype, self.device)
-            if h_last is None:
-                h_last = t.empty((n_seq, self.channels), dtype=t.float32, device=self.device)
-            _exact(h_last, "h_last", (n_seq, self.channels), t.float32, self.device)
-            saved = t.empty(max(n_saved, 256), dtype=t.uint8, device=self.device) if save else None
-            b.gs_scan_forward(dims, offsets, inputs, y, ldy, h_last, saved, self.workspace.get(n_ws, s), s)
+        return self._on(stream, self._forward, gate, x, h0, offsets, y, h_last, save)
+
+    def _forward(self, stream, gate, x, h0, offsets, y, h_last, save):
+        rows, n_seq, dims, (n_saved, n_ws), inputs = self._setup(gate, x, h0, offsets)
+        t, c = self.torch, self.channels
+        if y is None:
+            y = t.empty((rows, c), dtype=self.dtype, device=self.device)
+            ldy = c
+        else:
+            ldy = _matrix(y, "y", rows, c, self.dtype, self.device)
+        if h_last is None:
+            h_last = t.empty((n_seq, c), dtype=t.float32, device=self.device)
+        else:
+            _exact(h_last, "h_last", (n_seq, c), t.float32, self.device)
+        saved = t.empty(max(n_saved, 256), dtype=t.uint8, device=self.device) if save else None
+        b.gs_scan_forward(dims, offsets, inputs, y, ldy, h_last, saved, self._scratch(n_ws, stream), stream)
         return (y, h_last, saved) if save else (y, h_last)
 
     def backward(self, gate, x, saved, dy, dh_last=None, h0=None, offsets=None, grads=None, stream=None):
         """Gradients for dy [rows, channels] and dh_last [n_seq, channels]: a dict of gate, x, h0."""
-        rows, n_seq, dims, inputs = self._setup(gate, x, h0, offsets)
-        lddy = _matrix(dy, "dy", rows, self.channels, self.dtype, self.device)
-        n_saved, n_ws = b.gs_scan_sizes(dims)
-        t = self.torch
+        return self._on(stream, self._backward, gate, x, saved, dy, dh_last, h0, offsets, grads)
+
+    def _backward(self, stream, gate, x, saved, dy, dh_last, h0, offsets, grads):
+        rows, n_seq, dims, (n_saved, n_ws), inputs = self._setup(gate, x, h0, offsets)
+        t, c = self.torch, self.channels
+        lddy = _matrix(dy, "dy", rows, c, self.dtype, self.device)
         if saved is None or saved.numel() < n_saved or saved.device != self.device:
             raise ValueError("saved is not what forward(..., save=True) returned for these rows")
         if dh_last is not None:
-            _exact(dh_last, "dh_last", (n_seq, self.channels), t.float32, self.device)
-        s, scope = self._scope(stream)
-        with scope:
-            if grads is None:
-                like = dict(dtype=self.dtype, device=self.device)
-                grads = {"gate": t.empty((rows, self.channels), **like), "x": t.empty((rows, self.channels), **like),
-                         "h0": t.empty((n_seq, self.channels), dtype=t.float32, device=self.device)}
-            ld = {}
+            _exact(dh_last, "dh_last", (n_seq, c), t.float32, self.device)
+        ld = {"gate": c, "x": c}
+        if grads is None:
+            like = dict(dtype=self.dtype, device=self.device)
+            grads = {"gate": t.empty((rows, c), **like), "x": t.empty((rows, c), **like),
+                     "h0": t.empty((n_seq, c), dtype=t.float32, device=self.device)}
+        else:
             for name in ("gate", "x"):
-                ld[name] = self.channels
                 if grads.get(name) is not None:
-                    ld[name] = _matrix(grads[name], f"grads[{name!r}]", rows, self.channels, self.dtype, self.device)
+                    ld[name] = _matrix(grads[name], f"grads[{name!r}]", rows, c, self.dtype, self.device)
             if grads.get("h0") is not None:
-                _exact(grads["h0"], "grads['h0']", (n_seq, self.channels), t.float32, self.device)
-            ptr = {k: grads[k].data_ptr() if grads.get(k) is not None else None for k in ("gate", "x", "h0")}
-            out = b.gs_scan_grads(ptr["gate"], ptr["x"], ptr["h0"], ld["gate"], ld["x"])
-            b.gs_scan_backward(dims, offsets, inputs, saved, dy, lddy, dh_last, out, self.workspace.get(n_ws, s), s)
+                _exact(grads["h0"], "grads['h0']", (n_seq, c), t.float32, self.device)
+        ptr = {k: grads[k].data_ptr() if grads.get(k) is not None else None for k in ("gate", "x", "h0")}
+        out = b.gs_scan_grads(ptr["gate"], ptr["x"], ptr["h0"], ld["gate"], ld["x"])
+        b.gs_scan_backward(dims, offsets, inputs, saved, dy, lddy, dh_last, out, self._scratch(n_ws, stream), stream)
         return grads
 
 
@@ -261,12 +277,14 @@ class Orthogonalizer(_Op):
 
     def run(self, g, out=None, stream=None):
         """g [batch, rows, cols] (or [rows, cols] when batch is 1), contiguous."""
+        return self._on(stream, self._run, g, out)
+
+    def _run(self, stream, g, out):
         shape = self.shape if g.dim() != 2 or self.shape[0] != 1 else self.shape[1:]
         _exact(g, "g", shape, self.dtype, self.device)
-        s, scope = self._scope(stream)
-        with scope:
-            if out is None:
-                out = self.torch.empty(shape, dtype=self.out_dtype, device=self.device)
+        if out is None:
+            out = self.torch.empty(shape, dtype=self.out_dtype, device=self.device)
+        else:
             _exact(out, "out", shape, self.out_dtype, self.device)
-            b.gs_orthogonalize(self.dims, g, out, self.workspace.get(self.nbytes, s), s)
+        b.gs_orthogonalize(self.dims, g, out, self._scratch(self.nbytes, stream), stream)
         return out

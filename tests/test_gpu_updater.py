@@ -150,9 +150,9 @@ def test_ffn_keeps_bad_rows_apart(dtype, rows):
     (NaN bit patterns) reach nothing."""
     x, wg, wu, wd, dy = ffn_inputs(rows, 50, 70, 30, dtype, seed=6)
     block = gsr().GatedFFN(wg, wu, wd)
-    block.workspace.get(1 << 24, torch.cuda.current_stream()).fill_(255)
+    block._scratch(1 << 24, torch.cuda.current_stream()).fill_(255)
     y0, s0 = block.forward(x, save=True)
-    block.workspace.buf.fill_(255)
+    block.workspace.fill_(255)
     g0 = block.backward(x, s0, dy)
     bad = x.clone()
     bad[2, 7] = float("nan")
@@ -497,7 +497,7 @@ def test_ortho_repeats_and_refuses():
     g = randn(gen(3), 2, 100, 60)
     op = m.Orthogonalizer(2, 100, 60, torch.float32, torch.bfloat16, steps=3, coefficients=(1.5, -0.5, 0.0))
     first = op.run(g)
-    op.workspace.buf.fill_(255)
+    op.workspace.fill_(255)
     assert torch.equal(first, op.run(g))
     o.check(first[1], o.newton_schulz(g[1], 3, (1.5, -0.5, 0.0)), ortho_tol(torch.bfloat16), "out")
     one = m.Orthogonalizer(1, 100, 60, torch.float32, torch.bfloat16, steps=3, coefficients=(1.5, -0.5, 0.0))
