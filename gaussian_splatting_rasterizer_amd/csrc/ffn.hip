@@ -324,6 +324,7 @@ struct FewArgs {
     const void* w;
     const void* w2;  // the second projection of a dual product
     int M, N, K;
+    int cols;    // columns of a workgroup: 16, or 8 where 16 would leave CUs without one
     int64_t ldx, ldw;
 };
 
@@ -336,14 +337,14 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(const FewArgs p, const Epi
     constexpr int kAhead = MT == 1 ? 8 : 4;  // steps whose loads are issued together
     __shared__ __attribute__((aligned(16))) float red[NW][MT * 16][ND * 16 + 4];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * 16, li = lane & 15;
+    const int n0 = blockIdx.x * p.cols, li = lane & 15;
     const int steps = (p.K + R::kStep - 1) / R::kStep, per = (steps + NW - 1) / NW;
     const int s0 = wave * per, s1 = min(steps, s0 + per);
     const E* w0 = (const E*)p.w + (int64_t)n0 * p.ldw;
     const E* w1 = (const E*)(Epi::kDual ? p.w2 : p.w) + (int64_t)n0 * p.ldw;
     const __amdgpu_buffer_rsrc_t rw[2] = {gemm_rsrc(w0), gemm_rsrc(w1)};
     const __amdgpu_buffer_rsrc_t rx = gemm_rsrc(p.x);
-    const uint32_t wrow = n0 + li < p.N ? (uint32_t)li * (uint32_t)p.ldw * R::kElem : kOobOffset;
+    const uint32_t wrow = li < p.cols && n0 + li < p.N ? (uint32_t)li * (uint32_t)p.ldw * R::kElem : kOobOffset;
     uint32_t xrow[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -382,6 +383,7 @@ __global__ __launch_bounds__(NW * 64) void k_few_rows(const FewArgs p, const Epi
     // eight columns of one row (dual: of both products) a thread, the waves' sums in order
     for (int t = threadIdx.x; t < MT * 32; t += NW * 64) {
         const int m = t >> 1, c = (t & 1) * 8;
+        if (c >= p.cols) continue;
         f32x4 v[2 * ND];
 #pragma unroll
         for (int q = 0; q < 2 * ND; ++q) {
@@ -466,8 +468,9 @@ struct Packer {
 };
 
 template <class F, int NW, bool WIDE, class Epi>
-hipError_t launch_few(const FewArgs& p, const Epi& epi, hipStream_t st) {
-    const dim3 gd((unsigned)((p.N + 15) / 16)), bd(NW * 64);
+hipError_t launch_few(FewArgs p, const Epi& epi, hipStream_t st) {
+    p.cols = p.N > 8 * 128 ? 16 : 8;
+    const dim3 gd((unsigned)((p.N + p.cols - 1) / p.cols)), bd(NW * 64);
     if (p.M <= 16)
         k_few_rows<F, 1, NW, WIDE, Epi><<<gd, bd, 0, st>>>(p, epi);
     else if (p.M <= 32)
@@ -497,12 +500,12 @@ hipError_t forward_few(const gs_ffn_dims& d, const void* x, int64_t ldx, const g
     }
     // the 16-bit h that is kept is the next product's input too
     e1.h = saved && F::kPlanes == 1 ? (E*)e1.all.h : cv.take<E>(L.M * L.H8);
-    FewArgs a{x, w.gate, w.up, (int)L.M, (int)L.H, (int)L.D, ldx, L.D};
+    FewArgs a{x, w.gate, w.up, (int)L.M, (int)L.H, (int)L.D, 16, ldx, L.D};
     if (wide_rows<F>(x, L.D, ldx) && wide_rows<F>(w.gate, L.D, L.D) && wide_rows<F>(w.up, L.D, L.D))
         GSR_TRY((launch_few<F, 8, true>(a, e1, st)));
     else
         GSR_TRY((launch_few<F, 8, false>(a, e1, st)));
-    FewArgs b{e1.h, w.down, nullptr, (int)L.M, (int)L.O, (int)L.H, L.H8, L.H};
+    FewArgs b{e1.h, w.down, nullptr, (int)L.M, (int)L.O, (int)L.H, 16, L.H8, L.H};
     EpiStore<F> e2{(E*)y, nullptr, ldy, (int)L.M, 0, (int)L.O, vec_width(y, ldy, sizeof(E))};
     if (wide_rows<F>(w.down, L.H, L.H)) return launch_few<F, 16, true>(b, e2, st);
     return launch_few<F, 16, false>(b, e2, st);
