@@ -249,16 +249,31 @@ struct EpiPartial {
     }
 };
 
-// Sum of the partials in split order (the result does not depend on scheduling), stored like EpiStore.
+// Sum of the partials, stored like EpiStore.  Eight threads share four columns' splits and their sums are joined in a
+// fixed order (the result does not depend on scheduling); with one thread for all splits the many small loads in a
+// row took 18 us for 64 splits of 512 x 57.
 template <class F>
 __global__ __launch_bounds__(256) void k_reduce(const float* part, int splits, int M, int64_t n4, EpiStore<F> st) {
+    __shared__ f32x4 s_sum[8][32];
     const int64_t q4 = n4 / 4, n = (int64_t)M * q4;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        f32x4 s = *(const f32x4*)(part + i * 4);
-        for (int k = 1; k < splits; ++k) s += *(const f32x4*)(part + ((int64_t)k * M * n4) + i * 4);
-        const int64_t m = i / q4;
-        typename F::Elem* c = st.row_of((int)m);
-        if (c) st.put4(c, (int)(i - m * q4) * 4, s);
+    const int li = threadIdx.x & 31, g = threadIdx.x >> 5;
+    for (int64_t i0 = (int64_t)blockIdx.x * 32; i0 < n; i0 += (int64_t)gridDim.x * 32) {
+        const int64_t i = i0 + li;
+        f32x4 s{0.f, 0.f, 0.f, 0.f};
+        if (i < n) {
+#pragma unroll 4
+            for (int k = g; k < splits; k += 8) s += *(const f32x4*)(part + (int64_t)k * M * n4 + i * 4);
+        }
+        s_sum[g][li] = s;
+        __syncthreads();
+        if (g == 0 && i < n) {
+#pragma unroll
+            for (int k = 1; k < 8; ++k) s += s_sum[k][li];
+            const int64_t m = i / q4;
+            typename F::Elem* c = st.row_of((int)m);
+            if (c) st.put4(c, (int)(i - m * q4) * 4, s);
+        }
+        __syncthreads();
     }
 }
 
@@ -417,16 +432,11 @@ void add_segments(GemmArgs& g, const Operand& a, const Operand& b, const Operand
     g.ldb = b.ld;
 }
 
-// Splits of a weight gradient along its rows: enough workgroups to fill the GPU, at least 8 k tiles each.
-int grad_splits(int64_t M, int64_t N, int64_t K, int nseg) {
-    const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
-    const int64_t kt = (K + kGemmBK - 1) / kGemmBK * nseg;
-    int64_t s = 512 / (tiles > 0 ? tiles : 1);
-    if (s > kt / 8) s = kt / 8;
-    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+// Weight gradients may be split along the rows they sum over.
+constexpr int kMaxSplits = 64;
+GemmPlan grad_plan(int64_t M, int64_t N, int64_t K, int nseg) {
+    return plan_gemm(M, N, 1, (K + kGemmBK - 1) / kGemmBK * nseg, false, false, kMaxSplits);
 }
-
-// ---- workspace -----------------------------------------------------------------------------------------
 
 template <class F>
 struct Layout {
@@ -542,13 +552,11 @@ hipError_t forward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const 
     const int64_t h_plane = L.M * L.H8;
     GemmArgs g1 = make_args(L.M, L.H, L.D);
     add_segments<F>(g1, ox, og, &ou);
-    one_split(g1);
     EpiGate<F, ACT> e1{h, h_plane, gu, L.H8, (int)L.M};
     GSR_TRY((launch_gemm<typename F::Mma, true, true>(g1, e1, st)));
     GemmArgs g2 = make_args(L.M, L.O, L.H8);
     add_segments<F>(g2, Operand{h, h_plane, L.H8}, od, nullptr);
     g2.K = (int)L.H;
-    one_split(g2);
     EpiStore<F> e2{(E*)y, nullptr, ldy, (int)L.M, 0, (int)L.O, vec_width(y, ldy, sizeof(E))};
     return launch_gemm<typename F::Mma, true, true>(g2, e2, st);
 }
@@ -558,24 +566,21 @@ hipError_t weight_grad(const Operand& a, int64_t a_cols, const Operand& b, int64
                        EpiStore<F> store, float* part, hipStream_t st) {
     GemmArgs g = make_args(a_cols, b_cols, rows);
     add_segments<F>(g, a, b, nullptr);
+    const GemmPlan plan = grad_plan(a_cols, b_cols, rows, g.nseg);
+    if (plan.splits == 1) return launch_planned<typename F::Mma, false, false>(g, plan, store, st);
     const int64_t n4 = (store.N + 3) / 4 * 4;
-    g.splits = grad_splits(a_cols, b_cols, rows, g.nseg);
-    const int total = g.nseg * ((g.K + kGemmBK - 1) / kGemmBK);
-    g.tiles_per_split = (total + g.splits - 1) / g.splits;
-    if (g.splits == 1) return launch_gemm<typename F::Mma, false, false>(g, store, st);
     EpiPartial ep{part, n4, (int)a_cols};
-    GSR_TRY((launch_gemm<typename F::Mma, false, false>(g, ep, st)));
-    const int64_t n = a_cols * n4 / 4;
-    int64_t bx = (n + 255) / 256;
+    GSR_TRY((launch_planned<typename F::Mma, false, false>(g, plan, ep, st)));
+    int64_t bx = (a_cols * n4 / 4 + 31) / 32;
     if (bx > 8192) bx = 8192;
-    k_reduce<F><<<dim3((unsigned)bx), 256, 0, st>>>(part, g.splits, (int)a_cols, n4, store);
+    k_reduce<F><<<dim3((unsigned)bx), 256, 0, st>>>(part, plan.splits, (int)a_cols, n4, store);
     return hipGetLastError();
 }
 
 template <class F>
 int64_t part_elems(const Layout<F>& L) {
     const int nseg = F::kPlanes == 1 ? 1 : 6;
-    const int64_t s1 = grad_splits(2 * L.H8, L.D8, L.M, nseg), s2 = grad_splits(L.O8, L.H8, L.M, nseg);
+    const int64_t s1 = grad_plan(2 * L.H8, L.D8, L.M, nseg).splits, s2 = grad_plan(L.O8, L.H8, L.M, nseg).splits;
     const int64_t p1 = s1 > 1 ? s1 * 2 * L.H8 * L.D8 : 0, p2 = s2 > 1 ? s2 * L.O8 * L.H8 : 0;
     return p1 > p2 ? p1 : p2;
 }
@@ -606,7 +611,6 @@ hipError_t backward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const
 
     GemmArgs g1 = make_args(L.M, L.H8, L.O);
     add_segments<F>(g1, ody, od, nullptr);
-    one_split(g1);
     EpiGateGrad<F, ACT> e1{gu, dgu, plane, L.H8, (int)L.M};
     GSR_TRY((launch_gemm<T, true, false>(g1, e1, st)));
     const Operand odgu{dgu, plane, 2 * L.H8};
@@ -614,8 +618,7 @@ hipError_t backward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const
         GemmArgs g2 = make_args(L.M, L.D8, L.H);
         add_segments<F>(g2, odgu, og, nullptr, 0);
         add_segments<F>(g2, odgu, ou, nullptr, L.H8);
-        one_split(g2);
-        EpiStore<F> e2{(E*)out.x, nullptr, lddx, (int)L.M, 0, (int)L.D, vec_width(out.x, lddx, sizeof(E))};
+            EpiStore<F> e2{(E*)out.x, nullptr, lddx, (int)L.M, 0, (int)L.D, vec_width(out.x, lddx, sizeof(E))};
         GSR_TRY((launch_gemm<T, true, false>(g2, e2, st)));
     }
     if (out.gate || out.up) {

@@ -173,6 +173,14 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& p, int id, int& tm, in
     tn = in / rows;
 }
 
+// On and above the diagonal, column by column (the mirrored tile is written too).
+__device__ __forceinline__ void symmetric_tile(int id, int& tm, int& tn) {
+    tn = (int)((__builtin_sqrtf(8.f * (float)id + 1.f) - 1.f) * 0.5f);
+    while (tn * (tn + 1) / 2 > id) --tn;
+    while ((tn + 1) * (tn + 2) / 2 <= id) ++tn;
+    tm = id - tn * (tn + 1) / 2;
+}
+
 __device__ __forceinline__ int xcd_order(int bid, int n) {
     const int x = bid & 7, l = bid >> 3;
     const int q = n >> 3, r = n & 7;
@@ -193,14 +201,16 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p, con
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WN, wn = wave % WN;
-    const int tiles = p.tiles_m * p.tiles_n;
+    const int tiles = Epi::kSymmetric ? p.tiles_n * (p.tiles_n + 1) / 2 : p.tiles_m * p.tiles_n;
     int id = xcd_order(blockIdx.x, gridDim.x);
     const int batch = id / (tiles * p.splits);
     id -= batch * (tiles * p.splits);
     const int split = id / tiles;
     int tm, tn;
-    gemm_tile(p, id - split * tiles, tm, tn);
-    if (Epi::kSymmetric && tm > tn) return;  // the mirrored tile writes both
+    if (Epi::kSymmetric)
+        symmetric_tile(id - split * tiles, tm, tn);
+    else
+        gemm_tile(p, id - split * tiles, tm, tn);
 
     constexpr int BNR = Epi::kDual ? BN / 2 : BN;  // output columns of a tile
     const int m0 = tm * BM, n0 = tn * BNR;
@@ -429,25 +439,60 @@ inline hipError_t launch_tiles(GemmArgs p, const Epi& epi, hipStream_t st) {
     constexpr int BNR = Epi::kDual ? BN / 2 : BN;
     p.tiles_m = (p.M + BM - 1) / BM;
     p.tiles_n = (p.N + BNR - 1) / BNR;
-    const int64_t n = (int64_t)p.tiles_m * p.tiles_n * p.batch * p.splits;
+    const int64_t tiles = Epi::kSymmetric ? (int64_t)p.tiles_n * (p.tiles_n + 1) / 2 : (int64_t)p.tiles_m * p.tiles_n;
+    const int64_t n = tiles * p.batch * p.splits;
     if (n <= 0) return hipSuccess;
     if (n > 0x7fffffff) return hipErrorInvalidValue;
     k_gemm16<T, AKC, BKC, BM, BN, WM, WN, Epi><<<dim3((unsigned)n), dim3(WM * WN * 64), 0, st>>>(p, epi);
     return hipGetLastError();
 }
 
-inline int64_t tile_count(const GemmArgs& p, int bm, int bnr) {
-    return (int64_t)((p.M + bm - 1) / bm) * ((p.N + bnr - 1) / bnr) * p.batch * p.splits;
+inline int64_t tile_count(int64_t M, int64_t N, int t, bool symmetric) {
+    const int64_t tm = (M + t - 1) / t, tn = (N + t - 1) / t;
+    return symmetric ? tn * (tn + 1) / 2 : tm * tn;
 }
 
-// 256x256 tiles read each operand half as often as 128x128 ones but leave CUs idle below one tile per CU.
-constexpr int64_t kBigTiles = 192;
+// Tile size and splits along k of one product, from what the two kernels were measured to take: a 256x256 tile 2.1 us
+// per 64 k (one workgroup a CU) and 7 us around them, a 128x128 tile 1.15 us with two workgroups on a CU, 0.85 us
+// alone, and 3 us.  A split product writes and reads its float32 partial sums at 4 TB/s and needs one more kernel.
+// dual: N counts the columns of one of the two matrices.
+struct GemmPlan {
+    bool big;
+    int splits, tiles_per_split;
+    double us;
+};
+inline GemmPlan plan_gemm(int64_t M, int64_t N, int64_t batch, int64_t ktiles, bool dual, bool symmetric,
+                          int max_splits) {
+    GemmPlan best{false, 1, (int)ktiles, 1e30};
+    for (int big = 0; big < 2; ++big) {
+        const int t = big ? 256 : 128;
+        const int64_t tiles = (dual ? ((M + t - 1) / t) * ((N + t / 2 - 1) / (t / 2)) : tile_count(M, N, t, symmetric)) * batch;
+        for (int s = 1; s <= max_splits; s = s < 8 ? s + 1 : s + s / 4) {
+            const int64_t per = (ktiles + s - 1) / s, n = tiles * s;
+            if (s > 1 && (per < 4 || n > 1024)) break;
+            const int64_t rounds = big ? (n + 255) / 256 : (n + 511) / 512;
+            const double tile = big ? 2.1 * per + 7 : n <= 256 ? 0.85 * per + 3 : 1.15 * per + 3;
+            const double sums = s > 1 ? 6 + (double)tiles * t * t * 4 * 2 * s / 4e6 : 0;
+            const double us = rounds * tile + sums;
+            if (us < best.us) best = {big != 0, s, (int)per, us};
+        }
+    }
+    return best;
+}
 
 template <class T, bool AKC, bool BKC, class Epi>
-inline hipError_t launch_gemm(const GemmArgs& p, const Epi& epi, hipStream_t st) {
-    if (tile_count(p, 256, Epi::kDual ? 128 : 256) >= kBigTiles)
-        return launch_tiles<T, AKC, BKC, 256, 256, 2, 4, Epi>(p, epi, st);
+inline hipError_t launch_planned(GemmArgs p, const GemmPlan& plan, const Epi& epi, hipStream_t st) {
+    p.splits = plan.splits;
+    p.tiles_per_split = plan.tiles_per_split;
+    if (plan.big) return launch_tiles<T, AKC, BKC, 256, 256, 2, 4, Epi>(p, epi, st);
     return launch_tiles<T, AKC, BKC, 128, 128, 2, 2, Epi>(p, epi, st);
+}
+inline int64_t k_tiles(const GemmArgs& p) { return (int64_t)p.nseg * ((p.K + kGemmBK - 1) / kGemmBK); }
+
+// One product without splits.
+template <class T, bool AKC, bool BKC, class Epi>
+inline hipError_t launch_gemm(const GemmArgs& p, const Epi& epi, hipStream_t st) {
+    return launch_planned<T, AKC, BKC>(p, plan_gemm(p.M, p.N, p.batch, k_tiles(p), Epi::kDual, false, 1), epi, st);
 }
 
 // One stored matrix operand: planes (split operands) `plane` elements apart, rows of `ld` elements.
@@ -464,12 +509,6 @@ inline GemmArgs make_args(int64_t M, int64_t N, int64_t K) {
     g.batch = 1;
     g.splits = 1;
     return g;
-}
-
-// all k tiles in one workgroup per output tile
-inline void one_split(GemmArgs& g) {
-    g.splits = 1;
-    g.tiles_per_split = g.nseg * ((g.K + kGemmBK - 1) / kGemmBK);
 }
 
 // ---- workspace -----------------------------------------------------------------------------------------
