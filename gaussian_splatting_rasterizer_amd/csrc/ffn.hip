@@ -287,8 +287,6 @@ __global__ __launch_bounds__(256) void k_reduce(const float* part, int splits, i
 // elements are read one by one.
 constexpr int kFewRows = 64;
 
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-
 template <class F>
 struct FewRows {
     static constexpr int kStep = F::kPlanes == 1 ? 32 : 16;  // k of one set of fragments

@@ -16,12 +16,15 @@
 //
 // The loop keeps one half of a tile (32 k) in registers while it multiplies the other: the second half is read
 // during the first half's products, the next tile's first half during the second's, and the tile after it is fetched
-// there too, one 16-byte load per few products.  There is one barrier per tile, in front of which the wave already
-// holds the operands of its next 32 products.  Issuing all fetches at the top of a tile instead stalled the waves
-// behind the load queue: 8192^3 in bfloat16 took 1005 (both KC), 1209 (one KC), 1214 us (none) that way and 978,
-// 1005, 1022 us as it is, 1125, 1095, 1076 TFLOP/s.  The matrix pipes are then busy in 65 % of the cycles, at the
-// 1.9 GHz the card holds under this load.  32x32x16 instructions, 32-k tiles in a ring of four, and waves taking
-// turns between reading and multiplying were measured slower (1040, 1080, 1090 us).
+// there too, all pinned between rows of products.  There is one barrier per tile, in front of which the wave already
+// holds the operands of its next 32 products.  The fetches are asm because the compiler, not knowing which half of
+// LDS they write, puts a wait for all of them in front of every later transpose read.
+//
+// 8192^3 in bfloat16: 938 us with both operands KC, 941 with one, 955 with none (1172, 1168, 1151 TFLOP/s); fetches
+// at the top of a tile 1005, 1209, 1214 us; reads and fetches left to the compiler's order 978, 1005, 1022 us.  On
+// zeros the same kernel reaches 1600 TFLOP/s: on real data the card's power limit sets the clock (1.9 GHz here).
+// 32x32x16 instructions (995 us), four waves of 128x128 (1031 us), 32-k tiles in rings of three to five (1005 us) and
+// waves taking turns between reading and multiplying (1092 us) were measured slower.
 //
 // Fragments of the column operand take their 16 rows four apart, so that a lane ends up with 16 (dual: 8 + 8)
 // consecutive columns of a row and the epilogue reads and writes 16 bytes at a time.
@@ -37,6 +40,7 @@ namespace gsr {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
@@ -124,20 +128,21 @@ struct TileLoader {
             }
         }
     }
-    // first / second: the tile's first element in the (two) matrices; krem: k left from the tile's start
-    __device__ __forceinline__ void load(const uint16_t* first, const uint16_t* second, int krem, char* lds,
-                                         int tid) const {
-        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        const __amdgpu_buffer_rsrc_t ra = gemm_rsrc(first);
-        const __amdgpu_buffer_rsrc_t rb = DUAL ? gemm_rsrc(second) : ra;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const uint32_t o = kk[i] < krem ? off[i] : kOobOffset;
-            // dual: the 8 rows of one instruction belong to one matrix
-            const bool up = DUAL && (((i * NT + wave * 64) >> 3) % 64) >= 32;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? rb : ra, (lds_void*)(lds + (i * NT + wave * 64) * 16), 16, o,
-                                                     0, 0, 0);
-        }
+    // The i-th load of a tile.  first / second: the tile's first element in the (two) matrices; krem: k left from the
+    // tile's start.  The asm has no register outputs; what it writes in LDS is waited for with vmcnt before it is read.
+    __device__ __forceinline__ void load(int i, const uint16_t* first, const uint16_t* second, int krem, char* lds,
+                                         int wave) const {
+        const uint32_t o = kk[i] < krem ? off[i] : kOobOffset;
+        // dual: the 8 rows of one instruction belong to one matrix
+        const bool up = DUAL && (((i * NT + wave * 64) >> 3) % 64) >= 32;
+        const uint64_t base = (uint64_t)(up ? second : first);
+        const u32x4 rs = {(uint32_t)base, (uint32_t)(base >> 32) & 0xffffu, 0x7fffffffu, 0x00020000u};
+        const uint32_t dst = (uint32_t)(uintptr_t)(lds_void*)(lds + (i * NT + wave * 64) * 16);
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is a reserved register; it is clobbered all the same
+        asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(o), "s"(rs), "s"(dst)
+                     : "memory", "m0");
+#pragma clang diagnostic pop
     }
     // fragment j of the wave's rows from r0, k from kk0 (0 or 32): lane l holds row i = l % 16, k (l / 16) * 8 .. + 8
     static __device__ __forceinline__ s16x8 frag(const char* lds, int r0, int j, int kk0, int lane) {
@@ -234,72 +239,79 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p, con
         for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     if (t_begin < t_end) {
-        // next tile to fetch; past the last one nothing is read (krem 0: every lane is out of range)
+        // the tile to fetch; past the last one nothing is read (krem 0: every lane is out of range)
         int s = t_begin / ktiles, kt = t_begin - s * ktiles, left = t_end - t_begin, krem = 0;
-        const uint16_t *pa = nullptr, *pb = nullptr, *pb2 = nullptr;
+        const uint16_t* na = p.a[s] + a0 + kt * astep;
+        const uint16_t* nb = p.b[s] + b0 + kt * bstep;
+        const uint16_t* nb2 = Epi::kDual ? p.b2[s] + b0 + kt * bstep : nullptr;
+        const uint16_t *fa0 = na, *fb0 = nb, *fb2 = nb2;
         auto next = [&]() {
             krem = left > 0 ? p.K - kt * kGemmBK : 0;
-            pa = p.a[s] + a0 + kt * astep;
-            pb = p.b[s] + b0 + kt * bstep;
-            if (Epi::kDual) pb2 = p.b2[s] + b0 + kt * bstep;
+            fa0 = na, fb0 = nb, fb2 = nb2;
             --left;
+            na += astep, nb += bstep;
+            if (Epi::kDual) nb2 += bstep;
             if (++kt == ktiles) {
                 kt = 0;
                 if (s + 1 < p.nseg) ++s;
+                na = p.a[s] + a0, nb = p.b[s] + b0;
+                if (Epi::kDual) nb2 = p.b2[s] + b0;
             }
         };
-        auto fetch = [&](char* buf) {
-            la.load(pa, nullptr, krem, buf, tid);
-            lb.load(pb, pb2, krem, buf + LA::kBytes, tid);
+        auto fetch = [&](int i, char* buf) {
+            if (i < LA::kLoads)
+                la.load(i, fa0, nullptr, krem, buf, wave);
+            else
+                lb.load(i - LA::kLoads, fb0, fb2, krem, buf + LA::kBytes, wave);
         };
         s16x8 fa[2][MI], fb[2][NI];
-        auto read = [&](int half, const char* buf) {
-#pragma unroll
-            for (int j = 0; j < NI; ++j)
-                fb[half][j] = LB::frag(buf + LA::kBytes, wn * (BN / WN), j, half * 32, lane);
-#pragma unroll
-            for (int i = 0; i < MI; ++i) fa[half][i] = LA::frag(buf, wm * (BM / WM), i, half * 32, lane);
+        auto read = [&](int half, int f, const char* buf) {
+            if (f < NI)
+                fb[half][f] = LB::frag(buf + LA::kBytes, wn * (BN / WN), f, half * 32, lane);
+            else
+                fa[half][f - NI] = LA::frag(buf, wm * (BM / WM), f - NI, half * 32, lane);
         };
-        auto multiply = [&](int half) {
+        // fragments and fetches per row of products; the last rows read nothing, so nothing is waited for after them
+        constexpr int kFrags = MI + NI, kReads = (kFrags + MI * 3 / 4 - 1) / (MI * 3 / 4);
+        constexpr int kFetches = (kLoads + MI - 1) / MI;
+        // one half of a tile: NI products of each of the MI rows
+        auto multiply = [&](int half, const char* from, bool fetching, char* to) {
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
+            for (int g = 0; g < MI; ++g) {
 #pragma unroll
-                for (int j = 0; j < NI; ++j) acc[i][j] = Mfma<T>::run(fb[half][j], fa[half][i], acc[i][j]);
+                for (int f = g * kReads; f < (g + 1) * kReads && f < kFrags; ++f) read(half ^ 1, f, from);
+                if (fetching) {
+#pragma unroll
+                    for (int i = g * kFetches; i < (g + 1) * kFetches && i < kLoads; ++i) fetch(i, to);
+                }
+                __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+                for (int j = 0; j < NI; ++j) acc[g][j] = Mfma<T>::run(fb[half][j], fa[half][g], acc[g][j]);
+                __builtin_amdgcn_s_setprio(0);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         };
-        // LDS reads per row of products, so that the last rows have none left to wait for
-        constexpr int kReads = (MI * (AKC ? 1 : 2) + NI * (BKC ? 1 : 2) + MI - 3) / (MI - 2);
         next();
-        fetch(smem);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) fetch(i, smem);
         next();
-        fetch(smem + kStage);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) fetch(i, smem + kStage);
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        read(0, smem);
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f) read(0, f, smem);
         for (int t = t_begin; t < t_end; ++t) {
             char* cur = smem + ((t - t_begin) & 1) * kStage;
             char* nxt = smem + ((t - t_begin + 1) & 1) * kStage;
-            read(1, cur);
-            multiply(0);
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);  // LDS reads
-                __builtin_amdgcn_sched_group_barrier(0x8, NI, 0);        // matrix instructions
-            }
+            multiply(0, cur, false, nullptr);
+            next();
             // the wave has read all of cur, and its share of nxt has landed; after the barrier everyone's has
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
-            next();
-            read(0, nxt);
-            fetch(cur);
-            multiply(1);
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
-                __builtin_amdgcn_sched_group_barrier(0x20, (kLoads + MI - 1) / MI, 0);  // fetches
-                __builtin_amdgcn_sched_group_barrier(0x8, NI, 0);
-            }
+            multiply(1, nxt, true, cur);
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no fetch outlives the workgroup's LDS
     }
