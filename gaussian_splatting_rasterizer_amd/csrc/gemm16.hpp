@@ -464,9 +464,10 @@ inline int64_t tile_count(int64_t M, int64_t N, int t, bool symmetric) {
     return symmetric ? tn * (tn + 1) / 2 : tm * tn;
 }
 
-// Tile size and splits along k of one product, from what the two kernels were measured to take: a 256x256 tile 2.1 us
-// per 64 k (one workgroup a CU) and 7 us around them, a 128x128 tile 1.15 us with two workgroups on a CU, 0.85 us
-// alone, and 3 us.  A split product writes and reads its float32 partial sums at 4 TB/s and needs one more kernel.
+// Tile size and splits along k of one product, from what the two kernels were measured to take: a 256x256 tile 1.75 us
+// per 64 k (one workgroup a CU) and 7 us around them, a 128x128 tile 1.2 us with two workgroups on a CU, 0.85 us
+// alone, and 4 us.  A split product's float32 partial sums are read again at 4.5 TB/s by one more kernel
+// (symmetric products, whose kernel also mirrors: half as fast).
 // dual: N counts the columns of one of the two matrices.
 struct GemmPlan {
     bool big;
@@ -483,8 +484,8 @@ inline GemmPlan plan_gemm(int64_t M, int64_t N, int64_t batch, int64_t ktiles, b
             const int64_t per = (ktiles + s - 1) / s, n = tiles * s;
             if (s > 1 && (per < 4 || n > 1024)) break;
             const int64_t rounds = big ? (n + 255) / 256 : (n + 511) / 512;
-            const double tile = big ? 2.1 * per + 7 : n <= 256 ? 0.85 * per + 3 : 1.15 * per + 3;
-            const double sums = s > 1 ? 6 + (double)tiles * t * t * 4 * 2 * s / 4e6 : 0;
+            const double tile = big ? 1.75 * per + 7 : n <= 256 ? 0.85 * per + 4 : 1.2 * per + 4;
+            const double sums = s > 1 ? (symmetric ? 8 : 4) + (double)tiles * t * t * 4 * s / (symmetric ? 2e6 : 4.5e6) : 0;
             const double us = rounds * tile + sums;
             if (us < best.us) best = {big != 0, s, (int)per, us};
         }
