@@ -124,7 +124,7 @@ def test_scan_backward_arguments(lib):
 
 def ortho_dims(**kw):
     d = b.gs_default_ortho_dims()
-    for k, v in dict(dict(rows=8, cols=16, batch=2, dtype=b.GS_F32, out_dtype=b.GS_BF16), **kw).items():
+    for k, v in dict(dict(rows=200, cols=300, batch=2, dtype=b.GS_F32, out_dtype=b.GS_BF16), **kw).items():
         setattr(d, k, v)
     return d
 
