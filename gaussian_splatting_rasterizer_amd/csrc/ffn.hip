@@ -6,8 +6,9 @@
 //
 // Every product runs on k_gemm16: both projections share one pass over x, the activation and the gating are in the
 // first product's epilogue, their derivatives in the epilogue of dh, and dx sums its two products in one
-// accumulator.  float32 operands are split into three bfloat16 parts and multiplied with six partial products,
-// which keeps 24 bits (the parts left out are below 2^-24) at the bfloat16 matrix rate / 6.
+// accumulator.  float32 runs on the float32 matrix instructions (FmtF32) or, for large products, with operands split
+// into three bfloat16 parts and multiplied in six partial products (FmtF32Split), which keeps 24 bits (the parts left
+// out are below 2^-24) at the bfloat16 matrix rate / 6; see split_f32.
 //
 // Rows that are not 16-byte aligned, or whose length is not a multiple of 8 elements, are copied once into a
 // zero-padded layout in the workspace (k_pack); other operands are read in place.
@@ -24,7 +25,7 @@ namespace {
 
 struct PackJob {
     const void* src;
-    uint16_t* dst;
+    void* dst;
     int64_t rows, cols, ld, plane;  // dst rows are round8(cols) long, planes `plane` elements apart
 };
 struct PackJobs {
@@ -39,9 +40,9 @@ __global__ __launch_bounds__(256) void k_pack(const PackJobs jobs) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i / c8, c = (i - r * c8) * 8;
         const typename F::Elem* s = (const typename F::Elem*)jb.src + r * jb.ld + c;
-        uint16_t* d = jb.dst + i * 8;
+        OperandElem<F>* d = (OperandElem<F>*)jb.dst + i * 8;
         const int64_t left = jb.cols - c;
-        if constexpr (F::kPlanes == 1) {
+        if constexpr (sizeof(typename F::Elem) == 2) {
             u16x8 v;
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = e < left ? s[e] : (uint16_t)0;
@@ -70,7 +71,7 @@ __device__ __forceinline__ void activation(float g, float& a, float& da) {
     } else {
         const float e = __expf(-0.5f * g * g);
         float cdf;
-        if constexpr (F::kPlanes == 1) {
+        if constexpr (sizeof(typename F::Elem) == 2) {
             const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f * 0.70710678118654752f,
                                                                  __builtin_fabsf(g), 1.f));
             float q = __builtin_fmaf(t, 1.061405429f, -1.453152027f);
@@ -94,7 +95,7 @@ template <class F, int ACT>
 struct EpiGate {
     static constexpr bool kDual = true, kSymmetric = false;
     static constexpr int kAhead = 0;
-    uint16_t* h;
+    OperandElem<F>* h;
     int64_t h_plane;
     typename F::Elem* gu;  // [M][2 F8] or null
     int64_t f8;
@@ -146,9 +147,9 @@ struct EpiGateFew {
 template <class F, int ACT>
 struct EpiGateGrad {
     static constexpr bool kDual = false, kSymmetric = false;
-    static constexpr int kAhead = F::kPlanes == 1 ? 3 : 1;
+    static constexpr int kAhead = sizeof(typename F::Elem) == 2 ? 3 : 1;
     const typename F::Elem* gu;
-    uint16_t* dgu;  // [M][2 F8]
+    OperandElem<F>* dgu;  // [M][2 F8]
     int64_t plane;
     int64_t f8;
     int M;
@@ -289,9 +290,9 @@ constexpr int kFewRows = 64;
 
 template <class F>
 struct FewRows {
-    static constexpr int kStep = F::kPlanes == 1 ? 32 : 16;  // k of one set of fragments
-    static constexpr int kLane = kStep / 4;                  // elements of a lane
     static constexpr uint32_t kElem = sizeof(typename F::Elem);
+    static constexpr int kStep = 64 / kElem;   // k of one set of fragments
+    static constexpr int kLane = kStep / 4;    // elements of a lane
 
     // the lane's elements of one row, k0 .. of K; `row` is the byte offset of the row or kOobOffset
     template <bool WIDE>
@@ -320,15 +321,8 @@ struct FewRows {
         }
     }
     static __device__ __forceinline__ f32x4 multiply(u32x4 w, u32x4 x, f32x4 acc) {
-        if constexpr (F::kPlanes == 1) {
-            return Mfma<typename F::Mma>::run(__builtin_bit_cast(s16x8, w), __builtin_bit_cast(s16x8, x), acc);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, (uint32_t)w[j]),
-                                                           __builtin_bit_cast(float, (uint32_t)x[j]), acc, 0, 0, 0);
-            return acc;
-        }
+        using T = std::conditional_t<kElem == 4, float, typename F::Mma>;
+        return Mfma<T>::run(__builtin_bit_cast(s16x8, w), __builtin_bit_cast(s16x8, x), acc);
     }
 };
 
@@ -421,9 +415,10 @@ void add_segments(GemmArgs& g, const Operand& a, const Operand& b, const Operand
     const int n = F::kPlanes == 1 ? 1 : 6;
     for (int i = 0; i < n; ++i) {
         const int ia = F::kPlanes == 1 ? 0 : pa[i], ib = F::kPlanes == 1 ? 0 : pb[i];
-        g.a[g.nseg] = a.p + ia * a.plane + a_off;
-        g.b[g.nseg] = b.p + ib * b.plane;
-        g.b2[g.nseg] = b2 ? b2->p + ib * b2->plane : nullptr;
+        using E = OperandElem<F>;
+        g.a[g.nseg] = (const char*)((const E*)a.p + ia * a.plane + a_off);
+        g.b[g.nseg] = (const char*)((const E*)b.p + ib * b.plane);
+        g.b2[g.nseg] = b2 ? (const char*)((const E*)b2->p + ib * b2->plane) : nullptr;
         ++g.nseg;
     }
     g.lda = a.ld;
@@ -431,9 +426,12 @@ void add_segments(GemmArgs& g, const Operand& a, const Operand& b, const Operand
 }
 
 // Weight gradients may be split along the rows they sum over.
-constexpr int kMaxSplits = 64;
-GemmPlan grad_plan(int64_t M, int64_t N, int64_t K, int nseg) {
-    return plan_gemm(M, N, 1, (K + kGemmBK - 1) / kGemmBK * nseg, false, false, kMaxSplits);
+constexpr int kMaxSplits = 128;
+template <class F>
+GemmPlan grad_plan(int64_t M, int64_t N, int64_t K) {
+    constexpr int bk = kTileK<typename F::Mma>;
+    return plan_gemm(M, N, 1, (K + bk - 1) / bk * (F::kPlanes == 1 ? 1 : 6), false, false, kMaxSplits,
+                     sizeof(typename F::Mma) == 4);
 }
 
 template <class F>
@@ -443,12 +441,14 @@ struct Layout {
         : M(d.rows), D(d.d_in), H(d.d_hidden), O(d.d_out), D8(round8(D)), H8(round8(H)), O8(round8(O)) {}
     int64_t saved_gu_bytes() const { return round_up(M * 2 * H8 * (int64_t)sizeof(typename F::Elem), kAlign); }
     int64_t h_elems() const { return M * H8 * F::kPlanes; }
+    int64_t h_bytes() const { return round_up(h_elems() * (int64_t)sizeof(OperandElem<F>), kAlign); }
 };
 
-// An operand is read in place when its rows are 16-byte aligned and a multiple of 8 elements long.
+// An operand is read in place when its rows are 16-byte aligned and a multiple of 16 bytes long.
 template <class F>
 bool direct(const void* p, int64_t cols, int64_t ld) {
-    return F::kPlanes == 1 && cols % 8 == 0 && ld % 8 == 0 && ((uintptr_t)p % 16) == 0;
+    constexpr int64_t e = 16 / (int64_t)sizeof(OperandElem<F>);
+    return F::kPlanes == 1 && cols % e == 0 && ld % e == 0 && ((uintptr_t)p % 16) == 0;
 }
 
 struct Packer {
@@ -458,9 +458,9 @@ struct Packer {
     template <class F>
     Operand add(Carver& cv, const void* src, int64_t rows, int64_t cols, int64_t ld,
                 bool always = false) {
-        if (!always && direct<F>(src, cols, ld)) return {(const uint16_t*)src, 0, ld};
+        if (!always && direct<F>(src, cols, ld)) return {src, 0, ld};
         const int64_t c8 = round8(cols);
-        uint16_t* d = cv.take<uint16_t>(rows * c8 * F::kPlanes);
+        OperandElem<F>* d = cv.take<OperandElem<F>>(rows * c8 * F::kPlanes);
         jobs.j[n++] = {src, d, rows, cols, ld, rows * c8};
         if (rows * c8 / 8 > most) most = rows * c8 / 8;
         return {d, rows * c8, c8};
@@ -504,7 +504,7 @@ hipError_t forward_few(const gs_ffn_dims& d, const void* x, int64_t ldx, const g
     EpiGateFew<F, ACT> e1{{nullptr, L.M * L.H8, nullptr, L.H8, (int)L.M}, nullptr};
     if (saved) {
         e1.all.gu = (E*)saved;
-        e1.all.h = (uint16_t*)((char*)saved + L.saved_gu_bytes());
+        e1.all.h = (OperandElem<F>*)((char*)saved + L.saved_gu_bytes());
     }
     // the 16-bit h that is kept is the next product's input too
     e1.h = saved && F::kPlanes == 1 ? (E*)e1.all.h : cv.take<E>(L.M * L.H8);
@@ -531,21 +531,21 @@ hipError_t forward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const 
     const bool wdir = direct<F>(w.gate, L.D, L.D) && direct<F>(w.up, L.D, L.D);
     Operand og, ou;
     if (wdir) {
-        og = {(const uint16_t*)w.gate, 0, L.D};
-        ou = {(const uint16_t*)w.up, 0, L.D};
+        og = {w.gate, 0, L.D};
+        ou = {w.up, 0, L.D};
     } else {  // the dual product reads both with one row length
         og = pk.add<F>(cv, w.gate, L.H, L.D, L.D, true);
         ou = pk.add<F>(cv, w.up, L.H, L.D, L.D, true);
     }
     const Operand od = pk.add<F>(cv, w.down, L.O, L.H, L.H);
     GSR_TRY(pk.launch<F>(st));
-    uint16_t* h;
+    OperandElem<F>* h;
     E* gu = nullptr;
     if (saved) {
         gu = (E*)saved;
-        h = (uint16_t*)((char*)saved + L.saved_gu_bytes());
+        h = (OperandElem<F>*)((char*)saved + L.saved_gu_bytes());
     } else {
-        h = cv.take<uint16_t>(L.h_elems());
+        h = cv.take<OperandElem<F>>(L.h_elems());
     }
     const int64_t h_plane = L.M * L.H8;
     GemmArgs g1 = make_args(L.M, L.H, L.D);
@@ -564,7 +564,7 @@ hipError_t weight_grad(const Operand& a, int64_t a_cols, const Operand& b, int64
                        EpiStore<F> store, float* part, hipStream_t st) {
     GemmArgs g = make_args(a_cols, b_cols, rows);
     add_segments<F>(g, a, b, nullptr);
-    const GemmPlan plan = grad_plan(a_cols, b_cols, rows, g.nseg);
+    const GemmPlan plan = grad_plan<F>(a_cols, b_cols, rows);
     if (plan.splits == 1) return launch_planned<typename F::Mma, false, false>(g, plan, store, st);
     const int64_t n4 = (store.N + 3) / 4 * 4;
     EpiPartial ep{part, n4, (int)a_cols};
@@ -577,8 +577,7 @@ hipError_t weight_grad(const Operand& a, int64_t a_cols, const Operand& b, int64
 
 template <class F>
 int64_t part_elems(const Layout<F>& L) {
-    const int nseg = F::kPlanes == 1 ? 1 : 6;
-    const int64_t s1 = grad_plan(2 * L.H8, L.D8, L.M, nseg).splits, s2 = grad_plan(L.O8, L.H8, L.M, nseg).splits;
+    const int64_t s1 = grad_plan<F>(2 * L.H8, L.D8, L.M).splits, s2 = grad_plan<F>(L.O8, L.H8, L.M).splits;
     const int64_t p1 = s1 > 1 ? s1 * 2 * L.H8 * L.D8 : 0, p2 = s2 > 1 ? s2 * L.O8 * L.H8 : 0;
     return p1 > p2 ? p1 : p2;
 }
@@ -593,9 +592,9 @@ hipError_t backward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const
     Carver cv{ws};
     float* part = cv.take<float>(part_elems<F>(L));
     const int64_t plane = L.M * 2 * L.H8;
-    uint16_t* dgu = cv.take<uint16_t>(plane * F::kPlanes);
+    OperandElem<F>* dgu = cv.take<OperandElem<F>>(plane * F::kPlanes);
     const E* gu = (const E*)saved;
-    const uint16_t* h = (const uint16_t*)((const char*)saved + L.saved_gu_bytes());
+    const OperandElem<F>* h = (const OperandElem<F>*)((const char*)saved + L.saved_gu_bytes());
     const int64_t h_plane = L.M * L.H8;
     Packer pk;
     const Operand ody = pk.add<F>(cv, dy, L.M, L.O, lddy);
@@ -634,17 +633,39 @@ hipError_t backward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const
 template <class F>
 void sizes_impl(const gs_ffn_dims& d, size_t* saved, size_t* fwd, size_t* bwd) {
     const Layout<F> L(d);
-    auto pad = [](int64_t rows, int64_t c8) { return round_up(rows * c8 * F::kPlanes * 2, kAlign); };
-    *saved = (size_t)(L.saved_gu_bytes() + round_up(L.h_elems() * 2, kAlign));
+    auto pad = [](int64_t rows, int64_t c8) {
+        return round_up(rows * c8 * F::kPlanes * (int64_t)sizeof(OperandElem<F>), kAlign);
+    };
+    *saved = (size_t)(L.saved_gu_bytes() + L.h_bytes());
     // every operand counted as copied: whether one is depends on its address and stride
     const int64_t weights = 2 * pad(L.H, L.D8) + pad(L.O, L.H8) + pad(L.M, L.D8);
-    *fwd = (size_t)(weights + round_up(std::max(L.h_elems() * 2, L.M * L.H8 * (int64_t)sizeof(typename F::Elem)), kAlign));
+    *fwd = (size_t)(weights + std::max(L.h_bytes(), round_up(L.M * L.H8 * (int64_t)sizeof(typename F::Elem), kAlign)));
     *bwd = (size_t)(weights + pad(L.M, L.O8) + pad(L.M, 2 * L.H8) + round_up(part_elems<F>(L) * 4, kAlign));
 }
 
 }  // namespace
 
+namespace {
+
+// Whether float32 operands are split.  Six products at the bfloat16 rate take half the time of one at the float32
+// rate, but move 6 bytes per value instead of 4, convert every operand, and want large tiles.  Measured, forward and
+// backward together in us:
+//   rows x in x hidden x out       f32    split      rows x in x hidden x out       f32    split
+//   23040 x 57 x 256 x 128         190      207      23040 x 256 x 512 x 256        628      543
+//   131072 x 64 x 256 x 64         577      901      65536 x 192 x 768 x 192       1875     1535
+//   131072 x 128 x 512 x 128      1618     1856      8192 x 512 x 2048 x 512       1289     1149
+//   2048 x 512 x 2048 x 512        409      525      4000 x 2048 x 4096 x 2048     4461     3185
+//   1000 x 1000 x 2731 x 1000      642      805      16384 x 1024 x 4096 x 1024    9047     6065
+// (4000 x 512 x 2048 x 512 and 16384 x 256 x 1024 x 256 are even.)  So: rows of at least 192 values and enough work.
+bool split_f32(const gs_ffn_dims& d) {
+    return d.d_in >= 192 && d.d_out >= 192 &&
+           (double)d.rows * d.d_hidden * (2.0 * d.d_in + d.d_out) >= 8589934592.0;  // 2^33 multiplications
+}
+
+}  // namespace
+
 void ffn_sizes(const gs_ffn_dims& d, size_t* saved, size_t* fwd, size_t* bwd) {
+    if (d.dtype == GS_F32 && split_f32(d)) return sizes_impl<FmtF32Split>(d, saved, fwd, bwd);
     if (d.dtype == GS_F32) return sizes_impl<FmtF32>(d, saved, fwd, bwd);
     return sizes_impl<FmtBf16>(d, saved, fwd, bwd);
 }
@@ -659,6 +680,9 @@ hipError_t launch_ffn_forward(const gs_ffn_dims& d, const void* x, int64_t ldx, 
     if (d.dtype == GS_F16)
         return silu ? forward_impl<FmtF16, GS_ACT_SILU>(d, x, ldx, w, y, ldy, saved, b, st)
                     : forward_impl<FmtF16, GS_ACT_GELU>(d, x, ldx, w, y, ldy, saved, b, st);
+    if (split_f32(d))
+        return silu ? forward_impl<FmtF32Split, GS_ACT_SILU>(d, x, ldx, w, y, ldy, saved, b, st)
+                    : forward_impl<FmtF32Split, GS_ACT_GELU>(d, x, ldx, w, y, ldy, saved, b, st);
     return silu ? forward_impl<FmtF32, GS_ACT_SILU>(d, x, ldx, w, y, ldy, saved, b, st)
                 : forward_impl<FmtF32, GS_ACT_GELU>(d, x, ldx, w, y, ldy, saved, b, st);
 }
@@ -674,6 +698,9 @@ hipError_t launch_ffn_backward(const gs_ffn_dims& d, const void* x, int64_t ldx,
     if (d.dtype == GS_F16)
         return silu ? backward_impl<FmtF16, GS_ACT_SILU>(d, x, ldx, w, saved, dy, lddy, out, lddx, b, st)
                     : backward_impl<FmtF16, GS_ACT_GELU>(d, x, ldx, w, saved, dy, lddy, out, lddx, b, st);
+    if (split_f32(d))
+        return silu ? backward_impl<FmtF32Split, GS_ACT_SILU>(d, x, ldx, w, saved, dy, lddy, out, lddx, b, st)
+                    : backward_impl<FmtF32Split, GS_ACT_GELU>(d, x, ldx, w, saved, dy, lddy, out, lddx, b, st);
     return silu ? backward_impl<FmtF32, GS_ACT_SILU>(d, x, ldx, w, saved, dy, lddy, out, lddx, b, st)
                 : backward_impl<FmtF32, GS_ACT_GELU>(d, x, ldx, w, saved, dy, lddy, out, lddx, b, st);
 }

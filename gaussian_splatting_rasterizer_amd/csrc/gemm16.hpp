@@ -1,20 +1,23 @@
 // gemm16.hpp -- the matrix-core product of the updater's operators (device code and its launcher).
 //
-//   C[m][n] = sum over segments s, k of A_s(m, k) B_s(n, k),   16-bit operands, float32 accumulation.
+//   C[m][n] = sum over segments s, k of A_s(m, k) B_s(n, k),   16-bit or float32 operands, float32 accumulation.
 //
 // Each operand is stored either with k contiguous ([rows][k], "KC") or with its rows contiguous ([k][rows]); the
 // four products of a block's forward and backward pass then need no transposed copies.  A list of segments adds up
 // several products in one accumulator: two weight matrices of one gradient, or the six (three) partial products
 // that make a float32 product out of operands split into bfloat16 (float16) parts.
 //
-// Tile BM x BN x 64 per workgroup, split over WM x WN waves of 16x16x32 matrix instructions.  Tiles go from global
+// Tile BM x BN x 64 (float32: 32) per workgroup, split over WM x WN waves of 16x16x32 (16x16x4) matrix instructions.  Tiles go from global
 // memory to LDS directly (16 bytes per lane, no registers), double buffered.  A row of a KC tile is 128 bytes = 8
 // chunks; chunk c of row r lies at chunk position c ^ f(r), so the 16-byte fragment reads of 8 lanes cover all 32
 // banks (no conflicts measured).  A tile with rows contiguous keeps its [k][row] order and is read with the LDS
 // transpose read (4 k x 16 rows per 16 lanes); chunk position c ^ f(k) spreads the four k rows over the banks.
 // Out-of-range rows and k read as zero through the buffer descriptor's range check.
 //
-// The loop keeps one half of a tile (32 k) in registers while it multiplies the other: the second half is read
+// There is no such read for 32 bits: float32 tiles of this order are read element by element, four rows of 16
+// consecutive floats at a time on different banks.
+//
+// The loop keeps one half of a tile (64 bytes of k) in registers while it multiplies the other: the second half is read
 // during the first half's products, the next tile's first half during the second's, and the tile after it is fetched
 // there too, all pinned between rows of products.  There is one barrier per tile, in front of which the wave already
 // holds the operands of its next 32 products.  The fetches are asm because the compiler, not knowing which half of
@@ -34,6 +37,7 @@
 #include <stdint.h>
 
 #include <initializer_list>
+#include <type_traits>
 
 namespace gsr {
 
@@ -45,12 +49,14 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kGemmSegs = 12;
-constexpr int kGemmBK = 64;
+// k of a tile: 128 bytes of an operand's row
+template <class T>
+constexpr int kTileK = 128 / (int)sizeof(T);
 
 struct GemmArgs {
-    const uint16_t* a[kGemmSegs];
-    const uint16_t* b[kGemmSegs];
-    const uint16_t* b2[kGemmSegs];  // second matrix of a dual product (same layout as b)
+    const char* a[kGemmSegs];
+    const char* b[kGemmSegs];
+    const char* b2[kGemmSegs];  // second matrix of a dual product (same layout as b)
     int nseg;
     int M, N, K;
     int64_t lda, ldb;                  // elements between rows of the stored arrays
@@ -77,6 +83,17 @@ struct Mfma<_Float16> {
     }
 };
 
+// float32: four 16x16x4 products, the j-th with element j of the lanes' four (both operands permute k alike)
+template <>
+struct Mfma<float> {
+    static __device__ __forceinline__ f32x4 run(s16x8 a, s16x8 b, f32x4 c) {
+        const f32x4 fa = __builtin_bit_cast(f32x4, a), fb = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(fa[j], fb[j], c, 0, 0, 0);
+        return c;
+    }
+};
+
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
@@ -87,11 +104,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t gemm_rsrc(const void* p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, 0x7fffffff, 0x00020000);
 }
 
-// Loader of one operand's tiles: R rows x 64 k by NT threads.  SPREAD: 0, fragment j holds rows 16 j + i; otherwise
-// rows 4 SPREAD (i >> 2) + 4 (j % SPREAD) + (i & 3) of its group of 16 SPREAD rows (i: the lane's row, 0..15).
+// Loader of one operand's tiles: R rows x 128 bytes of k by NT threads, elements of ES bytes.  SPREAD: 0, fragment j
+// holds rows 16 j + i; otherwise rows 4 SPREAD (i >> 2) + 4 (j % SPREAD) + (i & 3) of its group of 16 SPREAD rows
+// (i: the lane's row, 0..15).
 // DUAL: each group of 64 rows is 32 rows of the first matrix and the same 32 of the second.
-template <bool KC, int R, int NT, int SPREAD, bool DUAL>
+template <bool KC, int R, int NT, int SPREAD, bool DUAL, int ES>
 struct TileLoader {
+    static constexpr int kChunk = 16 / ES;  // elements of a 16-byte chunk
     static constexpr int kLoads = R * 8 / NT;
     static constexpr int kBytes = R * 128;
     uint32_t off[kLoads];  // byte offset within the tile, kOobOffset for rows out of range
@@ -103,6 +122,8 @@ struct TileLoader {
         return r & 7;
     }
     static __device__ __forceinline__ int k_swizzle(int k) {
+        if (ES == 4) return ((k >> 2) & 1) * (SPREAD ? 2 : 4);
+        if (R == 64) return SPREAD ? k & 1 : 2 * (k & 3);  // 8 chunks a row
         return SPREAD ? (k & 1) | ((k & 2) << 2) : 2 * ((k & 3) | ((k >> 1) & 4));
     }
     static __device__ __forceinline__ int frag_row(int j, int i) {
@@ -117,20 +138,20 @@ struct TileLoader {
                 int r = q >> 3;
                 const int c = (q & 7) ^ row_swizzle(r);
                 if (DUAL) r = (r / 64) * 32 + (r % 32);
-                kk[i] = c * 8;
-                off[i] = row0 + r < rows ? (uint32_t)(r * (uint32_t)ld * 2u + c * 16u) : kOobOffset;
+                kk[i] = c * kChunk;
+                off[i] = row0 + r < rows ? (uint32_t)(r * (uint32_t)ld * ES + c * 16u) : kOobOffset;
             } else {
-                constexpr int CH = R / 8;
+                constexpr int CH = R / kChunk;
                 const int k = q / CH;
                 const int c = (q % CH) ^ k_swizzle(k);
                 kk[i] = k;
-                off[i] = row0 + c * 8 < rows ? (uint32_t)(k * (uint32_t)ld * 2u + c * 16u) : kOobOffset;
+                off[i] = row0 + c * kChunk < rows ? (uint32_t)(k * (uint32_t)ld * ES + c * 16u) : kOobOffset;
             }
         }
     }
     // The i-th load of a tile.  first / second: the tile's first element in the (two) matrices; krem: k left from the
     // tile's start.  The asm has no register outputs; what it writes in LDS is waited for with vmcnt before it is read.
-    __device__ __forceinline__ void load(int i, const uint16_t* first, const uint16_t* second, int krem, char* lds,
+    __device__ __forceinline__ void load(int i, const char* first, const char* second, int krem, char* lds,
                                          int wave) const {
         const uint32_t o = kk[i] < krem ? off[i] : kOobOffset;
         // dual: the 8 rows of one instruction belong to one matrix
@@ -144,17 +165,28 @@ struct TileLoader {
                      : "memory", "m0");
 #pragma clang diagnostic pop
     }
-    // fragment j of the wave's rows from r0, k from kk0 (0 or 32): lane l holds row i = l % 16, k (l / 16) * 8 .. + 8
-    static __device__ __forceinline__ s16x8 frag(const char* lds, int r0, int j, int kk0, int lane) {
-        if (KC) {
+    // fragment j of the wave's rows from r0, first or second half of the tile's k: lane l holds row i = l % 16 and
+    // 16 bytes of k from chunk l / 16 of the half
+    static __device__ __forceinline__ s16x8 frag(const char* lds, int r0, int j, int half, int lane) {
+        if constexpr (KC) {
             const int r = r0 + frag_row(j, lane & 15);
-            const int c = ((kk0 >> 3) + (lane >> 4)) ^ row_swizzle(r);
+            const int c = (half * 4 + (lane >> 4)) ^ row_swizzle(r);
             return *reinterpret_cast<const s16x8*>(lds + r * 128 + c * 16);
+        } else if constexpr (ES == 4) {  // no transpose read for 32 bits: one element at a time
+            f32x4 v;
+            const int col = r0 + frag_row(j, lane & 15);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int k = half * 16 + (lane >> 4) * 4 + e;
+                v[e] = *reinterpret_cast<const float*>(lds + k * (R * 4) + (((col >> 2) ^ k_swizzle(k)) << 4) +
+                                                       (col & 3) * 4);
+            }
+            return __builtin_bit_cast(s16x8, v);
         } else {
             s16x8 v;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int k = kk0 + (lane >> 4) * 8 + h * 4 + ((lane & 15) >> 2);
+                const int k = half * 32 + (lane >> 4) * 8 + h * 4 + ((lane & 15) >> 2);
                 const int col = r0 + frag_row(j, (lane & 3) * 4);
                 const char* p = lds + k * (R * 2) + (((col >> 3) ^ k_swizzle(k)) << 4) + (col & 4) * 2;
                 const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
@@ -197,8 +229,9 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p, con
     constexpr int NT = WM * WN * 64;
     constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
     static_assert(NI == 4, "a wave covers 64 columns");
-    using LA = TileLoader<AKC, BM, NT, 0, false>;
-    using LB = TileLoader<BKC, BN, NT, Epi::kDual ? 2 : 4, Epi::kDual>;
+    constexpr int ES = (int)sizeof(T), BK = kTileK<T>;
+    using LA = TileLoader<AKC, BM, NT, 0, false, ES>;
+    using LB = TileLoader<BKC, BN, NT, Epi::kDual ? 2 : 4, Epi::kDual, ES>;
     constexpr int kStage = LA::kBytes + LB::kBytes;
     constexpr int kLoads = LA::kLoads + LB::kLoads;
     __shared__ __attribute__((aligned(1024))) char smem[2 * kStage];
@@ -224,13 +257,13 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p, con
     la.init(tid, m0, p.M, p.lda);
     lb.init(tid, n0, p.N, p.ldb);
 
-    const int ktiles = (p.K + kGemmBK - 1) / kGemmBK;
+    const int ktiles = (p.K + BK - 1) / BK;
     const int t_begin = split * p.tiles_per_split;
     const int t_end = min(ktiles * p.nseg, t_begin + p.tiles_per_split);
-    const int64_t a0 = batch * p.batch_a + (AKC ? (int64_t)m0 * p.lda : m0);
-    const int64_t b0 = batch * p.batch_b + (BKC ? (int64_t)n0 * p.ldb : n0);
-    const int64_t astep = AKC ? kGemmBK : kGemmBK * p.lda;
-    const int64_t bstep = BKC ? kGemmBK : kGemmBK * p.ldb;
+    const int64_t a0 = (batch * p.batch_a + (AKC ? (int64_t)m0 * p.lda : m0)) * ES;  // bytes, like the steps
+    const int64_t b0 = (batch * p.batch_b + (BKC ? (int64_t)n0 * p.ldb : n0)) * ES;
+    const int64_t astep = AKC ? 128 : 128 * p.lda;
+    const int64_t bstep = BKC ? 128 : 128 * p.ldb;
 
     f32x4 acc[MI][NI];
 #pragma unroll
@@ -241,12 +274,12 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p, con
     if (t_begin < t_end) {
         // the tile to fetch; past the last one nothing is read (krem 0: every lane is out of range)
         int s = t_begin / ktiles, kt = t_begin - s * ktiles, left = t_end - t_begin, krem = 0;
-        const uint16_t* na = p.a[s] + a0 + kt * astep;
-        const uint16_t* nb = p.b[s] + b0 + kt * bstep;
-        const uint16_t* nb2 = Epi::kDual ? p.b2[s] + b0 + kt * bstep : nullptr;
-        const uint16_t *fa0 = na, *fb0 = nb, *fb2 = nb2;
+        const char* na = p.a[s] + a0 + kt * astep;
+        const char* nb = p.b[s] + b0 + kt * bstep;
+        const char* nb2 = Epi::kDual ? p.b2[s] + b0 + kt * bstep : nullptr;
+        const char *fa0 = na, *fb0 = nb, *fb2 = nb2;
         auto next = [&]() {
-            krem = left > 0 ? p.K - kt * kGemmBK : 0;
+            krem = left > 0 ? p.K - kt * BK : 0;
             fa0 = na, fb0 = nb, fb2 = nb2;
             --left;
             na += astep, nb += bstep;
@@ -267,12 +300,13 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p, con
         s16x8 fa[2][MI], fb[2][NI];
         auto read = [&](int half, int f, const char* buf) {
             if (f < NI)
-                fb[half][f] = LB::frag(buf + LA::kBytes, wn * (BN / WN), f, half * 32, lane);
+                fb[half][f] = LB::frag(buf + LA::kBytes, wn * (BN / WN), f, half, lane);
             else
-                fa[half][f - NI] = LA::frag(buf, wm * (BM / WM), f - NI, half * 32, lane);
+                fa[half][f - NI] = LA::frag(buf, wm * (BM / WM), f - NI, half, lane);
         };
         // fragments and fetches per row of products; the last rows read nothing, so nothing is waited for after them
-        constexpr int kFrags = MI + NI, kReads = (kFrags + MI * 3 / 4 - 1) / (MI * 3 / 4);
+        constexpr int kFrags = MI + NI, kReadRows = MI > 1 ? MI * 3 / 4 : 1;
+        constexpr int kReads = (kFrags + kReadRows - 1) / kReadRows;
         constexpr int kFetches = (kLoads + MI - 1) / MI;
         // one half of a tile: NI products of each of the MI rows
         auto multiply = [&](int half, const char* from, bool fetching, char* to) {
@@ -404,10 +438,8 @@ struct FmtF16 {
     static __device__ __forceinline__ float get1(const Elem* p) { return to_float(*p); }
     static __device__ __forceinline__ void put1(Elem* p, float v) { *p = from_float(v); }
 };
-struct FmtF32 {
-    using Mma = __bf16;
+struct F32Values {
     using Elem = float;
-    static constexpr int kPlanes = 3;  // matrix operands are split into three bfloat16 planes
     static __device__ __forceinline__ f32x4 get(const Elem* p) { return *(const f32x4*)p; }
     static __device__ __forceinline__ void put(Elem* p, f32x4 v) { *(f32x4*)p = v; }
     struct Raw8 {
@@ -421,12 +453,24 @@ struct FmtF32 {
     static __device__ __forceinline__ float get1(const Elem* p) { return *p; }
     static __device__ __forceinline__ void put1(Elem* p, float v) { *p = v; }
 };
+struct FmtF32 : F32Values {  // float32 matrix instructions
+    using Mma = float;
+    static constexpr int kPlanes = 1;
+};
+struct FmtF32Split : F32Values {  // matrix operands split into three bfloat16 planes
+    using Mma = __bf16;
+    static constexpr int kPlanes = 3;
+};
+
+// What a matrix operand is stored as.
+template <class F>
+using OperandElem = std::conditional_t<sizeof(typename F::Mma) == 4, float, uint16_t>;
 
 // Eight consecutive values of a matrix operand (one or three planes), 16-byte aligned.
 template <class F>
-__device__ __forceinline__ void put_operand8(uint16_t* p, int64_t plane, f32x4 v0, f32x4 v1) {
+__device__ __forceinline__ void put_operand8(OperandElem<F>* p, int64_t plane, f32x4 v0, f32x4 v1) {
     if constexpr (F::kPlanes == 1) {
-        *(u16x8*)p = pack8(to16<typename F::Mma>(v0), to16<typename F::Mma>(v1));
+        F::put8(p, v0, v1);
     } else {
         u16x8 h, m, l;
 #pragma unroll
@@ -464,30 +508,40 @@ inline int64_t tile_count(int64_t M, int64_t N, int t, bool symmetric) {
     return symmetric ? tn * (tn + 1) / 2 : tm * tn;
 }
 
-// Tile size and splits along k of one product, from what the two kernels were measured to take: a 256x256 tile 1.75 us
-// per 64 k (one workgroup a CU) and 7 us around them, a 128x128 tile 1.2 us with two workgroups on a CU, 0.85 us
-// alone, and 4 us.  A split product's float32 partial sums are read again at 4.5 TB/s by one more kernel
-// (symmetric products, whose kernel also mirrors: half as fast).
-// dual: N counts the columns of one of the two matrices.
+// Tile size and splits along k of one product, from what the tiles were measured to take (TileTimes).  Small tiles
+// read each operand more often but fill the CUs with several workgroups, which hide each other's epilogues and waits:
+// 23040 x 256 x 57 in float32 37 us with 64x64 tiles, 44 with 128x128; 1366 x 1366 x 500 float16 (three products)
+// 17 and 25 us; a k tile of 256x256 costs 1.75 us a CU, four of 128x128 2.4, sixteen of 64x64 4.2.  A split product's
+// float32 partial sums are read again at 4.5 TB/s by one more kernel (symmetric products, whose kernel also mirrors:
+// half as fast).  dual: N counts the columns of one of the two matrices.
 struct GemmPlan {
-    bool big;
-    int splits, tiles_per_split;
+    int tile, splits, tiles_per_split;
     double us;
 };
+// One tile size: workgroups a CU holds, microseconds per k tile of a lone workgroup and with the CU full, and around.
+struct TileTimes {
+    int tile, per_cu;
+    double alone, full, around;
+};
 inline GemmPlan plan_gemm(int64_t M, int64_t N, int64_t batch, int64_t ktiles, bool dual, bool symmetric,
-                          int max_splits) {
-    GemmPlan best{false, 1, (int)ktiles, 1e30};
-    for (int big = 0; big < 2; ++big) {
-        const int t = big ? 256 : 128;
-        const int64_t tiles = (dual ? ((M + t - 1) / t) * ((N + t / 2 - 1) / (t / 2)) : tile_count(M, N, t, symmetric)) * batch;
+                          int max_splits, bool f32 = false) {
+    static const TileTimes t16[3] = {{256, 1, 1.75, 1.75, 7}, {128, 2, 0.85, 1.2, 4}, {64, 4, 0.5, 1.05, 3}};
+    static const TileTimes t32[3] = {{256, 1, 8.4, 8.4, 7}, {128, 2, 2.3, 4.3, 4}, {64, 4, 0.85, 3.2, 3}};
+    GemmPlan best{128, 1, (int)ktiles, 1e30};
+    for (int i = 0; i < 3; ++i) {
+        const TileTimes& tt = f32 ? t32[i] : t16[i];
+        const int t = tt.tile;
+        const int64_t tiles =
+            (dual ? ((M + t - 1) / t) * ((N + t / 2 - 1) / (t / 2)) : tile_count(M, N, t, symmetric)) * batch;
         for (int s = 1; s <= max_splits; s = s < 8 ? s + 1 : s + s / 4) {
-            const int64_t per = (ktiles + s - 1) / s, n = tiles * s;
+            const int64_t per = (ktiles + s - 1) / s, n = tiles * s, slots = 256 * tt.per_cu;
             if (s > 1 && (per < 4 || n > 1024)) break;
-            const int64_t rounds = big ? (n + 255) / 256 : (n + 511) / 512;
-            const double tile = big ? 1.75 * per + 7 : n <= 256 ? 0.85 * per + 4 : 1.2 * per + 4;
+            const int64_t rounds = (n + slots - 1) / slots;
+            const double busy = rounds > 1 ? 1.0 : (double)((n + 255) / 256) / tt.per_cu;
+            const double per_k = tt.full * busy > tt.alone ? tt.full * busy : tt.alone;
             const double sums = s > 1 ? (symmetric ? 8 : 4) + (double)tiles * t * t * 4 * s / (symmetric ? 2e6 : 4.5e6) : 0;
-            const double us = rounds * tile + sums;
-            if (us < best.us) best = {big != 0, s, (int)per, us};
+            const double us = rounds * (per_k * per + tt.around) + sums;
+            if (us < best.us) best = {t, s, (int)per, us};
         }
     }
     return best;
@@ -497,20 +551,25 @@ template <class T, bool AKC, bool BKC, class Epi>
 inline hipError_t launch_planned(GemmArgs p, const GemmPlan& plan, const Epi& epi, hipStream_t st) {
     p.splits = plan.splits;
     p.tiles_per_split = plan.tiles_per_split;
-    if (plan.big) return launch_tiles<T, AKC, BKC, 256, 256, 2, 4, Epi>(p, epi, st);
-    return launch_tiles<T, AKC, BKC, 128, 128, 2, 2, Epi>(p, epi, st);
+    if (plan.tile == 256) return launch_tiles<T, AKC, BKC, 256, 256, 2, 4, Epi>(p, epi, st);
+    if (plan.tile == 128) return launch_tiles<T, AKC, BKC, 128, 128, 2, 2, Epi>(p, epi, st);
+    return launch_tiles<T, AKC, BKC, 64, 64, 4, 1, Epi>(p, epi, st);
 }
-inline int64_t k_tiles(const GemmArgs& p) { return (int64_t)p.nseg * ((p.K + kGemmBK - 1) / kGemmBK); }
+template <class T>
+inline int64_t k_tiles(const GemmArgs& p) {
+    return (int64_t)p.nseg * ((p.K + kTileK<T> - 1) / kTileK<T>);
+}
 
 // One product without splits.
 template <class T, bool AKC, bool BKC, class Epi>
 inline hipError_t launch_gemm(const GemmArgs& p, const Epi& epi, hipStream_t st) {
-    return launch_planned<T, AKC, BKC>(p, plan_gemm(p.M, p.N, p.batch, k_tiles(p), Epi::kDual, false, 1), epi, st);
+    const GemmPlan plan = plan_gemm(p.M, p.N, p.batch, k_tiles<T>(p), Epi::kDual, false, 1, sizeof(T) == 4);
+    return launch_planned<T, AKC, BKC>(p, plan, epi, st);
 }
 
 // One stored matrix operand: planes (split operands) `plane` elements apart, rows of `ld` elements.
 struct Operand {
-    const uint16_t* p;
+    const void* p;
     int64_t plane, ld;
 };
 

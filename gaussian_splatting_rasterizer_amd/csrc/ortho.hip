@@ -209,10 +209,10 @@ struct EpiUpdate {
 template <int PL>
 void ortho_segments(GemmArgs& g, const uint16_t* a, int64_t pa, const uint16_t* b, int64_t pb) {
     if (PL == 2) {
-        g.a[g.nseg] = a + pa, g.b[g.nseg] = b, ++g.nseg;
-        g.a[g.nseg] = a, g.b[g.nseg] = b + pb, ++g.nseg;
+        g.a[g.nseg] = (const char*)(a + pa), g.b[g.nseg] = (const char*)b, ++g.nseg;
+        g.a[g.nseg] = (const char*)a, g.b[g.nseg] = (const char*)(b + pb), ++g.nseg;
     }
-    g.a[g.nseg] = a, g.b[g.nseg] = b, ++g.nseg;
+    g.a[g.nseg] = (const char*)a, g.b[g.nseg] = (const char*)b, ++g.nseg;
 }
 
 // float32 partial sums of a symmetric product split along k: part[split][batch][tile][256 or 128]^2, one tile after
@@ -263,18 +263,18 @@ GemmPlan sym_plan(int64_t n, int64_t batch, int64_t ktiles) {
 }
 int64_t sym_part_elems(int64_t n, int64_t batch, int64_t ktiles) {
     const GemmPlan p = sym_plan(n, batch, ktiles);
-    const int t = p.big ? 256 : 128;
+    const int t = p.tile;
     return p.splits > 1 ? p.splits * batch * tile_count(n, n, t, true) * t * t : 0;
 }
 
 template <int PL, bool KC>
 hipError_t launch_symmetric(const GemmArgs& p, EpiSymmetric<PL> epi, float* part, hipStream_t st) {
-    const GemmPlan plan = sym_plan(p.N, p.batch, k_tiles(p));
-    const int t = plan.big ? 256 : 128;
+    const GemmPlan plan = sym_plan(p.N, p.batch, k_tiles<_Float16>(p));
+    const int t = plan.tile;
     epi.bm = t;
     if (plan.splits == 1) return launch_planned<_Float16, KC, KC>(p, plan, epi, st);
     const int64_t tiles = tile_count(p.N, p.N, t, true);
-    EpiSymPartial ep{part, p.batch * tiles * t * t, tiles * t * t, plan.big ? 8 : 7};
+    EpiSymPartial ep{part, p.batch * tiles * t * t, tiles * t * t, t == 256 ? 8 : t == 128 ? 7 : 6};
     GSR_TRY((launch_planned<_Float16, KC, KC>(p, plan, ep, st)));
     int64_t bx = (tiles * t * t / 16 + 255) / 256;
     if (bx > 4096) bx = 4096;
@@ -291,8 +291,8 @@ struct OrthoLayout {
     // float32 partial sums of X X^T and P P
     int64_t part_elems() const {
         const int64_t seg = planes == 2 ? 3 : 1, hi = R < C ? C : R, side = R > C ? lo8 : lo;
-        const int64_t a = sym_part_elems(side, B, seg * ((hi + kGemmBK - 1) / kGemmBK));
-        const int64_t b = sym_part_elems(lo, B, seg * ((lo + kGemmBK - 1) / kGemmBK));
+        const int64_t a = sym_part_elems(side, B, seg * ((hi + kTileK<_Float16> - 1) / kTileK<_Float16>));
+        const int64_t b = sym_part_elems(lo, B, seg * ((lo + kTileK<_Float16> - 1) / kTileK<_Float16>));
         return a > b ? a : b;
     }
 };

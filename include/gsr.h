@@ -306,7 +306,8 @@ GSR_API gs_status gs_attribute(gs_context* ctx, const float* pixel_map, int32_t 
  * be kept or cleared between calls.
  *
  * Arithmetic: sums, activations, recurrent states and norms are float32 (or
- * wider); results are rounded to the array's type once when stored.  Results
+ * wider); results are rounded to the array's type once when stored.  float32
+ * products keep float32's 24 bits; infinities in them may come out as NaN.  Results
  * do not depend on scheduling: the same call gives the same bits. */
 typedef enum { GS_F32 = 0, GS_BF16 = 1, GS_F16 = 2 } gs_dtype;
 typedef enum { GS_ACT_SILU = 0, GS_ACT_GELU = 1 } gs_activation;  /* GELU: the exact form, g Phi(g) */
@@ -412,6 +413,7 @@ typedef struct {
 } gs_ortho_dims;
 /* steps 5, coefficients 3.4445, -4.7750, 2.0315, eps 1e-7; everything else 0. */
 GSR_API gs_status gs_default_ortho_dims(gs_ortho_dims* out);
+/* 0 bytes (the workspace may then be null) for matrices that fit a workgroup's memory. */
 GSR_API gs_status gs_ortho_size(const gs_ortho_dims* dims, size_t* workspace_bytes);
 GSR_API gs_status gs_orthogonalize(const gs_ortho_dims* dims, const void* g, void* out, void* workspace,
                                    size_t workspace_bytes, hipStream_t stream);

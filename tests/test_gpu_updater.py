@@ -2,7 +2,7 @@
 
 Tolerances (relative L2; per element see updater_oracle.check), u = unit roundoff of the type:
 - block, 16-bit: every rounding to the type on the way to a result counts one u -- y: h, y (2 u); w_down: h, w_down
-  (2 u); x, w_gate, w_up: g, u, dg or du, the result (4 u).  float32: the split products leave out 2^-24 of each
+  (2 u); x, w_gate, w_up: g, u, dg or du, the result (4 u).  float32: split products leave out 2^-24 of each
   product and a sum of K terms in float32 loses at most about sqrt(K) u, over the two or three products in a row:
   16 u + 2 sqrt(K) u with K the longest sum.
 - recurrence: one rounding for 16-bit results (1 u); float32: the sigmoid's few u, kept over the state's memory of at
@@ -90,6 +90,31 @@ def test_ffn_large_tiles_and_split_gradients(dtype, shape):
     again = block.backward(x, saved, dy)
     for name in got:
         assert torch.equal(got[name], again[name]), name
+
+
+@pytest.mark.parametrize("shape, act", [((33000, 200, 520, 193), "silu"), ((2100, 1024, 1366, 1024), "gelu"),
+                                        ((70001, 256, 250, 192), "gelu")], ids=str)
+def test_ffn_float32_large(shape, act):
+    """float32 products large enough to run on split operands; one NaN and one infinite row, strided x."""
+    m, d, f, out = shape
+    x, wg, wu, wd, dy = ffn_inputs(m, d, f, out, torch.float32, seed=8)
+    wide = torch.zeros(m, d + 3, device="cuda")
+    wide[:, 1:d + 1] = x
+    xv = wide[:, 1:d + 1]
+    block = gsr().GatedFFN(wg, wu, wd, activation=act)
+    y, saved = block.forward(xv, save=True)
+    got = block.backward(xv, saved, dy)
+    ref = o.ffn(x, wg, wu, wd, act, dy)
+    tol = ffn_tol(torch.float32, 0, max(m, 2 * f, d, out))
+    o.check(y, ref["y"], tol, "y")
+    assert torch.equal(block.forward(xv), y)
+    for name in ("w_down", "x", "w_gate", "w_up"):
+        o.check(got[name], ref[name], tol, name)
+    xv[130, 7], xv[m - 1, d - 1] = float("nan"), float("inf")
+    bad = block.forward(xv)
+    keep = torch.ones(m, dtype=torch.bool, device="cuda")
+    keep[[130, m - 1]] = False
+    assert torch.equal(bad[keep], y[keep]) and torch.isnan(bad[130]).all() and not torch.isfinite(bad[m - 1]).any()
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=str)
