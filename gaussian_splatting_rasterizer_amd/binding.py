@@ -328,6 +328,16 @@ def gs_profile_read(ctx) -> dict:
     return {name: (float(ms[i]), int(calls[i])) for i, name in enumerate(STAGES)}
 
 
+# The small updater calls take microseconds, so their pointers go as plain integers (the declared argument types
+# convert them) instead of one ctypes object each.
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _stream(stream):
+    return stream.cuda_stream if stream is not None else _stream_handle(None)
+
+
 def gs_ffn_sizes(dims: gs_ffn_dims) -> tuple:
     """(saved bytes, forward workspace bytes, backward workspace bytes)"""
     out = [ctypes.c_size_t(0) for _ in range(3)]
@@ -336,16 +346,16 @@ def gs_ffn_sizes(dims: gs_ffn_dims) -> tuple:
 
 
 def gs_ffn_forward(dims, x, ld_x, weights: gs_ffn_weights, y, ld_y, saved, workspace, stream=None) -> None:
-    _check(load_library().gs_ffn_forward(ctypes.byref(dims), _dev_ptr(x), ld_x, ctypes.byref(weights), _dev_ptr(y),
-                                         ld_y, _dev_ptr(saved), _dev_ptr(workspace), _nbytes(workspace),
-                                         _stream_handle(stream)), "gs_ffn_forward")
+    _check(load_library().gs_ffn_forward(ctypes.byref(dims), _ptr(x), ld_x, ctypes.byref(weights), _ptr(y),
+                                         ld_y, _ptr(saved), _ptr(workspace), _nbytes(workspace),
+                                         _stream(stream)), "gs_ffn_forward")
 
 
 def gs_ffn_backward(dims, x, ld_x, weights: gs_ffn_weights, saved, dy, ld_dy, grads: gs_ffn_grads, workspace,
                     stream=None) -> None:
-    _check(load_library().gs_ffn_backward(ctypes.byref(dims), _dev_ptr(x), ld_x, ctypes.byref(weights),
-                                          _dev_ptr(saved), _dev_ptr(dy), ld_dy, ctypes.byref(grads),
-                                          _dev_ptr(workspace), _nbytes(workspace), _stream_handle(stream)),
+    _check(load_library().gs_ffn_backward(ctypes.byref(dims), _ptr(x), ld_x, ctypes.byref(weights),
+                                          _ptr(saved), _ptr(dy), ld_dy, ctypes.byref(grads),
+                                          _ptr(workspace), _nbytes(workspace), _stream(stream)),
            "gs_ffn_backward")
 
 
@@ -357,17 +367,17 @@ def gs_scan_sizes(dims: gs_scan_dims) -> tuple:
 
 
 def gs_scan_forward(dims, offsets, inputs: gs_scan_inputs, y, ld_y, h_last, saved, workspace, stream=None) -> None:
-    _check(load_library().gs_scan_forward(ctypes.byref(dims), _dev_ptr(offsets), ctypes.byref(inputs), _dev_ptr(y),
-                                          ld_y, _dev_ptr(h_last), _dev_ptr(saved), _dev_ptr(workspace),
-                                          _nbytes(workspace), _stream_handle(stream)), "gs_scan_forward")
+    _check(load_library().gs_scan_forward(ctypes.byref(dims), _ptr(offsets), ctypes.byref(inputs), _ptr(y),
+                                          ld_y, _ptr(h_last), _ptr(saved), _ptr(workspace),
+                                          _nbytes(workspace), _stream(stream)), "gs_scan_forward")
 
 
 def gs_scan_backward(dims, offsets, inputs: gs_scan_inputs, saved, dy, ld_dy, dh_last, grads: gs_scan_grads,
                      workspace, stream=None) -> None:
-    _check(load_library().gs_scan_backward(ctypes.byref(dims), _dev_ptr(offsets), ctypes.byref(inputs),
-                                           _dev_ptr(saved), _dev_ptr(dy), ld_dy, _dev_ptr(dh_last),
-                                           ctypes.byref(grads), _dev_ptr(workspace), _nbytes(workspace),
-                                           _stream_handle(stream)), "gs_scan_backward")
+    _check(load_library().gs_scan_backward(ctypes.byref(dims), _ptr(offsets), ctypes.byref(inputs),
+                                           _ptr(saved), _ptr(dy), ld_dy, _ptr(dh_last),
+                                           ctypes.byref(grads), _ptr(workspace), _nbytes(workspace),
+                                           _stream(stream)), "gs_scan_backward")
 
 
 def gs_default_ortho_dims() -> gs_ortho_dims:
@@ -383,8 +393,8 @@ def gs_ortho_size(dims: gs_ortho_dims) -> int:
 
 
 def gs_orthogonalize(dims: gs_ortho_dims, g, out, workspace, stream=None) -> None:
-    _check(load_library().gs_orthogonalize(ctypes.byref(dims), _dev_ptr(g), _dev_ptr(out), _dev_ptr(workspace),
-                                           _nbytes(workspace), _stream_handle(stream)), "gs_orthogonalize")
+    _check(load_library().gs_orthogonalize(ctypes.byref(dims), _ptr(g), _ptr(out), _ptr(workspace),
+                                           _nbytes(workspace), _stream(stream)), "gs_orthogonalize")
 
 
 # ---- convenience wrapper ----------------------------------------------------------------------------

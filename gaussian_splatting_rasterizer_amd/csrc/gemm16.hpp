@@ -526,7 +526,7 @@ struct TileTimes {
 inline GemmPlan plan_gemm(int64_t M, int64_t N, int64_t batch, int64_t ktiles, bool dual, bool symmetric,
                           int max_splits, bool f32 = false) {
     static const TileTimes t16[3] = {{256, 1, 1.75, 1.75, 7}, {128, 2, 0.85, 1.2, 4}, {64, 4, 0.5, 1.05, 3}};
-    static const TileTimes t32[3] = {{256, 1, 8.4, 8.4, 7}, {128, 2, 2.3, 4.3, 4}, {64, 4, 0.85, 3.2, 3}};
+    static const TileTimes t32[3] = {{256, 1, 8.4, 8.4, 20}, {128, 2, 2.3, 4.3, 16}, {64, 4, 0.85, 3.2, 3}};
     GemmPlan best{128, 1, (int)ktiles, 1e30};
     for (int i = 0; i < 3; ++i) {
         const TileTimes& tt = f32 ? t32[i] : t16[i];
