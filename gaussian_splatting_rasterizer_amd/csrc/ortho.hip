@@ -363,12 +363,14 @@ hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* 
 // ---- small matrices ------------------------------------------------------------------------------------
 
 // A matrix whose padded X and P fit in LDS takes one workgroup and one launch for all steps (12 matrices of 128 x 512:
-// 17 launches took 123 us).  X lies as m rows of n (m the smaller side) with n contiguous, rows of a multiple of 128
-// bytes, chunk c of row r at position c ^ (r & 7); P and then Q share a second buffer of the same form.
+// 72 us, 17 launches took 123; 11 us a step, the rest for reading, norm and result).  X lies as m rows of n (m the
+// smaller side) with n contiguous, rows of a multiple of 128 bytes (see at); P and then Q share a second buffer of the
+// same form.
 //   P: every wave takes a 32 x 64 block of X X^T and keeps it in registers;
 //   Q: the same block of P P (P from LDS), plus b P; then Q replaces P;
 //   X: every wave takes strips of 32 columns, which depend on nothing but themselves and Q, in place.
-// LDS reads bound it: a block needs six 16-byte fragments a lane for eight products.
+// LDS reads bound it: a block needs six 16-byte fragments a lane for eight products, 7 us of the 11.  Reading the next
+// fragments during the products gained nothing, strips of 64 columns did not fit the registers.
 constexpr int kSmallWaves = 8;
 constexpr int kSmallLds = 160 * 1024;  // all of a CU's: the kernel has no other shared memory
 constexpr int kSmallSide = 128;
@@ -377,7 +379,11 @@ template <int PL>
 struct SmallView {
     char* base;
     int pitch, plane;  // bytes of a row, of a plane
-    __device__ __forceinline__ int at(int r, int c8) const { return r * pitch + ((c8 ^ (r & 7)) << 4); }
+    // chunk c8 of row r: any 8 consecutive rows differ (fragments along k), and the 4 rows of a transpose read differ by
+    // whole pairs of chunks
+    __device__ __forceinline__ int at(int r, int c8) const {
+        return r * pitch + ((c8 ^ ((r & 3) << 1 | (r >> 2 & 1))) << 4);
+    }
     // 16 rows from r0 (lane: row l % 16), k (l / 16) * 8 .. + 8 from k0
     __device__ __forceinline__ s16x8 rows(int pl, int r0, int k0, int lane) const {
         return *(const s16x8*)(base + pl * plane + at(r0 + (lane & 15), (k0 >> 3) + (lane >> 4)));
@@ -408,6 +414,12 @@ struct SmallView {
         *(u16x4*)(base + o) = hi;
         if constexpr (PL == 2) *(u16x4*)(base + plane + o) = to16<_Float16>(v - from16<_Float16>(hi));
     }
+    __device__ __forceinline__ float get1(int r, int c) const {
+        const int o = at(r, c >> 3) + (c & 7) * 2;
+        float v = (float)*(const _Float16*)(base + o);
+        if constexpr (PL == 2) v += (float)*(const _Float16*)(base + plane + o);
+        return v;
+    }
     __device__ __forceinline__ void put1(int r, int c, float v) const {
         const int o = at(r, c >> 3) + (c & 7) * 2;
         const _Float16 hi = (_Float16)v;
@@ -434,6 +446,49 @@ __device__ __forceinline__ f32x4 rounded(f32x4 v) {
     return hi + from16<_Float16>(to16<_Float16>(v - hi));
 }
 
+// X = a X + Q X for 32 columns from c0, in place
+template <int PL>
+__device__ __forceinline__ void small_update(const SmallView<PL>& X, const SmallView<PL>& Q, int c0, int mp, float a,
+                                             int lane) {
+    constexpr int kTiles = kSmallSide / 16, J = 2;
+    const int row = lane & 15, col = (lane >> 4) * 4;
+    f32x4 x[kTiles][J];
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j) x[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < mp; k += 32) {
+        s16x8 fb[J][PL];
+#pragma unroll
+        for (int q = 0; q < PL; ++q)
+#pragma unroll
+            for (int j = 0; j < J; ++j) fb[j][q] = X.cols(q, c0 + j * 16, k, lane);
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i)
+            if (i * 16 < mp) {
+                s16x8 fa[PL];
+#pragma unroll
+                for (int q = 0; q < PL; ++q) fa[q] = Q.rows(q, i * 16, k, lane);
+#pragma unroll
+                for (int j = 0; j < J; ++j) x[i][j] = small_product<PL>(fb[j], fa, x[i][j]);
+            }
+    }
+    // the columns are read before they are written: other waves read other columns
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+        if (i * 16 < mp) {
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                x[i][j] = a * X.get(i * 16 + row, c0 + j * 16 + col) + x[i][j] * (1.f / kPScale);
+        }
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i)
+        if (i * 16 < mp) {
+#pragma unroll
+            for (int j = 0; j < J; ++j) X.put(i * 16 + row, c0 + j * 16 + col, x[i][j]);
+        }
+}
+
 struct SmallArgs {
     const void* g;
     void* out;
@@ -441,35 +496,18 @@ struct SmallArgs {
     float a, b, c, eps;
 };
 
-// f(i, values i .. i + 3, how many of them exist) over n values, four a thread
-template <int NT, class In, class Fn>
-__device__ __forceinline__ void for_fours(const In* g, int n, int tid, Fn f) {
-    typedef In In4 __attribute__((ext_vector_type(4)));
-    const bool vec = (uintptr_t)g % sizeof(In4) == 0;
-    constexpr int kFlight = 8;
-    for (int i0 = tid * 4; i0 < n; i0 += NT * 4 * kFlight) {
-        f32x4 v[kFlight];
-#pragma unroll
-        for (int k = 0; k < kFlight; ++k) {
-            const int i = i0 + k * NT * 4;
-            v[k] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (vec && i + 4 <= n) {
-                const In4 q = *(const In4*)(g + i);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[k][e] = (float)q[e];
-            } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (i + e < n) v[k][e] = load_value(g + i + e);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kFlight; ++k) {
-            const int i = i0 + k * NT * 4;
-            if (i < n) f(i, v[k], n - i);
-        }
+// Row and column of every NT-th four elements of a matrix with `cols` columns, without a division for each.
+struct Walk {
+    int cols, dr, dc, r, c;
+    __device__ __forceinline__ Walk(int cols, int first, int step) : cols(cols) {
+        dr = step / cols, dc = step - dr * cols;
+        r = first / cols, c = first - r * cols;
     }
-}
+    __device__ __forceinline__ void next() {
+        r += dr, c += dc;
+        if (c >= cols) c -= cols, ++r;
+    }
+};
 
 template <class In, class Out, int PL>
 __global__ __launch_bounds__(kSmallWaves * 64) void k_ortho_small(const SmallArgs p) {
@@ -478,18 +516,44 @@ __global__ __launch_bounds__(kSmallWaves * 64) void k_ortho_small(const SmallArg
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const SmallView<PL> X{lds, p.np * 2, p.mp * p.np * 2};
-    const SmallView<PL> P{lds + PL * p.mp * p.np * 2, p.mp * 2, p.mp * p.mp * 2};
+    const SmallView<PL> P{lds + PL * X.plane, p.mp * 2, p.mp * p.mp * 2};
     const int64_t size = (int64_t)p.rows * p.cols;
     const In* g = (const In*)p.g + blockIdx.x * size;
     Out* out = (Out*)p.out + blockIdx.x * size;
 
-    // four consecutive values a thread, eight times in flight (one at a time, reading the matrix twice took 60 us)
-    double s = 0.0;
-    for_fours<NT>(g, (int)size, tid, [&](int, const f32x4& v, int n) {
+    // Four consecutive values a thread, up to 32 times: the matrix is read once and stays in registers until its norm
+    // is known; what is left of a larger one is read again.
+    typedef In In4 __attribute__((ext_vector_type(4)));
+    constexpr int kHeld = 32;
+    const int n = (int)size;
+    const bool vec = (uintptr_t)g % sizeof(In4) == 0;
+    auto four = [&](int i) {
+        f32x4 v{0.f, 0.f, 0.f, 0.f};
+        if (vec && i + 4 <= n) {
+            const In4 q = *(const In4*)(g + i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < n) s += (double)v[e] * (double)v[e];
-    });
+            for (int e = 0; e < 4; ++e) v[e] = (float)q[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < n) v[e] = load_value(g + i + e);
+        }
+        return v;
+    };
+    f32x4 held[kHeld];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) held[k] = four((k * NT + tid) * 4);
+    double s = 0.0;
+    auto square = [&](const f32x4& v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s += (double)v[e] * (double)v[e];
+    };
+    // zero everything meanwhile: the padding stays zero
+    for (int i = tid; i < PL * (X.plane + P.plane) / 16; i += NT) *(u32x4*)(lds + i * 16) = u32x4{0, 0, 0, 0};
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) square(held[k]);
+    for (int i = (kHeld * NT + tid) * 4; i < n; i += NT * 4) square(four(i));
 #pragma unroll
     for (int w = 32; w > 0; w >>= 1) s += __shfl_xor(s, w, 64);
     double* red = (double*)P.base;
@@ -499,23 +563,34 @@ __global__ __launch_bounds__(kSmallWaves * 64) void k_ortho_small(const SmallArg
 #pragma unroll
     for (int w = 0; w < kSmallWaves; ++w) s += red[w];
     __syncthreads();
-    // zero everything: the padding stays zero
-    for (int i = tid; i < PL * p.mp * (p.np + p.mp) / 8; i += NT) *(u32x4*)(lds + i * 16) = u32x4{0, 0, 0, 0};
-    __syncthreads();
+    if (tid < kSmallWaves) red[tid] = 0.0;  // P's padding again
+    // the factor as a power of two and a rest in [1/2, 1): neither over- nor underflows float32
     const double norm = sqrt(s);
-    const double inv = (double)kXScale / (norm < (double)p.eps ? (double)p.eps : norm);
+    int ex;
+    const float rest = (float)frexp((double)kXScale / (norm < (double)p.eps ? (double)p.eps : norm), &ex);
     const bool tall = p.rows > p.cols;
-    for_fours<NT>(g, (int)size, tid, [&](int i, const f32x4& v, int n) {
-        int r = i / p.cols, c = i - r * p.cols;
+    Walk at(p.cols, tid * 4, NT * 4);
+    auto place = [&](int i, f32x4 v) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (e < n) X.put1(tall ? c : r, tall ? r : c, (float)((double)v[e] * inv));
-            if (++c == p.cols) c = 0, ++r;
+        for (int e = 0; e < 4; ++e) v[e] = ldexpf(v[e], ex) * rest;
+        if (!tall && p.cols % 4 == 0) {
+            if (i < n) X.put(at.r, at.c, v);
+        } else {
+            int r = at.r, c = at.c;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (i + e < n) X.put1(tall ? c : r, tall ? r : c, v[e]);
+                if (++c == p.cols) c = 0, ++r;
+            }
         }
-    });
+        at.next();
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) place((k * NT + tid) * 4, held[k]);
+    for (int i = (kHeld * NT + tid) * 4; i < n; i += NT * 4) place(i, four(i));
     __syncthreads();
 
-    const int across = p.mp / 64, blocks = p.mp / 32 * across, strips = p.np / 32;
+    const int across = p.mp / 64, blocks = p.mp / 32 * across;
     const int row = lane & 15, col = (lane >> 4) * 4;  // of the lane's four results in a 16 x 16 tile
     const bool mine = wave < blocks;                   // at most 4 x 2 blocks
     const int r0 = mine ? wave / across * 32 : 0, c0 = mine ? wave % across * 64 : 0;
@@ -567,63 +642,35 @@ __global__ __launch_bounds__(kSmallWaves * 64) void k_ortho_small(const SmallArg
         __syncthreads();
         if (mine) keep();
         __syncthreads();
-        for (int t = wave; t < strips; t += kSmallWaves) {
-            constexpr int kTiles = kSmallSide / 16;
-            f32x4 x[kTiles][2];
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) x[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-            for (int k = 0; k < p.mp; k += 32) {
-                s16x8 fb[2][PL];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int q = 0; q < PL; ++q) fb[j][q] = X.cols(q, t * 32 + j * 16, k, lane);
-#pragma unroll
-                for (int i = 0; i < kTiles; ++i) {
-                    if (i * 16 < p.mp) {
-                        s16x8 fa[PL];
-#pragma unroll
-                        for (int q = 0; q < PL; ++q) fa[q] = P.rows(q, i * 16, k, lane);
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) x[i][j] = small_product<PL>(fb[j], fa, x[i][j]);
-                    }
-                }
-            }
-            // the strip is read before it is written: other waves read other columns
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                if (i * 16 < p.mp) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int c = t * 32 + j * 16 + col;
-                        x[i][j] = p.a * X.get(i * 16 + row, c) + x[i][j] * (1.f / kPScale);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                if (i * 16 < p.mp) {
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) X.put(i * 16 + row, t * 32 + j * 16 + col, x[i][j]);
-                }
-            }
-        }
+        for (int t = wave; t < p.np / 32; t += kSmallWaves) small_update<PL>(X, P, t * 32, p.mp, p.a, lane);
         __syncthreads();
     }
-    for (int i = tid * 4; i < (int)size; i += NT * 4) {
-        int r = i / p.cols, c = i - r * p.cols;
+    typedef Out Out4 __attribute__((ext_vector_type(4)));
+    const bool vec_out = (uintptr_t)out % sizeof(Out4) == 0;
+    Walk to(p.cols, tid * 4, NT * 4);
+#pragma unroll 4
+    for (int i = tid * 4; i < n; i += NT * 4) {
+        f32x4 v;
+        if (!tall && p.cols % 4 == 0) {
+            v = X.get(to.r, to.c);
+        } else {
+            int r = to.r, c = to.c;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (i + e < (int)size) {
-                const int xr = tall ? c : r, xc = tall ? r : c;
-                const int o = X.at(xr, xc >> 3) + (xc & 7) * 2;
-                float v = (float)*(const _Float16*)(X.base + o);
-                if constexpr (PL == 2) v += (float)*(const _Float16*)(X.base + X.plane + o);
-                out[i + e] = (Out)(v * (1.f / kXScale));
+            for (int e = 0; e < 4; ++e) {
+                v[e] = i + e < n ? X.get1(tall ? c : r, tall ? r : c) : 0.f;
+                if (++c == p.cols) c = 0, ++r;
             }
-            if (++c == p.cols) c = 0, ++r;
+        }
+        to.next();
+        Out4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = (Out)(v[e] * (1.f / kXScale));
+        if (vec_out && i + 4 <= n) {
+            *(Out4*)(out + i) = o;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < n) out[i + e] = o[e];
         }
     }
 }
