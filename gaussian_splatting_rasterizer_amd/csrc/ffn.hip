@@ -12,6 +12,21 @@
 //
 // Rows that are not 16-byte aligned, or whose length is not a multiple of 8 elements, are copied once into a
 // zero-padded layout in the workspace (k_pack); other operands are read in place.
+//
+// Roundings of the 16-bit types: the matrix instructions take 16-bit operands, so h, dg and du are rounded to the type
+// once before their products, and g and u once where they are kept for the backward pass (kept in float32 they would
+// add 4 GB of traffic, 0.8 ms, to the 2.8 ms of 131072 rows of 512 x 2048 x 512).  With the result's own rounding y and
+// dWd carry two roundings, dx, dWg and dWu four.  Everything else is float32.
+//
+// Measured, bfloat16 SiLU, 131072 rows of 512 x 2048 x 512, forward and backward 2.77 ms (890 TFLOP/s; the power limit
+// lowers the shader clock to 1.9 GHz); in a kernel trace, us:
+//   g, u, h  730  1.6 GB of results (310 at a copy's rate) and products (360) alternate in a workgroup
+//   y        310  products, 890 TFLOP/s
+//   dg, du   690  2.3 GB read and written (450) after the products (180)
+//   dx       470  products, 1170 TFLOP/s
+//   dWg, dWu 450, dWd 250: products split along the rows, 1220 and 1110 TFLOP/s; the sums of the parts 13 each
+// Asking for the tile's g and u during its products made the third 770 us: the lines arrive, but the fetches of
+// operands wait behind them.
 #include <algorithm>
 
 #include "gsr_internal.hpp"
@@ -282,7 +297,10 @@ __global__ __launch_bounds__(256) void k_reduce(const float* part, int splits, i
 
 // At most 64 rows: the weights are read once, straight into the matrix instructions' operands, and that is all the
 // work there is.  A workgroup takes 16 columns (of both projections) and splits k over its waves; the partial sums
-// meet in LDS.  Every wave's loads are independent, so the whole weight matrix is in flight at once.
+// meet in LDS.  Every wave's loads are independent, so the whole weight matrix is in flight at once.  One row of 1024 x
+// 4096 x 1024 bfloat16: 6.2 + 6.3 us for 16.8 and 8.4 MB, half of it the launch and the first load's latency.  48 rows
+// of 1024 x 2816 x 1024: 9.0 + 12.8 us; the second is bound by its rows, which every workgroup reads in full (393 KB a
+// CU).
 // 16-bit: lane l holds row l % 16, k (l / 16) * 8 .. + 8 of a 16x16x32 product.  float32: k (l / 16) * 4 + j for the
 // j-th of four 16x16x4 products (both operands permute k alike).  WIDE: rows allow 16-byte loads; otherwise
 // elements are read one by one.

@@ -7,8 +7,8 @@
 // several products in one accumulator: two weight matrices of one gradient, or the six (three) partial products
 // that make a float32 product out of operands split into bfloat16 (float16) parts.
 //
-// Tile BM x BN x 64 (float32: 32) per workgroup, split over WM x WN waves of 16x16x32 (16x16x4) matrix instructions.  Tiles go from global
-// memory to LDS directly (16 bytes per lane, no registers), double buffered.  A row of a KC tile is 128 bytes = 8
+// Tile BM x BN x 64 (float32: 32) per workgroup, split over WM x WN waves of 16x16x32 (16x16x4) matrix instructions.
+// Tiles go from global memory to LDS directly (16 bytes per lane, no registers), double buffered.  A row of a KC tile is 128 bytes = 8
 // chunks; chunk c of row r lies at chunk position c ^ f(r), so the 16-byte fragment reads of 8 lanes cover all 32
 // banks (no conflicts measured).  A tile with rows contiguous keeps its [k][row] order and is read with the LDS
 // transpose read (4 k x 16 rows per 16 lanes); chunk position c ^ f(k) spreads the four k rows over the banks.

@@ -4,11 +4,16 @@
 //   and with P = X^T X, X = a X + X Q for rows > cols, so that P is the smaller square.
 //
 // All products run on k_gemm16 in float16 with float32 accumulation.  P and Q are symmetric: only tiles on and above
-// the diagonal are computed and each writes its mirror image; with few tiles and many k the sums are split along k.  Every singular value of X stays below 1.2 after the
-// normalisation, so X is held as 2^12 X and P, Q as 2^13 P, 2^13 Q: far from float16's overflow (|Q| <= 5) and, for
-// the entries that matter, above its subnormals.  float16 keeps 11 bits; in bfloat16 the same steps lose 8 times as
-// much.  For a float32 result each of X, P, Q is a pair hi + lo of float16 (22 bits) and a product is
-// lo hi + hi lo + hi hi.
+// the diagonal are computed and each writes its mirror image; with few tiles and many k the sums are split along k.
+// Every singular value of X stays below 1.2 after the normalisation, so X is held as 2^12 X and P, Q as 2^13 P, 2^13 Q:
+// far from float16's overflow (|Q| <= 5) and, for the entries that matter, above its subnormals.  float16 keeps 11
+// bits; in bfloat16 the same steps lose 8 times as much.  For a float32 result each of X, P, Q is a pair hi + lo of
+// float16 (22 bits) and a product is lo hi + hi lo + hi hi.
+//
+// Measured: 2048 x 5632 bfloat16 640 us, of each step's 147 us P 44 + 12 (its split sums), Q 25, X 64 (740 TFLOP/s on
+// 176 of 256 CUs; tiles of 192 x 256 on 242 CUs gained 1 %, the power limit lowers the clock instead).  Two matrices of
+// 1366 x 500 float32: 247 us, of each step's 49 us P 13 + 6, Q 14, X 16; these products have 11 to 24 k tiles in 72 to
+// 432 workgroups and wait for LDS and barriers (a ring of four tiles in LDS instead of two changed nothing).
 #include "gsr_internal.hpp"
 #include "gemm16.hpp"
 

@@ -16,6 +16,11 @@
 //
 // The forward pass keeps the state in front of every 8 rows in float32; the backward pass reruns the states from
 // there, instead of reading back rounded ones.
+//
+// Bound by memory.  311,296 rows x 256 bfloat16 channels in one sequence, us and TB/s: forward spans 86 (3.7), join 16,
+// recurrence 88 (5.9, part of it from the last-level cache); backward spans 90 (3.5), join 16, recurrence 172 (4.9); a
+// large copy reaches 5.2.  One pass over the data, workgroups waiting for the state of the one before, took 249 us
+// forward and 373 backward: the chain through 1216 chunks is longer than the second reading.
 #include "gsr_internal.hpp"
 #include "gemm16.hpp"
 

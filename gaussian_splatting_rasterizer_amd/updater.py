@@ -44,7 +44,8 @@ def _exact(t, name, shape, dtype, device):
 
 class _Op:
     """A device, and scratch memory that grows when a call needs more (released in the order of the streams that used
-    it)."""
+    it).  A captured graph keeps using the scratch memory it was captured with: an object that was captured makes no
+    larger call afterwards."""
 
     def __init__(self, device):
         import torch

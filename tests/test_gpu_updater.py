@@ -93,9 +93,10 @@ def test_ffn_large_tiles_and_split_gradients(dtype, shape):
 
 
 @pytest.mark.parametrize("shape, act", [((33000, 200, 520, 193), "silu"), ((2100, 1024, 1366, 1024), "gelu"),
-                                        ((70001, 256, 250, 192), "gelu")], ids=str)
+                                        ((70001, 256, 250, 192), "gelu"), ((70000, 120, 500, 130), "silu")], ids=str)
 def test_ffn_float32_large(shape, act):
-    """float32 products large enough to run on split operands; one NaN and one infinite row, strided x."""
+    """float32 products large enough to run on split operands, or (narrow rows) on large tiles of the float32 ones; one
+    NaN and one infinite row, strided x."""
     m, d, f, out = shape
     x, wg, wu, wd, dy = ffn_inputs(m, d, f, out, torch.float32, seed=8)
     wide = torch.zeros(m, d + 3, device="cuda")
@@ -536,3 +537,48 @@ def test_ortho_repeats_and_refuses():
         m.Orthogonalizer(1, 4, 4, torch.float16)
     with pytest.raises(m.GsrError):
         m.Orthogonalizer(1, 4, 4, torch.float32, steps=0)
+
+
+def test_all_in_a_graph():
+    """Training form of block and recurrence, single-step forms and both orthogonalisations, captured once and replayed
+    with new inputs and other work in between: every replay equals the eager calls."""
+    m, d, f, out, n = 200, 40, 72, 48, 5
+    x, wg, wu, wd, dy = ffn_inputs(m, d, f, out, torch.bfloat16, seed=40)
+    g = gen(41)
+    block = gsr().GatedFFN(wg, wu, wd)
+    scan = gsr().GatedScan(24, torch.bfloat16)
+    small, large = gsr().Orthogonalizer(2, 30, 50, torch.float32), gsr().Orthogonalizer(1, 150, 180, torch.bfloat16)
+    h0 = randn(g, n, 24)
+    offsets = torch.tensor([0, 7, 7, 90, 91, m], device="cuda")
+    m1, m2 = randn(g, 2, 30, 50), randn(g, 150, 180, dtype=torch.bfloat16)
+
+    def run():
+        y, saved = block.forward(x, save=True)
+        grads = block.backward(x, saved, dy)
+        z, v = y[:, :24], y[:, 24:]
+        s, last, kept = scan.forward(z, v, h0=h0, offsets=offsets, save=True)
+        sg = scan.backward(z, v, kept, s, dh_last=last, h0=h0, offsets=offsets)
+        one = block.forward(x[:1])
+        step, state = scan.forward(z[:n], v[:n], h0=h0)
+        return [y, s, last, one, step, state, small.run(m1), large.run(m2), *grads.values(), *sg.values()]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    for i in range(4):
+        x.copy_(randn(g, m, d, dtype=torch.bfloat16))
+        h0.copy_(randn(g, n, 24))
+        m1.copy_(randn(g, 2, 30, 50))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        want = run()
+        torch.cuda.synchronize()
+        for k, (a, w) in enumerate(zip(got, want)):
+            assert torch.equal(a, w), (i, k)
