@@ -476,11 +476,12 @@ struct Layout {
     int64_t h_bytes() const { return round_up(h_elems() * (int64_t)sizeof(OperandElem<F>), kAlign); }
 };
 
-// An operand is read in place when its rows are 16-byte aligned and a multiple of 16 bytes long.
+// An operand is read in place when its rows are 16-byte aligned and a multiple of 8 elements long: the backward products
+// run over row lengths rounded up to 8, which an unpadded array does not have.
 template <class F>
 bool direct(const void* p, int64_t cols, int64_t ld) {
     constexpr int64_t e = 16 / (int64_t)sizeof(OperandElem<F>);
-    return F::kPlanes == 1 && cols % e == 0 && ld % e == 0 && ((uintptr_t)p % 16) == 0;
+    return F::kPlanes == 1 && cols % 8 == 0 && ld % e == 0 && ((uintptr_t)p % 16) == 0;
 }
 
 struct Packer {
@@ -647,7 +648,7 @@ hipError_t backward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const
         GemmArgs g2 = make_args(L.M, L.D8, L.H);
         add_segments<F>(g2, odgu, og, nullptr, 0);
         add_segments<F>(g2, odgu, ou, nullptr, L.H8);
-            EpiStore<F> e2{(E*)out.x, nullptr, lddx, (int)L.M, 0, (int)L.D, vec_width(out.x, lddx, sizeof(E))};
+        EpiStore<F> e2{(E*)out.x, nullptr, lddx, (int)L.M, 0, (int)L.D, vec_width(out.x, lddx, sizeof(E))};
         GSR_TRY((launch_gemm<T, true, false>(g2, e2, st)));
     }
     if (out.gate || out.up) {

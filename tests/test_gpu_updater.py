@@ -539,6 +539,30 @@ def test_ortho_repeats_and_refuses():
         m.Orthogonalizer(1, 4, 4, torch.float32, steps=0)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("shape", [(130, 60, 76, 20), (70, 12, 100, 36)], ids=str)
+def test_ffn_ends_of_arrays(shape, dtype):
+    """Row lengths of 4 modulo 8 with arrays that end where NaN begins."""
+    m, d, f, out = shape
+    tensors = ffn_inputs(m, d, f, out, dtype, seed=43)
+
+    def end(t):
+        room = torch.full((t.numel() + 64,), float("nan"), dtype=dtype, device="cuda")
+        room[:t.numel()] = t.flatten()
+        return room[:t.numel()].view(t.shape)
+
+    x, wg, wu, wd, dy = (end(t) for t in tensors)
+    block = gsr().GatedFFN(wg, wu, wd)
+    y, saved = block.forward(x, save=True)
+    got = block.backward(x, saved, dy)
+    ref = o.ffn(*tensors[:4], "silu", tensors[4])
+    k = max(m, 2 * f, d, out)
+    o.check(y, ref["y"], ffn_tol(dtype, 2, k), "y")
+    o.check(got["w_down"], ref["w_down"], ffn_tol(dtype, 2, k), "w_down")
+    for name in ("x", "w_gate", "w_up"):
+        o.check(got[name], ref[name], ffn_tol(dtype, 4, k), name)
+
+
 def test_all_in_a_graph():
     """Training form of block and recurrence, single-step forms and both orthogonalisations, captured once and replayed
     with new inputs and other work in between: every replay equals the eager calls."""
