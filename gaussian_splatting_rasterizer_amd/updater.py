@@ -205,7 +205,8 @@ class GatedScan(_Op):
         return rows, n_seq, dims, sizes, inputs
 
     def forward(self, gate, x, h0=None, offsets=None, y=None, h_last=None, save=False, stream=None):
-        """-> (y, h_last); with save, (y, h_last, saved) for backward.  h_last may be h0 (updated in place)."""
+        """-> (y, h_last); with save, (y, h_last, saved) for backward.  h_last may be h0 (updated in place;
+        backward needs the h0 from before)."""
         return self._on(stream, self._forward, gate, x, h0, offsets, y, h_last, save)
 
     def _forward(self, stream, gate, x, h0, offsets, y, h_last, save):

@@ -361,7 +361,8 @@ GSR_API gs_status gs_ffn_backward(const gs_ffn_dims* dims, const void* x, int64_
  * not non-decreasing give unspecified results but no access out of range.
  * gate, x and y [rows, channels] in the type of dims, row strides in elements;
  * h0 (state before the first row, null: zero) and h_last (state after the last
- * row, null: not wanted) float32 [n_seq, channels].  h_last may be h0.
+ * row, null: not wanted) float32 [n_seq, channels].  h_last may be h0 (a backward
+ * pass wants the states from before, though).
  * rows and n_seq are 0 .. 2^31 - 512, channels 1 .. 2^20. */
 typedef struct {
     int64_t rows;
