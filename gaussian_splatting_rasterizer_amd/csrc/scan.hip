@@ -593,7 +593,8 @@ hipError_t launch_scan(ScanArgs p, hipStream_t st) {
         k_scan_spans<F, VC, BWD><<<gd, bd, 0, st>>>(p);
         GSR_TRY(hipGetLastError());
         if (p.nchunks > 1) {
-            k_scan_join<BWD><<<dim3((unsigned)((p.C + kJoinLanes - 1) / kJoinLanes)), kJoinLanes * kJoinRuns, 0, st>>>(p);
+            const dim3 gj((unsigned)((p.C + kJoinLanes - 1) / kJoinLanes));
+            k_scan_join<BWD><<<gj, kJoinLanes * kJoinRuns, 0, st>>>(p);
             GSR_TRY(hipGetLastError());
         } else {
             p.state = nullptr;
