@@ -14,6 +14,11 @@
 // A row that starts a sequence replaces the state instead of multiplying it by zero, so nothing of one sequence, NaN
 // included, reaches the next.  All orders are fixed: results are reproducible.
 //
+// h_last may be h0 (and dh0 may be dh_last): one wave of the last kernel then writes a sequence's final state where
+// another would read its first.  Only the last sequence that starts in a span can end outside of it, so k_scan_spans
+// keeps that one's first state beside the span's (A, H) and the last kernel takes it from there.  Every other sequence
+// starts and ends in one span, whose wave reads before it writes.
+//
 // The forward pass keeps the state in front of every 8 rows in float32; the backward pass reruns the states from
 // there, instead of reading back rounded ones.
 //
@@ -49,7 +54,9 @@ struct ScanArgs {
     const int64_t* offsets;
     int64_t n_seq, seq_len, rows, nchunks;
     int C, ncb, span;  // span: rows of a span
-    float* agg1;       // [chunk * 8 + span][2][C], null: no state passes between spans
+    // [chunk * 8 + span][3][C]: A, H, and the given state of the last sequence that starts (backward: ends) in the span
+    // on the way through it, unwritten where none does.  Null: no state passes between spans.
+    float* agg1;
     float* agg2;       // [chunk][2][C]
     float* state;      // [chunk][C] state entering the chunk
 };
@@ -218,6 +225,19 @@ struct Place {
     }
 };
 
+// The span's row with the last mark of st[0 .. n) (backward: the first), -1 where there is none.
+template <bool BWD>
+__device__ __forceinline__ int outer_mark(const int* st, int n, int lane) {
+    int at = -1;
+#pragma unroll
+    for (int i = 0; i < kMaxSpan; i += 64) {
+        const int r = (BWD ? kMaxSpan - 64 - i : i);
+        const uint64_t m = __ballot(r + lane < n && st[r + lane] >= 0);
+        if (m) at = r + (BWD ? __builtin_ctzll(m) : 63 - __builtin_clzll(m));
+    }
+    return at;
+}
+
 // bit r: a sequence starts at row r of the batch, one of the first n
 __device__ __forceinline__ uint32_t start_bits(const int* st, int n) {
     uint32_t m = 0;
@@ -239,10 +259,10 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_spans(const ScanArgs p) {
     const RowPtr pz = RowPtr::make<E>(p.z, at.base, p.ldz, at.c, at.live);
     const RowPtr px = BWD ? RowPtr::make<E>(p.dy, at.base, p.lddy, at.c, at.live)
                           : RowPtr::make<E>(p.x, at.base, p.ldx, at.c, at.live);
-    float A[VC], H[VC];
+    float A[VC], H[VC], given_state[VC];
     bool reset = false;
 #pragma unroll
-    for (int e = 0; e < VC; ++e) A[e] = 1.f, H[e] = 0.f;
+    for (int e = 0; e < VC; ++e) A[e] = 1.f, H[e] = 0.f, given_state[e] = 0.f;
     const int nb = (at.n + kBatch - 1) / kBatch;
     Rows<F, VC> z[2], x[2];
     auto fetch = [&](int k, int b) {
@@ -265,7 +285,8 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_spans(const ScanArgs p) {
                 const int64_t q = BWD ? sequence_of(s_start, at.g * p.span + r0 + r, before) : start_of(st, r0 + r);
                 const bool given = src && q >= 0 && q < p.n_seq && at.live;
 #pragma unroll
-                for (int e = 0; e < VC; ++e) H[e] = given ? lane_at<const float>(src + q * p.C, at.c)[e] : 0.f;
+                for (int e = 0; e < VC; ++e)
+                    given_state[e] = H[e] = given ? lane_at<const float>(src + q * p.C, at.c)[e] : 0.f;
             }
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
@@ -287,9 +308,13 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_spans(const ScanArgs p) {
         for (int e = 0; e < VC; ++e) A[e] = -1.f;
     }
     if (at.live && nb > 0) {
-        float* d = lane_at<float>(p.agg1 + (at.chunk * kSpans + at.g) * 2 * p.C, at.c);
+        float* d = lane_at<float>(p.agg1 + (at.chunk * kSpans + at.g) * 3 * p.C, at.c);
 #pragma unroll
         for (int e = 0; e < VC; ++e) d[e] = A[e], d[p.C + e] = H[e];
+        if (reset) {
+#pragma unroll
+            for (int e = 0; e < VC; ++e) d[2 * p.C + e] = given_state[e];
+        }
     }
 #pragma unroll
     for (int e = 0; e < VC; ++e) s_a[at.g][at.li * VC + e] = A[e], s_h[at.g][at.li * VC + e] = H[e];
@@ -372,7 +397,7 @@ __device__ __forceinline__ void span_state(const ScanArgs& p, const Place<VC>& a
     for (int e = 0; e < VC; ++e) h[e] = 0.f;
     if (!p.agg1) return;
     const bool mine = at.live && at.n > 0;
-    const float* d = lane_at<const float>(p.agg1 + (at.chunk * kSpans + at.g) * 2 * p.C, at.c);
+    const float* d = lane_at<const float>(p.agg1 + (at.chunk * kSpans + at.g) * 3 * p.C, at.c);
     const float* s = lane_at<const float>(p.state + at.chunk * p.C, at.c);
 #pragma unroll
     for (int e = 0; e < VC; ++e) {
@@ -412,6 +437,9 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_forward(const ScanArgs p) 
     const int64_t before = sequence_starts(p, at.row0, s_start, threadIdx.x, NT);
     float h[VC];
     span_state<VC, false>(p, at, s_a, s_h, h);
+    // the row whose first state h_last may overwrite, and that state's copy
+    const int kept_row = p.agg1 ? outer_mark<false>(st, at.n, at.li) : -1;
+    const float* kept = p.agg1 + ((at.chunk * kSpans + at.g) * 3 + 2) * p.C;
     auto run = [&](int k, int b) {
         const int r0 = k * kBatch;
         const uint32_t starts = start_bits(st + r0, at.n - r0);
@@ -427,9 +455,9 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_forward(const ScanArgs p) 
             for (int r = 0; r < kBatch; ++r) {
                 const int s = (starts >> r) & 1 ? start_of(st, r0 + r) : -1;
                 const bool given = p.h0 && s >= 0 && s < p.n_seq && at.live;
+                const float* src = r0 + r == kept_row ? kept : p.h0 + (int64_t)s * p.C;
 #pragma unroll
-                for (int e = 0; e < VC; ++e)
-                    first[r][e] = given ? lane_at<const float>(p.h0 + (int64_t)s * p.C, at.c)[e] : 0.f;
+                for (int e = 0; e < VC; ++e) first[r][e] = given ? lane_at<const float>(src, at.c)[e] : 0.f;
             }
         }
 #pragma unroll
@@ -490,6 +518,9 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_backward(const ScanArgs p)
     const int64_t before = sequence_starts(p, at.row0, s_start, threadIdx.x, NT);
     float ev[VC];
     span_state<VC, true>(p, at, s_a, s_h, ev);
+    // the row whose final gradient dh0 may overwrite, and that gradient's copy
+    const int kept_row = p.agg1 ? outer_mark<true>(st + 1, at.n, at.li) : -1;
+    const float* kept = p.agg1 + ((at.chunk * kSpans + at.g) * 3 + 2) * p.C;
     for (int k = nb - 1; k >= 0; --k) {
         const int r0 = k * kBatch;
         const uint32_t starts = start_bits(st + r0, at.n - r0), ends = start_bits(st + r0 + 1, at.n - r0);
@@ -531,9 +562,9 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_backward(const ScanArgs p)
             for (int r = 0; r < kBatch; ++r) {
                 const int64_t s = (ends >> r) & 1 ? sequence_of(s_start, at.g * p.span + r0 + r, before) : -1;
                 const bool given = p.dh_last && s >= 0 && s < p.n_seq && at.live;
+                const float* src = r0 + r == kept_row ? kept : p.dh_last + s * p.C;
 #pragma unroll
-                for (int e = 0; e < VC; ++e)
-                    last[r][e] = given ? lane_at<const float>(p.dh_last + s * p.C, at.c)[e] : 0.f;
+                for (int e = 0; e < VC; ++e) last[r][e] = given ? lane_at<const float>(src, at.c)[e] : 0.f;
             }
         }
 #pragma unroll
@@ -627,7 +658,7 @@ bool pairs_ok(const gs_scan_dims& d, std::initializer_list<const void*> ptrs, st
 int64_t carve_scan(const gs_scan_dims& d, char* ws, ScanArgs* p) {
     Carver cv{ws};
     const int64_t n = chunks_of(d), C = d.channels;
-    p->agg1 = cv.take<float>(n * kSpans * 2 * C);
+    p->agg1 = cv.take<float>(n * kSpans * 3 * C);
     p->agg2 = cv.take<float>(n * 2 * C);
     p->state = cv.take<float>(n * C);
     return cv.used;

@@ -102,6 +102,15 @@ gs_status check_scan_inputs(const char* call, const gs_scan_dims* d, const int64
     return GS_OK;
 }
 
+// States that go in and out may be one array, but not parts of each other's: a sequence's result would replace what
+// another one still reads.
+gs_status check_in_place(const char* call, const gs_scan_dims* d, const char* in_name, const float* in,
+                         const char* out_name, const float* out) {
+    const uintptr_t a = (uintptr_t)in, b = (uintptr_t)out, n = (uintptr_t)d->n_seq * (uintptr_t)d->channels * 4;
+    if (!in || !out || a == b || a + n <= b || b + n <= a) return GS_OK;
+    return fail(GS_ERR_INVALID_ARGUMENT, "%s: %s overlaps %s without being it", call, out_name, in_name);
+}
+
 gs_status check_ortho(const char* call, const gs_ortho_dims* d) {
     if (!d) return fail(GS_ERR_INVALID_ARGUMENT, "%s: dims is null", call);
     for (int t : {d->dtype, d->out_dtype})
@@ -187,6 +196,7 @@ gs_status gs_scan_forward(const gs_scan_dims* dims, const int64_t* offsets, cons
     GSR_CHECK(check_array(call, "y", y, dims->rows, dims->channels, ld_y, elem(dims->dtype)));
     if (!aligned(h_last, 4) || !aligned(saved, 256))
         return fail(GS_ERR_INVALID_ARGUMENT, "%s: h_last or saved is misaligned", call);
+    GSR_CHECK(check_in_place(call, dims, "h0", in->h0, "h_last", h_last));
     size_t s, w;
     scan_sizes(*dims, &s, &w);
     GSR_CHECK(check_workspace(call, workspace, workspace_bytes, w));
@@ -207,6 +217,8 @@ gs_status gs_scan_backward(const gs_scan_dims* dims, const int64_t* offsets, con
     if (grads->x) GSR_CHECK(check_array(call, "grads.x", grads->x, dims->rows, dims->channels, grads->ld_x, e));
     if (!aligned(dh_last, 4) || !aligned(grads->h0, 4))
         return fail(GS_ERR_INVALID_ARGUMENT, "%s: dh_last or grads.h0 is not 4-byte aligned", call);
+    GSR_CHECK(check_in_place(call, dims, "dh_last", dh_last, "grads.h0", grads->h0));
+    GSR_CHECK(check_in_place(call, dims, "h0", in->h0, "grads.h0", grads->h0));
     size_t s, w;
     scan_sizes(*dims, &s, &w);
     GSR_CHECK(check_workspace(call, workspace, workspace_bytes, w));

@@ -226,7 +226,8 @@ class GatedScan(_Op):
         return (y, h_last, saved) if save else (y, h_last)
 
     def backward(self, gate, x, saved, dy, dh_last=None, h0=None, offsets=None, grads=None, stream=None):
-        """Gradients for dy [rows, channels] and dh_last [n_seq, channels]: a dict of gate, x, h0."""
+        """Gradients for dy [rows, channels] and dh_last [n_seq, channels]: a dict of gate, x, h0 (written; with a
+        given dict, only the tensors it holds; its h0 may be dh_last)."""
         return self._on(stream, self._backward, gate, x, saved, dy, dh_last, h0, offsets, grads)
 
     def _backward(self, stream, gate, x, saved, dy, dh_last, h0, offsets, grads):

@@ -362,7 +362,8 @@ GSR_API gs_status gs_ffn_backward(const gs_ffn_dims* dims, const void* x, int64_
  * gate, x and y [rows, channels] in the type of dims, row strides in elements;
  * h0 (state before the first row, null: zero) and h_last (state after the last
  * row, null: not wanted) float32 [n_seq, channels].  h_last may be h0 (a backward
- * pass wants the states from before, though).
+ * pass wants the states from before, though) and the gradient of h0 may be written
+ * to dh_last or h0; arrays that overlap in any other way are GS_ERR_INVALID_ARGUMENT.
  * rows and n_seq are 0 .. 2^31 - 512, channels 1 .. 2^20. */
 typedef struct {
     int64_t rows;

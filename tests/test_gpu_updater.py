@@ -606,3 +606,32 @@ def test_all_in_a_graph():
         torch.cuda.synchronize()
         for k, (a, w) in enumerate(zip(got, want)):
             assert torch.equal(a, w), (i, k)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("c, offsets", [
+    (70, [0, 2]), (70, [0, 300]), (40, [0, 7, 9, 15, 17, 400]), (70, [0, 63, 65, 65, 129, 1500, 1501, 2600]),
+    (70, [0, 0, 5, 700, 700]), (64, [0, 150000]), (130, [0, 40000, 40001, 90000])], ids=lambda v: str(v).replace(" ", ""))
+def test_scan_in_place(c, offsets, dtype):
+    """h_last in h0's memory and dh0 in dh_last's, for sequences within a span, over spans, chunks and many chunks, with
+    offsets and (where the lengths allow) without: y, states, what is saved and the gradients are what separate arrays
+    give."""
+    z, x, h0, dy, dl, off = scan_case(offsets[-1], c, offsets, dtype, seed=11, gate_mean=4.0)
+    op = gsr().GatedScan(c, dtype)
+    lengths = {b_ - a for a, b_ in zip(offsets, offsets[1:])}
+    for kw in [dict(offsets=off)] + ([dict()] if len(lengths) == 1 else []):
+        y, hl, saved = op.forward(z, x, h0=h0, save=True, **kw)
+        want = op.backward(z, x, saved, dy, dl, h0=h0, **kw)
+        state = h0.clone()
+        y2, hl2, saved2 = op.forward(z, x, h0=state, h_last=state, save=True, **kw)
+        assert hl2 is state
+        assert torch.equal(y2, y) and torch.equal(state, hl)
+        n = (offsets[-1] + 7) // 8 * c * 4
+        assert torch.equal(saved2[:n], saved[:n])
+        end = dl.clone()
+        got = {"gate": torch.empty_like(z), "x": torch.empty_like(x), "h0": end}
+        op.backward(z, x, saved, dy, end, h0=h0, grads=got, **kw)
+        assert all(torch.equal(got[k], want[k]) for k in want)
+        start = h0.clone()
+        op.backward(z, x, saved, dy, dl, h0=start, grads={"h0": start}, **kw)
+        assert torch.equal(start, want["h0"])

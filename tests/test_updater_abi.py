@@ -122,6 +122,22 @@ def test_scan_backward_arguments(lib):
     assert call(nbytes=16) == SMALL
 
 
+def test_scan_states_in_place(lib):
+    """h_last may be h0 (and dh0 dh_last or h0), but no other overlap: 3 sequences of 8 channels are 96 bytes."""
+    for shift in (-92, -32, 4, 92):
+        assert scan_forward(lib, scan_dims(), h_last=PTR + shift) == INVALID
+        assert "overlaps" in b.last_error()
+        i, g = b.gs_scan_inputs(PTR, PTR, PTR, 8, 8), b.gs_scan_grads(PTR, PTR, PTR + shift, 8, 8)
+        for h0, dhl in ((PTR, None), (None, PTR)):
+            i.h0 = h0
+            assert lib.gs_scan_backward(ctypes.byref(scan_dims()), None, ctypes.byref(i), PTR, PTR, 8, dhl,
+                                        ctypes.byref(g), PTR, 1 << 20, None) == INVALID
+            assert "overlaps" in b.last_error()
+    # the same array and neighbouring ones get as far as the workspace
+    for h_last in (PTR, PTR + 96, PTR - 96):
+        assert scan_forward(lib, scan_dims(), h_last=h_last, nbytes=8) == SMALL
+
+
 def ortho_dims(**kw):
     d = b.gs_default_ortho_dims()
     for k, v in dict(dict(rows=200, cols=300, batch=2, dtype=b.GS_F32, out_dtype=b.GS_BF16), **kw).items():
