@@ -220,6 +220,8 @@ hipError_t launch_scan_forward(const gs_scan_dims& d, const int64_t* offsets, co
 hipError_t launch_scan_backward(const gs_scan_dims& d, const int64_t* offsets, const gs_scan_inputs& in,
                                 const float* saved, const void* dy, int64_t lddy, const float* dh_last,
                                 const gs_scan_grads& out, void* ws, hipStream_t st);
+// powers of two that X and P, Q are held with; false: the coefficients let them grow beyond float16's range
+bool ortho_scales(const gs_ortho_dims& d, float* x_scale, float* p_scale);
 size_t ortho_workspace(const gs_ortho_dims& d);
 hipError_t launch_ortho(const gs_ortho_dims& d, const void* g, void* out, void* ws, hipStream_t st);
 

@@ -5,15 +5,19 @@
 //
 // All products run on k_gemm16 in float16 with float32 accumulation.  P and Q are symmetric: only tiles on and above
 // the diagonal are computed and each writes its mirror image; with few tiles and many k the sums are split along k.
-// Every singular value of X stays below 1.2 after the normalisation, so X is held as 2^12 X and P, Q as 2^13 P, 2^13 Q:
-// far from float16's overflow (|Q| <= 5) and, for the entries that matter, above its subnormals.  float16 keeps 11
-// bits; in bfloat16 the same steps lose 8 times as much.  For a float32 result each of X, P, Q is a pair hi + lo of
+// The singular values of X start in [0, 1] and the default coefficients keep them below 1.3, so X is held as 2^12 X and
+// P, Q as 2^13 P, 2^13 Q: below float16's overflow (|P| <= 1.6, |Q| <= 2.9) and, for the entries that matter, above its
+// subnormals.  Coefficients that let them grow take smaller powers of two (ortho_scales).  float16 keeps 11 bits; in
+// bfloat16 the same steps lose 8 times as much.  For a float32 result each of X, P, Q is a pair hi + lo of
 // float16 (22 bits) and a product is lo hi + hi lo + hi hi.
 //
 // Measured: 2048 x 5632 bfloat16 640 us, of each step's 147 us P 44 + 12 (its split sums), Q 25, X 64 (740 TFLOP/s on
 // 176 of 256 CUs; tiles of 192 x 256 on 242 CUs gained 1 %, the power limit lowers the clock instead).  Two matrices of
 // 1366 x 500 float32: 247 us, of each step's 49 us P 13 + 6, Q 14, X 16; these products have 11 to 24 k tiles in 72 to
 // 432 workgroups and wait for LDS and barriers (a ring of four tiles in LDS instead of two changed nothing).
+#include <algorithm>
+#include <cmath>
+
 #include "gsr_internal.hpp"
 #include "gemm16.hpp"
 
@@ -21,8 +25,10 @@ namespace gsr {
 
 namespace {
 
-constexpr float kXScale = 4096.f;     // X is stored as 2^12 X
-constexpr float kPScale = 8192.f;     // P and Q as 2^13 P, 2^13 Q
+// X is stored as x X, P and Q as p P, p Q: powers of two, so that the scaling is exact.
+struct Scales {
+    float x, p;
+};
 constexpr int kNormBlocks = 256;      // partial sums of squares per matrix
 
 template <int PL>
@@ -94,10 +100,10 @@ __global__ __launch_bounds__(256) void k_norm(const E* g, int64_t n, double* par
     if (threadIdx.x == 0) part[blockIdx.y * kNormBlocks + blockIdx.x] = red[0];
 }
 
-// X = 2^12 G / max(|G|, eps) into padded float16 planes
+// scale G / max(|G|, eps) into padded float16 planes
 template <class E, int PL>
 __global__ __launch_bounds__(256) void k_normalise(const E* g, int64_t rows, int64_t cols, const double* part,
-                                                   float eps, uint16_t* x, int64_t plane) {
+                                                   float eps, float scale, uint16_t* x, int64_t plane) {
     const int64_t c8 = (cols + 7) / 8 * 8, n = rows * c8 / 8;
     const int64_t b = blockIdx.y;
     __shared__ double red[kNormBlocks];
@@ -109,7 +115,7 @@ __global__ __launch_bounds__(256) void k_normalise(const E* g, int64_t rows, int
         __syncthreads();
     }
     const double norm = sqrt(red[0]);
-    const double inv = (double)kXScale / (norm < (double)eps ? (double)eps : norm);
+    const double inv = (double)scale / (norm < (double)eps ? (double)eps : norm);
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
         const int64_t r = i * 8 / c8, c = i * 8 - r * c8;
         const E* p = g + (b * rows + r) * cols + c;
@@ -174,7 +180,7 @@ struct EpiUpdate {
     int64_t plane, ld, batch_stride;
     Out* out;  // null: another step follows
     int M, N;  // rows, columns of the matrix
-    float a, alpha;
+    float a, alpha, inv_scale;  // X = a X + alpha acc as stored; inv_scale of it is the result
     int vec;
     __device__ __forceinline__ Pre fetch(int batch, int m, int n) const {
         Pre r;
@@ -196,7 +202,7 @@ struct EpiUpdate {
         Out* d = out + ((int64_t)batch * M + m) * N + n;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            v[q] *= 1.f / kXScale;
+            v[q] *= inv_scale;
             if (vec >= 4 && n + q * 4 + 4 <= N) {
                 if constexpr (sizeof(Out) == 4)
                     *(f32x4*)(d + q * 4) = v[q];
@@ -305,6 +311,8 @@ struct OrthoLayout {
 template <class In, class Out, int PL>
 hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* ws, hipStream_t st) {
     const OrthoLayout L(d);
+    Scales sc;
+    if (!ortho_scales(d, &sc.x, &sc.p)) return hipErrorInvalidValue;
     Carver cv{ws};
     double* part = cv.take<double>(L.B * kNormBlocks);
     uint16_t* x = cv.take<uint16_t>(L.x_plane * PL);
@@ -317,12 +325,12 @@ hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* 
     GSR_TRY(hipGetLastError());
     int64_t bx = (L.R * L.C8 / 8 + 255) / 256;
     if (bx > 2048) bx = 2048;
-    k_normalise<In, PL><<<dim3((unsigned)bx, (unsigned)L.B), 256, 0, st>>>(g, L.R, L.C, part, d.eps, x, L.x_plane);
+    k_normalise<In, PL><<<dim3((unsigned)bx, (unsigned)L.B), 256, 0, st>>>(g, L.R, L.C, part, d.eps, sc.x, x,
+                                                                              L.x_plane);
     GSR_TRY(hipGetLastError());
     const bool tall = d.rows > d.cols;
     for (int step = 0; step < d.steps; ++step) {
-        EpiSymmetric<PL> es{P, nullptr, L.p_plane, L.lo8, L.lo * L.lo8, (int)L.lo, kPScale / (kXScale * kXScale), 0.f,
-                            128};
+        EpiSymmetric<PL> es{P, nullptr, L.p_plane, L.lo8, L.lo * L.lo8, (int)L.lo, sc.p / (sc.x * sc.x), 0.f, 128};
         GemmArgs gp = make_args(L.lo, L.lo, tall ? L.R : L.C);
         gp.batch = (int)L.B;
         gp.lda = gp.ldb = L.C8;
@@ -334,7 +342,7 @@ hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* 
         } else {
             GSR_TRY((launch_symmetric<PL, true>(gp, es, sums, st)));
         }
-        EpiSymmetric<PL> eq{Q, P, L.p_plane, L.lo8, L.lo * L.lo8, (int)L.lo, d.c / kPScale, d.b, 128};
+        EpiSymmetric<PL> eq{Q, P, L.p_plane, L.lo8, L.lo * L.lo8, (int)L.lo, d.c / sc.p, d.b, 128};
         GemmArgs gq = make_args(L.lo, L.lo, L.lo);
         gq.batch = (int)L.B;
         gq.lda = gq.ldb = L.lo8;
@@ -343,7 +351,7 @@ hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* 
         GSR_TRY((launch_symmetric<PL, true>(gq, eq, sums, st)));
         const bool last = step + 1 == d.steps;
         EpiUpdate<PL, Out> eu{x, xn, L.x_plane, L.C8, L.R * L.C8, last ? (Out*)out : nullptr, (int)L.R, (int)L.C,
-                              d.a, 1.f / kPScale, vec_width(out, L.C, sizeof(Out))};
+                              d.a, 1.f / sc.p, 1.f / sc.x, vec_width(out, L.C, sizeof(Out))};
         GemmArgs gu = make_args(L.R, L.C8, L.lo);
         gu.batch = (int)L.B;
         if (tall) {  // X Q, Q symmetric
@@ -368,7 +376,7 @@ hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* 
 // ---- small matrices ------------------------------------------------------------------------------------
 
 // A matrix whose padded X and P fit in LDS takes one workgroup and one launch for all steps (12 matrices of 128 x 512:
-// 72 us, 17 launches took 123; 11 us a step, the rest for reading, norm and result).  X lies as m rows of n (m the
+// 73 us, 17 launches took 123; 11 us a step, the rest for reading, norm and result).  X lies as m rows of n (m the
 // smaller side) with n contiguous, rows of a multiple of 128 bytes (see at); P and then Q share a second buffer of the
 // same form.
 //   P: every wave takes a 32 x 64 block of X X^T and keeps it in registers;
@@ -454,7 +462,7 @@ __device__ __forceinline__ f32x4 rounded(f32x4 v) {
 // X = a X + Q X for 32 columns from c0, in place
 template <int PL>
 __device__ __forceinline__ void small_update(const SmallView<PL>& X, const SmallView<PL>& Q, int c0, int mp, float a,
-                                             int lane) {
+                                             float inv_p, int lane) {
     constexpr int kTiles = kSmallSide / 16, J = 2;
     const int row = lane & 15, col = (lane >> 4) * 4;
     f32x4 x[kTiles][J];
@@ -484,7 +492,7 @@ __device__ __forceinline__ void small_update(const SmallView<PL>& X, const Small
         if (i * 16 < mp) {
 #pragma unroll
             for (int j = 0; j < J; ++j)
-                x[i][j] = a * X.get(i * 16 + row, c0 + j * 16 + col) + x[i][j] * (1.f / kPScale);
+                x[i][j] = a * X.get(i * 16 + row, c0 + j * 16 + col) + x[i][j] * inv_p;
         }
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
@@ -498,7 +506,8 @@ struct SmallArgs {
     const void* g;
     void* out;
     int rows, cols, m, n, mp, np, steps;  // m, n: smaller and larger side; mp, np: padded
-    float a, b, c, eps;
+    float a, b, c_p, eps;  // c_p: c / p scale
+    float x_scale, to_p, inv_p, inv_x;
 };
 
 // Row and column of every NT-th four elements of a matrix with `cols` columns, without a division for each.
@@ -572,7 +581,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void k_ortho_small(const SmallArg
     // the factor as a power of two and a rest in [1/2, 1): neither over- nor underflows float32
     const double norm = sqrt(s);
     int ex;
-    const float rest = (float)frexp((double)kXScale / (norm < (double)p.eps ? (double)p.eps : norm), &ex);
+    const float rest = (float)frexp((double)p.x_scale / (norm < (double)p.eps ? (double)p.eps : norm), &ex);
     const bool tall = p.rows > p.cols;
     Walk at(p.cols, tid * 4, NT * 4);
     auto place = [&](int i, f32x4 v) {
@@ -632,8 +641,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void k_ortho_small(const SmallArg
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    pv[i][j] = rounded<PL>(acc[i][j] * (kPScale / (kXScale * kXScale)));
+                for (int j = 0; j < 4; ++j) pv[i][j] = rounded<PL>(acc[i][j] * p.to_p);
             keep();
         }
         __syncthreads();
@@ -642,12 +650,12 @@ __global__ __launch_bounds__(kSmallWaves * 64) void k_ortho_small(const SmallArg
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) pv[i][j] = p.b * pv[i][j] + (p.c / kPScale) * acc[i][j];
+                for (int j = 0; j < 4; ++j) pv[i][j] = p.b * pv[i][j] + p.c_p * acc[i][j];
         }
         __syncthreads();
         if (mine) keep();
         __syncthreads();
-        for (int t = wave; t < p.np / 32; t += kSmallWaves) small_update<PL>(X, P, t * 32, p.mp, p.a, lane);
+        for (int t = wave; t < p.np / 32; t += kSmallWaves) small_update<PL>(X, P, t * 32, p.mp, p.a, p.inv_p, lane);
         __syncthreads();
     }
     typedef Out Out4 __attribute__((ext_vector_type(4)));
@@ -669,7 +677,7 @@ __global__ __launch_bounds__(kSmallWaves * 64) void k_ortho_small(const SmallArg
         to.next();
         Out4 o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = (Out)(v[e] * (1.f / kXScale));
+        for (int e = 0; e < 4; ++e) o[e] = (Out)(v[e] * p.inv_x);
         if (vec_out && i + 4 <= n) {
             *(Out4*)(out + i) = o;
         } else {
@@ -696,7 +704,10 @@ hipError_t ortho_small(const gs_ortho_dims& d, const void* g, void* out, hipStre
     p.rows = (int)d.rows, p.cols = (int)d.cols;
     p.m = d.rows < d.cols ? p.rows : p.cols, p.n = d.rows < d.cols ? p.cols : p.rows;
     p.mp = (int)round_up(p.m, 64), p.np = (int)round_up(p.n, 64);
-    p.steps = d.steps, p.a = d.a, p.b = d.b, p.c = d.c, p.eps = d.eps;
+    p.steps = d.steps, p.a = d.a, p.b = d.b, p.eps = d.eps;
+    Scales sc;
+    if (!ortho_scales(d, &sc.x, &sc.p)) return hipErrorInvalidValue;
+    p.x_scale = sc.x, p.to_p = sc.p / (sc.x * sc.x), p.c_p = d.c / sc.p, p.inv_p = 1.f / sc.p, p.inv_x = 1.f / sc.x;
     GSR_TRY(hipFuncSetAttribute((const void*)k_ortho_small<In, Out, PL>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                 kSmallLds));
     k_ortho_small<In, Out, PL><<<dim3((unsigned)d.batch), kSmallWaves * 64, bytes, st>>>(p);
@@ -709,6 +720,44 @@ hipError_t ortho_any(const gs_ortho_dims& d, const void* g, void* out, char* ws,
 }
 
 }  // namespace
+
+// Follows the interval [0, 1] of the singular values through the steps: P reaches s^2, Q the largest
+// |b s^2 + c s^4| and X the largest |a s + b s^3 + c s^5| for s in it (at its ends or where the derivative is zero), and
+// no entry of a matrix exceeds its largest singular value.  2 % a step cover the float16 roundings.  The scales are the
+// largest powers of two, up to 2^12 and 2^13, that keep these below float16's 65504.  Below 2^8 the entries that matter
+// come near float16's subnormals: false.
+bool ortho_scales(const gs_ortho_dims& d, float* x_scale, float* p_scale) {
+    const double a = d.a, b = d.b, c = d.c, slack = 1.02, most = 65504.0, least_scale = 256.0;
+    double s = slack, top_x = s, top_p = 0.0;
+    for (int step = 0; step < d.steps; ++step) {
+        const double s2 = s * s;
+        double q = std::fabs(b * s2 + c * s2 * s2), next = std::fabs(s * (a + b * s2 + c * s2 * s2));
+        if (c != 0.0) {
+            const double at = -b / (2.0 * c);
+            if (at > 0.0 && at < s2) q = std::max(q, std::fabs(b * at + c * at * at));
+        }
+        // a + 3 b t + 5 c t^2 = 0 in t = s^2
+        double roots[2] = {-1.0, -1.0};
+        const double disc = 9.0 * b * b - 20.0 * a * c;
+        if (c != 0.0 && disc >= 0.0) {
+            roots[0] = (-3.0 * b + std::sqrt(disc)) / (10.0 * c);
+            roots[1] = (-3.0 * b - std::sqrt(disc)) / (10.0 * c);
+        } else if (c == 0.0 && b != 0.0) {
+            roots[0] = -a / (3.0 * b);
+        }
+        for (double t : roots)
+            if (t > 0.0 && t < s2) next = std::max(next, std::fabs(std::sqrt(t) * (a + b * t + c * t * t)));
+        top_p = std::max(top_p, std::max(s2, q * slack));
+        s = next * slack;
+        top_x = std::max(top_x, s);
+        if (!(top_p * least_scale < most) || !(top_x * least_scale < most)) return false;
+    }
+    *x_scale = 4096.f;
+    *p_scale = 8192.f;
+    while (top_x * *x_scale >= most) *x_scale *= 0.5f;
+    while (top_p * *p_scale >= most) *p_scale *= 0.5f;
+    return true;
+}
 
 size_t ortho_workspace(const gs_ortho_dims& d) {
     if (small_lds(d)) return 0;

@@ -1,4 +1,6 @@
 // updater_api.hip -- the ABI calls of the learned updater's operators: argument checks and launches.
+#include <cmath>
+
 #include "gsr_internal.hpp"
 
 using namespace gsr;
@@ -124,6 +126,12 @@ gs_status check_ortho(const char* call, const gs_ortho_dims* d) {
         return fail(GS_ERR_UNSUPPORTED, "%s: rows %lld, cols %lld, batch %d, steps %d exceed the limits", call,
                     (long long)d->rows, (long long)d->cols, d->batch, d->steps);
     if (!(d->eps > 0.f)) return fail(GS_ERR_INVALID_ARGUMENT, "%s: eps must be positive", call);
+    if (!std::isfinite(d->a) || !std::isfinite(d->b) || !std::isfinite(d->c))
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: a coefficient is not finite", call);
+    float xs, ps;
+    if (!ortho_scales(*d, &xs, &ps))
+        return fail(GS_ERR_UNSUPPORTED, "%s: %d steps with coefficients %g, %g, %g leave float16's range", call,
+                    d->steps, (double)d->a, (double)d->b, (double)d->c);
     return GS_OK;
 }
 

@@ -635,3 +635,30 @@ def test_scan_in_place(c, offsets, dtype):
         start = h0.clone()
         op.backward(z, x, saved, dy, dl, h0=start, grads={"h0": start}, **kw)
         assert torch.equal(start, want["h0"])
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 40), (2, 33, 70), (1, 70, 33), (2, 128, 192), (1, 1, 2100), (1, 300, 511)],
+                         ids=str)
+@pytest.mark.parametrize("dout", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("coef, steps", [((3.0, -0.1, 0.0), 2), ((8.2872, -23.5959, 17.3004), 1), ((15.0, 0.0, 0.0), 2)],
+                         ids=str)
+def test_ortho_coefficients_near_the_limit(coef, steps, dout, shape):
+    """Coefficients that take P, Q or X past what the default scales hold, in the one-workgroup and the tiled form.
+    Error of a step, first order, u = 2^-11 (bfloat16 result) or 2^-20 (pairs): what came in times |p'(s)|, and every
+    factor of every term rounded once -- X in a s, X X X P and twice Q in b s^3, five X, two P and twice Q in c s^5 --
+    and the result; summed over the singular values, plus the result's own rounding."""
+    g = randn(gen(sum(shape)), *shape, dtype=torch.float32)
+    out = gsr().Orthogonalizer(*shape, torch.float32, dout, steps=steps, coefficients=coef).run(g)
+    a, b_, c = coef
+    u = 2.0 ** -11 if dout == torch.bfloat16 else 2.0 ** -20
+    for got, m in zip(out, g):
+        s = torch.linalg.svdvals(m.double().cpu())
+        s = s / s.norm()
+        e = u * s
+        for _ in range(steps):
+            slope = (a + 3 * b_ * s ** 2 + 5 * c * s ** 4).abs()
+            own = abs(a) * s + 6 * abs(b_) * s ** 3 + 9 * abs(c) * s ** 5
+            s = a * s + b_ * s ** 3 + c * s ** 5
+            e = slope * e + u * (own + s.abs())
+        tol = (e.norm() / s.norm()).item() + (o.UNIT[dout] if dout == torch.bfloat16 else 0.0)
+        o.check(got, o.newton_schulz(m, steps, coef), tol, "out")

@@ -157,6 +157,25 @@ def test_ortho_dims(lib, kw, status):
     assert lib.gs_orthogonalize(ctypes.byref(d), PTR, PTR, PTR, 1 << 40, None) == status
 
 
+@pytest.mark.parametrize("coef, steps, status", [
+    ((1.5, -0.5, 0.0), 64, b.GS_OK), ((3.4445, -4.7750, 2.0315), 64, b.GS_OK), ((1.875, -1.25, 0.375), 64, b.GS_OK),
+    ((3.0, -0.1, 0.0), 2, b.GS_OK),                   # s reaches 6.3, s^2 before the last step 8.4
+    ((8.2872, -23.5959, 17.3004), 1, b.GS_OK),        # |b s^2 + c s^4| reaches 8.05
+    ((8.2872, -23.5959, 17.3004), 5, UNSUP),          # s reaches 2, then 370
+    ((15.0, 0.0, 0.0), 2, b.GS_OK), ((15.0, 0.0, 0.0), 3, UNSUP),  # s = 15, 225, 3375
+    ((0.0, 0.0, 300.0), 1, UNSUP), ((1.0, 300.0, 0.0), 1, UNSUP), ((0.0, 0.0, 0.0), 3, b.GS_OK),
+    ((float("nan"), 0.0, 0.0), 1, INVALID), ((1.0, float("inf"), 0.0), 1, INVALID),
+    ((1.0, 0.0, float("-inf")), 1, INVALID)])
+@pytest.mark.parametrize("shape", [(64, 128), (200, 300)], ids=str)
+def test_ortho_coefficients(lib, shape, coef, steps, status):
+    """Accepted where X, P and Q stay in range, refused before anything is launched otherwise."""
+    d = ortho_dims(rows=shape[0], cols=shape[1], a=coef[0], b=coef[1], c=coef[2], steps=steps)
+    out = ctypes.c_size_t(0)
+    assert lib.gs_ortho_size(ctypes.byref(d), ctypes.byref(out)) == status
+    if status != b.GS_OK:
+        assert lib.gs_orthogonalize(ctypes.byref(d), PTR, PTR, PTR, 1 << 40, None) == status
+
+
 def test_ortho_arguments(lib):
     d = ortho_dims()
     assert lib.gs_orthogonalize(ctypes.byref(d), None, PTR, PTR, 1 << 30, None) == INVALID
