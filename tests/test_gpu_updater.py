@@ -662,3 +662,27 @@ def test_ortho_coefficients_near_the_limit(coef, steps, dout, shape):
             e = slope * e + u * (own + s.abs())
         tol = (e.norm() / s.norm()).item() + (o.UNIT[dout] if dout == torch.bfloat16 else 0.0)
         o.check(got, o.newton_schulz(m, steps, coef), tol, "out")
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("rows", [50, 800])
+def test_gelu_tail(rows, dtype):
+    """One hidden unit with u = 1 and dy = 1, element by element into the far tail: y and du are g Phi(g), dg is
+    Phi(g) + g phi(g) (relative to its two terms), each rounded to the type once.  Before that, float32 loses g^2 u to
+    the exponential's argument and a dozen u to the rest; for the 16-bit types Phi is good to 1e-5.  Results below the
+    type's normal numbers are good to half its least one."""
+    g = torch.linspace(-12, 8, rows, device="cuda").to(dtype)
+    one = torch.ones(rows, 1, device="cuda", dtype=dtype)
+    x = torch.cat([g[:, None], one], dim=1)
+    wg, wu = (torch.tensor([v], device="cuda", dtype=dtype) for v in ([1.0, 0.0], [0.0, 1.0]))
+    block = gsr().GatedFFN(wg, wu, one[:1], activation="gelu")
+    y, saved = block.forward(x, save=True)
+    dx = block.backward(x, saved, one)["x"].double()
+    g = g.double()
+    cdf, gpdf = torch.special.erfc(-g / math.sqrt(2)) / 2, g * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi)
+    rel = o.UNIT[dtype] + (1e-5 if dtype != torch.float32 else (12 + 1.5 * g * g) * o.UNIT[dtype])
+    least = torch.finfo(dtype).smallest_normal * o.UNIT[dtype]
+    for got, want, scale in ((y[:, 0].double(), g * cdf, g * cdf), (dx[:, 1], g * cdf, g * cdf),
+                             (dx[:, 0], cdf + gpdf, cdf + gpdf.abs())):
+        worst = (got - want).abs() / (rel * scale.abs() + least)
+        assert worst.max() <= 1.0, (worst.max(), g[worst.argmax()])
