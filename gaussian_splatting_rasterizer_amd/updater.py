@@ -44,8 +44,11 @@ def _exact(t, name, shape, dtype, device):
 
 class _Op:
     """A device, and scratch memory that grows when a call needs more (released in the order of the streams that used
-    it).  A captured graph keeps using the scratch memory it was captured with: an object that was captured makes no
-    larger call afterwards."""
+    it).  A captured graph goes on using the scratch memory it was captured with: the object keeps that memory as long
+    as it lives, so it has to outlive the graph."""
+
+    _captured = False  # a captured graph uses the workspace
+    _kept = ()         # earlier workspaces that captured graphs use
 
     def __init__(self, device):
         import torch
@@ -61,10 +64,15 @@ class _Op:
 
     def _scratch(self, nbytes, stream):
         if self.workspace is None or self.workspace.numel() < nbytes:
+            if self._captured:
+                self._kept = (*self._kept, self.workspace)
+                self._captured = False
             self.workspace = self.torch.empty(max(int(nbytes), 256), dtype=self.torch.uint8, device=self.device)
             self._home = stream.cuda_stream
         elif stream.cuda_stream != self._home:
             self.workspace.record_stream(stream)
+        if self.torch.cuda.is_current_stream_capturing():
+            self._captured = True
         return self.workspace
 
     def _on(self, stream, call, *args):

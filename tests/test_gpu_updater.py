@@ -686,3 +686,36 @@ def test_gelu_tail(rows, dtype):
                              (dx[:, 0], cdf + gpdf, cdf + gpdf.abs())):
         worst = (got - want).abs() / (rel * scale.abs() + least)
         assert worst.max() <= 1.0, (worst.max(), g[worst.argmax()])
+
+
+def test_larger_call_after_a_capture():
+    """The graph's scratch memory stays its own: a replay after a larger eager call gives the captured results and
+    writes into nothing that was allocated meanwhile."""
+    x, wg, wu, wd, dy = ffn_inputs(100, 40, 72, 48, torch.bfloat16, seed=50)
+    block = gsr().GatedFFN(wg, wu, wd)
+
+    def run():
+        y, saved = block.forward(x, save=True)
+        return [y, *block.backward(x, saved, dy).values()]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = run()
+    small = block.workspace.numel()
+    big, *_ = ffn_inputs(5000, 40, 72, 48, torch.bfloat16, seed=51)
+    want_big = block.forward(big)
+    assert block.workspace.numel() > small
+    filled = [torch.full((small,), 77, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    for i in range(3):
+        x.copy_(randn(gen(52 + i), 100, 40, dtype=torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        assert all(torch.equal(a, w) for a, w in zip(got, run())), i
+        assert all((f == 77).all() for f in filled) and torch.equal(block.forward(big), want_big)
