@@ -4,7 +4,9 @@ update to update) and the orthogonalisation of a weight's update.
 
 Each class checks its tensors, owns the workspace its calls need (grown when a
 call needs more) and runs on the current stream or the one given; like a
-Rasterizer, an object is used from one thread and one stream at a time.  The
+Rasterizer, an object is used from one thread and one stream at a time.  With a
+stream given, the caller orders it with the current one (wait_stream, both
+ways); tensors of either may be dropped as soon as the call has returned.  The
 backward passes are explicit calls, as in Rasterizer.backward.
 """
 from __future__ import annotations
@@ -49,6 +51,7 @@ class _Op:
 
     _captured = False  # a captured graph uses the workspace
     _kept = ()         # earlier workspaces that captured graphs use
+    _held = ()         # tensors that every call uses beside its arguments
 
     def __init__(self, device):
         import torch
@@ -81,8 +84,26 @@ class _Op:
         current = t.cuda.current_stream(self.device)
         if (stream is None or stream == current) and t.cuda.current_device() == self.device.index:
             return call(current, *args)
-        with t.cuda.stream(current if stream is None else stream) as _, t.cuda.device(self.device):
-            return call(current if stream is None else stream, *args)
+        if stream is None or stream == current:
+            with t.cuda.stream(current), t.cuda.device(self.device):
+                return call(current, *args)
+        with t.cuda.stream(stream), t.cuda.device(self.device):
+            out = call(stream, *args)
+        # the allocator reuses a tensor in the order of its own stream: tell it of the other one
+        for v in self._tensors(args, self._held):
+            v.record_stream(stream)
+        for v in self._tensors(out):
+            v.record_stream(current)
+        return out
+
+    def _tensors(self, *values):
+        for v in values:
+            if isinstance(v, self.torch.Tensor):
+                yield v
+            elif isinstance(v, (tuple, list)):
+                yield from self._tensors(*v)
+            elif isinstance(v, dict):
+                yield from self._tensors(*v.values())
 
 
 class GatedFFN(_Op):
@@ -106,6 +127,7 @@ class GatedFFN(_Op):
         self.w_gate = _exact(w_gate, "w_gate", (self.d_hidden, self.d_in), self.dtype, self.device)
         self.w_up = _exact(w_up, "w_up", (self.d_hidden, self.d_in), self.dtype, self.device)
         self.w_down = _exact(w_down, "w_down", (self.d_out, self.d_hidden), self.dtype, self.device)
+        self._held = (self.w_gate, self.w_up, self.w_down)
         self._sizes = {}
 
     @property

@@ -1,4 +1,5 @@
 """What the updater's Python objects hold on to, with stand-ins for the GPU's streams and allocator (no GPU needed)."""
+import contextlib
 import types
 import weakref
 
@@ -49,3 +50,46 @@ def test_other_scratch_memory_is_given_back():
     second = weakref.ref(op._scratch(9000, stream))
     op._scratch(20000, stream)
     assert second() is None and captured() is not None
+
+
+class Recorded:
+    """A tensor that notes the streams it was recorded on."""
+
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+def stream_object(current):
+    op = updater._Op.__new__(updater._Op)
+    op.device = types.SimpleNamespace(index=0)
+    op.torch = types.SimpleNamespace(
+        Tensor=Recorded,
+        cuda=types.SimpleNamespace(current_stream=lambda device: current, current_device=lambda: 0,
+                                   stream=lambda s: contextlib.nullcontext(),
+                                   device=lambda d: contextlib.nullcontext()))
+    return op
+
+
+def test_tensors_of_another_stream_are_recorded():
+    """Given a stream, the arguments' and the weights' memory must not be reused before its work is done, nor the
+    results' before the current stream's."""
+    here, side = Stream(1), Stream(2)
+    op = stream_object(here)
+    x, grad, weight, y, dx = (Recorded() for _ in range(5))
+    op._held = (weight,)
+    out = op._on(side, lambda stream, *a: (y, {"x": dx}), x, {"x": grad, "w": None}, True, None)
+    assert out == (y, {"x": dx})
+    assert all(t.streams == [side] for t in (x, grad, weight))
+    assert y.streams == [here] and dx.streams == [here]
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_nothing_is_recorded_on_the_current_stream(given):
+    here = Stream(1)
+    op = stream_object(here)
+    x, y = Recorded(), Recorded()
+    assert op._on(here if given else None, lambda stream, *a: y, x) is y
+    assert x.streams == [] and y.streams == []
