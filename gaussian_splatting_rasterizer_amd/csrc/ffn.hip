@@ -14,9 +14,11 @@
 // zero-padded layout in the workspace (k_pack); other operands are read in place.
 //
 // Roundings of the 16-bit types: the matrix instructions take 16-bit operands, so h, dg and du are rounded to the type
-// once before their products, and g and u once where they are kept for the backward pass (kept in float32 they would
-// add 4 GB of traffic, 0.8 ms, to the 2.8 ms of 131072 rows of 512 x 2048 x 512).  With the result's own rounding y and
-// dWd carry two roundings, dx, dWg and dWu four.  Everything else is float32.
+// once before their products (for float16 they have to stay within its range).  g and u are kept for the backward pass
+// in float32 for float16, whose range they may leave (h = act(g) u of a closed gate is small at any g), and rounded once
+// for bfloat16, which has float32's range (in float32 they would add 4 GB of traffic, 0.8 ms, to the 2.8 ms of 131072
+// rows of 512 x 2048 x 512).  With the result's own rounding y and dWd carry two roundings, dx, dWg and dWu two in
+// float16 and four in bfloat16.  Everything else is float32.
 //
 // Measured, bfloat16 SiLU, 131072 rows of 512 x 2048 x 512, forward and backward 2.77 ms (890 TFLOP/s; the power limit
 // lowers the shader clock to 1.9 GHz); in a kernel trace, us:
@@ -119,14 +121,14 @@ struct EpiGate {
     static constexpr int kAhead = 0;
     OperandElem<F>* h;
     int64_t h_plane;
-    typename F::Elem* gu;  // [M][2 F8] or null
+    typename F::Keep::Elem* gu;  // [M][2 F8] or null
     int64_t f8;
     int M;
     __device__ __forceinline__ void row(int m, int n, f32x4 g0, f32x4 g1, f32x4 u0, f32x4 u1) const {
         if (m >= M || n >= f8) return;
         if (gu) {
-            F::put8(gu + (int64_t)m * 2 * f8 + n, g0, g1);
-            F::put8(gu + (int64_t)m * 2 * f8 + f8 + n, u0, u1);
+            F::Keep::put8(gu + (int64_t)m * 2 * f8 + n, g0, g1);
+            F::Keep::put8(gu + (int64_t)m * 2 * f8 + f8 + n, u0, u1);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -169,14 +171,15 @@ struct EpiGateFew {
 template <class F, int ACT>
 struct EpiGateGrad {
     static constexpr bool kDual = false, kSymmetric = false;
-    static constexpr int kAhead = sizeof(typename F::Elem) == 2 ? 3 : 1;
-    const typename F::Elem* gu;
+    using K = typename F::Keep;
+    static constexpr int kAhead = sizeof(typename K::Elem) == 2 ? 3 : 1;
+    const typename K::Elem* gu;
     OperandElem<F>* dgu;  // [M][2 F8]
     int64_t plane;
     int64_t f8;
     int M;
     struct Pre {
-        typename F::Raw8 g[2], u[2];
+        typename K::Raw8 g[2], u[2];
     };
     __device__ __forceinline__ Pre fetch(int, int m, int n) const {
         Pre r;
@@ -184,8 +187,8 @@ struct EpiGateGrad {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             if (m < M && n + h * 8 < f8) {
-                r.g[h] = *(const typename F::Raw8*)(gu + at + h * 8);
-                r.u[h] = *(const typename F::Raw8*)(gu + at + f8 + h * 8);
+                r.g[h] = *(const typename K::Raw8*)(gu + at + h * 8);
+                r.u[h] = *(const typename K::Raw8*)(gu + at + f8 + h * 8);
             }
         return r;
     }
@@ -197,7 +200,7 @@ struct EpiGateGrad {
             f32x4 dg[2], du[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const f32x4 g = F::unpack(pre.g[h], q), u = F::unpack(pre.u[h], q), d = dh[h * 2 + q];
+                const f32x4 g = K::unpack(pre.g[h], q), u = K::unpack(pre.u[h], q), d = dh[h * 2 + q];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float a, da;
@@ -478,7 +481,7 @@ struct Layout {
     int64_t M, D, H, O, D8, H8, O8;
     explicit Layout(const gs_ffn_dims& d)
         : M(d.rows), D(d.d_in), H(d.d_hidden), O(d.d_out), D8(round8(D)), H8(round8(H)), O8(round8(O)) {}
-    int64_t saved_gu_bytes() const { return round_up(M * 2 * H8 * (int64_t)sizeof(typename F::Elem), kAlign); }
+    int64_t saved_gu_bytes() const { return round_up(M * 2 * H8 * (int64_t)sizeof(typename F::Keep::Elem), kAlign); }
     int64_t h_elems() const { return M * H8 * F::kPlanes; }
     int64_t h_bytes() const { return round_up(h_elems() * (int64_t)sizeof(OperandElem<F>), kAlign); }
 };
@@ -543,7 +546,7 @@ hipError_t forward_few(const gs_ffn_dims& d, const void* x, int64_t ldx, const g
     Carver cv{ws};
     EpiGateFew<F, ACT> e1{{nullptr, L.M * L.H8, nullptr, L.H8, (int)L.M}, nullptr};
     if (saved) {
-        e1.all.gu = (E*)saved;
+        e1.all.gu = (typename F::Keep::Elem*)saved;
         e1.all.h = (OperandElem<F>*)((char*)saved + L.saved_gu_bytes());
     }
     // the 16-bit h that is kept is the next product's input too
@@ -580,9 +583,9 @@ hipError_t forward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const 
     const Operand od = pk.add<F>(cv, w.down, L.O, L.H, L.H);
     GSR_TRY(pk.launch<F>(st));
     OperandElem<F>* h;
-    E* gu = nullptr;
+    typename F::Keep::Elem* gu = nullptr;
     if (saved) {
-        gu = (E*)saved;
+        gu = (typename F::Keep::Elem*)saved;
         h = (OperandElem<F>*)((char*)saved + L.saved_gu_bytes());
     } else {
         h = cv.take<OperandElem<F>>(L.h_elems());
@@ -633,7 +636,7 @@ hipError_t backward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const
     float* part = cv.take<float>(part_elems<F>(L));
     const int64_t plane = L.M * 2 * L.H8;
     OperandElem<F>* dgu = cv.take<OperandElem<F>>(plane * F::kPlanes);
-    const E* gu = (const E*)saved;
+    const auto* gu = (const typename F::Keep::Elem*)saved;
     const OperandElem<F>* h = (const OperandElem<F>*)((const char*)saved + L.saved_gu_bytes());
     const int64_t h_plane = L.M * L.H8;
     Packer pk;
@@ -707,6 +710,7 @@ bool split_f32(const gs_ffn_dims& d) {
 void ffn_sizes(const gs_ffn_dims& d, size_t* saved, size_t* fwd, size_t* bwd) {
     if (d.dtype == GS_F32 && split_f32(d)) return sizes_impl<FmtF32Split>(d, saved, fwd, bwd);
     if (d.dtype == GS_F32) return sizes_impl<FmtF32>(d, saved, fwd, bwd);
+    if (d.dtype == GS_F16) return sizes_impl<FmtF16>(d, saved, fwd, bwd);
     return sizes_impl<FmtBf16>(d, saved, fwd, bwd);
 }
 

@@ -410,9 +410,11 @@ __device__ __forceinline__ void split3(float v, uint16_t& hi, uint16_t& mid, uin
 }
 
 // Element formats of the block: what a stored 16-bit matrix operand and a value array look like for each type.
+struct F32Values;
 struct FmtBf16 {
     using Mma = __bf16;
-    using Elem = uint16_t;  // value arrays (inputs, outputs, saved pre-activations)
+    using Elem = uint16_t;   // value arrays (inputs, outputs)
+    using Keep = FmtBf16;    // saved pre-activations
     static constexpr int kPlanes = 1;
     static __device__ __forceinline__ f32x4 get(const Elem* p) { return from16<__bf16>(*(const u16x4*)p); }
     static __device__ __forceinline__ void put(Elem* p, f32x4 v) { *(u16x4*)p = to16<__bf16>(v); }
@@ -427,6 +429,7 @@ struct FmtBf16 {
 struct FmtF16 {
     using Mma = _Float16;
     using Elem = uint16_t;
+    using Keep = F32Values;  // float16 has no room for the pre-activation of an open or a closed gate beyond 65504
     static constexpr int kPlanes = 1;
     static __device__ __forceinline__ f32x4 get(const Elem* p) { return from16<_Float16>(*(const u16x4*)p); }
     static __device__ __forceinline__ void put(Elem* p, f32x4 v) { *(u16x4*)p = to16<_Float16>(v); }
@@ -440,6 +443,7 @@ struct FmtF16 {
 };
 struct F32Values {
     using Elem = float;
+    using Keep = F32Values;
     static __device__ __forceinline__ f32x4 get(const Elem* p) { return *(const f32x4*)p; }
     static __device__ __forceinline__ void put(Elem* p, f32x4 v) { *(f32x4*)p = v; }
     struct Raw8 {

@@ -336,11 +336,15 @@ typedef struct {
     void* up;
     void* down;
 } gs_ffn_grads;
-/* Bytes of the saved activations and of the two calls' workspaces (any pointer may be null). */
+/* The 16-bit types round h once, as the operand of y's product, and dh's results dg and du of the two projections
+ * likewise; bfloat16 also g and u where they are kept for the backward pass.  In float16 |h|, |dg| and |du| above
+ * 65504 therefore become infinite and values below 2^-24 vanish, as between float16 layers: scale the loss.
+ *
+ * Bytes of the saved activations and of the two calls' workspaces (any pointer may be null). */
 GSR_API gs_status gs_ffn_sizes(const gs_ffn_dims* dims, size_t* saved_bytes, size_t* forward_bytes,
                                size_t* backward_bytes);
-/* Forward pass.  saved (may be null: inference) receives the pre-activations and h in the block's type, which
- * gs_ffn_backward reads.  saved and workspace are 256-byte aligned.  Errors: GS_ERR_INVALID_ARGUMENT (null or
+/* Forward pass.  saved (may be null: inference) receives the pre-activations and h, which gs_ffn_backward
+ * reads.  saved and workspace are 256-byte aligned.  Errors: GS_ERR_INVALID_ARGUMENT (null or
  * misaligned arrays, bad sizes or enums), GS_ERR_UNSUPPORTED (beyond the limits above),
  * GS_ERR_WORKSPACE_TOO_SMALL, GS_ERR_HIP; nothing is launched for the first three. */
 GSR_API gs_status gs_ffn_forward(const gs_ffn_dims* dims, const void* x, int64_t ld_x, const gs_ffn_weights* weights,

@@ -719,3 +719,27 @@ def test_larger_call_after_a_capture():
         got = [t.clone() for t in held]
         assert all(torch.equal(a, w) for a, w in zip(got, run())), i
         assert all((f == 77).all() for f in filled) and torch.equal(block.forward(big), want_big)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("rows", [5, 200])
+def test_float16_gates_beyond_the_range(rows, act):
+    """Row 0 drives half of the gates to 120000 and closes the others at -120000, row 1 drives u to 120000: beyond
+    float16's 65504 while h, y and every gradient are within it.  Tolerances as everywhere."""
+    d, f, out = 24, 16, 8
+    x, wg, wu, wd, dy = ffn_inputs(rows, d, f, out, torch.float16, seed=60)
+    x[:2], x[:, :2] = 0, 0
+    x[0, 0] = x[1, 1] = 300
+    wg[0::2, 0], wg[1::2, 0], wu[:, 0] = 400, -400, 0.25 / 300
+    wg[:, 1], wu[:, 1] = -1 / 300, 400
+    dy[:2] *= 2.0 ** -12
+    block = gsr().GatedFFN(wg, wu, wd, activation=act)
+    y, saved = block.forward(x, save=True)
+    got = block.backward(x, saved, dy)
+    ref = o.ffn(x, wg, wu, wd, act, dy)
+    for k in (slice(0, 1), slice(1, 2), slice(2, None)):
+        o.check(y[k], ref["y"][k], ffn_tol(torch.float16, 2, 0), "y")
+        o.check(got["x"][k], ref["x"][k], ffn_tol(torch.float16, 4, 0), "x")
+    o.check(got["w_down"], ref["w_down"], ffn_tol(torch.float16, 2, 0), "w_down")
+    for name in ("w_gate", "w_up"):
+        o.check(got[name], ref[name], ffn_tol(torch.float16, 4, 0), name)
