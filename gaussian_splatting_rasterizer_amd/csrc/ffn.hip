@@ -306,7 +306,7 @@ __global__ __launch_bounds__(256) void k_reduce(const float* part, int splits, i
 // ---- few rows ------------------------------------------------------------------------------------------
 
 // At most 64 rows: the weights are read once, straight into the matrix instructions' operands, and that is all the
-// work there is.  A workgroup takes 16 columns (of both projections) and splits k over its waves; the partial sums
+// work there is.  A workgroup takes 16 or 8 columns (of both projections) and splits k over its waves; the partial sums
 // meet in LDS.  Every wave's loads are independent, so the whole weight matrix is in flight at once.  One row of 1024 x
 // 4096 x 1024 bfloat16: 6.2 + 6.3 us for 16.8 and 8.4 MB, half of it the launch and the first load's latency.  48 rows
 // of 1024 x 2816 x 1024: 9.0 + 12.8 us; the second is bound by its rows, which every workgroup reads in full (393 KB a
@@ -359,7 +359,7 @@ struct FewArgs {
     const void* w;
     const void* w2;  // the second projection of a dual product
     int M, N, K;
-    int cols;    // columns of a workgroup: 16, or 8 where 16 would leave CUs without one
+    int cols;    // columns of a workgroup: 16 or 8
     int64_t ldx, ldw;
 };
 
@@ -520,7 +520,19 @@ struct Packer {
 
 template <class F, int NW, bool WIDE, class Epi>
 hipError_t launch_few(FewArgs p, const Epi& epi, hipStream_t st) {
-    p.cols = p.N > 8 * 128 ? 16 : 8;
+    // Eight columns a workgroup as long as that makes at most one workgroup a CU, else 16.  The whole forward pass in us
+    // with 8 and with 16 columns in the product named, bfloat16, the other product small and the same:
+    //   projections, 1024 wide         1 row          16 rows        48 rows
+    //     1024 columns             10.2 / 10.8    11.5 / 12.1    15.9 / 16.5
+    //     2048 columns             10.5 / 11.1    12.6 / 13.1    18.4 / 18.8
+    //     2816 columns             12.6 / 11.2    15.8 / 13.8    24.4 / 20.4
+    //   down product, 2816 wide
+    //     1024 columns              9.7 / 10.4    11.8 / 12.4    17.8 / 18.5
+    //     2048 columns              9.9 / 10.6    12.0 / 12.6    18.2 / 18.8
+    //     2816 columns             12.3 / 10.6    16.2 / 12.7    29.0 / 18.9
+    // (float32 alike: one row of 2816 to 2048 15.9 / 16.9, to 2816 22.0 / 18.0.)
+    constexpr int kCus = 256;
+    p.cols = p.N <= 8 * kCus ? 8 : 16;
     const dim3 gd((unsigned)((p.N + p.cols - 1) / p.cols)), bd(NW * 64);
     if (p.M <= 16)
         k_few_rows<F, 1, NW, WIDE, Epi><<<gd, bd, 0, st>>>(p, epi);

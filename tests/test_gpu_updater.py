@@ -743,3 +743,12 @@ def test_float16_gates_beyond_the_range(rows, act):
     o.check(got["w_down"], ref["w_down"], ffn_tol(torch.float16, 2, 0), "w_down")
     for name in ("w_gate", "w_up"):
         o.check(got[name], ref[name], ffn_tol(torch.float16, 4, 0), name)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("shape", [(3, 40, 1500, 2050), (20, 72, 2048, 1100), (50, 33, 2056, 1999)], ids=str)
+def test_ffn_few_rows_wide(shape, dtype):
+    """Few rows on both sides of 2048 columns, where the workgroups' width changes."""
+    x, wg, wu, wd, _ = ffn_inputs(*shape, dtype, seed=70)
+    y = gsr().GatedFFN(wg, wu, wd).forward(x)
+    o.check(y, o.ffn(x, wg, wu, wd, "silu"), ffn_tol(dtype, 2, max(shape)), "y")
