@@ -14,11 +14,11 @@
 // zero-padded layout in the workspace (k_pack); other operands are read in place.
 //
 // Roundings of the 16-bit types: the matrix instructions take 16-bit operands, so h, dg and du are rounded to the type
-// once before their products (for float16 they have to stay within its range).  g and u are kept for the backward pass
-// in float32 for float16, whose range they may leave (h = act(g) u of a closed gate is small at any g), and rounded once
-// for bfloat16, which has float32's range (in float32 they would add 4 GB of traffic, 0.8 ms, to the 2.8 ms of 131072
-// rows of 512 x 2048 x 512).  With the result's own rounding y and dWd carry two roundings, dx, dWg and dWu two in
-// float16 and four in bfloat16.  Everything else is float32.
+// once before their products (for float16 they have to stay within its range).  With the result's own rounding, every
+// result carries two.  g and u are kept for the backward pass with 4 (bfloat16) or 5 (float16) bits more than the type
+// has, and with float32's range (KeepHigh): kept in the type they doubled the variance of dx, dWg and dWu, and in
+// float16 the infinite g of a closed gate made NaN of its gradients.  131072 rows of 512 x 2048 x 512 bfloat16: 3.00 ms,
+// 2.82 with g and u in the type, 3.11 with 24 bits of each.  Everything else is float32.
 //
 // Measured, bfloat16 SiLU, 131072 rows of 512 x 2048 x 512, forward and backward 2.77 ms (890 TFLOP/s; the power limit
 // lowers the shader clock to 1.9 GHz); in a kernel trace, us:
@@ -121,15 +121,12 @@ struct EpiGate {
     static constexpr int kAhead = 0;
     OperandElem<F>* h;
     int64_t h_plane;
-    typename F::Keep::Elem* gu;  // [M][2 F8] or null
+    Kept gu;  // of F::Keep; p null: not kept
     int64_t f8;
     int M;
     __device__ __forceinline__ void row(int m, int n, f32x4 g0, f32x4 g1, f32x4 u0, f32x4 u1) const {
         if (m >= M || n >= f8) return;
-        if (gu) {
-            F::Keep::put8(gu + (int64_t)m * 2 * f8 + n, g0, g1);
-            F::Keep::put8(gu + (int64_t)m * 2 * f8 + f8 + n, u0, u1);
-        }
+        if (gu.p) F::Keep::put(gu, m, n, g0, g1, u0, u1);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float a, da;
@@ -172,24 +169,20 @@ template <class F, int ACT>
 struct EpiGateGrad {
     static constexpr bool kDual = false, kSymmetric = false;
     using K = typename F::Keep;
-    static constexpr int kAhead = sizeof(typename K::Elem) == 2 ? 3 : 1;
-    const typename K::Elem* gu;
+    static constexpr int kAhead = K::kAhead;
+    Kept gu;
     OperandElem<F>* dgu;  // [M][2 F8]
     int64_t plane;
     int64_t f8;
     int M;
     struct Pre {
-        typename K::Raw8 g[2], u[2];
+        typename K::Raw gu[2];
     };
     __device__ __forceinline__ Pre fetch(int, int m, int n) const {
         Pre r;
-        const int64_t at = (int64_t)m * 2 * f8 + n;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (m < M && n + h * 8 < f8) {
-                r.g[h] = *(const typename K::Raw8*)(gu + at + h * 8);
-                r.u[h] = *(const typename K::Raw8*)(gu + at + f8 + h * 8);
-            }
+            if (m < M && n + h * 8 < f8) r.gu[h] = K::get(gu, m, n + h * 8);
         return r;
     }
     __device__ __forceinline__ void row(int, int, int m, int n, const f32x4 (&dh)[4], const Pre& pre) const {
@@ -200,7 +193,7 @@ struct EpiGateGrad {
             f32x4 dg[2], du[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const f32x4 g = K::unpack(pre.g[h], q), u = K::unpack(pre.u[h], q), d = dh[h * 2 + q];
+                const f32x4 g = K::g(pre.gu[h], q), u = K::u(pre.gu[h], q), d = dh[h * 2 + q];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float a, da;
@@ -481,7 +474,8 @@ struct Layout {
     int64_t M, D, H, O, D8, H8, O8;
     explicit Layout(const gs_ffn_dims& d)
         : M(d.rows), D(d.d_in), H(d.d_hidden), O(d.d_out), D8(round8(D)), H8(round8(H)), O8(round8(O)) {}
-    int64_t saved_gu_bytes() const { return round_up(M * 2 * H8 * (int64_t)sizeof(typename F::Keep::Elem), kAlign); }
+    int64_t saved_gu_bytes() const { return round_up(F::Keep::bytes(M * H8), kAlign); }
+    Kept kept(const void* saved) const { return {(char*)saved, H8, M * H8}; }
     int64_t h_elems() const { return M * H8 * F::kPlanes; }
     int64_t h_bytes() const { return round_up(h_elems() * (int64_t)sizeof(OperandElem<F>), kAlign); }
 };
@@ -556,9 +550,9 @@ hipError_t forward_few(const gs_ffn_dims& d, const void* x, int64_t ldx, const g
     using E = typename F::Elem;
     const Layout<F> L(d);
     Carver cv{ws};
-    EpiGateFew<F, ACT> e1{{nullptr, L.M * L.H8, nullptr, L.H8, (int)L.M}, nullptr};
+    EpiGateFew<F, ACT> e1{{nullptr, L.M * L.H8, L.kept(nullptr), L.H8, (int)L.M}, nullptr};
     if (saved) {
-        e1.all.gu = (typename F::Keep::Elem*)saved;
+        e1.all.gu = L.kept(saved);
         e1.all.h = (OperandElem<F>*)((char*)saved + L.saved_gu_bytes());
     }
     // the 16-bit h that is kept is the next product's input too
@@ -595,9 +589,7 @@ hipError_t forward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const 
     const Operand od = pk.add<F>(cv, w.down, L.O, L.H, L.H);
     GSR_TRY(pk.launch<F>(st));
     OperandElem<F>* h;
-    typename F::Keep::Elem* gu = nullptr;
     if (saved) {
-        gu = (typename F::Keep::Elem*)saved;
         h = (OperandElem<F>*)((char*)saved + L.saved_gu_bytes());
     } else {
         h = cv.take<OperandElem<F>>(L.h_elems());
@@ -605,7 +597,7 @@ hipError_t forward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const 
     const int64_t h_plane = L.M * L.H8;
     GemmArgs g1 = make_args(L.M, L.H, L.D);
     add_segments<F>(g1, ox, og, &ou);
-    EpiGate<F, ACT> e1{h, h_plane, gu, L.H8, (int)L.M};
+    EpiGate<F, ACT> e1{h, h_plane, L.kept(saved), L.H8, (int)L.M};
     GSR_TRY((launch_gemm<typename F::Mma, true, true>(g1, e1, st)));
     GemmArgs g2 = make_args(L.M, L.O, L.H8);
     add_segments<F>(g2, Operand{h, h_plane, L.H8}, od, nullptr);
@@ -648,7 +640,6 @@ hipError_t backward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const
     float* part = cv.take<float>(part_elems<F>(L));
     const int64_t plane = L.M * 2 * L.H8;
     OperandElem<F>* dgu = cv.take<OperandElem<F>>(plane * F::kPlanes);
-    const auto* gu = (const typename F::Keep::Elem*)saved;
     const OperandElem<F>* h = (const OperandElem<F>*)((const char*)saved + L.saved_gu_bytes());
     const int64_t h_plane = L.M * L.H8;
     Packer pk;
@@ -663,7 +654,7 @@ hipError_t backward_impl(const gs_ffn_dims& d, const void* x, int64_t ldx, const
 
     GemmArgs g1 = make_args(L.M, L.H8, L.O);
     add_segments<F>(g1, ody, od, nullptr);
-    EpiGateGrad<F, ACT> e1{gu, dgu, plane, L.H8, (int)L.M};
+    EpiGateGrad<F, ACT> e1{L.kept(saved), dgu, plane, L.H8, (int)L.M};
     GSR_TRY((launch_gemm<T, true, false>(g1, e1, st)));
     const Operand odgu{dgu, plane, 2 * L.H8};
     if (out.x) {

@@ -44,6 +44,7 @@ namespace gsr {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -409,17 +410,104 @@ __device__ __forceinline__ void split3(float v, uint16_t& hi, uint16_t& mid, uin
     lo = __builtin_bit_cast(uint16_t, l);
 }
 
+// Pre-activations kept for the backward pass: g and u of rows x cols (cols a multiple of 8), eight of each at a time.
+struct Kept {
+    char* p;
+    int64_t cols, n;  // n = rows * cols
+};
+
+// Float32 as it is: [rows][2][cols].
+struct Keep32 {
+    static constexpr int64_t bytes(int64_t n) { return n * 8; }
+    static constexpr int kAhead = 1;  // rows whose values fit the registers ahead of their use
+    struct Raw {
+        f32x4 v[4];
+    };
+    static __device__ __forceinline__ void put(const Kept& k, int64_t row, int col, f32x4 g0, f32x4 g1, f32x4 u0,
+                                               f32x4 u1) {
+        f32x4* g = (f32x4*)((float*)k.p + row * 2 * k.cols + col);
+        f32x4* u = (f32x4*)((float*)k.p + (row * 2 + 1) * k.cols + col);
+        g[0] = g0, g[1] = g1, u[0] = u0, u[1] = u1;
+    }
+    static __device__ __forceinline__ Raw get(const Kept& k, int64_t row, int col) {
+        const f32x4* g = (const f32x4*)((const float*)k.p + row * 2 * k.cols + col);
+        const f32x4* u = (const f32x4*)((const float*)k.p + (row * 2 + 1) * k.cols + col);
+        return {{g[0], g[1], u[0], u[1]}};
+    }
+    static __device__ __forceinline__ f32x4 g(const Raw& r, int h) { return r.v[h]; }
+    static __device__ __forceinline__ f32x4 u(const Raw& r, int h) { return r.v[2 + h]; }
+};
+// The upper 16 + LO bits of a float32, rounded: float32's range and 8 + LO significant bits.  First the upper 16 bits of
+// all values, [rows][2][cols], then the lower bits, LO / 4 words for eight g and as many for the eight u beside them.
+// Records of all bits of eight g and u one after another were slower (lines are written in more parts).
+template <int LO>
+struct KeepHigh {
+    static_assert(LO == 4 || LO == 8);
+    static constexpr int kWords = LO / 4;
+    static constexpr int64_t bytes(int64_t n) { return n * 4 + n / 4 * LO; }
+    static constexpr int kAhead = 2;
+    typedef uint32_t Low __attribute__((ext_vector_type(2 * kWords)));
+    struct Raw {
+        u32x4 g, u;
+        Low lo;
+    };
+    // four values: two words of upper halves, and their lower bits into lo from word w
+    static __device__ __forceinline__ void pack(f32x4 x, int h, u32x4& hi, Low& lo, int w) {
+        uint32_t t[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float f = x[e];  // an element of a vector cannot be cast in place
+            t[e] = __builtin_bit_cast(uint32_t, f) + (LO == 8 ? 0x80u : 0x800u);
+        }
+        hi[h * 2] = __builtin_amdgcn_perm(t[1], t[0], 0x07060302u);
+        hi[h * 2 + 1] = __builtin_amdgcn_perm(t[3], t[2], 0x07060302u);
+        const uint32_t b = __builtin_amdgcn_perm(__builtin_amdgcn_perm(t[3], t[2], 0x0c0c0501u),
+                                                 __builtin_amdgcn_perm(t[1], t[0], 0x0c0c0501u), 0x05040100u);
+        if constexpr (LO == 8)
+            lo[w + h] = b;
+        else if (h == 0)
+            lo[w] = (b >> 4) & 0x0f0f0f0fu;
+        else
+            lo[w] |= b & 0xf0f0f0f0u;
+    }
+    static __device__ __forceinline__ void put(const Kept& k, int64_t row, int col, f32x4 g0, f32x4 g1, f32x4 u0,
+                                               f32x4 u1) {
+        Raw r;
+        pack(g0, 0, r.g, r.lo, 0);
+        pack(g1, 1, r.g, r.lo, 0);
+        pack(u0, 0, r.u, r.lo, kWords);
+        pack(u1, 1, r.u, r.lo, kWords);
+        char* p = k.p + (row * 2 * k.cols + col) * 2;
+        *(u32x4*)p = r.g;
+        *(u32x4*)(p + k.cols * 2) = r.u;
+        *(Low*)(k.p + k.n * 4 + (row * k.cols + col) / 4 * LO) = r.lo;
+    }
+    static __device__ __forceinline__ Raw get(const Kept& k, int64_t row, int col) {
+        const char* p = k.p + (row * 2 * k.cols + col) * 2;
+        return {*(const u32x4*)p, *(const u32x4*)(p + k.cols * 2),
+                *(const Low*)(k.p + k.n * 4 + (row * k.cols + col) / 4 * LO)};
+    }
+    static __device__ __forceinline__ f32x4 unpack(u32x4 hi, const Low& lo, int w, int h) {
+        const uint32_t b = LO == 8 ? lo[w + (LO == 8 ? h : 0)] : h ? lo[w] & 0xf0f0f0f0u : (lo[w] & 0x0f0f0f0fu) << 4;
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = __builtin_bit_cast(
+                float, __builtin_amdgcn_perm(hi[h * 2 + (e >> 1)], b, (e & 1 ? 0x0706000cu : 0x0504000cu) | e << 8));
+        return v;
+    }
+    static __device__ __forceinline__ f32x4 g(const Raw& r, int h) { return unpack(r.g, r.lo, 0, h); }
+    static __device__ __forceinline__ f32x4 u(const Raw& r, int h) { return unpack(r.u, r.lo, kWords, h); }
+};
+
 // Element formats of the block: what a stored 16-bit matrix operand and a value array look like for each type.
-struct F32Values;
 struct FmtBf16 {
     using Mma = __bf16;
-    using Elem = uint16_t;   // value arrays (inputs, outputs)
-    using Keep = FmtBf16;    // saved pre-activations
+    using Elem = uint16_t;     // value arrays (inputs, outputs)
+    using Keep = KeepHigh<4>;  // saved pre-activations
     static constexpr int kPlanes = 1;
     static __device__ __forceinline__ f32x4 get(const Elem* p) { return from16<__bf16>(*(const u16x4*)p); }
     static __device__ __forceinline__ void put(Elem* p, f32x4 v) { *(u16x4*)p = to16<__bf16>(v); }
-    typedef u16x8 Raw8;  // eight values, 16-byte aligned
-    static __device__ __forceinline__ f32x4 unpack(Raw8 v, int h) { return from16<__bf16>(half8(v, h)); }
     static __device__ __forceinline__ void put8(Elem* p, f32x4 a, f32x4 b) { *(u16x8*)p = pack8(to16<__bf16>(a), to16<__bf16>(b)); }
     static __device__ __forceinline__ float to_float(uint16_t v) { return (float)__builtin_bit_cast(__bf16, v); }
     static __device__ __forceinline__ uint16_t from_float(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
@@ -429,12 +517,10 @@ struct FmtBf16 {
 struct FmtF16 {
     using Mma = _Float16;
     using Elem = uint16_t;
-    using Keep = F32Values;  // float16 has no room for the pre-activation of an open or a closed gate beyond 65504
+    using Keep = KeepHigh<8>;
     static constexpr int kPlanes = 1;
     static __device__ __forceinline__ f32x4 get(const Elem* p) { return from16<_Float16>(*(const u16x4*)p); }
     static __device__ __forceinline__ void put(Elem* p, f32x4 v) { *(u16x4*)p = to16<_Float16>(v); }
-    typedef u16x8 Raw8;  // eight values, 16-byte aligned
-    static __device__ __forceinline__ f32x4 unpack(Raw8 v, int h) { return from16<_Float16>(half8(v, h)); }
     static __device__ __forceinline__ void put8(Elem* p, f32x4 a, f32x4 b) { *(u16x8*)p = pack8(to16<_Float16>(a), to16<_Float16>(b)); }
     static __device__ __forceinline__ float to_float(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
     static __device__ __forceinline__ uint16_t from_float(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
@@ -443,13 +529,9 @@ struct FmtF16 {
 };
 struct F32Values {
     using Elem = float;
-    using Keep = F32Values;
+    using Keep = Keep32;
     static __device__ __forceinline__ f32x4 get(const Elem* p) { return *(const f32x4*)p; }
     static __device__ __forceinline__ void put(Elem* p, f32x4 v) { *(f32x4*)p = v; }
-    struct Raw8 {
-        f32x4 v[2];
-    };
-    static __device__ __forceinline__ f32x4 unpack(Raw8 v, int h) { return v.v[h]; }
     static __device__ __forceinline__ void put8(Elem* p, f32x4 a, f32x4 b) {
         *(f32x4*)p = a;
         *(f32x4*)(p + 4) = b;

@@ -70,8 +70,6 @@ __device__ __forceinline__ void gate(float z, float& a, float& na) {
     na = z >= 0.f ? er : r;
 }
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-
 // What a run of rows does to the state: h_out = A h_in + H, or h_out = H where a sequence starts (backward: ends) in
 // it, which a negative A says (a product of gates never is negative).
 struct Span {

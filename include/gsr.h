@@ -336,9 +336,9 @@ typedef struct {
     void* up;
     void* down;
 } gs_ffn_grads;
-/* The 16-bit types round h once, as the operand of y's product, and dh's results dg and du of the two projections
- * likewise; bfloat16 also g and u where they are kept for the backward pass.  In float16 |h|, |dg| and |du| above
- * 65504 therefore become infinite and values below 2^-24 vanish, as between float16 layers: scale the loss.
+/* The 16-bit types round h once, as the operand of y's product, and the gradients dg and du of the two projections
+ * likewise.  In float16 |h|, |dg| and |du| above 65504 therefore become infinite and values below 2^-25 vanish, as
+ * between float16 layers: scale the loss.
  *
  * Bytes of the saved activations and of the two calls' workspaces (any pointer may be null). */
 GSR_API gs_status gs_ffn_sizes(const gs_ffn_dims* dims, size_t* saved_bytes, size_t* forward_bytes,

@@ -752,3 +752,19 @@ def test_ffn_few_rows_wide(shape, dtype):
     x, wg, wu, wd, _ = ffn_inputs(*shape, dtype, seed=70)
     y = gsr().GatedFFN(wg, wu, wd).forward(x)
     o.check(y, o.ffn(x, wg, wu, wd, "silu"), ffn_tol(dtype, 2, max(shape)), "y")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=str)
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("shape", [(40, 192, 640, 256), (700, 320, 1000, 200)], ids=str)
+def test_ffn_gradients_carry_two_roundings(shape, act, dtype):
+    """Rounding to nearest is off by 0.4247 u in the mean (root mean square over a mantissa spread evenly in its
+    logarithm).  Every result carries two independent ones, the operand's and its own: sqrt(2) of that in its L2 error,
+    and 6 % for everything else (four, with g and u kept in the type, would be up to 2)."""
+    x, wg, wu, wd, dy = ffn_inputs(*shape, dtype, seed=80)
+    block = gsr().GatedFFN(wg, wu, wd, activation=act)
+    y, saved = block.forward(x, save=True)
+    got = dict(block.backward(x, saved, dy), y=y)
+    for k, ref in o.ffn(x, wg, wu, wd, act, dy).items():
+        err = ((got[k].double() - ref).norm() / ref.norm()).item()
+        assert err <= 1.5 * 0.4247 * o.UNIT[dtype], (k, err / (0.4247 * o.UNIT[dtype]))
