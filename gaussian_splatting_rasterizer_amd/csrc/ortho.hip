@@ -3,10 +3,14 @@
 //   X = G / max(|G|_F, eps);  repeat: P = X X^T, Q = b P + c P P, X = a X + Q X        (rows <= cols)
 //   and with P = X^T X, X = a X + X Q for rows > cols, so that P is the smaller square.
 //
+// computed as Q = (a - 1) I + b P + c P P, X = X + Q X: a X and Q X of the first form nearly cancel where a singular value
+// has arrived near 1, and what float16 loses of Q then counts several times (12 x 128 x 512: error 1.34 times that of
+// the result's own bfloat16 rounding, 1.14 in this form; 40 x 77: 1.56 and 1.30).
+//
 // All products run on k_gemm16 in float16 with float32 accumulation.  P and Q are symmetric: only tiles on and above
 // the diagonal are computed and each writes its mirror image; with few tiles and many k the sums are split along k.
 // The singular values of X start in [0, 1] and the default coefficients keep them below 1.3, so X is held as 2^12 X and
-// P, Q as 2^13 P, 2^13 Q: below float16's overflow (|P| <= 1.6, |Q| <= 2.9) and, for the entries that matter, above its
+// P, Q as 2^13 P, 2^13 Q: below float16's overflow (|P| <= 1.6, |Q| <= 2.5) and, for the entries that matter, above its
 // subnormals.  Coefficients that let them grow take smaller powers of two (ortho_scales).  float16 keeps 11 bits; in
 // bfloat16 the same steps lose 8 times as much.  For a float32 result each of X, P, Q is a pair hi + lo of
 // float16 (22 bits) and a product is lo hi + hi lo + hi hi.
@@ -126,7 +130,7 @@ __global__ __launch_bounds__(256) void k_normalise(const E* g, int64_t rows, int
     }
 }
 
-// C = alpha acc + beta S on and above the diagonal, mirrored below (S: null for P, the stored P for Q)
+// C = alpha acc + beta S + diag I on and above the diagonal, mirrored below (S: null for P, the stored P for Q)
 template <int PL>
 struct EpiSymmetric {
     static constexpr bool kDual = false, kSymmetric = true;
@@ -136,7 +140,7 @@ struct EpiSymmetric {
     const uint16_t* s;
     int64_t plane, ld, batch_stride;
     int n;
-    float alpha, beta;
+    float alpha, beta, diag;
     int bm;  // tile size, to tell diagonal tiles
     __device__ __forceinline__ Pre fetch(int batch, int m, int col) const {
         Pre r;
@@ -151,7 +155,11 @@ struct EpiSymmetric {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             v[q] = acc[q] * alpha;
-            if (s) v[q] += beta * pre.get(q);
+            if (s) {
+                v[q] += beta * pre.get(q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[q][e] += m == col + q * 4 + e ? diag : 0.f;
+            }
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -169,7 +177,7 @@ struct EpiSymmetric {
     }
 };
 
-// X' = a X + alpha acc, stored again in float16 planes, or in the result's type after the last step
+// X' = X + alpha acc, stored again in float16 planes, or in the result's type after the last step
 template <int PL, class Out>
 struct EpiUpdate {
     static constexpr bool kDual = false, kSymmetric = false;
@@ -180,7 +188,7 @@ struct EpiUpdate {
     int64_t plane, ld, batch_stride;
     Out* out;  // null: another step follows
     int M, N;  // rows, columns of the matrix
-    float a, alpha, inv_scale;  // X = a X + alpha acc as stored; inv_scale of it is the result
+    float alpha, inv_scale;  // inv_scale times what is stored is the result
     int vec;
     __device__ __forceinline__ Pre fetch(int batch, int m, int n) const {
         Pre r;
@@ -191,7 +199,7 @@ struct EpiUpdate {
         if (m >= M) return;
         f32x4 v[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = a * pre.get(q) + alpha * acc[q];
+        for (int q = 0; q < 4; ++q) v[q] = pre.get(q) + alpha * acc[q];
         if (!out) {
             uint16_t* d = xn + batch * batch_stride + (int64_t)m * ld + n;
 #pragma unroll
@@ -330,7 +338,7 @@ hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* 
     GSR_TRY(hipGetLastError());
     const bool tall = d.rows > d.cols;
     for (int step = 0; step < d.steps; ++step) {
-        EpiSymmetric<PL> es{P, nullptr, L.p_plane, L.lo8, L.lo * L.lo8, (int)L.lo, sc.p / (sc.x * sc.x), 0.f, 128};
+        EpiSymmetric<PL> es{P, nullptr, L.p_plane, L.lo8, L.lo * L.lo8, (int)L.lo, sc.p / (sc.x * sc.x), 0.f, 0.f, 128};
         GemmArgs gp = make_args(L.lo, L.lo, tall ? L.R : L.C);
         gp.batch = (int)L.B;
         gp.lda = gp.ldb = L.C8;
@@ -342,7 +350,8 @@ hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* 
         } else {
             GSR_TRY((launch_symmetric<PL, true>(gp, es, sums, st)));
         }
-        EpiSymmetric<PL> eq{Q, P, L.p_plane, L.lo8, L.lo * L.lo8, (int)L.lo, d.c / sc.p, d.b, 128};
+        EpiSymmetric<PL> eq{Q, P, L.p_plane, L.lo8, L.lo * L.lo8, (int)L.lo, d.c / sc.p, d.b,
+                            (float)(((double)d.a - 1.0) * sc.p), 128};
         GemmArgs gq = make_args(L.lo, L.lo, L.lo);
         gq.batch = (int)L.B;
         gq.lda = gq.ldb = L.lo8;
@@ -351,7 +360,7 @@ hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* 
         GSR_TRY((launch_symmetric<PL, true>(gq, eq, sums, st)));
         const bool last = step + 1 == d.steps;
         EpiUpdate<PL, Out> eu{x, xn, L.x_plane, L.C8, L.R * L.C8, last ? (Out*)out : nullptr, (int)L.R, (int)L.C,
-                              d.a, 1.f / sc.p, 1.f / sc.x, vec_width(out, L.C, sizeof(Out))};
+                              1.f / sc.p, 1.f / sc.x, vec_width(out, L.C, sizeof(Out))};
         GemmArgs gu = make_args(L.R, L.C8, L.lo);
         gu.batch = (int)L.B;
         if (tall) {  // X Q, Q symmetric
@@ -376,11 +385,11 @@ hipError_t ortho_impl(const gs_ortho_dims& d, const void* gin, void* out, char* 
 // ---- small matrices ------------------------------------------------------------------------------------
 
 // A matrix whose padded X and P fit in LDS takes one workgroup and one launch for all steps (12 matrices of 128 x 512:
-// 73 us, 17 launches took 123; 11 us a step, the rest for reading, norm and result).  X lies as m rows of n (m the
+// 72 us, 17 launches took 123; 11 us a step, the rest for reading, norm and result).  X lies as m rows of n (m the
 // smaller side) with n contiguous, rows of a multiple of 128 bytes (see at); P and then Q share a second buffer of the
 // same form.
 //   P: every wave takes a 32 x 64 block of X X^T and keeps it in registers;
-//   Q: the same block of P P (P from LDS), plus b P; then Q replaces P;
+//   Q: the same block of P P (P from LDS), plus b P and (a - 1) I; then Q replaces P;
 //   X: every wave takes strips of 32 columns, which depend on nothing but themselves and Q, in place.
 // LDS reads bound it: a block needs six 16-byte fragments a lane for eight products, 7 us of the 11.  Reading the next
 // fragments during the products gained nothing, strips of 64 columns did not fit the registers.
@@ -459,9 +468,9 @@ __device__ __forceinline__ f32x4 rounded(f32x4 v) {
     return hi + from16<_Float16>(to16<_Float16>(v - hi));
 }
 
-// X = a X + Q X for 32 columns from c0, in place
+// X = X + Q X for 32 columns from c0, in place
 template <int PL>
-__device__ __forceinline__ void small_update(const SmallView<PL>& X, const SmallView<PL>& Q, int c0, int mp, float a,
+__device__ __forceinline__ void small_update(const SmallView<PL>& X, const SmallView<PL>& Q, int c0, int mp,
                                              float inv_p, int lane) {
     constexpr int kTiles = kSmallSide / 16, J = 2;
     const int row = lane & 15, col = (lane >> 4) * 4;
@@ -492,7 +501,7 @@ __device__ __forceinline__ void small_update(const SmallView<PL>& X, const Small
         if (i * 16 < mp) {
 #pragma unroll
             for (int j = 0; j < J; ++j)
-                x[i][j] = a * X.get(i * 16 + row, c0 + j * 16 + col) + x[i][j] * inv_p;
+                x[i][j] = X.get(i * 16 + row, c0 + j * 16 + col) + x[i][j] * inv_p;
         }
 #pragma unroll
     for (int i = 0; i < kTiles; ++i)
@@ -506,7 +515,7 @@ struct SmallArgs {
     const void* g;
     void* out;
     int rows, cols, m, n, mp, np, steps;  // m, n: smaller and larger side; mp, np: padded
-    float a, b, c_p, eps;  // c_p: c / p scale
+    float diag, b, c_p, eps;  // (a - 1) p scale, b, c / p scale
     float x_scale, to_p, inv_p, inv_x;
 };
 
@@ -650,12 +659,17 @@ __global__ __launch_bounds__(kSmallWaves * 64) void k_ortho_small(const SmallArg
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) pv[i][j] = p.b * pv[i][j] + p.c_p * acc[i][j];
+                for (int j = 0; j < 4; ++j) {
+                    pv[i][j] = p.b * pv[i][j] + p.c_p * acc[i][j];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        pv[i][j][e] += r0 + i * 16 + row == c0 + j * 16 + col + e ? p.diag : 0.f;
+                }
         }
         __syncthreads();
         if (mine) keep();
         __syncthreads();
-        for (int t = wave; t < p.np / 32; t += kSmallWaves) small_update<PL>(X, P, t * 32, p.mp, p.a, p.inv_p, lane);
+        for (int t = wave; t < p.np / 32; t += kSmallWaves) small_update<PL>(X, P, t * 32, p.mp, p.inv_p, lane);
         __syncthreads();
     }
     typedef Out Out4 __attribute__((ext_vector_type(4)));
@@ -704,10 +718,11 @@ hipError_t ortho_small(const gs_ortho_dims& d, const void* g, void* out, hipStre
     p.rows = (int)d.rows, p.cols = (int)d.cols;
     p.m = d.rows < d.cols ? p.rows : p.cols, p.n = d.rows < d.cols ? p.cols : p.rows;
     p.mp = (int)round_up(p.m, 64), p.np = (int)round_up(p.n, 64);
-    p.steps = d.steps, p.a = d.a, p.b = d.b, p.eps = d.eps;
+    p.steps = d.steps, p.b = d.b, p.eps = d.eps;
     Scales sc;
     if (!ortho_scales(d, &sc.x, &sc.p)) return hipErrorInvalidValue;
-    p.x_scale = sc.x, p.to_p = sc.p / (sc.x * sc.x), p.c_p = d.c / sc.p, p.inv_p = 1.f / sc.p, p.inv_x = 1.f / sc.x;
+    p.x_scale = sc.x, p.to_p = sc.p / (sc.x * sc.x), p.c_p = d.c / sc.p;
+    p.diag = (float)(((double)d.a - 1.0) * sc.p), p.inv_p = 1.f / sc.p, p.inv_x = 1.f / sc.x;
     GSR_TRY(hipFuncSetAttribute((const void*)k_ortho_small<In, Out, PL>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                 kSmallLds));
     k_ortho_small<In, Out, PL><<<dim3((unsigned)d.batch), kSmallWaves * 64, bytes, st>>>(p);
@@ -722,7 +737,7 @@ hipError_t ortho_any(const gs_ortho_dims& d, const void* g, void* out, char* ws,
 }  // namespace
 
 // Follows the interval [0, 1] of the singular values through the steps: P reaches s^2, Q the largest
-// |b s^2 + c s^4| and X the largest |a s + b s^3 + c s^5| for s in it (at its ends or where the derivative is zero), and
+// |a - 1 + b s^2 + c s^4| and X the largest |a s + b s^3 + c s^5| for s in it (at its ends or where the derivative is zero), and
 // no entry of a matrix exceeds its largest singular value.  2 % a step cover the float16 roundings.  The scales are the
 // largest powers of two, up to 2^12 and 2^13, that keep these below float16's 65504.  Below 2^8 the entries that matter
 // come near float16's subnormals: false.
@@ -731,10 +746,10 @@ bool ortho_scales(const gs_ortho_dims& d, float* x_scale, float* p_scale) {
     double s = slack, top_x = s, top_p = 0.0;
     for (int step = 0; step < d.steps; ++step) {
         const double s2 = s * s;
-        double q = std::fabs(b * s2 + c * s2 * s2), next = std::fabs(s * (a + b * s2 + c * s2 * s2));
+        double q = std::max(std::fabs(a - 1.0), std::fabs(a - 1.0 + b * s2 + c * s2 * s2)), next = std::fabs(s * (a + b * s2 + c * s2 * s2));
         if (c != 0.0) {
             const double at = -b / (2.0 * c);
-            if (at > 0.0 && at < s2) q = std::max(q, std::fabs(b * at + c * at * at));
+            if (at > 0.0 && at < s2) q = std::max(q, std::fabs(a - 1.0 + b * at + c * at * at));
         }
         // a + 3 b t + 5 c t^2 = 0 in t = s^2
         double roots[2] = {-1.0, -1.0};

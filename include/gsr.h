@@ -406,10 +406,10 @@ GSR_API gs_status gs_scan_backward(const gs_scan_dims* dims, const int64_t* offs
  * it is taken off a weight.  dtype and out_dtype: GS_F32 or GS_BF16.  A bfloat16 result
  * is computed from float16 operands (11 bits), a float32 result from pairs of
  * them (22 bits).  P and Q are held in float16 too: over singular values s
- * that start in [0, 1], no step may start with s^2, reach |b s^2 + c s^4| or end
- * with |s| above 250 (2 % of it a step are kept in hand), or the call is
- * GS_ERR_UNSUPPORTED.  Smaller side 1 .. 2^15, larger
- * 1 .. 2^20, steps 1 .. 64, batch 0 .. 2^16 - 1.
+ * that start in [0, 1], no step may start with s^2, reach |a - 1 + b s^2 + c s^4|
+ * or end with |s| above 250 (2 % of it a step are kept in hand), or the call is
+ * GS_ERR_UNSUPPORTED.  Smaller side 1 .. 2^15, larger 1 .. 2^20, steps 1 .. 64,
+ * batch 0 .. 2^16 - 1.
  * A matrix with an infinite or NaN entry gives NaN (that matrix only). */
 typedef struct {
     int64_t rows, cols;

@@ -768,3 +768,15 @@ def test_ffn_gradients_carry_two_roundings(shape, act, dtype):
     for k, ref in o.ffn(x, wg, wu, wd, act, dy).items():
         err = ((got[k].double() - ref).norm() / ref.norm()).item()
         assert err <= 1.5 * 0.4247 * o.UNIT[dtype], (k, err / (0.4247 * o.UNIT[dtype]))
+
+
+@pytest.mark.parametrize("shape", [(12, 40, 77), (12, 108, 39), (12, 128, 512), (2, 200, 300)], ids=str)
+def test_ortho_small_operand_error(shape):
+    """float16 operands (2^-12 a rounding) may add as much to a bfloat16 result's error as its own rounding (0.4247 2^-8
+    in the mean): sqrt(2) of that in all, and 3 % for the batch's spread.  The default coefficients' terms nearly cancel
+    on singular values near 1, where Q holding them apart would cost 1.56."""
+    g = randn(gen(90), *shape)
+    out = gsr().Orthogonalizer(*shape, torch.float32, torch.bfloat16).run(g)
+    ref = torch.stack([o.newton_schulz(m, 5, NS) for m in g])
+    err = ((out.double() - ref).norm() / ref.norm()).item()
+    assert err <= 1.45 * 0.4247 * 2.0 ** -8, err / (0.4247 * 2.0 ** -8)
