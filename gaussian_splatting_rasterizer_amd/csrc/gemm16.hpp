@@ -225,6 +225,12 @@ __device__ __forceinline__ int xcd_order(int bid, int n) {
     return x * q + min(x, r) + l;
 }
 
+// k tiles after which a float32 product's sums go over to a second accumulator.  The error of a sum of K terms in one
+// float32 accumulator grows like sqrt(K); in chains of 256 it stays at a chain's, about 12 roundings (K = 2575: 1.0e-6 of
+// the result in one chain, 0.4e-6 so).  The 16-bit instructions round once in 32 terms and need no second accumulator,
+// for which a 256 x 256 tile has no registers.
+constexpr int kChainTiles = 8;
+
 template <class T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, class Epi>
 __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p, const Epi epi) {
     constexpr int NT = WM * WN * 64;
@@ -266,11 +272,15 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p, con
     const int64_t astep = AKC ? 128 : 128 * p.lda;
     const int64_t bstep = BKC ? 128 : 128 * p.ldb;
 
-    f32x4 acc[MI][NI];
+    constexpr bool kChains = sizeof(T) == 4 && BM < 256;
+    f32x4 acc[MI][NI], total[kChains ? MI : 1][kChains ? NI : 1];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NI; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NI; ++j) {
+            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if constexpr (kChains) total[i][j] = acc[i][j];
+        }
 
     if (t_begin < t_end) {
         // the tile to fetch; past the last one nothing is read (krem 0: every lane is out of range)
@@ -347,6 +357,22 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void k_gemm16(const GemmArgs p, con
             __builtin_amdgcn_s_barrier();
             asm volatile("" ::: "memory");
             multiply(1, nxt, true, cur);
+            if constexpr (kChains)
+                if ((t - t_begin) % kChainTiles == kChainTiles - 1) {
+#pragma unroll
+                    for (int i = 0; i < MI; ++i)
+#pragma unroll
+                        for (int j = 0; j < NI; ++j) {
+                            total[i][j] += acc[i][j];
+                            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                        }
+                }
+        }
+        if constexpr (kChains) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j) acc[i][j] += total[i][j];
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no fetch outlives the workgroup's LDS
     }
@@ -614,7 +640,8 @@ inline GemmPlan plan_gemm(int64_t M, int64_t N, int64_t batch, int64_t ktiles, b
     static const TileTimes t16[3] = {{256, 1, 1.75, 1.75, 7}, {128, 2, 0.85, 1.2, 4}, {64, 4, 0.5, 1.05, 3}};
     static const TileTimes t32[3] = {{256, 1, 8.4, 8.4, 20}, {128, 2, 2.3, 4.3, 16}, {64, 4, 0.85, 3.2, 3}};
     GemmPlan best{128, 1, (int)ktiles, 1e30};
-    for (int i = 0; i < 3; ++i) {
+    // a long float32 sum needs a tile with two accumulators (kChainTiles)
+    for (int i = f32 && ktiles > 2 * kChainTiles ? 1 : 0; i < 3; ++i) {
         const TileTimes& tt = f32 ? t32[i] : t16[i];
         const int t = tt.tile;
         const int64_t tiles =

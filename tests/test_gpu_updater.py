@@ -780,3 +780,20 @@ def test_ortho_small_operand_error(shape):
     ref = torch.stack([o.newton_schulz(m, 5, NS) for m in g])
     err = ((out.double() - ref).norm() / ref.norm()).item()
     assert err <= 1.45 * 0.4247 * 2.0 ** -8, err / (0.4247 * 2.0 ** -8)
+
+
+@pytest.mark.parametrize("shape", [(200, 64, 6000, 48), (1500, 48, 3100, 64)], ids=str)
+def test_ffn_float32_long_sums(shape):
+    """A rounding is off by 0.4247 u in the mean.  A sum of K float32 terms in chains of 256 carries sqrt(128 + K / 512)
+    of them (one chain: sqrt(K / 2), 55 of them for K = 6000, 77 for dx's 12000), the sums in front of it of up to 64
+    terms and two more operands sqrt(4 * 64); half as much again for the activations."""
+    m, d, f, out = shape
+    x, wg, wu, wd, dy = ffn_inputs(*shape, torch.float32, seed=91)
+    block = gsr().GatedFFN(wg, wu, wd)
+    y, saved = block.forward(x, save=True)
+    dx = block.backward(x, saved, dy)["x"]
+    ref = o.ffn(x, wg, wu, wd, "silu", dy)
+    for got, want, k in ((y, ref["y"], f), (dx, ref["x"], 2 * f)):
+        err = ((got.double() - want).norm() / want.norm()).item()
+        tol = 1.5 * 0.4247 * o.UNIT[torch.float32] * math.sqrt(128 + k / 512 + 4 * 64)
+        assert err <= tol, (err, tol)
