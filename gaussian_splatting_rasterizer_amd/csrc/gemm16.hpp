@@ -602,6 +602,8 @@ struct NoPre {};
 
 // ---- launchers -----------------------------------------------------------------------------------------
 
+constexpr int64_t kMaxThreads = (1ll << 32) - 1;  // of a launch
+
 template <class T, bool AKC, bool BKC, int BM, int BN, int WM, int WN, class Epi>
 inline hipError_t launch_tiles(GemmArgs p, const Epi& epi, hipStream_t st) {
     constexpr int BNR = Epi::kDual ? BN / 2 : BN;
@@ -610,7 +612,7 @@ inline hipError_t launch_tiles(GemmArgs p, const Epi& epi, hipStream_t st) {
     const int64_t tiles = Epi::kSymmetric ? (int64_t)p.tiles_n * (p.tiles_n + 1) / 2 : (int64_t)p.tiles_m * p.tiles_n;
     const int64_t n = tiles * p.batch * p.splits;
     if (n <= 0) return hipSuccess;
-    if (n > 0x7fffffff) return hipErrorInvalidValue;
+    if (n > kMaxThreads / (WM * WN * 64)) return hipErrorInvalidValue;
     k_gemm16<T, AKC, BKC, BM, BN, WM, WN, Epi><<<dim3((unsigned)n), dim3(WM * WN * 64), 0, st>>>(p, epi);
     return hipGetLastError();
 }
@@ -649,6 +651,7 @@ inline GemmPlan plan_gemm(int64_t M, int64_t N, int64_t batch, int64_t ktiles, b
         for (int s = 1; s <= max_splits; s = s < 8 ? s + 1 : s + s / 4) {
             const int64_t per = (ktiles + s - 1) / s, n = tiles * s, slots = 256 * tt.per_cu;
             if (s > 1 && (per < 4 || n > 1024)) break;
+            if (n > kMaxThreads / (t == 256 ? 512 : 256)) break;
             const int64_t rounds = (n + slots - 1) / slots;
             const double busy = rounds > 1 ? 1.0 : (double)((n + 255) / 256) / tt.per_cu;
             const double per_k = tt.full * busy > tt.alone ? tt.full * busy : tt.alone;

@@ -797,3 +797,33 @@ def test_ffn_float32_long_sums(shape):
         err = ((got.double() - want).norm() / want.norm()).item()
         tol = 1.5 * 0.4247 * o.UNIT[torch.float32] * math.sqrt(128 + k / 512 + 4 * 64)
         assert err <= tol, (err, tol)
+
+
+def test_ffn_a_billion_rows():
+    """More tiles of 64 rows than a launch has room for: larger tiles take them.  One input, hidden unit and output each,
+    y = silu(x) x to two roundings."""
+    rows = (1 << 30) + 3
+    x = torch.empty(rows, 1, dtype=torch.bfloat16, device="cuda")
+    for i in range(0, rows, 1 << 27):
+        x[i:i + (1 << 27)].normal_(generator=gen(i >> 27))
+    one = torch.ones(1, 1, dtype=torch.bfloat16, device="cuda")
+    y = gsr().GatedFFN(one, one, one).forward(x)
+    for i in range(0, rows, 1 << 27):
+        v = x[i:i + (1 << 27)].float()
+        want = v * torch.sigmoid(v) * v
+        assert ((y[i:i + (1 << 27)].float() - want).abs() <= 2.1 * o.UNIT[torch.bfloat16] * want + 1e-37).all(), i
+
+
+def test_ffn_float32_few_rows_of_a_large_block():
+    """Few rows whose backward pass runs on split operands: the forward pass keeps h in both forms."""
+    m, d, f, out = 64, 2048, 16384, 4608
+    x, wg, wu, wd, dy = ffn_inputs(m, d, f, out, torch.float32, seed=92)
+    block = gsr().GatedFFN(wg, wu, wd)
+    y, saved = block.forward(x, save=True)
+    assert torch.equal(block.forward(x), y)
+    got = block.backward(x, saved, dy)
+    ref = o.ffn(x, wg, wu, wd, "silu", dy)
+    tol = ffn_tol(torch.float32, 0, 2 * f)
+    o.check(y, ref["y"], tol, "y")
+    for name in ("x", "w_gate", "w_up", "w_down"):
+        o.check(got[name], ref[name], tol, name)
