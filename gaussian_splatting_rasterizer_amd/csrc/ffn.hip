@@ -20,14 +20,14 @@
 // float16 the infinite g of a closed gate made NaN of its gradients.  131072 rows of 512 x 2048 x 512 bfloat16: 3.00 ms,
 // 2.82 with g and u in the type, 3.11 with 24 bits of each.  Everything else is float32.
 //
-// Measured, bfloat16 SiLU, 131072 rows of 512 x 2048 x 512, forward and backward 2.77 ms (890 TFLOP/s; the power limit
+// Measured, bfloat16 SiLU, 131072 rows of 512 x 2048 x 512, forward and backward 2.93 ms (840 TFLOP/s; the power limit
 // lowers the shader clock to 1.9 GHz); in a kernel trace, us:
-//   g, u, h  730  1.6 GB of results (310 at a copy's rate) and products (360) alternate in a workgroup
-//   y        310  products, 890 TFLOP/s
-//   dg, du   690  2.3 GB read and written (450) after the products (180)
+//   g, u, h  860  1.9 GB of results (370 at a copy's rate) and products (360) alternate in a workgroup
+//   y        285  products, 970 TFLOP/s
+//   dg, du   750  2.5 GB read and written (490) after the products (180)
 //   dx       470  products, 1170 TFLOP/s
-//   dWg, dWu 450, dWd 250: products split along the rows, 1220 and 1110 TFLOP/s; the sums of the parts 13 each
-// Asking for the tile's g and u during its products made the third 770 us: the lines arrive, but the fetches of
+//   dWg, dWu 440, dWd 245: products split along the rows, 1250 and 1120 TFLOP/s; the sums of the parts 13 each
+// Asking for the tile's g and u during its products made the third 80 us slower: the lines arrive, but the fetches of
 // operands wait behind them.
 #include <algorithm>
 
@@ -697,12 +697,12 @@ namespace {
 // rate, but move 6 bytes per value instead of 4, convert every operand, and want large tiles.  Measured, forward and
 // backward together in us:
 //   rows x in x hidden x out       f32    split      rows x in x hidden x out       f32    split
-//   23040 x 57 x 256 x 128         190      207      23040 x 256 x 512 x 256        628      543
-//   131072 x 64 x 256 x 64         577      901      65536 x 192 x 768 x 192       1875     1535
-//   131072 x 128 x 512 x 128      1618     1856      8192 x 512 x 2048 x 512       1289     1149
-//   2048 x 512 x 2048 x 512        409      525      4000 x 2048 x 4096 x 2048     4461     3185
-//   1000 x 1000 x 2731 x 1000      642      805      16384 x 1024 x 4096 x 1024    9047     6065
-// (4000 x 512 x 2048 x 512 and 16384 x 256 x 1024 x 256 are even.)  So: rows of at least 192 values and enough work.
+//   23040 x 57 x 256 x 128         176      204      23040 x 256 x 512 x 256        602      559
+//   131072 x 64 x 256 x 64         604      932      65536 x 192 x 768 x 192       1897     1563
+//   131072 x 128 x 512 x 128      1668     1919      8192 x 512 x 2048 x 512       1331     1176
+//   2048 x 512 x 2048 x 512        419      518      4000 x 2048 x 4096 x 2048     4626     3187
+//   1000 x 1000 x 2731 x 1000      609      798      16384 x 1024 x 4096 x 1024    9381     6148
+// (4000 x 512 x 2048 x 512 and 16384 x 256 x 1024 x 256 are within 4 %.)  So: rows of at least 192 values and enough work.
 bool split_f32(const gs_ffn_dims& d) {
     return d.d_in >= 192 && d.d_out >= 192 &&
            (double)d.rows * d.d_hidden * (2.0 * d.d_in + d.d_out) >= 8589934592.0;  // 2^33 multiplications

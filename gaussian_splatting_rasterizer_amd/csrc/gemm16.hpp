@@ -25,7 +25,8 @@
 //
 // 8192^3 in bfloat16: 938 us with both operands KC, 941 with one, 955 with none (1172, 1168, 1151 TFLOP/s); fetches
 // at the top of a tile 1005, 1209, 1214 us; reads and fetches left to the compiler's order 978, 1005, 1022 us.  On
-// zeros the same kernel reaches 1600 TFLOP/s: on real data the card's power limit sets the clock (1.9 GHz here).
+// zeros the same kernel reaches 1600 TFLOP/s: on real data the card's power limit sets the clock (1.9 GHz here), which
+// is not all of it: a library's product reaches 1511 TFLOP/s on such data.
 // 32x32x16 instructions (995 us), four waves of 128x128 (1031 us), 32-k tiles in rings of three to five (1005 us) and
 // waves taking turns between reading and multiplying (1092 us) were measured slower.
 //

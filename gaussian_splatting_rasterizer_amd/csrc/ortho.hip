@@ -17,7 +17,7 @@
 //
 // Measured: 2048 x 5632 bfloat16 640 us, of each step's 147 us P 44 + 12 (its split sums), Q 25, X 64 (740 TFLOP/s on
 // 176 of 256 CUs; tiles of 192 x 256 on 242 CUs gained 1 %, the power limit lowers the clock instead).  Two matrices of
-// 1366 x 500 float32: 247 us, of each step's 49 us P 13 + 6, Q 14, X 16; these products have 11 to 24 k tiles in 72 to
+// 1366 x 500 float32: 250 us, of each step's 50 us P 13 + 7, Q 14, X 16; these products have 11 to 24 k tiles in 72 to
 // 432 workgroups and wait for LDS and barriers (a ring of four tiles in LDS instead of two changed nothing).
 #include <algorithm>
 #include <cmath>

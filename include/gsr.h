@@ -306,7 +306,8 @@ GSR_API gs_status gs_attribute(gs_context* ctx, const float* pixel_map, int32_t 
  * be kept or cleared between calls.
  *
  * Arithmetic: sums, activations, recurrent states and norms are float32 (or
- * wider); results are rounded to the array's type once when stored.  float32
+ * wider); results are rounded to the array's type once when stored, and so is
+ * what goes from one matrix product into the next (see the operators).  float32
  * products keep float32's 24 bits; infinities in them may come out as NaN.  Results
  * do not depend on scheduling: the same call gives the same bits. */
 typedef enum { GS_F32 = 0, GS_BF16 = 1, GS_F16 = 2 } gs_dtype;
@@ -361,7 +362,8 @@ GSR_API gs_status gs_ffn_backward(const gs_ffn_dims* dims, const void* x, int64_
  * over n_seq sequences that lie one after another in `rows` rows.  offsets
  * (device, [n_seq + 1], non-decreasing, first 0, last rows) gives the first row
  * of each sequence; null means n_seq sequences of equal length.  Sequences may
- * be empty.  Offsets outside [0, rows] are not followed; other values that are
+ * be empty.  A state that becomes infinite may come out as NaN in later rows.
+ * Offsets outside [0, rows] are not followed; other values that are
  * not non-decreasing give unspecified results but no access out of range.
  * gate, x and y [rows, channels] in the type of dims, row strides in elements;
  * h0 (state before the first row, null: zero) and h_last (state after the last
