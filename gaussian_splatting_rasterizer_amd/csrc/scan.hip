@@ -22,8 +22,8 @@
 // The forward pass keeps the state in front of every 8 rows in float32; the backward pass reruns the states from
 // there, instead of reading back rounded ones.
 //
-// Bound by memory.  311,296 rows x 256 bfloat16 channels in one sequence, us and TB/s: forward spans 86 (3.7), join 16,
-// recurrence 88 (5.9, part of it from the last-level cache); backward spans 90 (3.5), join 16, recurrence 172 (4.9); a
+// Bound by memory.  311,296 rows x 256 bfloat16 channels in one sequence, us and TB/s: forward spans 88 (3.6), join 21,
+// recurrence 91 (5.7, part of it from the last-level cache); backward spans 96 (3.3), join 21, recurrence 174 (4.8); a
 // large copy reaches 5.2.  One pass over the data, workgroups waiting for the state of the one before, took 249 us
 // forward and 373 backward: the chain through 1216 chunks is longer than the second reading.
 #include "gsr_internal.hpp"
@@ -54,34 +54,60 @@ struct ScanArgs {
     const int64_t* offsets;
     int64_t n_seq, seq_len, rows, nchunks;
     int C, ncb, span;  // span: rows of a span
-    // [chunk * 8 + span][3][C]: A, H, and the given state of the last sequence that starts (backward: ends) in the span
+    // [chunk * 8 + span][3][C]: a Span's c and H, and the given state of the last sequence that starts (backward: ends) in the span
     // on the way through it, unwritten where none does.  Null: no state passes between spans.
     float* agg1;
     float* agg2;       // [chunk][2][C]
     float* state;      // [chunk][C] state entering the chunk
 };
 
-// a = sigma(z) and 1 - a, each to its own relative precision
-__device__ __forceinline__ void gate(float z, float& a, float& na) {
-    const float e = __expf(-__builtin_fabsf(z));
-    const float r = __builtin_amdgcn_rcpf(1.f + e);
-    const float er = e * r;
-    a = z >= 0.f ? r : er;
-    na = z >= 0.f ? er : r;
-}
+// A gate is held as the smaller of a = sigma(z) and 1 - a, to its own relative precision, and which of the two it is.
+// The larger one, rounded, would be off by 2^-25, and a state that remembers 1 / (1 - a) rows by 2^-25 / (1 - a) of
+// itself (z = 10: 1.4e-4), so it is never multiplied by: a v = v - (1 - a) v.
+struct Gate {
+    float s;
+    bool keeps;  // s = 1 - a, else s = a
+    __device__ __forceinline__ explicit Gate(float z) {
+        const float e = __expf(-__builtin_fabsf(z));
+        s = e * __builtin_amdgcn_rcpf(1.f + e);
+        keeps = z >= 0.f;
+    }
+    __device__ __forceinline__ Gate(float s, bool keeps) : s(s), keeps(keeps) {}
+    // a h + (1 - a) x; d = x - h
+    __device__ __forceinline__ float mix(float h, float x, float d) const {
+        return __builtin_fmaf(keeps ? s : -s, d, keeps ? h : x);
+    }
+    // a v and (1 - a) v
+    __device__ __forceinline__ void split(float v, float& kept, float& rest) const {
+        const float small = s * v, large = __builtin_fmaf(-s, v, v);
+        kept = keeps ? large : small;
+        rest = keeps ? small : large;
+    }
+};
 
 // What a run of rows does to the state: h_out = A h_in + H, or h_out = H where a sequence starts (backward: ends) in
-// it, which a negative A says (a product of gates never is negative).
+// it.  A product of gates is held like a gate, as A or as -(1 - A), whichever is smaller, in one number; kReset says
+// that there is no A.
+constexpr float kReset = 2.f;
 struct Span {
-    float A, H;
-    __device__ __forceinline__ bool reset() const { return A < 0.f; }
+    float c, H;
+    __device__ __forceinline__ bool reset() const { return c > 1.f; }
+    __device__ __forceinline__ bool keeps() const { return __builtin_bit_cast(int, c) < 0; }
+    // of a product A and its complement, each to its own precision
+    static __device__ __forceinline__ float code(float A, float rest) { return A > 0.5f ? -rest : A; }
 };
+constexpr float kIdentity = -0.f;  // c of the span that changes nothing
+__device__ __forceinline__ float apply(const Span& s, float h) {
+    const float in = s.reset() ? 0.f : h;
+    return (s.keeps() ? in : 0.f) + __builtin_fmaf(s.c, in, s.H);
+}
 __device__ __forceinline__ Span join(const Span& first, const Span& then) {
     if (then.reset()) return then;
-    return {first.reset() ? first.A : first.A * then.A, __builtin_fmaf(then.A, first.H, then.H)};
-}
-__device__ __forceinline__ float apply(const Span& s, float h) {
-    return s.reset() ? s.H : __builtin_fmaf(s.A, h, s.H);
+    const float H = apply(then, first.H);
+    if (first.reset()) return {kReset, H};
+    const float A = (first.keeps() ? 1.f + first.c : first.c) * (then.keeps() ? 1.f + then.c : then.c);
+    const float rest = -(first.c + then.c + first.c * then.c);  // where both keep: 1 - (1 + c)(1 + c')
+    return {first.keeps() && then.keeps() ? Span::code(A, rest) : A, H};
 }
 
 // Sequence starts of a chunk: s_start[i] is the sequence that starts at row row0 + i (the last one, where empty
@@ -257,10 +283,10 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_spans(const ScanArgs p) {
     const RowPtr pz = RowPtr::make<E>(p.z, at.base, p.ldz, at.c, at.live);
     const RowPtr px = BWD ? RowPtr::make<E>(p.dy, at.base, p.lddy, at.c, at.live)
                           : RowPtr::make<E>(p.x, at.base, p.ldx, at.c, at.live);
-    float A[VC], H[VC], given_state[VC];
+    float A[VC], rest[VC], H[VC], given_state[VC];  // A and 1 - A
     bool reset = false;
 #pragma unroll
-    for (int e = 0; e < VC; ++e) A[e] = 1.f, H[e] = 0.f, given_state[e] = 0.f;
+    for (int e = 0; e < VC; ++e) A[e] = 1.f, rest[e] = 0.f, H[e] = 0.f, given_state[e] = 0.f;
     const int nb = (at.n + kBatch - 1) / kBatch;
     Rows<F, VC> z[2], x[2];
     auto fetch = [&](int k, int b) {
@@ -288,10 +314,15 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_spans(const ScanArgs p) {
             }
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
-                float a, na;
-                gate(z[b].get(r, e), a, na);
-                H[e] = BWD ? a * (x[b].get(r, e) + H[e]) : __builtin_fmaf(a, H[e], na * x[b].get(r, e));
-                A[e] *= a;
+                const Gate a(z[b].get(r, e));
+                const float xv = x[b].get(r, e);
+                float gone;
+                if (BWD)
+                    a.split(xv + H[e], H[e], gone);
+                else
+                    H[e] = a.mix(H[e], xv, xv - H[e]);
+                a.split(A[e], A[e], gone);
+                rest[e] += gone;
             }
         }
     };
@@ -301,10 +332,8 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_spans(const ScanArgs p) {
         if (k + 2 < nb) fetch(k + 2, 0);
         if (k + 1 < nb) run(k + 1, 1);
     }
-    if (reset) {
 #pragma unroll
-        for (int e = 0; e < VC; ++e) A[e] = -1.f;
-    }
+    for (int e = 0; e < VC; ++e) A[e] = reset ? kReset : Span::code(A[e], rest[e]);
     if (at.live && nb > 0) {
         float* d = lane_at<float>(p.agg1 + (at.chunk * kSpans + at.g) * 3 * p.C, at.c);
 #pragma unroll
@@ -318,14 +347,14 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_spans(const ScanArgs p) {
     for (int e = 0; e < VC; ++e) s_a[at.g][at.li * VC + e] = A[e], s_h[at.g][at.li * VC + e] = H[e];
     __syncthreads();
     if (tid < CB && at.c0 + tid < p.C) {
-        Span own{1.f, 0.f};
+        Span own{kIdentity, 0.f};
 #pragma unroll
         for (int i = 0; i < kSpans; ++i) {
             const int k = BWD ? kSpans - 1 - i : i;
             own = join(own, Span{s_a[k][tid], s_h[k][tid]});
         }
         float* d = p.agg2 + at.chunk * 2 * p.C + at.c0 + tid;
-        d[0] = own.A;
+        d[0] = own.c;
         d[p.C] = own.H;
     }
     // an empty sequence passes its state through
@@ -361,16 +390,16 @@ __global__ __launch_bounds__(kJoinLanes* kJoinRuns) void k_scan_join(const ScanA
         const int64_t o0 = o + w * kJoinChunks;
 #pragma unroll
         for (int i = 0; i < kJoinChunks; ++i) {
-            v[i] = {1.f, 0.f};
+            v[i] = {kIdentity, 0.f};
             if (live && o0 + i < p.nchunks) {
                 const float* a = p.agg2 + (BWD ? p.nchunks - 1 - o0 - i : o0 + i) * 2 * p.C + c;
                 v[i] = {a[0], a[p.C]};
             }
         }
-        Span own{1.f, 0.f};
+        Span own{kIdentity, 0.f};
 #pragma unroll
         for (int i = 0; i < kJoinChunks; ++i) own = join(own, v[i]);
-        s_a[w][lane] = own.A, s_h[w][lane] = own.H;
+        s_a[w][lane] = own.c, s_h[w][lane] = own.H;
         __syncthreads();
         float h = run;
 #pragma unroll 8
@@ -399,7 +428,7 @@ __device__ __forceinline__ void span_state(const ScanArgs& p, const Place<VC>& a
     const float* s = lane_at<const float>(p.state + at.chunk * p.C, at.c);
 #pragma unroll
     for (int e = 0; e < VC; ++e) {
-        s_a[at.g][at.li * VC + e] = mine ? d[e] : 1.f;
+        s_a[at.g][at.li * VC + e] = mine ? d[e] : kIdentity;
         s_h[at.g][at.li * VC + e] = mine ? d[p.C + e] : 0.f;
         if (at.live && p.state) h[e] = s[e];
     }
@@ -464,9 +493,8 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_forward(const ScanArgs p) 
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
                 if ((starts >> r) & 1) h[e] = first[r][e];
-                float a, na;
-                gate(z[b].get(r, e), a, na);
-                h[e] = __builtin_fmaf(a, h[e], na * x[b].get(r, e));
+                const float xv = x[b].get(r, e);
+                h[e] = Gate(z[b].get(r, e)).mix(h[e], xv, xv - h[e]);
                 y.set(e, h[e]);
             }
             store_row(py, r0 + r, at.n, y);
@@ -522,7 +550,7 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_backward(const ScanArgs p)
     for (int k = nb - 1; k >= 0; --k) {
         const int r0 = k * kBatch;
         const uint32_t starts = start_bits(st + r0, at.n - r0), ends = start_bits(st + r0 + 1, at.n - r0);
-        // the smaller of a and 1 - a, negative when that is a; a (1 - a) (h_{t-1} - x)
+        // the gate, s negative where it is a; a (1 - a) (h_{t-1} - x)
         float q[kBatch][VC], w[kBatch][VC];
         float h[VC];
 #pragma unroll
@@ -544,12 +572,11 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_backward(const ScanArgs p)
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
                 if ((starts >> r) & 1) h[e] = first[r][e];
-                float a, na;
-                gate(z.get(r, e), a, na);
-                const float xv = x.get(r, e);
-                q[r][e] = __builtin_bit_cast(int, z.get(r, e)) < 0 ? -a : na;
-                w[r][e] = a * na * (h[e] - xv);
-                h[e] = __builtin_fmaf(a, h[e], na * xv);
+                const Gate a(z.get(r, e));
+                const float xv = x.get(r, e), d = xv - h[e];
+                q[r][e] = a.keeps ? a.s : -a.s;
+                w[r][e] = __builtin_fmaf(a.s, a.s, -a.s) * d;
+                h[e] = a.mix(h[e], xv, d);
             }
         }
         const Rows<F, VC> d = dy;
@@ -571,12 +598,12 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_backward(const ScanArgs p)
 #pragma unroll
             for (int e = 0; e < VC; ++e) {
                 if ((ends >> r) & 1) ev[e] = last[r][e];
-                const float small = __builtin_fabsf(q[r][e]), large = 1.f - small;
-                const bool keeps = __builtin_bit_cast(int, q[r][e]) >= 0;
+                const Gate a(__builtin_fabsf(q[r][e]), __builtin_bit_cast(int, q[r][e]) >= 0);
                 const float G = d.get(r, e) + ev[e];
-                vx.set(e, (keeps ? small : large) * G);
+                float gx;
+                a.split(G, ev[e], gx);
+                vx.set(e, gx);
                 vz.set(e, w[r][e] * G);
-                ev[e] = (keeps ? large : small) * G;
                 first[r][e] = ev[e];
             }
             store_row(oz, r0 + r, at.n, vz);

@@ -362,7 +362,7 @@ GSR_API gs_status gs_ffn_backward(const gs_ffn_dims* dims, const void* x, int64_
  * over n_seq sequences that lie one after another in `rows` rows.  offsets
  * (device, [n_seq + 1], non-decreasing, first 0, last rows) gives the first row
  * of each sequence; null means n_seq sequences of equal length.  Sequences may
- * be empty.  A state that becomes infinite may come out as NaN in later rows.
+ * be empty.  Infinities in x and the states come out as infinities or NaN.
  * Offsets outside [0, rows] are not followed; other values that are
  * not non-decreasing give unspecified results but no access out of range.
  * gate, x and y [rows, channels] in the type of dims, row strides in elements;

@@ -827,3 +827,17 @@ def test_ffn_float32_few_rows_of_a_large_block():
     o.check(y, ref["y"], tol, "y")
     for name in ("x", "w_gate", "w_up", "w_down"):
         o.check(got[name], ref[name], tol, name)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+@pytest.mark.parametrize("mean", [6.0, 8.0, 10.0, 12.0])
+def test_scan_long_memory(mean, dtype):
+    """Gates that keep the state for 400 to 160,000 rows.  The tolerances of the recurrence, which do not grow with the
+    memory: a itself, rounded next to 1, would leave the state 2^-25 / (1 - a) off, 1.4e-4 for gates of 10."""
+    rows, c = 40000, 6
+    g = gen(93)
+    z = (torch.randn(rows, c, generator=g, device="cuda") * 0.1 + mean).to(dtype)
+    x, dy = ((torch.randn(rows, c, generator=g, device="cuda") + 1).to(dtype) for _ in range(2))
+    offsets = [0, 39000, rows]
+    h0, dl = randn(g, 2, c), randn(g, 2, c)
+    scan_check(z, x, h0, dy, dl, offsets, torch.tensor(offsets, device="cuda"), dtype)
