@@ -626,8 +626,8 @@ __global__ __launch_bounds__(64 * kSpans) void k_scan_backward(const ScanArgs p)
 
 // Rows of a span.  Longer spans leave fewer states to join, shorter ones more waves: 16 rows while that gives 4096
 // waves (16 a CU), longer ones only from 16384 waves on.  Forward + backward of one sequence of 311,296 rows x 256
-// bfloat16 channels took 464 us with spans of 32, 475 with 64, 586 with 128; 50,021 x 192 float32 140 us with spans of
-// 16, 145 with 8.
+// bfloat16 channels took 482 us with spans of 16, 468 with 32, 464 with 64, 607 with 128; 50,021 x 192 float32 161 us
+// with spans of 8, 150 with 16, 166 with 32, 215 with 64.
 int span_rows(const gs_scan_dims& d) {
     const int64_t waves = d.rows * ((d.channels + 127) / 128);
     int s = kBatch;
