@@ -17,8 +17,8 @@
 // once before their products (for float16 they have to stay within its range).  With the result's own rounding, every
 // result carries two.  g and u are kept for the backward pass with 4 (bfloat16) or 5 (float16) bits more than the type
 // has, and with float32's range (KeepHigh): kept in the type they doubled the variance of dx, dWg and dWu, and in
-// float16 the infinite g of a closed gate made NaN of its gradients.  131072 rows of 512 x 2048 x 512 bfloat16: 3.00 ms,
-// 2.82 with g and u in the type, 3.11 with 24 bits of each.  Everything else is float32.
+// float16 the infinite g of a closed gate made NaN of its gradients.  131072 rows of 512 x 2048 x 512 bfloat16 took 3.00
+// ms, 2.82 with g and u in the type, 3.11 with 24 bits of each.  Everything else is float32.
 //
 // Measured, bfloat16 SiLU, 131072 rows of 512 x 2048 x 512, forward and backward 2.93 ms (840 TFLOP/s; the power limit
 // lowers the shader clock to 1.9 GHz); in a kernel trace, us:
@@ -702,7 +702,8 @@ namespace {
 //   131072 x 128 x 512 x 128      1668     1919      8192 x 512 x 2048 x 512       1331     1176
 //   2048 x 512 x 2048 x 512        419      518      4000 x 2048 x 4096 x 2048     4626     3187
 //   1000 x 1000 x 2731 x 1000      609      798      16384 x 1024 x 4096 x 1024    9381     6148
-// (4000 x 512 x 2048 x 512 and 16384 x 256 x 1024 x 256 are within 4 %.)  So: rows of at least 192 values and enough work.
+// (4000 x 512 x 2048 x 512 and 16384 x 256 x 1024 x 256 are within 4 %.)  So: rows of at least 192 values and
+// enough work.
 bool split_f32(const gs_ffn_dims& d) {
     return d.d_in >= 192 && d.d_out >= 192 &&
            (double)d.rows * d.d_hidden * (2.0 * d.d_in + d.d_out) >= 8589934592.0;  // 2^33 multiplications

@@ -3,9 +3,9 @@
 //   X = G / max(|G|_F, eps);  repeat: P = X X^T, Q = b P + c P P, X = a X + Q X        (rows <= cols)
 //   and with P = X^T X, X = a X + X Q for rows > cols, so that P is the smaller square.
 //
-// computed as Q = (a - 1) I + b P + c P P, X = X + Q X: a X and Q X of the first form nearly cancel where a singular value
-// has arrived near 1, and what float16 loses of Q then counts several times (12 x 128 x 512: error 1.34 times that of
-// the result's own bfloat16 rounding, 1.14 in this form; 40 x 77: 1.56 and 1.30).
+// computed as Q = (a - 1) I + b P + c P P, X = X + Q X: a X and Q X of the first form nearly cancel where a singular
+// value has arrived near 1, and what float16 loses of Q then counts several times (12 x 128 x 512: error 1.34 times that
+// of the result's own bfloat16 rounding, 1.15 in this form; 40 x 77: 1.57 and 1.33).
 //
 // All products run on k_gemm16 in float16 with float32 accumulation.  P and Q are symmetric: only tiles on and above
 // the diagonal are computed and each writes its mirror image; with few tiles and many k the sums are split along k.
@@ -737,16 +737,17 @@ hipError_t ortho_any(const gs_ortho_dims& d, const void* g, void* out, char* ws,
 }  // namespace
 
 // Follows the interval [0, 1] of the singular values through the steps: P reaches s^2, Q the largest
-// |a - 1 + b s^2 + c s^4| and X the largest |a s + b s^3 + c s^5| for s in it (at its ends or where the derivative is zero), and
-// no entry of a matrix exceeds its largest singular value.  2 % a step cover the float16 roundings.  The scales are the
-// largest powers of two, up to 2^12 and 2^13, that keep these below float16's 65504.  Below 2^8 the entries that matter
-// come near float16's subnormals: false.
+// |a - 1 + b s^2 + c s^4| and X the largest |a s + b s^3 + c s^5| for s in it (at its ends or where the derivative is
+// zero), and no entry of a matrix exceeds its largest singular value.  2 % a step cover the float16 roundings.  The scales
+// are the largest powers of two, up to 2^12 and 2^13, that keep these below float16's 65504.  Below 2^8 the entries that
+// matter come near float16's subnormals: false.
 bool ortho_scales(const gs_ortho_dims& d, float* x_scale, float* p_scale) {
     const double a = d.a, b = d.b, c = d.c, slack = 1.02, most = 65504.0, least_scale = 256.0;
     double s = slack, top_x = s, top_p = 0.0;
     for (int step = 0; step < d.steps; ++step) {
         const double s2 = s * s;
-        double q = std::max(std::fabs(a - 1.0), std::fabs(a - 1.0 + b * s2 + c * s2 * s2)), next = std::fabs(s * (a + b * s2 + c * s2 * s2));
+        double q = std::max(std::fabs(a - 1.0), std::fabs(a - 1.0 + b * s2 + c * s2 * s2));
+        double next = std::fabs(s * (a + b * s2 + c * s2 * s2));
         if (c != 0.0) {
             const double at = -b / (2.0 * c);
             if (at > 0.0 && at < s2) q = std::max(q, std::fabs(a - 1.0 + b * at + c * at * at));

@@ -54,8 +54,8 @@ struct ScanArgs {
     const int64_t* offsets;
     int64_t n_seq, seq_len, rows, nchunks;
     int C, ncb, span;  // span: rows of a span
-    // [chunk * 8 + span][3][C]: a Span's c and H, and the given state of the last sequence that starts (backward: ends) in the span
-    // on the way through it, unwritten where none does.  Null: no state passes between spans.
+    // [chunk * 8 + span][3][C]: a Span's c and H, and the given state of the last sequence that starts (backward: ends)
+    // in the span on the way through it, unwritten where none does.  Null: no state passes between spans.
     float* agg1;
     float* agg2;       // [chunk][2][C]
     float* state;      // [chunk][C] state entering the chunk
