@@ -42,7 +42,8 @@ ABI_SYMBOLS = ("gs_default_params", "gs_workspace_size", "gs_context_create", "g
                "gs_last_error", "gs_debug_exp2", "gs_debug_export", "gs_debug_topk", "gs_profile_enable",
                "gs_profile_stages", "gs_profile_read", "gs_render_score_noalloc",
                "gs_ffn_sizes", "gs_ffn_forward", "gs_ffn_backward", "gs_scan_sizes", "gs_scan_forward",
-               "gs_scan_backward", "gs_default_ortho_dims", "gs_ortho_size", "gs_orthogonalize")
+               "gs_scan_backward", "gs_default_ortho_dims", "gs_ortho_size", "gs_orthogonalize",
+               "gs_norm_forward", "gs_norm_forward8", "gs_norm_size", "gs_norm_backward", "gs_adamw_step")
 
 
 class gs_gaussians(ctypes.Structure):
@@ -105,6 +106,34 @@ class gs_ortho_dims(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("batch", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("steps", ctypes.c_int32),
                 ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class gs_norm_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("width", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("stream_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32), ("scale_group", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class gs_norm_inputs(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("ld_x", ctypes.c_int64), ("ld_residual", ctypes.c_int64)]
+
+
+class gs_norm_grads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("ld_x", ctypes.c_int64), ("ld_residual", ctypes.c_int64)]
+
+
+class gs_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("lr", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("copy_dtype", ctypes.c_int32)]
+
+
+class gs_adamw_dims(ctypes.Structure):
+    _fields_ = [("n_tensors", ctypes.c_int32), ("state_bits", ctypes.c_int32), ("beta1", ctypes.c_double),
+                ("beta2", ctypes.c_double), ("eps", ctypes.c_double)]
 
 
 class GsrError(RuntimeError):
@@ -187,6 +216,16 @@ def load_library(path: str = LIB_PATH):
     lib.gs_ortho_size.argtypes = [R(gs_ortho_dims), R(Z)]
     lib.gs_orthogonalize.restype = St
     lib.gs_orthogonalize.argtypes = [R(gs_ortho_dims), P, P, P, Z, P]
+    lib.gs_norm_forward.restype = St
+    lib.gs_norm_forward.argtypes = [R(gs_norm_dims), R(gs_norm_inputs), P, I64, P, I64, P]
+    lib.gs_norm_forward8.restype = St
+    lib.gs_norm_forward8.argtypes = [R(gs_norm_dims), R(gs_norm_inputs), P, I64, P, P, I64, P]
+    lib.gs_norm_size.restype = St
+    lib.gs_norm_size.argtypes = [R(gs_norm_dims), R(Z)]
+    lib.gs_norm_backward.restype = St
+    lib.gs_norm_backward.argtypes = [R(gs_norm_dims), P, I64, P, P, I64, P, I64, R(gs_norm_grads), P, Z, P]
+    lib.gs_adamw_step.restype = St
+    lib.gs_adamw_step.argtypes = [R(gs_adamw_dims), R(gs_adamw_tensor), P, P, P, P]
     _lib = lib
     return lib
 
@@ -395,6 +434,35 @@ def gs_ortho_size(dims: gs_ortho_dims) -> int:
 def gs_orthogonalize(dims: gs_ortho_dims, g, out, workspace, stream=None) -> None:
     _check(load_library().gs_orthogonalize(ctypes.byref(dims), _ptr(g), _ptr(out), _ptr(workspace),
                                            _nbytes(workspace), _stream(stream)), "gs_orthogonalize")
+
+
+def gs_norm_forward(dims, inputs: gs_norm_inputs, y, ld_y, h, ld_h, stream=None) -> None:
+    _check(load_library().gs_norm_forward(ctypes.byref(dims), ctypes.byref(inputs), _ptr(y), ld_y, _ptr(h), ld_h,
+                                          _stream(stream)), "gs_norm_forward")
+
+
+def gs_norm_forward8(dims, inputs: gs_norm_inputs, codes, ld_codes, scales, h, ld_h, stream=None) -> None:
+    _check(load_library().gs_norm_forward8(ctypes.byref(dims), ctypes.byref(inputs), _ptr(codes), ld_codes,
+                                           _ptr(scales), _ptr(h), ld_h, _stream(stream)), "gs_norm_forward8")
+
+
+def gs_norm_size(dims: gs_norm_dims) -> int:
+    w = ctypes.c_size_t(0)
+    _check(load_library().gs_norm_size(ctypes.byref(dims), ctypes.byref(w)), "gs_norm_size")
+    return int(w.value)
+
+
+def gs_norm_backward(dims, h, ld_h, weight, dy, ld_dy, dh, ld_dh, grads: gs_norm_grads, workspace,
+                     stream=None) -> None:
+    _check(load_library().gs_norm_backward(ctypes.byref(dims), _ptr(h), ld_h, _ptr(weight), _ptr(dy), ld_dy, _ptr(dh),
+                                           ld_dh, ctypes.byref(grads), _ptr(workspace), _nbytes(workspace),
+                                           _stream(stream)), "gs_norm_backward")
+
+
+def gs_adamw_step(dims: gs_adamw_dims, tensors, steps, grad_scale=None, rate_scale=None, stream=None) -> None:
+    """tensors: a ctypes array of gs_adamw_tensor"""
+    _check(load_library().gs_adamw_step(ctypes.byref(dims), tensors, _ptr(steps), _ptr(grad_scale), _ptr(rate_scale),
+                                        _stream(stream)), "gs_adamw_step")
 
 
 # ---- convenience wrapper ----------------------------------------------------------------------------

@@ -1,0 +1,259 @@
+// adamw.hip -- AdamW step over many tensors in one launch, states in float32 or in 8 bits.
+//
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
+//   p = p - lr wd p - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+//
+// Bound by memory: parameter, gradient and states are read once, parameter, states (and a copy in another type) written
+// once.  The tensors' pointers and sizes travel in the kernel's arguments, so nothing is laid out on the device and
+// gradients may be other tensors at every call; kTensors of them fit, longer lists take several launches.
+//
+// States in 8 bits hold m and sqrt(v) as 8-bit floats with one float32 scale for 256 values (one wave's four a lane): the
+// relative error of a code is at most 2^-4 over a range of 2^15 below the block's largest value, and the root takes v's
+// range down to it.  The update uses the new m and v before they are rounded.  A root above zero never rounds to zero: m
+// would be divided by eps alone where the next gradients are zero (a Gaussian that no view sees).
+//
+// The number of steps done is in device memory, so that a captured step goes on counting when it is replayed.  Every
+// workgroup reads it and then takes a ticket; the last one has to wait for nobody and writes the next number.
+#include <algorithm>
+#include <cmath>
+
+#include "gsr_internal.hpp"
+#include "values.hpp"
+
+namespace gsr {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTensors = 40;    // of one launch: 3.5 KB of arguments
+constexpr int kBlock = 256;     // values that share a scale; one wave takes a block at a time
+constexpr int kChunk = 16;      // blocks a workgroup takes at a time
+constexpr int kGrid = 2048;     // workgroups: 8 on every CU
+
+struct AdamTensor {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    void* copy;
+    int64_t n;
+    float lr, decay;       // decay: lr wd
+    uint32_t chunks_end;   // chunks of the tensors up to this one
+    uint32_t types;        // gs_dtype of p, g (<< 2), copy (<< 4)
+};
+struct AdamArgs {
+    AdamTensor t[kTensors];
+    int64_t* steps;        // [0] done, [1] tickets
+    const float* grad_scale;
+    const float* rate_scale;
+    double log_b1, log_b2;
+    float b1, b2, rest1, rest2, eps;
+    uint32_t chunks;
+    int last;              // the launch that counts the step
+};
+
+// Four values of a type known at run time, from element i; n < 4: the others are zero (not written).
+__device__ __forceinline__ void load4(const void* base, uint32_t type, int64_t i, int n, float* out) {
+    if (type == GS_F32) {
+        const float* p = (const float*)base + i;
+        if (n >= 4)
+            __builtin_memcpy(out, p, 16);
+        else
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[e] = e < n ? p[e] : 0.f;
+        return;
+    }
+    uint16_t h[4];
+    const uint16_t* p = (const uint16_t*)base + i;
+    if (n >= 4)
+        __builtin_memcpy(h, p, 8);
+    else
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = e < n ? p[e] : 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        out[e] = type == GS_BF16 ? (float)__builtin_bit_cast(__bf16, h[e]) : (float)__builtin_bit_cast(_Float16, h[e]);
+}
+__device__ __forceinline__ void store4(void* base, uint32_t type, int64_t i, int n, const float* v) {
+    if (type == GS_F32) {
+        float* p = (float*)base + i;
+        if (n >= 4)
+            __builtin_memcpy(p, v, 16);
+        else
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < n) p[e] = v[e];
+        return;
+    }
+    uint16_t h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        h[e] = type == GS_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)v[e]) : __builtin_bit_cast(uint16_t, (_Float16)v[e]);
+    uint16_t* p = (uint16_t*)base + i;
+    if (n >= 4)
+        __builtin_memcpy(p, h, 8);
+    else
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n) p[e] = h[e];
+}
+
+__device__ __forceinline__ void store_codes4(void* base, int64_t i, int n, uint32_t w) {
+    uint8_t* p = (uint8_t*)base + i;
+    if (n >= 4)
+        __builtin_memcpy(p, &w, 4);
+    else
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n) p[e] = (uint8_t)(w >> (8 * e));
+}
+__device__ __forceinline__ void load_codes4(const void* base, int64_t i, int n, float scale, float* out) {
+    const uint8_t* p = (const uint8_t*)base + i;
+    uint32_t w = 0;
+    if (n >= 4)
+        __builtin_memcpy(&w, p, 4);
+    else
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n) w |= (uint32_t)p[e] << (8 * e);
+    out[0] = __builtin_amdgcn_cvt_f32_fp8((int)w, 0) * scale;
+    out[1] = __builtin_amdgcn_cvt_f32_fp8((int)w, 1) * scale;
+    out[2] = __builtin_amdgcn_cvt_f32_fp8((int)w, 2) * scale;
+    out[3] = __builtin_amdgcn_cvt_f32_fp8((int)w, 3) * scale;
+}
+
+// Codes of a block: the wave's largest magnitude is its scale.
+__device__ __forceinline__ uint32_t encode4(const float* x, bool root, float* scale) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(top, magnitude(x[e]));
+    for (int m = 32; m > 0; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+    const F8Scale s(top);
+    *scale = s.scale;
+    float c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        c[e] = s.code(x[e]);
+        if (root && x[e] > 0.f && c[e] < kF8Min) c[e] = kF8Min;
+    }
+    return pack_f8(c[0], c[1], c[2], c[3]);
+}
+
+template <bool BITS8>
+__global__ __launch_bounds__(kThreads) void k_adamw(const AdamArgs a) {
+    __shared__ int64_t s_step;
+    if (threadIdx.x == 0) {
+        s_step = __hip_atomic_load(&a.steps[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1;
+        if (a.last) {
+            const int64_t ticket = __hip_atomic_fetch_add(&a.steps[1], 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+            if (ticket == (int64_t)gridDim.x - 1) {
+                __hip_atomic_store(&a.steps[1], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                __hip_atomic_store(&a.steps[0], s_step, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+    }
+    __syncthreads();
+    // 1 - b^t = -expm1(t log b), the product in float64
+    const double t = (double)s_step;
+    const float unbias1 = 1.f / -expm1f((float)(t * a.log_b1));
+    const float unbias2 = 1.f / -expm1f((float)(t * a.log_b2));
+    const float gs = a.grad_scale ? *a.grad_scale : 1.f;
+    const float rs = a.rate_scale ? *a.rate_scale : 1.f;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    int k = 0;
+    for (uint32_t chunk = blockIdx.x; chunk < a.chunks; chunk += gridDim.x) {
+        while (chunk >= a.t[k].chunks_end) ++k;
+        const AdamTensor& w = a.t[k];
+        const int64_t block0 = (int64_t)(chunk - (k ? a.t[k - 1].chunks_end : 0)) * kChunk;
+        const uint32_t tp = w.types & 3, tg = (w.types >> 2) & 3, tc = (w.types >> 4) & 3;
+        const float lr = w.lr * rs, decay = w.decay * rs;
+        for (int b = wave; b < kChunk; b += kThreads / 64) {
+            const int64_t block = block0 + b, i = block * kBlock + lane * 4;
+            if (block * kBlock >= w.n) break;
+            const int n = (int)min((int64_t)4, w.n - i);
+            float p[4], g[4], m[4], v[4];
+            load4(w.p, tp, i, n, p);
+            load4(w.g, tg, i, n, g);
+            if constexpr (BITS8) {
+                load_codes4(w.m, i, n, w.m_scale[block], m);
+                load_codes4(w.v, i, n, w.v_scale[block], v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] *= v[e];
+            } else {
+                load4(w.m, GS_F32, i, n, m);
+                load4(w.v, GS_F32, i, n, v);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = g[e] * gs;
+                m[e] = __builtin_fmaf(a.b1, m[e], a.rest1 * x);
+                v[e] = __builtin_fmaf(a.b2, v[e], (a.rest2 * x) * x);
+                const float down = __builtin_sqrtf(v[e] * unbias2) + a.eps;
+                p[e] = p[e] - __builtin_fmaf(decay, p[e], lr * ((m[e] * unbias1) / down));
+            }
+            store4(w.p, tp, i, n, p);
+            if (w.copy) store4(w.copy, tc, i, n, p);
+            if constexpr (BITS8) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = __builtin_sqrtf(v[e]);
+                float sm, sv;
+                const uint32_t cm = encode4(m, false, &sm), cv = encode4(v, true, &sv);
+                store_codes4(w.m, i, n, cm);
+                store_codes4(w.v, i, n, cv);
+                if (lane == 0) {
+                    w.m_scale[block] = sm;
+                    w.v_scale[block] = sv;
+                }
+            } else {
+                store4(w.m, GS_F32, i, n, m);
+                store4(w.v, GS_F32, i, n, v);
+            }
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_adamw(const gs_adamw_dims& d, const gs_adamw_tensor* tensors, int64_t* steps, const float* grad_scale,
+                        const float* rate_scale, hipStream_t st) {
+    AdamArgs a{};
+    a.steps = steps;
+    a.grad_scale = grad_scale;
+    a.rate_scale = rate_scale;
+    a.log_b1 = std::log(d.beta1);
+    a.log_b2 = std::log(d.beta2);
+    a.b1 = (float)d.beta1;
+    a.b2 = (float)d.beta2;
+    a.rest1 = (float)(1.0 - d.beta1);
+    a.rest2 = (float)(1.0 - d.beta2);
+    a.eps = (float)d.eps;
+    int in = 0;
+    auto launch = [&]() {
+        const dim3 grid(std::max<uint32_t>(1, std::min<uint32_t>(a.chunks, kGrid)));
+        if (d.state_bits == 8)
+            k_adamw<true><<<grid, kThreads, 0, st>>>(a);
+        else
+            k_adamw<false><<<grid, kThreads, 0, st>>>(a);
+        a.chunks = 0;
+        in = 0;
+        return hipGetLastError();
+    };
+    for (int i = 0; i < d.n_tensors; ++i) {
+        const gs_adamw_tensor& t = tensors[i];
+        if (!t.grad || t.n == 0) continue;
+        if (in == kTensors) {
+            const hipError_t e = launch();
+            if (e != hipSuccess) return e;
+        }
+        a.chunks += (uint32_t)((t.n + kChunk * kBlock - 1) / (kChunk * kBlock));
+        a.t[in++] = {t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.copy, t.n, t.lr, t.lr * t.weight_decay,
+                     a.chunks, (uint32_t)(t.dtype | t.grad_dtype << 2 | t.copy_dtype << 4)};
+    }
+    a.last = 1;
+    return launch();
+}
+
+}  // namespace gsr

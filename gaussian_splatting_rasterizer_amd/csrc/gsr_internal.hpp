@@ -225,6 +225,18 @@ bool ortho_scales(const gs_ortho_dims& d, float* x_scale, float* p_scale);
 size_t ortho_workspace(const gs_ortho_dims& d);
 hipError_t launch_ortho(const gs_ortho_dims& d, const void* g, void* out, void* ws, hipStream_t st);
 
+// norm.hip, adamw.hip
+constexpr int kNormRegisters = 8192;  // columns of a row that a workgroup holds; longer rows are read again
+size_t norm_workspace(const gs_norm_dims& d);
+// scales: the output is in 8 bits
+hipError_t launch_norm_forward(const gs_norm_dims& d, const gs_norm_inputs& in, void* y, int64_t ldy, float* scales,
+                               void* h, int64_t ldh, hipStream_t st);
+hipError_t launch_norm_backward(const gs_norm_dims& d, const void* h, int64_t ldh, const void* weight, const void* dy,
+                                int64_t lddy, const void* dh, int64_t lddh, const gs_norm_grads& out, void* ws,
+                                hipStream_t st);
+hipError_t launch_adamw(const gs_adamw_dims& d, const gs_adamw_tensor* tensors, int64_t* steps, const float* grad_scale,
+                        const float* rate_scale, hipStream_t st);
+
 // the calling thread's last error message (gs_last_error) and the status to return with it
 gs_status fail(gs_status s, const char* fmt, ...);
 

@@ -1,0 +1,556 @@
+// norm.hip -- root-mean-square norm with the residual's addition, its output in the input's type or in 8 bits, and its
+// gradients.
+//
+//   h = x + residual,  y = h r w,  r = 1 / sqrt(mean(h^2) + eps)
+//   with n = h r and u = dy w:  d = r (u - n mean(u n)) + dh,  dx = dresidual = d,  dw = sum over rows of dy n
+//
+// Bound by memory: every value is read and written once.  A row stays in registers between its sum and its outputs: 16,
+// 32 or 64 lanes hold up to 512 columns (eight each), one wave up to 2048, a workgroup up to 8192; longer rows are read
+// again (from the caches) instead.  Sums are float32.  The forward pass normalises h before it is rounded to the
+// stream's type; the backward pass is given the rounded one and takes r from it again, which costs no reading.
+//
+// The weight's gradient: every workgroup sums its rows in registers and leaves one row of partial sums, which
+// k_norm_weight adds up in a fixed order, so results are the same from run to run.
+#include <algorithm>
+
+#include "gsr_internal.hpp"
+#include "values.hpp"
+
+namespace gsr {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct NormArgs {
+    const void* x;
+    const void* residual;
+    const void* w;
+    void* y;
+    void* h;
+    float* scales;
+    int64_t ldx, ldr, ldy, ldh;
+    int64_t rows;
+    int width, w_f32, group, lanes;  // lanes: of a row, where a wave holds several rows
+    float eps, inv_width;
+};
+
+struct NormBackArgs {
+    const void* h;
+    const void* w;
+    const void* dy;
+    const void* dh;
+    void* dx;
+    void* dr;
+    float* partial;  // [workgroup][width]
+    int64_t ldh, lddy, lddh, lddx, lddr;
+    int64_t rows;
+    int width, w_f32, lanes;
+    float eps, inv_width;
+};
+
+// Reductions over the lanes of a row: `lanes` of a wave, or (WG) the whole workgroup.  LDS is used alternately, so that
+// one barrier a reduction is enough.
+template <bool WG>
+struct RowReduce {
+    uint32_t* lds;  // [2][4]
+    int lanes, turn;
+    __device__ __forceinline__ float sum(float v) {
+        for (int m = (WG ? 64 : lanes) / 2; m > 0; m >>= 1) v += __shfl_xor(v, m);
+        if constexpr (WG) {
+            uint32_t* s = lds + 4 * (turn ^= 1);
+            if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = __builtin_bit_cast(uint32_t, v);
+            __syncthreads();
+            const float* f = (const float*)s;
+            v = (f[0] + f[1]) + (f[2] + f[3]);
+        }
+        return v;
+    }
+    __device__ __forceinline__ uint32_t top(uint32_t v) {
+        for (int m = (WG ? 64 : lanes) / 2; m > 0; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+        if constexpr (WG) {
+            uint32_t* s = lds + 4 * (turn ^= 1);
+            if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+            __syncthreads();
+            v = max(max(s[0], s[1]), max(s[2], s[3]));
+        }
+        return v;
+    }
+};
+
+// Columns of a thread's i-th run and how many of them there are.
+template <bool WG>
+__device__ __forceinline__ int column(int i, int lane_in_row, int lanes) {
+    return (i * (WG ? kThreads : lanes) + lane_in_row) * 8;
+}
+
+template <class T>
+__device__ __forceinline__ void load_weight(const void* w, bool f32, int col, int n, float* out) {
+    if (f32) {
+        Run8<float> r;
+        r.load((const float*)w + col, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[e] = r.get(e);
+    } else {
+        Run8<T> r;
+        r.load((const T*)w + col, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) out[e] = r.get(e);
+    }
+}
+
+// Codes of one run: the scale of its group (of `share` lanes; the row's where `row_top` is given) and eight bytes.
+__device__ __forceinline__ void store_codes(const NormArgs& p, int64_t row, int col, int n, const float* v, int share,
+                                            bool whole, uint32_t row_top) {
+    uint32_t top = row_top;
+    if (!whole) {
+        top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[e]));
+        for (int m = share / 2; m > 0; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+    }
+    const F8Scale s(top);
+    if (n <= 0) return;
+    if (whole) {
+        if (col == 0) p.scales[row] = s.scale;
+    } else if (col % p.group == 0) {
+        p.scales[row * ((p.width + p.group - 1) / p.group) + col / p.group] = s.scale;
+    }
+    float c[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) c[e] = s.code(v[e]);
+    const uint32_t words[2] = {pack_f8(c[0], c[1], c[2], c[3]), pack_f8(c[4], c[5], c[6], c[7])};
+    uint8_t* out = (uint8_t*)p.y + row * p.ldy + col;
+    if (n >= 8) {
+        __builtin_memcpy(out, words, 8);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < n) out[e] = (uint8_t)(words[e >> 2] >> (8 * (e & 3)));
+    }
+}
+
+// NV runs of a thread; WG: a row per workgroup.  OUT8: y are codes.
+template <class T, class R, int NV, bool WG, bool OUT8>
+__global__ __launch_bounds__(kThreads) void k_norm(const NormArgs p) {
+    __shared__ uint32_t s_red[8];
+    const int lanes = WG ? kThreads : p.lanes;
+    const int per = kThreads / lanes, slot = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    RowReduce<WG> red{s_red, lanes, 0};
+    float w[NV][8];
+    int n[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int col = column<WG>(i, lane, lanes);
+        n[i] = min(8, p.width - col);
+        load_weight<T>(p.w, p.w_f32, col, n[i], w[i]);
+    }
+    // all threads make the same number of turns: rows past the end are read as row rows - 1 and not written
+    const int64_t step = (int64_t)gridDim.x * per;
+    for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < p.rows; row0 += step) {
+        const bool live = row0 + slot < p.rows;
+        const int64_t row = live ? row0 + slot : p.rows - 1;
+        Run8<T> x[NV];
+        Run8<R> r[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) x[i].load((const T*)p.x + row * p.ldx + column<WG>(i, lane, lanes), n[i]);
+        if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                r[i].load((const R*)p.residual + row * p.ldr + column<WG>(i, lane, lanes), n[i]);
+        }
+        float h[NV][8], s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                h[i][e] = p.residual ? x[i].get(e) + r[i].get(e) : x[i].get(e);
+                s = __builtin_fmaf(h[i][e], h[i][e], s);
+            }
+        const float rstd = 1.f / __builtin_sqrtf(__builtin_fmaf(red.sum(s), p.inv_width, p.eps));
+        if (p.h && live) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                Run8<R> o;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o.set(e, h[i][e]);
+                o.store((R*)p.h + row * p.ldh + column<WG>(i, lane, lanes), n[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[i][e] = (h[i][e] * rstd) * w[i][e];
+        if constexpr (OUT8) {
+            uint32_t top = 0;
+            if (p.group == 0) {
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = max(top, magnitude(h[i][e]));
+                top = red.top(top);
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                store_codes(p, row, column<WG>(i, lane, lanes), live ? n[i] : 0, h[i], p.group / 8, p.group == 0, top);
+        } else if (live) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                Run8<T> o;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o.set(e, h[i][e]);
+                o.store((T*)p.y + row * p.ldy + column<WG>(i, lane, lanes), n[i]);
+            }
+        }
+    }
+}
+
+// Rows longer than a workgroup's registers: one workgroup a row, which reads it once for the sum, (codes of a whole row)
+// once for the largest value and once for the outputs.
+template <class T, class R, bool OUT8>
+__global__ __launch_bounds__(kThreads) void k_norm_wide(const NormArgs p) {
+    __shared__ uint32_t s_red[8];
+    RowReduce<true> red{s_red, kThreads, 0};
+    const int turns = (p.width + kThreads * 8 - 1) / (kThreads * 8);
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        auto sum_of = [&](int col, int n, float* h) {
+            Run8<T> x;
+            x.load((const T*)p.x + row * p.ldx + col, n);
+            Run8<R> r;
+            if (p.residual) r.load((const R*)p.residual + row * p.ldr + col, n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = p.residual ? x.get(e) + r.get(e) : x.get(e);
+        };
+        float s = 0.f;
+        for (int i = 0; i < turns; ++i) {
+            const int col = column<true>(i, threadIdx.x, kThreads);
+            float h[8];
+            sum_of(col, min(8, p.width - col), h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = __builtin_fmaf(h[e], h[e], s);
+        }
+        const float rstd = 1.f / __builtin_sqrtf(__builtin_fmaf(red.sum(s), p.inv_width, p.eps));
+        uint32_t top = 0;
+        if (OUT8 && p.group == 0) {
+            for (int i = 0; i < turns; ++i) {
+                const int col = column<true>(i, threadIdx.x, kThreads), n = min(8, p.width - col);
+                float h[8], w[8];
+                sum_of(col, n, h);
+                load_weight<T>(p.w, p.w_f32, col, n, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = max(top, magnitude((h[e] * rstd) * w[e]));
+            }
+            top = red.top(top);
+        }
+        for (int i = 0; i < turns; ++i) {
+            const int col = column<true>(i, threadIdx.x, kThreads), n = min(8, p.width - col);
+            float h[8], w[8];
+            sum_of(col, n, h);
+            load_weight<T>(p.w, p.w_f32, col, n, w);
+            if (p.h) {
+                Run8<R> o;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o.set(e, h[e]);
+                o.store((R*)p.h + row * p.ldh + col, n);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = (h[e] * rstd) * w[e];
+            if constexpr (OUT8) {
+                store_codes(p, row, col, n, h, p.group / 8, p.group == 0, top);
+            } else {
+                Run8<T> o;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o.set(e, h[e]);
+                o.store((T*)p.y + row * p.ldy + col, n);
+            }
+        }
+    }
+}
+
+template <class T, class R>
+__device__ __forceinline__ void store_grads(const NormBackArgs& p, int64_t row, int col, int n, const float* d) {
+    if (p.dx) {
+        Run8<T> o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o.set(e, d[e]);
+        o.store((T*)p.dx + row * p.lddx + col, n);
+    }
+    if (p.dr) {
+        Run8<R> o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o.set(e, d[e]);
+        o.store((R*)p.dr + row * p.lddr + col, n);
+    }
+}
+
+template <class T, class R, int NV, bool WG>
+__global__ __launch_bounds__(kThreads) void k_norm_backward(const NormBackArgs p) {
+    __shared__ uint32_t s_red[8];
+    __shared__ float s_dw[WG ? 1 : kThreads * 8];
+    const int lanes = WG ? kThreads : p.lanes;
+    const int per = kThreads / lanes, slot = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+    RowReduce<WG> red{s_red, lanes, 0};
+    float w[NV][8], dw[NV][8];
+    int n[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int col = column<WG>(i, lane, lanes);
+        n[i] = min(8, p.width - col);
+        load_weight<T>(p.w, p.w_f32, col, n[i], w[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
+    }
+    const int64_t step = (int64_t)gridDim.x * per;
+    for (int64_t row0 = (int64_t)blockIdx.x * per; row0 < p.rows; row0 += step) {
+        const bool live = row0 + slot < p.rows;
+        const int64_t row = live ? row0 + slot : p.rows - 1;
+        Run8<R> h[NV], g[NV];
+        Run8<T> dy[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) h[i].load((const R*)p.h + row * p.ldh + column<WG>(i, lane, lanes), n[i]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) dy[i].load((const T*)p.dy + row * p.lddy + column<WG>(i, lane, lanes), n[i]);
+        if (p.dh) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) g[i].load((const R*)p.dh + row * p.lddh + column<WG>(i, lane, lanes), n[i]);
+        }
+        float s = 0.f, t = 0.f;  // of h^2 and of u h
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = h[i].get(e);
+                s = __builtin_fmaf(v, v, s);
+                t = __builtin_fmaf(dy[i].get(e) * w[i][e], v, t);
+            }
+        const float rstd = 1.f / __builtin_sqrtf(__builtin_fmaf(red.sum(s), p.inv_width, p.eps));
+        const float c = red.sum(t) * rstd * p.inv_width;  // mean(u n)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float d[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float unit = h[i].get(e) * rstd;
+                if (live) dw[i][e] = __builtin_fmaf(dy[i].get(e), unit, dw[i][e]);
+                d[e] = rstd * __builtin_fmaf(-unit, c, dy[i].get(e) * w[i][e]);
+                if (p.dh) d[e] += g[i].get(e);
+            }
+            if (live) store_grads<T, R>(p, row, column<WG>(i, lane, lanes), n[i], d);
+        }
+    }
+    if (!p.partial) return;
+    // the workgroup's rows of one run after another: slots are added in their order
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int col = column<WG>(i, lane, lanes);
+        if constexpr (!WG) {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s_dw[threadIdx.x * 8 + e] = dw[i][e];
+            __syncthreads();
+            if (slot == 0)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    for (int k = 1; k < per; ++k) dw[i][e] += s_dw[(k * lanes + lane) * 8 + e];
+        }
+        if (WG || slot == 0)
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n[i]) p.partial[(int64_t)blockIdx.x * p.width + col + e] = dw[i][e];
+    }
+}
+
+// Long rows: r goes to rstd, from which k_norm_weight_wide takes the weight's sums column by column.
+template <class T, class R>
+__global__ __launch_bounds__(kThreads) void k_norm_backward_wide(const NormBackArgs p, float* rstds) {
+    __shared__ uint32_t s_red[8];
+    RowReduce<true> red{s_red, kThreads, 0};
+    const int turns = (p.width + kThreads * 8 - 1) / (kThreads * 8);
+    for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+        float s = 0.f, t = 0.f;
+        for (int i = 0; i < turns; ++i) {
+            const int col = column<true>(i, threadIdx.x, kThreads), n = min(8, p.width - col);
+            Run8<R> h;
+            Run8<T> dy;
+            float w[8];
+            h.load((const R*)p.h + row * p.ldh + col, n);
+            dy.load((const T*)p.dy + row * p.lddy + col, n);
+            load_weight<T>(p.w, p.w_f32, col, n, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s = __builtin_fmaf(h.get(e), h.get(e), s);
+                t = __builtin_fmaf(dy.get(e) * w[e], h.get(e), t);
+            }
+        }
+        const float rstd = 1.f / __builtin_sqrtf(__builtin_fmaf(red.sum(s), p.inv_width, p.eps));
+        const float c = red.sum(t) * rstd * p.inv_width;
+        if (rstds && threadIdx.x == 0) rstds[row] = rstd;
+        for (int i = 0; i < turns; ++i) {
+            const int col = column<true>(i, threadIdx.x, kThreads), n = min(8, p.width - col);
+            Run8<R> h, g;
+            Run8<T> dy;
+            float w[8], d[8];
+            h.load((const R*)p.h + row * p.ldh + col, n);
+            dy.load((const T*)p.dy + row * p.lddy + col, n);
+            if (p.dh) g.load((const R*)p.dh + row * p.lddh + col, n);
+            load_weight<T>(p.w, p.w_f32, col, n, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                d[e] = rstd * __builtin_fmaf(-(h.get(e) * rstd), c, dy.get(e) * w[e]);
+                if (p.dh) d[e] += g.get(e);
+            }
+            store_grads<T, R>(p, row, col, n, d);
+        }
+    }
+}
+
+// Partial sums of the weight's gradient over every gridDim.y-th row, a thread per column.
+template <class T, class R>
+__global__ __launch_bounds__(kThreads) void k_norm_partial_wide(const NormBackArgs p, const float* rstds) {
+    const int col = blockIdx.x * kThreads + threadIdx.x;
+    if (col >= p.width) return;
+    float s = 0.f;
+    for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y)
+        s = __builtin_fmaf((float)((const T*)p.dy)[row * p.lddy + col], (float)((const R*)p.h)[row * p.ldh + col] * rstds[row],
+                           s);
+    p.partial[(int64_t)blockIdx.y * p.width + col] = s;
+}
+
+// Adds up `parts` rows of partial sums: 16 columns a workgroup, 16 threads a column, each every 16th row.
+template <class W>
+__global__ __launch_bounds__(kThreads) void k_norm_weight(const float* partial, int parts, int width, W* dw) {
+    __shared__ float s_sum[16][17];
+    const int c = threadIdx.x & 15, k = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
+    float s = 0.f;
+    if (col < width) {
+#pragma unroll 8
+        for (int i = k; i < parts; i += 16) s += partial[(int64_t)i * width + col];
+    }
+    s_sum[k][c] = s;
+    __syncthreads();
+    if (k == 0 && col < width) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) s += s_sum[i][c];
+        dw[col] = (W)s;
+    }
+}
+
+// How a width is spread: NV runs a thread (0: long rows), a row per workgroup, lanes of a row
+struct NormShape {
+    int nv;
+    bool wg;
+    int lanes;
+};
+NormShape norm_shape(int width) {
+    if (width <= 512) return {1, false, width <= 128 ? 16 : width <= 256 ? 32 : 64};
+    if (width <= 1024) return {2, false, 64};
+    if (width <= 2048) return {4, false, 64};
+    if (width <= kNormRegisters) return {4, true, kThreads};
+    return {0, true, kThreads};
+}
+
+// Workgroups: enough to fill the card several times over; a workgroup of the backward pass leaves a row of partial sums.
+int64_t norm_grid(const gs_norm_dims& d, int64_t most) {
+    const NormShape s = norm_shape(d.width);
+    const int64_t per = s.wg ? 1 : kThreads / s.lanes;
+    return std::min<int64_t>(most, (d.rows + per - 1) / per);
+}
+constexpr int64_t kForwardGrid = 4096, kBackwardGrid = 1024;
+constexpr int kWideParts = 64;
+
+template <class F>
+hipError_t with_types(const gs_norm_dims& d, F&& f) {
+    if (d.dtype == GS_F32) return f(float{}, float{});
+    if (d.dtype == GS_BF16) return d.stream_dtype == GS_F32 ? f(__bf16{}, float{}) : f(__bf16{}, __bf16{});
+    return d.stream_dtype == GS_F32 ? f(_Float16{}, float{}) : f(_Float16{}, _Float16{});
+}
+
+template <bool OUT8>
+hipError_t norm_forward(const gs_norm_dims& d, const NormArgs& a, hipStream_t st) {
+    const NormShape s = norm_shape(d.width);
+    const dim3 grid((unsigned)norm_grid(d, kForwardGrid));
+    return with_types(d, [&](auto t, auto r) {
+        using T = decltype(t);
+        using R = decltype(r);
+        if (s.nv == 0)
+            k_norm_wide<T, R, OUT8><<<grid, kThreads, 0, st>>>(a);
+        else if (s.wg)
+            k_norm<T, R, 4, true, OUT8><<<grid, kThreads, 0, st>>>(a);
+        else if (s.nv == 4)
+            k_norm<T, R, 4, false, OUT8><<<grid, kThreads, 0, st>>>(a);
+        else if (s.nv == 2)
+            k_norm<T, R, 2, false, OUT8><<<grid, kThreads, 0, st>>>(a);
+        else
+            k_norm<T, R, 1, false, OUT8><<<grid, kThreads, 0, st>>>(a);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace
+
+size_t norm_workspace(const gs_norm_dims& d) {
+    if (d.rows == 0) return 0;
+    if (norm_shape(d.width).nv == 0)
+        return ((size_t)d.rows * 4 + 255) / 256 * 256 + (size_t)std::min<int64_t>(kWideParts, d.rows) * d.width * 4;
+    return (size_t)norm_grid(d, kBackwardGrid) * d.width * 4;
+}
+
+hipError_t launch_norm_forward(const gs_norm_dims& d, const gs_norm_inputs& in, void* y, int64_t ldy, float* scales,
+                               void* h, int64_t ldh, hipStream_t st) {
+    if (d.rows == 0) return hipSuccess;
+    const NormArgs a{in.x,  in.residual, in.weight, y,       h,
+                     scales, in.ld_x,     in.ld_residual, ldy, ldh,
+                     d.rows, d.width,     d.weight_dtype == GS_F32, d.scale_group, norm_shape(d.width).lanes,
+                     d.eps,  1.f / (float)d.width};
+    return scales ? norm_forward<true>(d, a, st) : norm_forward<false>(d, a, st);
+}
+
+hipError_t launch_norm_backward(const gs_norm_dims& d, const void* h, int64_t ldh, const void* weight, const void* dy,
+                                int64_t lddy, const void* dh, int64_t lddh, const gs_norm_grads& out, void* ws,
+                                hipStream_t st) {
+    const NormShape s = norm_shape(d.width);
+    const bool wide = s.nv == 0;
+    float* rstds = wide && out.weight ? (float*)ws : nullptr;
+    float* partial = !out.weight ? nullptr : wide ? (float*)((char*)ws + ((size_t)d.rows * 4 + 255) / 256 * 256) : (float*)ws;
+    const NormBackArgs a{h,    weight, dy,      dh,         out.x,          out.residual, partial, ldh,
+                         lddy, lddh,   out.ld_x, out.ld_residual, d.rows, d.width, d.weight_dtype == GS_F32, s.lanes,
+                         d.eps, 1.f / (float)d.width};
+    int parts = 0;
+    if (d.rows > 0) {
+        const dim3 grid((unsigned)norm_grid(d, kBackwardGrid));
+        parts = (int)grid.x;
+        const hipError_t e = with_types(d, [&](auto t, auto r) {
+            using T = decltype(t);
+            using R = decltype(r);
+            if (wide) {
+                k_norm_backward_wide<T, R><<<grid, kThreads, 0, st>>>(a, rstds);
+                if (partial) {
+                    parts = (int)std::min<int64_t>(kWideParts, d.rows);
+                    k_norm_partial_wide<T, R>
+                        <<<dim3((d.width + kThreads - 1) / kThreads, parts), kThreads, 0, st>>>(a, rstds);
+                }
+            } else if (s.wg) {
+                k_norm_backward<T, R, 4, true><<<grid, kThreads, 0, st>>>(a);
+            } else if (s.nv == 4) {
+                k_norm_backward<T, R, 4, false><<<grid, kThreads, 0, st>>>(a);
+            } else if (s.nv == 2) {
+                k_norm_backward<T, R, 2, false><<<grid, kThreads, 0, st>>>(a);
+            } else {
+                k_norm_backward<T, R, 1, false><<<grid, kThreads, 0, st>>>(a);
+            }
+            return hipGetLastError();
+        });
+        if (e != hipSuccess) return e;
+    }
+    if (!out.weight) return hipSuccess;
+    const dim3 grid((d.width + 15) / 16);
+    if (d.weight_dtype == GS_F32)
+        k_norm_weight<<<grid, kThreads, 0, st>>>(partial, parts, d.width, (float*)out.weight);
+    else if (d.weight_dtype == GS_BF16)
+        k_norm_weight<<<grid, kThreads, 0, st>>>(partial, parts, d.width, (__bf16*)out.weight);
+    else
+        k_norm_weight<<<grid, kThreads, 0, st>>>(partial, parts, d.width, (_Float16*)out.weight);
+    return hipGetLastError();
+}
+
+}  // namespace gsr

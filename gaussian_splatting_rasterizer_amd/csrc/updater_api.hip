@@ -1,5 +1,7 @@
 // updater_api.hip -- the ABI calls of the learned updater's operators: argument checks and launches.
+#include <algorithm>
 #include <cmath>
+#include <vector>
 
 #include "gsr_internal.hpp"
 
@@ -10,6 +12,7 @@ namespace {
 constexpr int64_t kMaxRows = (1ll << 31) - 512;
 constexpr int64_t kMaxWidth = 1 << 20;
 constexpr int64_t kMaxStride = 1 << 21;
+constexpr int64_t kMaxAdamValues = 1ll << 40;
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 size_t elem(int dtype) { return dtype == GS_F32 ? 4 : 2; }
@@ -132,6 +135,107 @@ gs_status check_ortho(const char* call, const gs_ortho_dims* d) {
     if (!ortho_scales(*d, &xs, &ps))
         return fail(GS_ERR_UNSUPPORTED, "%s: %d steps with coefficients %g, %g, %g leave float16's range", call,
                     d->steps, (double)d->a, (double)d->b, (double)d->c);
+    return GS_OK;
+}
+
+// Rows of an array in memory, as an interval.
+struct Extent {
+    uintptr_t lo, hi;
+    const void* p;
+    int64_t ld;
+    const char* name;
+    static Extent of(const char* name, const void* p, int64_t rows, int64_t width, int64_t ld, size_t e) {
+        if (!p || rows == 0) return {0, 0, nullptr, 0, name};
+        const uintptr_t a = (uintptr_t)p;
+        return {a, a + (uintptr_t)(((rows - 1) * ld + width) * (int64_t)e), p, ld, name};
+    }
+};
+
+// An output may be an input that `same` allows it to replace element by element, and nothing else.
+gs_status check_output(const char* call, const Extent& out, const Extent& other, bool same) {
+    if (!out.p || !other.p || out.hi <= other.lo || other.hi <= out.lo) return GS_OK;
+    if (same && out.p == other.p && out.ld == other.ld) return GS_OK;
+    return fail(GS_ERR_INVALID_ARGUMENT, "%s: %s overlaps %s%s", call, out.name, other.name,
+                same ? " without being it" : "");
+}
+
+gs_status check_norm(const char* call, const gs_norm_dims* d, bool codes) {
+    if (!d) return fail(GS_ERR_INVALID_ARGUMENT, "%s: dims is null", call);
+    GSR_CHECK(check_dtype(call, d->dtype));
+    for (int t : {d->stream_dtype, d->weight_dtype})
+        if (t != d->dtype && t != GS_F32)
+            return fail(GS_ERR_INVALID_ARGUMENT, "%s: stream and weight are of dtype or float32, got %d", call, t);
+    if (codes && d->scale_group != 0 && d->scale_group != 32 && d->scale_group != 64 && d->scale_group != 128)
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: scale_group %d is not 0, 32, 64 or 128", call, d->scale_group);
+    if (!(d->eps >= 0.f) || !std::isfinite(d->eps))
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: eps must be finite and not negative", call);
+    if (d->rows < 0 || d->width < 1)
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: rows %lld, width %d", call, (long long)d->rows, d->width);
+    if (d->rows > kMaxRows || d->width > kMaxWidth)
+        return fail(GS_ERR_UNSUPPORTED, "%s: rows %lld, width %d exceed the limits", call, (long long)d->rows, d->width);
+    return GS_OK;
+}
+
+gs_status norm_forward(const char* call, const gs_norm_dims* d, const gs_norm_inputs* in, void* y, int64_t ld_y,
+                       bool codes, float* scales, void* h, int64_t ld_h, hipStream_t stream) {
+    GSR_CHECK(check_norm(call, d, codes));
+    if (!in) return fail(GS_ERR_INVALID_ARGUMENT, "%s: inputs is null", call);
+    const size_t e = elem(d->dtype), es = elem(d->stream_dtype), ew = elem(d->weight_dtype), ey = codes ? 1 : e;
+    GSR_CHECK(check_array(call, "x", in->x, d->rows, d->width, in->ld_x, e));
+    if (in->residual) GSR_CHECK(check_array(call, "residual", in->residual, d->rows, d->width, in->ld_residual, es));
+    GSR_CHECK(check_array(call, "weight", in->weight, d->rows, d->width, d->width, ew));
+    GSR_CHECK(check_array(call, codes ? "codes" : "y", y, d->rows, d->width, ld_y, ey));
+    if (codes) GSR_CHECK(check_array(call, "scales", scales, d->rows, 0, 0, 4));
+    if (h) GSR_CHECK(check_array(call, "h", h, d->rows, d->width, ld_h, es));
+    if (d->rows == 0) return GS_OK;
+    const int64_t groups = codes && d->scale_group ? (d->width + d->scale_group - 1) / d->scale_group : 1;
+    const Extent x = Extent::of("x", in->x, d->rows, d->width, in->ld_x, e),
+                 r = Extent::of("residual", in->residual, d->rows, d->width, in->ld_residual, es),
+                 w = Extent::of("weight", in->weight, 1, d->width, d->width, ew),
+                 oy = Extent::of(codes ? "codes" : "y", y, d->rows, d->width, ld_y, ey),
+                 oh = Extent::of("h", h, d->rows, d->width, ld_h, es),
+                 os = Extent::of("scales", codes ? scales : nullptr, d->rows, groups, groups, 4);
+    GSR_CHECK(check_output(call, oy, x, !codes));
+    GSR_CHECK(check_output(call, oy, r, false));
+    GSR_CHECK(check_output(call, oh, r, true));
+    GSR_CHECK(check_output(call, oh, x, false));
+    for (const Extent& o : {oy, oh, os}) GSR_CHECK(check_output(call, o, w, false));
+    for (const Extent& o : {x, r, oy, oh}) GSR_CHECK(check_output(call, os, o, false));
+    GSR_CHECK(check_output(call, oy, oh, false));
+    return launched(launch_norm_forward(*d, *in, y, ld_y, codes ? scales : nullptr, h, ld_h, stream), call);
+}
+
+// Arrays that are written must not overlap each other or one that is read.
+gs_status check_adamw_overlap(const char* call, const gs_adamw_dims* d, const gs_adamw_tensor* tensors,
+                              const int64_t* steps) {
+    std::vector<Extent> written;
+    written.reserve(6 * (size_t)d->n_tensors + 1);
+    written.push_back(Extent::of("steps", steps, 1, 2, 2, 8));
+    for (int i = 0; i < d->n_tensors; ++i) {
+        const gs_adamw_tensor& t = tensors[i];
+        if (!t.grad || t.n == 0) continue;
+        const size_t es = d->state_bits == 8 ? 1 : 4;
+        const int64_t blocks = (t.n + 255) / 256;
+        written.push_back(Extent::of("param", t.param, 1, t.n, t.n, elem(t.dtype)));
+        written.push_back(Extent::of("m", t.m, 1, t.n, t.n, es));
+        written.push_back(Extent::of("v", t.v, 1, t.n, t.n, es));
+        if (t.copy) written.push_back(Extent::of("copy", t.copy, 1, t.n, t.n, elem(t.copy_dtype)));
+        if (d->state_bits == 8) {
+            written.push_back(Extent::of("m_scale", t.m_scale, 1, blocks, blocks, 4));
+            written.push_back(Extent::of("v_scale", t.v_scale, 1, blocks, blocks, 4));
+        }
+    }
+    std::sort(written.begin(), written.end(), [](const Extent& a, const Extent& b) { return a.lo < b.lo; });
+    for (size_t i = 1; i < written.size(); ++i) GSR_CHECK(check_output(call, written[i], written[i - 1], false));
+    for (int i = 0; i < d->n_tensors; ++i) {
+        const gs_adamw_tensor& t = tensors[i];
+        if (!t.grad || t.n == 0) continue;
+        const Extent g = Extent::of("a gradient", t.grad, 1, t.n, t.n, elem(t.grad_dtype));
+        // the first that ends behind the gradient's start
+        const auto at = std::upper_bound(written.begin(), written.end(), g.lo,
+                                         [](uintptr_t lo, const Extent& w) { return lo < w.hi; });
+        if (at != written.end()) GSR_CHECK(check_output(call, *at, g, false));
+    }
     return GS_OK;
 }
 
@@ -261,6 +365,108 @@ gs_status gs_orthogonalize(const gs_ortho_dims* dims, const void* g, void* out, 
     GSR_CHECK(check_array(call, "out", out, 1, 0, 0, elem(dims->out_dtype)));
     GSR_CHECK(check_workspace(call, workspace, workspace_bytes, ortho_workspace(*dims)));
     return launched(launch_ortho(*dims, g, out, workspace, stream), call);
+}
+
+gs_status gs_norm_forward(const gs_norm_dims* dims, const gs_norm_inputs* in, void* y, int64_t ld_y, void* h,
+                          int64_t ld_h, hipStream_t stream) {
+    return norm_forward("gs_norm_forward", dims, in, y, ld_y, false, nullptr, h, ld_h, stream);
+}
+
+gs_status gs_norm_forward8(const gs_norm_dims* dims, const gs_norm_inputs* in, void* codes, int64_t ld_codes,
+                           float* scales, void* h, int64_t ld_h, hipStream_t stream) {
+    return norm_forward("gs_norm_forward8", dims, in, codes, ld_codes, true, scales, h, ld_h, stream);
+}
+
+gs_status gs_norm_size(const gs_norm_dims* dims, size_t* backward_bytes) {
+    GSR_CHECK(check_norm("gs_norm_size", dims, false));
+    if (!backward_bytes) return fail(GS_ERR_INVALID_ARGUMENT, "gs_norm_size: null argument");
+    *backward_bytes = norm_workspace(*dims);
+    return GS_OK;
+}
+
+gs_status gs_norm_backward(const gs_norm_dims* dims, const void* h, int64_t ld_h, const void* weight, const void* dy,
+                           int64_t ld_dy, const void* dh, int64_t ld_dh, const gs_norm_grads* grads, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+    const char* call = "gs_norm_backward";
+    const gs_norm_dims* d = dims;
+    GSR_CHECK(check_norm(call, d, false));
+    if (!grads) return fail(GS_ERR_INVALID_ARGUMENT, "%s: grads is null", call);
+    const size_t e = elem(d->dtype), es = elem(d->stream_dtype), ew = elem(d->weight_dtype);
+    GSR_CHECK(check_array(call, "h", h, d->rows, d->width, ld_h, es));
+    GSR_CHECK(check_array(call, "weight", weight, d->rows, d->width, d->width, ew));
+    GSR_CHECK(check_array(call, "dy", dy, d->rows, d->width, ld_dy, e));
+    if (dh) GSR_CHECK(check_array(call, "dh", dh, d->rows, d->width, ld_dh, es));
+    if (grads->x) GSR_CHECK(check_array(call, "grads.x", grads->x, d->rows, d->width, grads->ld_x, e));
+    if (grads->residual)
+        GSR_CHECK(check_array(call, "grads.residual", grads->residual, d->rows, d->width, grads->ld_residual, es));
+    if (!aligned(grads->weight, ew))
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: grads.weight is not %zu-byte aligned", call, ew);
+    const Extent ih = Extent::of("h", h, d->rows, d->width, ld_h, es),
+                 iw = Extent::of("weight", weight, 1, d->width, d->width, ew),
+                 iy = Extent::of("dy", dy, d->rows, d->width, ld_dy, e),
+                 ig = Extent::of("dh", dh, d->rows, d->width, ld_dh, es),
+                 ox = Extent::of("grads.x", grads->x, d->rows, d->width, grads->ld_x, e),
+                 orr = Extent::of("grads.residual", grads->residual, d->rows, d->width, grads->ld_residual, es),
+                 ow = Extent::of("grads.weight", grads->weight, 1, d->width, d->width, ew);
+    // the long rows' weight gradient reads dy and h after the other gradients are written
+    const bool in_place = !grads->weight || d->width <= kNormRegisters;
+    for (const Extent& o : {ox, orr}) {
+        GSR_CHECK(check_output(call, o, ih, false));
+        GSR_CHECK(check_output(call, o, iw, false));
+        GSR_CHECK(check_output(call, o, ow, false));
+    }
+    GSR_CHECK(check_output(call, ox, iy, in_place));
+    GSR_CHECK(check_output(call, ox, ig, e == es));
+    GSR_CHECK(check_output(call, orr, iy, in_place && e == es));
+    GSR_CHECK(check_output(call, orr, ig, true));
+    GSR_CHECK(check_output(call, ox, orr, false));
+    for (const Extent& i : {ih, iw, iy, ig}) GSR_CHECK(check_output(call, ow, i, false));
+    const size_t need = grads->weight ? norm_workspace(*d) : 0;
+    GSR_CHECK(check_workspace(call, workspace, workspace_bytes, need));
+    return launched(launch_norm_backward(*d, h, ld_h, weight, dy, ld_dy, dh, ld_dh, *grads, workspace, stream), call);
+}
+
+gs_status gs_adamw_step(const gs_adamw_dims* dims, const gs_adamw_tensor* tensors, int64_t* steps,
+                        const float* grad_scale, const float* rate_scale, hipStream_t stream) {
+    const char* call = "gs_adamw_step";
+    if (!dims) return fail(GS_ERR_INVALID_ARGUMENT, "%s: dims is null", call);
+    const gs_adamw_dims& d = *dims;
+    if (d.n_tensors < 0 || (d.n_tensors > 0 && !tensors))
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: %d tensors, or their array is null", call, d.n_tensors);
+    if (d.state_bits != 32 && d.state_bits != 8)
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: state_bits %d is not 32 or 8", call, d.state_bits);
+    for (double b : {d.beta1, d.beta2})
+        if (!(b >= 0.0 && b < 1.0)) return fail(GS_ERR_INVALID_ARGUMENT, "%s: beta %g is not in [0, 1)", call, b);
+    if (!((float)d.eps > 0.f) || !std::isfinite(d.eps))
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: eps must be positive (as a float32) and finite", call);
+    if (!steps || !aligned(steps, 8) || !aligned(grad_scale, 4) || !aligned(rate_scale, 4))
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: steps is null, or a scalar is misaligned", call);
+    int64_t values = 0;
+    for (int i = 0; i < d.n_tensors; ++i) {
+        const gs_adamw_tensor& t = tensors[i];
+        if (t.n < 0) return fail(GS_ERR_INVALID_ARGUMENT, "%s: tensor %d has %lld values", call, i, (long long)t.n);
+        if (t.n > kMaxAdamValues || (values += t.n) > kMaxAdamValues)
+            return fail(GS_ERR_UNSUPPORTED, "%s: more than 2^40 values", call);
+        if (!t.grad || t.n == 0) continue;
+        GSR_CHECK(check_dtype(call, t.dtype));
+        GSR_CHECK(check_dtype(call, t.grad_dtype));
+        if (t.copy) GSR_CHECK(check_dtype(call, t.copy_dtype));
+        if (!std::isfinite(t.lr) || !std::isfinite(t.weight_decay))
+            return fail(GS_ERR_INVALID_ARGUMENT, "%s: the rates of tensor %d are not finite", call, i);
+        const size_t es = d.state_bits == 8 ? 1 : 4;
+        GSR_CHECK(check_array(call, "param", t.param, 1, 0, 0, elem(t.dtype)));
+        GSR_CHECK(check_array(call, "grad", t.grad, 1, 0, 0, elem(t.grad_dtype)));
+        GSR_CHECK(check_array(call, "m", t.m, 1, 0, 0, es));
+        GSR_CHECK(check_array(call, "v", t.v, 1, 0, 0, es));
+        if (t.copy && !aligned(t.copy, elem(t.copy_dtype)))
+            return fail(GS_ERR_INVALID_ARGUMENT, "%s: copy of tensor %d is misaligned", call, i);
+        if (d.state_bits == 8) {
+            GSR_CHECK(check_array(call, "m_scale", t.m_scale, 1, 0, 0, 4));
+            GSR_CHECK(check_array(call, "v_scale", t.v_scale, 1, 0, 0, 4));
+        }
+    }
+    GSR_CHECK(check_adamw_overlap(call, dims, tensors, steps));
+    return launched(launch_adamw(d, tensors, steps, grad_scale, rate_scale, stream), call);
 }
 
 }  // extern "C"

@@ -1,0 +1,63 @@
+// values.hpp -- runs of eight values of one type in registers (device code).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gsr {
+
+// Eight values as they lie in memory.  Rows of odd length and views start anywhere, and the memory system takes 16-byte
+// accesses at any element's address, so a whole run is always one (float32: two) of them; only the last run of a row
+// goes element by element.
+template <class T>
+struct Run8 {
+    T v[8];
+    // n values from p; the rest zero
+    __device__ __forceinline__ void load(const T* p, int n) {
+        if (n >= 8) {
+            __builtin_memcpy(v, p, sizeof(v));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : (T)0.f;
+        }
+    }
+    __device__ __forceinline__ void store(T* p, int n) const {
+        if (n >= 8) {
+            __builtin_memcpy(p, v, sizeof(v));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n) p[e] = v[e];
+        }
+    }
+    __device__ __forceinline__ float get(int e) const { return (float)v[e]; }
+    __device__ __forceinline__ void set(int e, float x) { v[e] = (T)x; }
+};
+
+// The largest value of the nearest 8-bit type (4 exponent bits, 3 fraction bits, no infinities) and its smallest step.
+constexpr float kF8Max = 448.f, kF8Min = 0x1p-9f;
+
+// Magnitudes as integers: their order is the floats', and NaN lies above infinity, so a maximum keeps it.
+__device__ __forceinline__ uint32_t magnitude(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
+
+// Scale of a group whose largest magnitude is top, and how its values become codes: code(x) rounds x / scale.  A group
+// without a value above zero has scale 1.
+struct F8Scale {
+    float scale, lift, inv;
+    __device__ __forceinline__ explicit F8Scale(uint32_t top_bits) {
+        const float top = __builtin_bit_cast(float, top_bits);
+        const bool some = top > 0.f;
+        scale = some ? top / kF8Max : 1.f;
+        lift = top < 0x1p-90f ? 0x1p64f : 1.f;  // 1 / top stays finite
+        inv = some ? kF8Max / (top * lift) : 1.f;
+    }
+    __device__ __forceinline__ float code(float x) const { return (x * lift) * inv; }
+};
+
+// Four codes in a word, rounded to nearest even.
+__device__ __forceinline__ uint32_t pack_f8(float a, float b, float c, float d) {
+    int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true);
+}
+
+}  // namespace gsr

@@ -321,3 +321,226 @@ class Orthogonalizer(_Op):
             _exact(out, "out", shape, self.out_dtype, self.device)
         b.gs_orthogonalize(self.dims, g, out, self._scratch(self.nbytes, stream), stream)
         return out
+
+
+class ResidualNorm(_Op):
+    """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, over rows of the weight's length.
+
+    x and y [rows, width] in dtype (float32, bfloat16 or float16), weight [width] and the stream (residual and h) in
+    dtype or float32, rows contiguous.  The weight is borrowed, not copied.
+    """
+
+    def __init__(self, weight, dtype, eps=1e-6):
+        super().__init__(weight.device)
+        if weight.dim() != 1 or weight.shape[0] < 1:
+            raise ValueError("weight must be a vector")
+        self.width = int(weight.shape[0])
+        self.dtype = dtype
+        self.code = _dtype_code(dtype)
+        if weight.dtype not in (dtype, self.torch.float32):
+            raise ValueError(f"weight is {weight.dtype}, expected {dtype} or float32")
+        self.weight = _exact(weight, "weight", (self.width,), weight.dtype, self.device)
+        self.eps = float(eps)
+        self._held = (self.weight,)
+        self._sizes = {}
+
+    def _dims(self, rows, stream_dtype, group=0):
+        if stream_dtype not in (self.dtype, self.torch.float32):
+            raise ValueError(f"the residual stream is {stream_dtype}, expected {self.dtype} or float32")
+        return b.gs_norm_dims(rows, self.width, self.code, _dtype_code(stream_dtype), _dtype_code(self.weight.dtype),
+                              group, self.eps)
+
+    def forward(self, x, residual=None, y=None, h=None, stream=None):
+        """-> (y, h).  h may be residual and y may be x (overwritten).  Without a residual h is x, and written only
+        where it is given (in dtype or float32: the start of a stream)."""
+        return self._on(stream, self._forward, x, residual, y, h)
+
+    def _inputs(self, x, residual, h):
+        """(rows, type of the stream, inputs, h, its row stride; h None: x itself)"""
+        rows = int(x.shape[0])
+        ldx = _matrix(x, "x", rows, self.width, self.dtype, self.device)
+        kind = residual.dtype if residual is not None else h.dtype if h is not None else self.dtype
+        ldr = _matrix(residual, "residual", rows, self.width, kind, self.device) if residual is not None else 0
+        ldh = self.width
+        if h is not None:
+            ldh = _matrix(h, "h", rows, self.width, kind, self.device)
+        elif residual is not None:
+            h = self.torch.empty((rows, self.width), dtype=kind, device=self.device)
+        inputs = b.gs_norm_inputs(x.data_ptr(), residual.data_ptr() if residual is not None else None,
+                                  self.weight.data_ptr(), ldx, ldr)
+        return rows, kind, inputs, h, ldh
+
+    def _forward(self, stream, x, residual, y, h):
+        rows, kind, inputs, h, ldh = self._inputs(x, residual, h)
+        dims = self._dims(rows, kind)
+        ldy = self.width
+        if y is None:
+            y = self.torch.empty((rows, self.width), dtype=self.dtype, device=self.device)
+        else:
+            ldy = _matrix(y, "y", rows, self.width, self.dtype, self.device)
+        b.gs_norm_forward(dims, inputs, y, ldy, h, ldh, stream)
+        return y, h if h is not None else x
+
+    def forward8(self, x, residual=None, group=0, codes=None, scales=None, h=None, stream=None):
+        """The same with y in 8 bits -> (codes, scales, h): y is about codes (float8_e4m3fn [rows, width]) times scales
+        (float32 [rows, groups]), one scale for `group` columns (32, 64 or 128; 0: the row)."""
+        return self._on(stream, self._forward8, x, residual, group, codes, scales, h)
+
+    def _forward8(self, stream, x, residual, group, codes, scales, h):
+        t = self.torch
+        rows, kind, inputs, h, ldh = self._inputs(x, residual, h)
+        if group not in (0, 32, 64, 128):
+            raise ValueError(f"group {group} is not 0, 32, 64 or 128")
+        dims = self._dims(rows, kind, group)
+        groups = -(-self.width // group) if group else 1
+        ldc = self.width
+        if codes is None:
+            codes = t.empty((rows, self.width), dtype=t.float8_e4m3fn, device=self.device)
+        else:
+            ldc = _matrix(codes, "codes", rows, self.width, t.float8_e4m3fn, self.device)
+        if scales is None:
+            scales = t.empty((rows, groups), dtype=t.float32, device=self.device)
+        else:
+            _exact(scales, "scales", (rows, groups), t.float32, self.device)
+        b.gs_norm_forward8(dims, inputs, codes, ldc, scales, h, ldh, stream)
+        return codes, scales, h if h is not None else x
+
+    def backward(self, h, dy, dh=None, grads=None, stream=None):
+        """Gradients for dy and dh (what reaches h from elsewhere) at the h of the forward pass: a dict of x, residual
+        (one tensor where the types agree) and weight (written; with a given dict, only the tensors it holds)."""
+        return self._on(stream, self._backward, h, dy, dh, grads)
+
+    def _backward(self, stream, h, dy, dh, grads):
+        t, rows = self.torch, int(h.shape[0])
+        kind = h.dtype
+        dims = self._dims(rows, kind)
+        ldh = _matrix(h, "h", rows, self.width, kind, self.device)
+        lddy = _matrix(dy, "dy", rows, self.width, self.dtype, self.device)
+        lddh = _matrix(dh, "dh", rows, self.width, kind, self.device) if dh is not None else 0
+        ld = {"x": self.width, "residual": self.width}
+        if grads is None:
+            like = dict(device=self.device)
+            grads = {"x": t.empty((rows, self.width), dtype=self.dtype, **like), "weight": t.empty_like(self.weight)}
+            if kind != self.dtype:
+                grads["residual"] = t.empty((rows, self.width), dtype=kind, **like)
+            out = dict(grads)
+            grads.setdefault("residual", grads["x"])
+        else:
+            out = {k: v for k, v in grads.items() if v is not None}
+            for name, want in (("x", self.dtype), ("residual", kind)):
+                if name in out:
+                    ld[name] = _matrix(out[name], f"grads[{name!r}]", rows, self.width, want, self.device)
+            if "weight" in out:
+                _exact(out["weight"], "grads['weight']", (self.width,), self.weight.dtype, self.device)
+            if "x" in out and out.get("residual") is out["x"]:
+                del out["residual"]
+        ptr = {k: out[k].data_ptr() if k in out else None for k in ("x", "residual", "weight")}
+        if (rows, kind) not in self._sizes:
+            if len(self._sizes) > 64:
+                self._sizes.clear()
+            self._sizes[rows, kind] = b.gs_norm_size(dims)
+        ws = self._scratch(self._sizes[rows, kind], stream) if ptr["weight"] else None
+        b.gs_norm_backward(dims, h, ldh, self.weight, dy, lddy, dh, lddh,
+                           b.gs_norm_grads(ptr["x"], ptr["residual"], ptr["weight"], ld["x"], ld["residual"]), ws, stream)
+        return grads
+
+
+class AdamW(_Op):
+    """AdamW step over many tensors in one launch: step(grads).
+
+    params: contiguous tensors (float32, bfloat16 or float16), borrowed and updated in place.  lr and weight_decay: one
+    for all or one for each (lr may be changed between steps).  copies: tensors of the parameters' shapes that receive
+    the new values in their own type (None entries: no copy), e.g. what the products read.
+
+    State (zeros at the start, may be written to): m and v, with state_bits 32 float32 tensors of a parameter's number of
+    values; with state_bits 8 float8_e4m3fn codes of m and of the root of v, with one float32 scale for every 256 values in
+    m_scale and v_scale.  steps: the number of steps done, on the GPU, so a captured step counts on when it is replayed
+    (lr and weight_decay keep the values they were captured with; rate_scale and grad_scale are read anew).
+    """
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=32, copies=None):
+        params = list(params)
+        if not params:
+            raise ValueError("no parameters")
+        super().__init__(params[0].device)
+        t, n = self.torch, len(params)
+        if state_bits not in (32, 8):
+            raise ValueError(f"state_bits {state_bits} is not 32 or 8")
+        copies = list(copies) if copies is not None else [None] * n
+        if len(copies) != n:
+            raise ValueError(f"{len(copies)} copies for {n} parameters")
+        self.params, self.copies = params, copies
+        self.lr = [float(v) for v in lr] if isinstance(lr, (tuple, list)) else [float(lr)] * n
+        decay = weight_decay if isinstance(weight_decay, (tuple, list)) else [weight_decay] * n
+        self.weight_decay = [float(v) for v in decay]
+        if len(self.lr) != n or len(self.weight_decay) != n:
+            raise ValueError("lr and weight_decay need one value, or one for each parameter")
+        self.dims = b.gs_adamw_dims(n, state_bits, float(betas[0]), float(betas[1]), float(eps))
+        self._shapes = [(p.shape, p.dtype) for p in params]
+        self._array = (b.gs_adamw_tensor * n)()
+        sizes = [p.numel() for p in params]
+        blocks = [-(-s // 256) for s in sizes]
+        like = dict(device=self.device)
+        starts = [0]
+        for k in blocks:
+            starts.append(starts[-1] + k)
+
+        def split(flat, unit, lengths):
+            return [flat[unit * a:unit * a + k] for a, k in zip(starts, lengths)]
+
+        # one allocation of each kind, tensors 256 values apart
+        kind = t.float32 if state_bits == 32 else t.uint8
+        flats = [t.zeros(256 * starts[-1], dtype=kind, **like) for _ in range(2)]
+        self.m, self.v = (split(f if state_bits == 32 else f.view(t.float8_e4m3fn), 256, sizes) for f in flats)
+        self.m_scale, self.v_scale = [], []
+        if state_bits == 8:
+            flats += [t.zeros(starts[-1], dtype=t.float32, **like) for _ in range(2)]
+            self.m_scale, self.v_scale = (split(f, 1, blocks) for f in flats[2:])
+        self._count = t.zeros(2, dtype=t.int64, **like)
+        self.steps = self._count[0]
+        self._held = (*params, *[c for c in copies if c is not None], *flats, self._count)
+        for i, (p, c, a) in enumerate(zip(params, copies, self._array)):
+            a.n, a.dtype = sizes[i], _dtype_code(p.dtype)
+            if c is not None:
+                a.copy_dtype = _dtype_code(c.dtype)
+            a.m, a.v = self.m[i].data_ptr(), self.v[i].data_ptr()
+            if state_bits == 8:
+                a.m_scale, a.v_scale = self.m_scale[i].data_ptr(), self.v_scale[i].data_ptr()
+        self._point()
+
+    def _point(self):
+        """Takes the addresses of the parameters and copies, as they are now."""
+        for i, (p, c, a, (shape, dtype)) in enumerate(zip(self.params, self.copies, self._array, self._shapes)):
+            if p.device != self.device or p.dtype != dtype or p.shape != shape or not p.is_contiguous():
+                raise ValueError(f"parameter {i} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                                 f"{self.device}")
+            a.param = p.data_ptr()
+            if c is not None:
+                if c.device != self.device or c.shape != shape or not c.is_contiguous():
+                    raise ValueError(f"copy {i} must be contiguous, of shape {tuple(shape)} on {self.device}")
+                a.copy_dtype = _dtype_code(c.dtype)
+                a.copy = c.data_ptr()
+
+    def step(self, grads, grad_scale=None, rate_scale=None, stream=None):
+        """grads: contiguous tensors of the parameters' shapes (float32, bfloat16 or float16; None: the parameter is left
+        as it is).  grad_scale, rate_scale: float32 tensors of one value on the GPU that multiply the gradients and the
+        rates."""
+        return self._on(stream, self._step, grads, grad_scale, rate_scale)
+
+    def _step(self, stream, grads, grad_scale, rate_scale):
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
+        self._point()
+        for i, (g, a, (shape, _)) in enumerate(zip(grads, self._array, self._shapes)):
+            a.lr, a.weight_decay = self.lr[i], self.weight_decay[i]
+            if g is None:
+                a.grad = None
+                continue
+            if g.device != self.device or g.shape != shape or not g.is_contiguous():
+                raise ValueError(f"gradient {i} must be contiguous, of shape {tuple(shape)} on {self.device}")
+            a.grad_dtype = _dtype_code(g.dtype)
+            a.grad = g.data_ptr()
+        for name, v in (("grad_scale", grad_scale), ("rate_scale", rate_scale)):
+            if v is not None and (v.numel() != 1 or v.dtype != self.torch.float32 or v.device != self.device):
+                raise ValueError(f"{name} must be one float32 value on {self.device}")
+        b.gs_adamw_step(self.dims, self._array, self._count, grad_scale, rate_scale, stream)

@@ -428,6 +428,85 @@ GSR_API gs_status gs_ortho_size(const gs_ortho_dims* dims, size_t* workspace_byt
 GSR_API gs_status gs_orthogonalize(const gs_ortho_dims* dims, const void* g, void* out, void* workspace,
                                    size_t workspace_bytes, hipStream_t stream);
 
+/* Root-mean-square norm with the residual's addition, on `rows` rows of `width` columns:
+ *   h = x + residual,  y = h / sqrt(mean(h^2) + eps) * weight
+ * x and y are of type dtype; residual and h (the sum, the next layer's residual) of
+ * stream_dtype, which is dtype or GS_F32; weight (contiguous) of weight_dtype, likewise.
+ * Row strides in elements.  residual null: h = x.  h null: not wanted.  y is taken from the sum
+ * before it is rounded to stream_dtype.  h may be residual and y may be x (same row stride);
+ * outputs that overlap anything else in any other way are GS_ERR_INVALID_ARGUMENT.
+ * width is 1 .. 2^20, rows 0 .. 2^31 - 512, row strides up to 2^21. */
+typedef struct {
+    int64_t rows;
+    int32_t width;
+    int32_t dtype, stream_dtype, weight_dtype; /* gs_dtype */
+    int32_t scale_group;  /* gs_norm_forward8: columns that share a scale (0: the row; 32, 64 or 128) */
+    float eps;            /* not negative */
+} gs_norm_dims;
+typedef struct {
+    const void* x;
+    const void* residual;
+    const void* weight;
+    int64_t ld_x, ld_residual;
+} gs_norm_inputs;
+/* Gradients, written; null members are skipped.  x and residual hold the same values, each in its type. */
+typedef struct {
+    void* x;
+    void* residual;
+    void* weight;
+    int64_t ld_x, ld_residual;
+} gs_norm_grads;
+GSR_API gs_status gs_norm_forward(const gs_norm_dims* dims, const gs_norm_inputs* in, void* y, int64_t ld_y, void* h,
+                                  int64_t ld_h, hipStream_t stream);
+/* The same with y in 8 bits (4 exponent and 3 fraction bits, no infinities, at most 448): codes [rows, width], one byte
+ * each, and float32 scales [rows, groups], contiguous, groups = 1 or ceil(width / scale_group).  A scale is the
+ * group's largest |y| / 448 (1 where that is 0 or NaN), a code y / scale rounded to nearest even. */
+GSR_API gs_status gs_norm_forward8(const gs_norm_dims* dims, const gs_norm_inputs* in, void* codes, int64_t ld_codes,
+                                   float* scales, void* h, int64_t ld_h, hipStream_t stream);
+GSR_API gs_status gs_norm_size(const gs_norm_dims* dims, size_t* backward_bytes);
+/* Gradients for dy [rows, width] (dtype) and dh (stream_dtype, null: zero), the gradient that reaches h from
+ * elsewhere, at the h that the forward pass wrote (x where there is no residual: pass it in stream_dtype).  With 8-bit
+ * outputs dy is the gradient of y, as if it had not been rounded.  The gradients may be written over dy and dh, each
+ * over one of its own type and row stride. */
+GSR_API gs_status gs_norm_backward(const gs_norm_dims* dims, const void* h, int64_t ld_h, const void* weight,
+                                   const void* dy, int64_t ld_dy, const void* dh, int64_t ld_dh,
+                                   const gs_norm_grads* grads, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+
+/* AdamW step over many tensors at once, for the updater's weights and the Gaussians' parameters:
+ *   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
+ *   p = p - lr weight_decay p - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
+ * in float32, t the number of this step.  A gradient is multiplied by *grad_scale and the rates by *rate_scale (device
+ * scalars, null: 1), so that both can change under a captured graph; lr and weight_decay go by value.
+ * state_bits 32: m and v are float32 arrays of n values.  state_bits 8: m and v are n 8-bit codes (the type of
+ * gs_norm_forward8) of m and of sqrt(v), with one float32 scale for every 256 values in m_scale and v_scale
+ * (ceil(n / 256)); a root above zero is at least the smallest code.  Not a number in a gradient reaches every value of
+ * its 256 at the next step.  All states start as zeros (scales too).
+ * steps: two int64 on the device, zeros at the start; the first is the number of steps done and may be set, the second
+ * belongs to the call.  Two calls with the same steps or tensors must not overlap in time. */
+typedef struct {
+    void* param;
+    const void* grad;  /* null: the tensor is left as it is */
+    void* m;
+    void* v;
+    float* m_scale;    /* state_bits 8 only */
+    float* v_scale;
+    void* copy;        /* the new values in copy_dtype (null: not wanted) */
+    int64_t n;         /* 0 .. 2^40 */
+    float lr, weight_decay;
+    int32_t dtype, grad_dtype, copy_dtype; /* gs_dtype */
+} gs_adamw_tensor;
+typedef struct {
+    int32_t n_tensors;
+    int32_t state_bits; /* 32 or 8 */
+    double beta1, beta2; /* [0, 1) */
+    double eps;          /* positive */
+} gs_adamw_dims;
+/* tensors: a host array, read during the call.  Arrays that are written must not overlap each other or a gradient
+ * (GS_ERR_INVALID_ARGUMENT). */
+GSR_API gs_status gs_adamw_step(const gs_adamw_dims* dims, const gs_adamw_tensor* tensors, int64_t* steps,
+                                const float* grad_scale, const float* rate_scale, hipStream_t stream);
+
 GSR_API const char* gs_status_string(gs_status s);
 GSR_API const char* gs_last_error(void);
 
