@@ -130,12 +130,11 @@ __device__ __forceinline__ uint32_t encode4(const float* x, bool root, float* sc
 #pragma unroll
     for (int e = 0; e < 4; ++e) top = max(top, magnitude(x[e]));
     for (int m = 32; m > 0; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
-    const F8Scale s(top);
-    *scale = s.scale;
+    *scale = f8_scale(__builtin_bit_cast(float, top));
     float c[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        c[e] = s.code(x[e]);
+        c[e] = x[e] / *scale;
         if (root && x[e] > 0.f && c[e] < kF8Min) c[e] = kF8Min;
     }
     return pack_f8(c[0], c[1], c[2], c[3]);
@@ -189,8 +188,8 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float x = g[e] * gs;
-                m[e] = __builtin_fmaf(a.b1, m[e], a.rest1 * x);
-                v[e] = __builtin_fmaf(a.b2, v[e], (a.rest2 * x) * x);
+                m[e] = a.b1 * m[e] + a.rest1 * x;
+                v[e] = a.b2 * v[e] + (a.rest2 * x) * x;
                 const float down = __builtin_sqrtf(v[e] * unbias2) + a.eps;
                 p[e] = p[e] - __builtin_fmaf(decay, p[e], lr * ((m[e] * unbias1) / down));
             }

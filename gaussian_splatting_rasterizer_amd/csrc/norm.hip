@@ -12,6 +12,7 @@
 // The weight's gradient: every workgroup sums its rows in registers and leaves one row of partial sums, which
 // k_norm_weight adds up in a fixed order, so results are the same from run to run.
 #include <algorithm>
+#include <type_traits>
 
 #include "gsr_internal.hpp"
 #include "values.hpp"
@@ -49,30 +50,32 @@ struct NormBackArgs {
     float eps, inv_width;
 };
 
+// The larger magnitude; NaN where one of them is.
+__device__ __forceinline__ double larger(double a, double b) { return !(b <= a) && a == a ? b : a; }
+
 // Reductions over the lanes of a row: `lanes` of a wave, or (WG) the whole workgroup.  LDS is used alternately, so that
 // one barrier a reduction is enough.
 template <bool WG>
 struct RowReduce {
-    uint32_t* lds;  // [2][4]
+    char* lds;  // [2][4] values of up to 8 bytes
     int lanes, turn;
     __device__ __forceinline__ float sum(float v) {
         for (int m = (WG ? 64 : lanes) / 2; m > 0; m >>= 1) v += __shfl_xor(v, m);
         if constexpr (WG) {
-            uint32_t* s = lds + 4 * (turn ^= 1);
-            if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = __builtin_bit_cast(uint32_t, v);
+            float* s = (float*)(lds + 32 * (turn ^= 1));
+            if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
             __syncthreads();
-            const float* f = (const float*)s;
-            v = (f[0] + f[1]) + (f[2] + f[3]);
+            v = (s[0] + s[1]) + (s[2] + s[3]);
         }
         return v;
     }
-    __device__ __forceinline__ uint32_t top(uint32_t v) {
-        for (int m = (WG ? 64 : lanes) / 2; m > 0; m >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+    __device__ __forceinline__ double top(double v) {
+        for (int m = (WG ? 64 : lanes) / 2; m > 0; m >>= 1) v = larger(v, __shfl_xor(v, m));
         if constexpr (WG) {
-            uint32_t* s = lds + 4 * (turn ^= 1);
+            double* s = (double*)(lds + 32 * (turn ^= 1));
             if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
             __syncthreads();
-            v = max(max(s[0], s[1]), max(s[2], s[3]));
+            v = larger(larger(s[0], s[1]), larger(s[2], s[3]));
         }
         return v;
     }
@@ -99,26 +102,34 @@ __device__ __forceinline__ void load_weight(const void* w, bool f32, int col, in
     }
 }
 
-// Codes of one run: the scale of its group (of `share` lanes; the row's where `row_top` is given) and eight bytes.
-__device__ __forceinline__ void store_codes(const NormArgs& p, int64_t row, int col, int n, const float* v, int share,
-                                            bool whole, uint32_t row_top) {
-    uint32_t top = row_top;
-    if (!whole) {
-        top = 0;
+// Codes of one run.  A code is y over the largest |y| of its group times 448, in which r falls out: it is taken from
+// h w in float64, so that its only error is its own rounding.  v: h w of the run's columns; share: lanes of a group; or
+// (whole) the largest magnitude of the row's.
+__device__ __forceinline__ double top_of(const double* v) {
+    double top = 0.0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, magnitude(v[e]));
-        for (int m = share / 2; m > 0; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+    for (int e = 0; e < 8; ++e) top = larger(top, __builtin_fabs(v[e]));
+    return top;
+}
+__device__ __forceinline__ void store_codes(const NormArgs& p, int64_t row, int col, int n, const double* v, float rstd,
+                                            int share, bool whole, double row_top) {
+    double top = row_top;
+    if (!whole) {
+        top = top_of(v);
+        for (int m = share / 2; m > 0; m >>= 1) top = larger(top, __shfl_xor(top, m));
     }
-    const F8Scale s(top);
     if (n <= 0) return;
+    // a row with an infinity or NaN (r is 0 or NaN), or without a value above zero: codes of y itself
+    const double inv = top > 0.0 && rstd > 0.f ? (double)kF8Max / top : (double)rstd;
+    const float scale = f8_scale((float)(top * (double)rstd));
     if (whole) {
-        if (col == 0) p.scales[row] = s.scale;
+        if (col == 0) p.scales[row] = scale;
     } else if (col % p.group == 0) {
-        p.scales[row * ((p.width + p.group - 1) / p.group) + col / p.group] = s.scale;
+        p.scales[row * ((p.width + p.group - 1) / p.group) + col / p.group] = scale;
     }
     float c[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) c[e] = s.code(v[e]);
+    for (int e = 0; e < 8; ++e) c[e] = (float)(v[e] * inv);
     const uint32_t words[2] = {pack_f8(c[0], c[1], c[2], c[3]), pack_f8(c[4], c[5], c[6], c[7])};
     uint8_t* out = (uint8_t*)p.y + row * p.ldy + col;
     if (n >= 8) {
@@ -133,7 +144,7 @@ __device__ __forceinline__ void store_codes(const NormArgs& p, int64_t row, int 
 // NV runs of a thread; WG: a row per workgroup.  OUT8: y are codes.
 template <class T, class R, int NV, bool WG, bool OUT8>
 __global__ __launch_bounds__(kThreads) void k_norm(const NormArgs p) {
-    __shared__ uint32_t s_red[8];
+    __shared__ __attribute__((aligned(8))) char s_red[64];
     const int lanes = WG ? kThreads : p.lanes;
     const int per = kThreads / lanes, slot = threadIdx.x / lanes, lane = threadIdx.x % lanes;
     RowReduce<WG> red{s_red, lanes, 0};
@@ -177,28 +188,34 @@ __global__ __launch_bounds__(kThreads) void k_norm(const NormArgs p) {
                 o.store((R*)p.h + row * p.ldh + column<WG>(i, lane, lanes), n[i]);
             }
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[i][e] = (h[i][e] * rstd) * w[i][e];
         if constexpr (OUT8) {
-            uint32_t top = 0;
+            double top = 0.0;
+            auto products = [&](int i, double* v) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = (p.residual ? (double)x[i].get(e) + (double)r[i].get(e) : (double)x[i].get(e)) * (double)w[i][e];
+            };
             if (p.group == 0) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) top = max(top, magnitude(h[i][e]));
+                for (int i = 0; i < NV; ++i) {
+                    double v[8];
+                    products(i, v);
+                    top = larger(top, top_of(v));
+                }
                 top = red.top(top);
             }
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
-                store_codes(p, row, column<WG>(i, lane, lanes), live ? n[i] : 0, h[i], p.group / 8, p.group == 0, top);
+            for (int i = 0; i < NV; ++i) {
+                double v[8];
+                products(i, v);
+                store_codes(p, row, column<WG>(i, lane, lanes), live ? n[i] : 0, v, rstd, p.group / 8, p.group == 0, top);
+            }
         } else if (live) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 Run8<T> o;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o.set(e, h[i][e]);
+                for (int e = 0; e < 8; ++e) o.set(e, (h[i][e] * rstd) * w[i][e]);
                 o.store((T*)p.y + row * p.ldy + column<WG>(i, lane, lanes), n[i]);
             }
         }
@@ -209,17 +226,20 @@ __global__ __launch_bounds__(kThreads) void k_norm(const NormArgs p) {
 // once for the largest value and once for the outputs.
 template <class T, class R, bool OUT8>
 __global__ __launch_bounds__(kThreads) void k_norm_wide(const NormArgs p) {
-    __shared__ uint32_t s_red[8];
+    __shared__ __attribute__((aligned(8))) char s_red[64];
     RowReduce<true> red{s_red, kThreads, 0};
     const int turns = (p.width + kThreads * 8 - 1) / (kThreads * 8);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
-        auto sum_of = [&](int col, int n, float* h) {
+        auto sum_of = [&](int col, int n, auto* h) {
             Run8<T> x;
             x.load((const T*)p.x + row * p.ldx + col, n);
             Run8<R> r;
             if (p.residual) r.load((const R*)p.residual + row * p.ldr + col, n);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] = p.residual ? x.get(e) + r.get(e) : x.get(e);
+            for (int e = 0; e < 8; ++e) {
+                using H = std::remove_reference_t<decltype(h[0])>;
+                h[e] = p.residual ? (H)x.get(e) + (H)r.get(e) : (H)x.get(e);
+            }
         };
         float s = 0.f;
         for (int i = 0; i < turns; ++i) {
@@ -230,37 +250,42 @@ __global__ __launch_bounds__(kThreads) void k_norm_wide(const NormArgs p) {
             for (int e = 0; e < 8; ++e) s = __builtin_fmaf(h[e], h[e], s);
         }
         const float rstd = 1.f / __builtin_sqrtf(__builtin_fmaf(red.sum(s), p.inv_width, p.eps));
-        uint32_t top = 0;
+        double top = 0.0;
+        auto products = [&](int col, int n, const float* w, double* v) {
+            sum_of(col, n, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= (double)w[e];
+        };
         if (OUT8 && p.group == 0) {
             for (int i = 0; i < turns; ++i) {
                 const int col = column<true>(i, threadIdx.x, kThreads), n = min(8, p.width - col);
-                float h[8], w[8];
-                sum_of(col, n, h);
+                float w[8];
+                double v[8];
                 load_weight<T>(p.w, p.w_f32, col, n, w);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = max(top, magnitude((h[e] * rstd) * w[e]));
+                products(col, n, w, v);
+                top = larger(top, top_of(v));
             }
             top = red.top(top);
         }
         for (int i = 0; i < turns; ++i) {
             const int col = column<true>(i, threadIdx.x, kThreads), n = min(8, p.width - col);
             float h[8], w[8];
+            double v[8];
             sum_of(col, n, h);
             load_weight<T>(p.w, p.w_f32, col, n, w);
+            if constexpr (OUT8) products(col, n, w, v);  // before h replaces what it is taken from
             if (p.h) {
                 Run8<R> o;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) o.set(e, h[e]);
                 o.store((R*)p.h + row * p.ldh + col, n);
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[e] = (h[e] * rstd) * w[e];
             if constexpr (OUT8) {
-                store_codes(p, row, col, n, h, p.group / 8, p.group == 0, top);
+                store_codes(p, row, col, n, v, rstd, p.group / 8, p.group == 0, top);
             } else {
                 Run8<T> o;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o.set(e, h[e]);
+                for (int e = 0; e < 8; ++e) o.set(e, (h[e] * rstd) * w[e]);
                 o.store((T*)p.y + row * p.ldy + col, n);
             }
         }
@@ -285,7 +310,7 @@ __device__ __forceinline__ void store_grads(const NormBackArgs& p, int64_t row, 
 
 template <class T, class R, int NV, bool WG>
 __global__ __launch_bounds__(kThreads) void k_norm_backward(const NormBackArgs p) {
-    __shared__ uint32_t s_red[8];
+    __shared__ __attribute__((aligned(8))) char s_red[64];
     __shared__ float s_dw[WG ? 1 : kThreads * 8];
     const int lanes = WG ? kThreads : p.lanes;
     const int per = kThreads / lanes, slot = threadIdx.x / lanes, lane = threadIdx.x % lanes;
@@ -363,7 +388,7 @@ __global__ __launch_bounds__(kThreads) void k_norm_backward(const NormBackArgs p
 // Long rows: r goes to rstd, from which k_norm_weight_wide takes the weight's sums column by column.
 template <class T, class R>
 __global__ __launch_bounds__(kThreads) void k_norm_backward_wide(const NormBackArgs p, float* rstds) {
-    __shared__ uint32_t s_red[8];
+    __shared__ __attribute__((aligned(8))) char s_red[64];
     RowReduce<true> red{s_red, kThreads, 0};
     const int turns = (p.width + kThreads * 8 - 1) / (kThreads * 8);
     for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {

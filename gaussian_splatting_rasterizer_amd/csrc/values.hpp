@@ -40,19 +40,8 @@ constexpr float kF8Max = 448.f, kF8Min = 0x1p-9f;
 // Magnitudes as integers: their order is the floats', and NaN lies above infinity, so a maximum keeps it.
 __device__ __forceinline__ uint32_t magnitude(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
 
-// Scale of a group whose largest magnitude is top, and how its values become codes: code(x) rounds x / scale.  A group
-// without a value above zero has scale 1.
-struct F8Scale {
-    float scale, lift, inv;
-    __device__ __forceinline__ explicit F8Scale(uint32_t top_bits) {
-        const float top = __builtin_bit_cast(float, top_bits);
-        const bool some = top > 0.f;
-        scale = some ? top / kF8Max : 1.f;
-        lift = top < 0x1p-90f ? 0x1p64f : 1.f;  // 1 / top stays finite
-        inv = some ? kF8Max / (top * lift) : 1.f;
-    }
-    __device__ __forceinline__ float code(float x) const { return (x * lift) * inv; }
-};
+// Scale of a group whose largest magnitude is top; a group without a value above zero has scale 1.
+__device__ __forceinline__ float f8_scale(float top) { return top > 0.f ? top * (1.f / kF8Max) : 1.f; }
 
 // Four codes in a word, rounded to nearest even.
 __device__ __forceinline__ uint32_t pack_f8(float a, float b, float c, float d) {

@@ -476,7 +476,7 @@ GSR_API gs_status gs_norm_backward(const gs_norm_dims* dims, const void* h, int6
 /* AdamW step over many tensors at once, for the updater's weights and the Gaussians' parameters:
  *   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
  *   p = p - lr weight_decay p - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
- * in float32, t the number of this step.  A gradient is multiplied by *grad_scale and the rates by *rate_scale (device
+ * in float32 (the states in exactly these operations, each rounded by itself), t the number of this step.  A gradient is multiplied by *grad_scale and the rates by *rate_scale (device
  * scalars, null: 1), so that both can change under a captured graph; lr and weight_decay go by value.
  * state_bits 32: m and v are float32 arrays of n values.  state_bits 8: m and v are n 8-bit codes (the type of
  * gs_norm_forward8) of m and of sqrt(v), with one float32 scale for every 256 values in m_scale and v_scale

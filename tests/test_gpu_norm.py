@@ -295,3 +295,15 @@ def test_refusals():
         norm.forward(wide[:4], y=wide[1:])
     with pytest.raises(m.GsrError):
         norm.forward(x, x, y=x)
+
+
+def test_8bit_rows_with_infinities():
+    """Codes of the y that the formula gives: NaN through the row of a NaN; zeros beside an infinity, NaN in its place."""
+    x = inputs(3, 300, torch.float32, torch.float32, seed=14)[0]
+    x[0, 40], x[1, 70] = float("nan"), float("inf")
+    for group in (0, 32):
+        codes, scales, _ = gsr().ResidualNorm(torch.ones(300, device="cuda"), torch.float32, eps=EPS).forward8(x, group=group)
+        codes = codes.float()
+        assert torch.isnan(codes[0]).all() and torch.isnan(codes[1, 70])
+        rest = torch.arange(300, device="cuda") != 70
+        assert (codes[1, rest] == 0).all() and (scales[:2] == 1).all() and torch.isfinite(codes[2]).all()
