@@ -9,4 +9,4 @@ from .binding import (GS_OK, GsrError, Rasterizer, gs_attribute, gs_backward, gs
                       gs_context_create, gs_context_destroy, gs_debug_exp2, gs_debug_export, gs_default_params,
                       gs_gaussian_grads, gs_profile_enable, gs_profile_read, gs_project, gs_render,
                       gs_render_features, gs_score_replay, gs_workspace_size, load_library, rasterizer_for_scene)
-from .updater import AdamW, GatedFFN, GatedScan, Orthogonalizer, ResidualNorm  # noqa: F401
+from .updater import AdamW, GatedFFN, GatedScan, LinearAttention, Orthogonalizer, ResidualNorm  # noqa: F401

@@ -43,7 +43,8 @@ ABI_SYMBOLS = ("gs_default_params", "gs_workspace_size", "gs_context_create", "g
                "gs_profile_stages", "gs_profile_read", "gs_render_score_noalloc",
                "gs_ffn_sizes", "gs_ffn_forward", "gs_ffn_backward", "gs_scan_sizes", "gs_scan_forward",
                "gs_scan_backward", "gs_default_ortho_dims", "gs_ortho_size", "gs_orthogonalize",
-               "gs_norm_forward", "gs_norm_forward8", "gs_norm_size", "gs_norm_backward", "gs_adamw_step")
+               "gs_norm_forward", "gs_norm_forward8", "gs_norm_size", "gs_norm_backward", "gs_adamw_step",
+               "gs_attn_sizes", "gs_attn_forward", "gs_attn_backward")
 
 
 class gs_gaussians(ctypes.Structure):
@@ -122,6 +123,27 @@ class gs_norm_inputs(ctypes.Structure):
 class gs_norm_grads(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("weight", ctypes.c_void_p),
                 ("ld_x", ctypes.c_int64), ("ld_residual", ctypes.c_int64)]
+
+
+class gs_attn_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("n_seq", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("d_key", ctypes.c_int32), ("d_value", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("gate_dtype", ctypes.c_int32), ("gate_per_row", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class gs_heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("ld_row", ctypes.c_int64), ("ld_head", ctypes.c_int64)]
+
+
+class gs_attn_inputs(ctypes.Structure):
+    _fields_ = [("q", gs_heads), ("k", gs_heads), ("v", gs_heads), ("gate", ctypes.c_void_p),
+                ("ld_gate", ctypes.c_int64), ("state", ctypes.c_void_p)]
+
+
+class gs_attn_grads(ctypes.Structure):
+    _fields_ = [("q", gs_heads), ("k", gs_heads), ("v", gs_heads), ("gate", ctypes.c_void_p),
+                ("ld_gate", ctypes.c_int64), ("state", ctypes.c_void_p)]
 
 
 class gs_adamw_tensor(ctypes.Structure):
@@ -226,6 +248,12 @@ def load_library(path: str = LIB_PATH):
     lib.gs_norm_backward.argtypes = [R(gs_norm_dims), P, I64, P, P, I64, P, I64, R(gs_norm_grads), P, Z, P]
     lib.gs_adamw_step.restype = St
     lib.gs_adamw_step.argtypes = [R(gs_adamw_dims), R(gs_adamw_tensor), P, P, P, P]
+    lib.gs_attn_sizes.restype = St
+    lib.gs_attn_sizes.argtypes = [R(gs_attn_dims), R(Z), R(Z), R(Z)]
+    lib.gs_attn_forward.restype = St
+    lib.gs_attn_forward.argtypes = [R(gs_attn_dims), P, R(gs_attn_inputs), R(gs_heads), P, P, P, Z, P]
+    lib.gs_attn_backward.restype = St
+    lib.gs_attn_backward.argtypes = [R(gs_attn_dims), P, R(gs_attn_inputs), P, R(gs_heads), P, R(gs_attn_grads), P, Z, P]
     _lib = lib
     return lib
 
@@ -457,6 +485,26 @@ def gs_norm_backward(dims, h, ld_h, weight, dy, ld_dy, dh, ld_dh, grads: gs_norm
     _check(load_library().gs_norm_backward(ctypes.byref(dims), _ptr(h), ld_h, _ptr(weight), _ptr(dy), ld_dy, _ptr(dh),
                                            ld_dh, ctypes.byref(grads), _ptr(workspace), _nbytes(workspace),
                                            _stream(stream)), "gs_norm_backward")
+
+
+def gs_attn_sizes(dims: gs_attn_dims) -> tuple:
+    """(saved bytes, forward workspace bytes, backward workspace bytes)"""
+    out = [ctypes.c_size_t(0) for _ in range(3)]
+    _check(load_library().gs_attn_sizes(ctypes.byref(dims), *[ctypes.byref(o) for o in out]), "gs_attn_sizes")
+    return tuple(int(o.value) for o in out)
+
+
+def gs_attn_forward(dims, offsets, inputs: gs_attn_inputs, y: gs_heads, last, saved, workspace, stream=None) -> None:
+    _check(load_library().gs_attn_forward(ctypes.byref(dims), _ptr(offsets), ctypes.byref(inputs), ctypes.byref(y),
+                                          _ptr(last), _ptr(saved), _ptr(workspace), _nbytes(workspace),
+                                          _stream(stream)), "gs_attn_forward")
+
+
+def gs_attn_backward(dims, offsets, inputs: gs_attn_inputs, saved, dy: gs_heads, d_last, grads: gs_attn_grads,
+                     workspace, stream=None) -> None:
+    _check(load_library().gs_attn_backward(ctypes.byref(dims), _ptr(offsets), ctypes.byref(inputs), _ptr(saved),
+                                           ctypes.byref(dy), _ptr(d_last), ctypes.byref(grads), _ptr(workspace),
+                                           _nbytes(workspace), _stream(stream)), "gs_attn_backward")
 
 
 def gs_adamw_step(dims: gs_adamw_dims, tensors, steps, grad_scale=None, rate_scale=None, stream=None) -> None:

@@ -1,0 +1,498 @@
+// attn.hip -- linear attention with a decay for each head: single tokens, what joins the spans, the gate's gradient and the
+// launches.  The matrix-core kernel is in attn.hpp.
+//
+// forward: spans' own contributions to the state (all but each sequence's last span), k_attn_join, then the outputs; one
+// launch where no sequence has two spans.  backward: the same for the adjoint from the last span to the first, then the
+// gradients of q, k and v, then the gate's:
+//   dg_t = <adjoint behind t, a_t S_{t-1}> = sum of w over the pairs of a source before t and a destination from t on.
+// With r_i = out_i . q_i (gradient of q) and c_j = out_j . k_j (gradient of k), each in two parts -- r', c' of pairs within a
+// chunk (the diagonal left out), r, c of the others -- and X the pairs that reach across the whole chunk,
+//   dg_t = X + sum_{i >= t} r_i + sum_{j < t} c_j + sum_{i >= t} (r'_i - c'_i)   over the chunk's rows
+// and the chunk before has X + sum r, less its own sum c.  In a span's last chunk X is <adjoint, faded state> itself, so that
+// differences are taken within a chunk and from chunk to chunk of one span only, between pairs that a gate parts.
+#include <algorithm>
+#include <cmath>
+
+#include "attn.hpp"
+
+namespace gsr {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kJoinValues = 4;  // of a state, each thread's
+constexpr int kJoinParts = 32;  // shares of the sequences
+
+// The state at every boundary between two spans, in place of what the span beside it adds; one thread runs through a
+// sequence's boundaries for its values.  The loads do not depend on the chain and are asked for eight at a time.
+__global__ __launch_bounds__(kThreads) void k_attn_join(const AttnArgs p, float* copies) {
+    const int64_t size = (int64_t)p.dk * p.dv;
+    const int kv = blockIdx.y, lane = threadIdx.x & 63;
+    const int64_t e0 = (int64_t)blockIdx.x * kThreads * kJoinValues + threadIdx.x;
+    const int64_t per = (p.n_seq + gridDim.z - 1) / gridDim.z;
+    const int64_t end = min(p.n_seq, (blockIdx.z + 1) * per);
+    for (int64_t s0 = blockIdx.z * per; s0 < end; s0 += 64) {
+        // the sequences of several spans among 64
+        int64_t lo = 0, len = 0;
+        if (s0 + lane < end) {
+            if (p.offsets) {
+                lo = attn_offset(p, s0 + lane);
+                len = attn_offset(p, s0 + lane + 1) - lo;
+            } else {
+                lo = (s0 + lane) * p.seq_len;
+                len = p.seq_len;
+            }
+        }
+        for (uint64_t todo = __ballot(len > p.span); todo; todo &= todo - 1) {
+            const int k = __builtin_ctzll(todo);
+            const int64_t s = s0 + k, slo = __shfl(lo, k);
+            const int spans = (int)((__shfl(len, k) + p.span - 1) / p.span);
+            const int64_t edge0 = p.offsets ? slo / p.span : s * (p.spans - 1);  // boundary between spans 0 and 1
+            const int64_t slot0 = p.offsets ? slo / p.span + s : s * p.spans;
+            float cur[kJoinValues];
+#pragma unroll
+            for (int i = 0; i < kJoinValues; ++i) {
+                const int64_t e = e0 + i * kThreads;
+                cur[i] = p.first && e < size ? p.first[(s * p.kv_heads + kv) * size + e] : 0.f;
+                if (copies && e < size) copies[(attn_copy(p, s, edge0) * p.kv_heads + kv) * size + e] = cur[i];
+            }
+            for (int b0 = 0; b0 < spans - 1; b0 += 8) {
+                float u[8][kJoinValues], t[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int b = min(b0 + j, spans - 2), at = p.against ? spans - 2 - b : b;  // boundary at, at + 1
+                    t[j] = p.totals[(slot0 + at + (p.against ? 1 : 0)) * p.kv_heads + kv];
+#pragma unroll
+                    for (int i = 0; i < kJoinValues; ++i) {
+                        const int64_t e = e0 + i * kThreads;
+                        u[j][i] = e < size ? p.edges[((edge0 + at) * p.kv_heads + kv) * size + e] : 0.f;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (b0 + j >= spans - 1) break;
+                    const int at = p.against ? spans - 2 - (b0 + j) : b0 + j;
+                    const float fade = -expm1f(t[j]);
+#pragma unroll
+                    for (int i = 0; i < kJoinValues; ++i) {
+                        const int64_t e = e0 + i * kThreads;
+                        cur[i] = __builtin_fmaf(-fade, cur[i], cur[i]) + u[j][i];
+                        if (e < size) p.edges[((edge0 + at) * p.kv_heads + kv) * size + e] = cur[i];
+                    }
+                }
+            }
+        }
+    }
+}
+
+struct AttnGateArgs {
+    const float* dots;   // [4][kv_heads][rows]: r, r', c, c'
+    void* grad;          // [rows, kv_heads], or (ld 0) null
+    int64_t ld;
+    double* sums;        // [slot][kv_heads] where the gate is one value for each head
+};
+
+// One workgroup a span and head: a half wave takes a chunk.
+__global__ __launch_bounds__(kThreads) void k_attn_gate(const AttnArgs p, const AttnGateArgs g) {
+    constexpr int kChunks = kAttnMaxSpan / kAttnChunk, kTurns = kChunks / (kThreads / 32);
+    __shared__ double s_r[kChunks], s_c[kChunks], s_x[kChunks], s_sum[kThreads / 32];
+    const int64_t slot = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int kv = blockIdx.z, lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+    if (slot >= p.slots) return;
+    const AttnSpan sp = attn_span(p, slot);
+    const int chunks = sp.live ? (sp.n + kAttnChunk - 1) / kAttnChunk : 0;
+    const int64_t plane = (int64_t)p.kv_heads * p.rows;
+    double known[kTurns];  // all of dg but X
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int c = part + k * (kThreads / 32), row = c * kAttnChunk + lane;
+        const bool in = c < chunks && row < sp.n;
+        const int64_t at = (int64_t)kv * p.rows + sp.row0 + row;
+        const double r = in ? (double)g.dots[at] : 0.0, own = in ? (double)g.dots[plane + at] : 0.0;
+        const double cc = in ? (double)g.dots[2 * plane + at] : 0.0, cown = in ? (double)g.dots[3 * plane + at] : 0.0;
+        double from = r + (own - cown), before = cc, sum_r = r;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const double x = __shfl_down(from, d, 32), y = __shfl_up(before, d, 32), z = __shfl_xor(sum_r, d, 32);
+            if (lane + d < 32) from += x;
+            if (lane >= d) before += y;
+            sum_r += z;
+        }
+        known[k] = from + (before - cc);
+        if (lane == 31 && c < chunks) {
+            s_r[c] = sum_r;
+            s_c[c] = before;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && chunks > 0) {
+        double x = (double)p.ends[slot * p.kv_heads + kv];
+        for (int c = chunks - 1; c >= 0; --c) {
+            s_x[c] = x;
+            x += s_r[c] - (c > 0 ? s_c[c - 1] : 0.0);
+        }
+    }
+    __syncthreads();
+    double sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int c = part + k * (kThreads / 32), row = c * kAttnChunk + lane;
+        if (c >= chunks || row >= sp.n) continue;
+        const float z = attn_gate(p, sp.row0 + row, kv);
+        const float rest = z > 0.f ? expf(-z) / (1.f + expf(-z)) : 1.f / (1.f + expf(z));  // 1 - sigma(z)
+        // where sigma is zero the pairs that the gate parts are too, whatever rounding left of the differences
+        const double dz = expf(z) == 0.f ? 0.0 : (known[k] + s_x[c]) * (double)rest;
+        sum += dz;
+        if (g.grad) {
+            const int64_t at = (sp.row0 + row) * g.ld + kv;
+            if (p.gate_type == GS_F32)
+                ((float*)g.grad)[at] = (float)dz;
+            else if (p.gate_type == GS_BF16)
+                ((__bf16*)g.grad)[at] = (__bf16)(float)dz;
+            else
+                ((_Float16*)g.grad)[at] = (_Float16)(float)dz;
+        }
+    }
+    if (g.sums) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 32);
+        if (lane == 0) s_sum[part] = sum;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int k = 1; k < kThreads / 32; ++k) sum += s_sum[k];
+            g.sums[slot * p.kv_heads + kv] = sum;
+        }
+    }
+}
+
+// Gradient of one gate for each head: the spans' sums in a fixed order.
+__global__ __launch_bounds__(kThreads) void k_attn_gate_sum(const double* sums, int64_t slots, int kv_heads, int type,
+                                                            void* out) {
+    __shared__ double s_sum[kThreads];
+    double v = 0.0;
+    for (int64_t k = threadIdx.x; k < slots; k += kThreads) v += sums[k * kv_heads + blockIdx.x];
+    s_sum[threadIdx.x] = v;
+    __syncthreads();
+    for (int n = kThreads / 2; n > 0; n >>= 1) {
+        if ((int)threadIdx.x < n) s_sum[threadIdx.x] += s_sum[threadIdx.x + n];
+        __syncthreads();
+    }
+    if (threadIdx.x != 0) return;
+    const float d = (float)s_sum[0];
+    if (type == GS_F32)
+        ((float*)out)[blockIdx.x] = d;
+    else if (type == GS_BF16)
+        ((__bf16*)out)[blockIdx.x] = (__bf16)d;
+    else
+        ((_Float16*)out)[blockIdx.x] = (_Float16)d;
+}
+
+// One token for each sequence: a workgroup a sequence and key head.  LV lanes lie along d_value (four values each), the
+// rest along d_key (R rows each); the state is read whole into registers, brought forward, written and multiplied by the
+// group's queries.  Bound by the state's bytes.
+template <class T, int LV, int R>
+__global__ __launch_bounds__(kThreads) void k_attn_step(const AttnArgs p) {
+    constexpr int kRows = kThreads / LV;  // threads along d_key
+    __shared__ float s_k[128], s_q[128], s_part[kThreads / 64][LV * 4];
+    const int64_t seq = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int kv = blockIdx.z;
+    if (seq >= p.n_seq) return;
+    const int v0 = (threadIdx.x % LV) * 4, r0 = threadIdx.x / LV;
+    const int64_t size = (int64_t)p.dk * p.dv, base = (seq * p.kv_heads + kv) * size;
+    attn_f32x4 S[R];
+    const int nv = p.dv - v0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int d = r0 + i * kRows;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (p.first && d < p.dk) attn_load4<float>(p.first + base + (int64_t)d * p.dv + v0, nv, v);
+        S[i] = attn_f32x4{v[0], v[1], v[2], v[3]};
+    }
+    if ((int)threadIdx.x < p.dk)
+        s_k[threadIdx.x] = (float)((const T*)p.y.p)[seq * p.y.row + kv * p.y.head + threadIdx.x];
+    float val[4];
+    attn_load4<T>((const T*)p.z.p + seq * p.z.row + kv * p.z.head + v0, nv, val);
+    const float z = attn_gate(p, seq, kv);
+    const float e = expf(-__builtin_fabsf(z));
+    const float fade = (z >= 0.f ? e : 1.f) / (1.f + e);  // 1 - a
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int d = r0 + i * kRows;
+        const float k = d < p.dk ? s_k[d] : 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) S[i][c] = __builtin_fmaf(k, val[c], __builtin_fmaf(-fade, S[i][c], S[i][c]));
+        if (p.last && d < p.dk) {
+            const float v[4] = {S[i][0], S[i][1], S[i][2], S[i][3]};
+            attn_store4<float>(p.last + base + (int64_t)d * p.dv + v0, nv, v);
+        }
+    }
+    for (int h = 0; h < p.group; ++h) {
+        const int head = kv * p.group + h;
+        __syncthreads();
+        if ((int)threadIdx.x < p.dk)
+            s_q[threadIdx.x] = (float)((const T*)p.x.p)[seq * p.x.row + head * p.x.head + threadIdx.x];
+        __syncthreads();
+        attn_f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int d = r0 + i * kRows;
+            const float q = d < p.dk ? s_q[d] : 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[c] = __builtin_fmaf(q, S[i][c], o[c]);
+        }
+        for (int m = LV; m < 64; m <<= 1)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[c] += __shfl_xor(o[c], m);
+        if ((threadIdx.x & 63) < LV)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s_part[threadIdx.x >> 6][v0 + c] = o[c];
+        __syncthreads();
+        if ((int)threadIdx.x < p.dv) {
+            float v = s_part[0][threadIdx.x];
+#pragma unroll
+            for (int k = 1; k < kThreads / 64; ++k) v += s_part[k][threadIdx.x];
+            ((T*)const_cast<void*>(p.out.p))[seq * p.out.row + head * p.out.head + threadIdx.x] = (T)(v * p.scale_out);
+        }
+    }
+}
+
+template <class T>
+hipError_t attn_step(const AttnArgs& a, hipStream_t st) {
+    constexpr int64_t kWide = 1 << 22;
+    const int64_t x = std::min<int64_t>(a.n_seq, kWide);
+    const dim3 grid((unsigned)x, (unsigned)((a.n_seq + x - 1) / x), (unsigned)a.kv_heads);
+    if (a.dv <= 64) {
+        if (a.dk <= 64)
+            k_attn_step<T, 16, 4><<<grid, kThreads, 0, st>>>(a);
+        else
+            k_attn_step<T, 16, 8><<<grid, kThreads, 0, st>>>(a);
+    } else if (a.dk <= 64) {
+        k_attn_step<T, 32, 8><<<grid, kThreads, 0, st>>>(a);
+    } else {
+        k_attn_step<T, 32, 16><<<grid, kThreads, 0, st>>>(a);
+    }
+    return hipGetLastError();
+}
+
+// Rows of a span: enough spans to fill the card, as long as they fit.
+int attn_span_rows(const gs_attn_dims& d) {
+    constexpr int64_t kSpans = 1024;
+    const int64_t rows = (d.rows * d.kv_heads + kSpans - 1) / kSpans;
+    const int64_t most = d.dtype == GS_BF16 ? kAttnMaxSpan : kAttnMaxSpan / 2;
+    return (int)std::min<int64_t>(most, std::max<int64_t>(128, (rows + kAttnChunk - 1) / kAttnChunk * kAttnChunk));
+}
+
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+
+struct AttnPlan {
+    int64_t edges, copies, slots;  // counts
+    size_t state, edge_bytes, copy_bytes, total_bytes;
+};
+AttnPlan attn_plan(const gs_attn_dims& d) {
+    AttnPlan r;
+    const int span = attn_span_rows(d);
+    r.edges = d.rows / span;
+    r.slots = r.edges + d.n_seq;  // at least what equal lengths need
+    r.copies = std::min<int64_t>(r.edges, d.n_seq);
+    r.state = (size_t)d.kv_heads * d.d_key * d.d_value * 4;
+    r.edge_bytes = up(r.edges * r.state);
+    r.copy_bytes = up(r.copies * r.state);
+    r.total_bytes = r.edges ? up((size_t)r.slots * d.kv_heads * 4) : 0;
+    return r;
+}
+
+AttnArgs attn_args(const gs_attn_dims& d, const int64_t* offsets, const gs_attn_inputs& in) {
+    AttnArgs a{};
+    a.gate = in.gate;
+    a.ld_gate = d.gate_per_row ? in.ld_gate : 0;
+    a.gate_type = d.gate_dtype;
+    a.offsets = offsets;
+    a.rows = d.rows;
+    a.n_seq = d.n_seq;
+    a.span = attn_span_rows(d);
+    a.seq_len = offsets ? 0 : d.rows / d.n_seq;
+    a.spans = offsets ? 0 : (int)std::max<int64_t>(1, (a.seq_len + a.span - 1) / a.span);
+    a.slots = offsets ? d.rows / a.span + d.n_seq : d.n_seq * a.spans;
+    a.kv_heads = d.kv_heads;
+    a.group = d.heads / d.kv_heads;
+    a.dk = d.d_key;
+    a.dv = d.d_value;
+    const AttnPlan pl = attn_plan(d);
+    a.copies_by_sequence = d.n_seq <= pl.edges;
+    return a;
+}
+
+AttnArray array(const gs_heads& h) { return {h.p, h.ld_row, h.ld_head}; }
+
+hipError_t launch_kernel(int dtype, AttnKind kind, const AttnArgs& a, hipStream_t st) {
+    if (dtype == GS_BF16) return launch_attn_kernel<__bf16>(kind, a, st);
+    if (dtype == GS_F16) return launch_attn_kernel<_Float16>(kind, a, st);
+    return launch_attn_kernel<float>(kind, a, st);
+}
+
+// A sequence has more than one span.
+bool attn_splits(const AttnArgs& a) { return a.offsets ? a.rows > a.span : a.spans > 1; }
+
+hipError_t join(const AttnArgs& a, float* copies, hipStream_t st) {
+    const int64_t size = (int64_t)a.dk * a.dv;
+    k_attn_join<<<dim3((unsigned)((size + kThreads * kJoinValues - 1) / (kThreads * kJoinValues)), a.kv_heads,
+                       (unsigned)std::min<int64_t>(a.n_seq, kJoinParts)),
+                  kThreads, 0, st>>>(a, copies);
+    return hipGetLastError();
+}
+
+#define GSR_HIP(x)                      \
+    do {                                \
+        const hipError_t e_ = (x);      \
+        if (e_ != hipSuccess) return e_; \
+    } while (0)
+
+}  // namespace
+
+void attn_sizes(const gs_attn_dims& d, size_t* saved, size_t* fwd, size_t* bwd) {
+    const AttnPlan pl = attn_plan(d);
+    *saved = pl.edge_bytes;
+    *fwd = pl.edge_bytes + pl.total_bytes + pl.copy_bytes;
+    *bwd = pl.edge_bytes + pl.total_bytes + pl.copy_bytes + up((size_t)pl.slots * d.kv_heads * 4) +
+           up((size_t)4 * d.kv_heads * d.rows * 4) + (d.gate_per_row ? 0 : up((size_t)pl.slots * d.kv_heads * 8));
+}
+
+hipError_t launch_attn_forward(const gs_attn_dims& d, const int64_t* offsets, const gs_attn_inputs& in, const gs_heads& y,
+                               float* last, float* saved, void* ws, hipStream_t st) {
+    if (d.n_seq == 0) return hipSuccess;
+    AttnArgs a = attn_args(d, offsets, in);
+    a.first = in.state;
+    a.last = last;
+    a.x = array(in.q);
+    a.y = array(in.k);
+    a.z = array(in.v);
+    a.out = array(y);
+    a.dc = d.d_key;
+    a.dout = d.d_value;
+    a.scale_pair = a.scale_state = 1.f;
+    a.scale_out = d.scale;
+    if (!offsets && a.seq_len == 1) {
+        if (d.dtype == GS_BF16) return attn_step<__bf16>(a, st);
+        if (d.dtype == GS_F16) return attn_step<_Float16>(a, st);
+        return attn_step<float>(a, st);
+    }
+    const AttnPlan pl = attn_plan(d);
+    char* at = (char*)ws;
+    a.edges = saved ? saved : (float*)at;
+    a.totals = (float*)(at + pl.edge_bytes);
+    if (attn_splits(a)) {
+        AttnArgs g = a;
+        GSR_HIP(launch_kernel(d.dtype, kAttnAggregate, g, st));
+        float* copies = in.state && in.state == last ? (float*)(at + pl.edge_bytes + pl.total_bytes) : nullptr;
+        GSR_HIP(join(a, copies, st));
+        a.copies = copies;
+    }
+    return launch_kernel(d.dtype, kAttnForward, a, st);
+}
+
+hipError_t launch_attn_backward(const gs_attn_dims& d, const int64_t* offsets, const gs_attn_inputs& in,
+                                const float* saved, const gs_heads& dy, const float* d_last, const gs_attn_grads& out,
+                                void* ws, hipStream_t st) {
+    if (d.n_seq == 0) {
+        if (out.gate && !d.gate_per_row) {
+            k_attn_gate_sum<<<d.kv_heads, kThreads, 0, st>>>(nullptr, 0, d.kv_heads, d.gate_dtype, out.gate);
+            return hipGetLastError();
+        }
+        return hipSuccess;
+    }
+    const AttnPlan pl = attn_plan(d);
+    const AttnArgs base = attn_args(d, offsets, in);
+    char* at = (char*)ws;
+    float* edges = (float*)at;
+    at += pl.edge_bytes;
+    float* totals = (float*)at;
+    at += pl.total_bytes;
+    float* copies = d_last && d_last == out.state ? (float*)at : nullptr;
+    at += pl.copy_bytes;
+    float* ends = (float*)at;
+    at += up((size_t)pl.slots * d.kv_heads * 4);
+    float* dots = (float*)at;
+    at += up((size_t)4 * d.kv_heads * d.rows * 4);
+    double* sums = d.gate_per_row ? nullptr : (double*)at;
+    const size_t plane = (size_t)d.kv_heads * d.rows;
+
+    AttnArgs rev = base;  // on the adjoint
+    rev.first = d_last;
+    rev.edges = edges;
+    rev.totals = totals;
+    rev.against = true;
+    rev.scale_pair = rev.scale_state = d.scale;
+    rev.scale_out = 1.f;
+    const bool split = attn_splits(base);
+    if (split) {
+        AttnArgs g = rev;  // [dk][dv]: q contracted
+        g.y = array(in.q);
+        g.z = array(dy);
+        g.dc = d.d_key;
+        g.dout = d.d_value;
+        GSR_HIP(launch_kernel(d.dtype, kAttnAggregate, g, st));
+        GSR_HIP(join(g, copies, st));
+    }
+    rev.copies = split ? copies : nullptr;
+    if (out.q.p || out.gate) {
+        AttnArgs a = base;
+        a.x = array(dy);
+        a.y = array(in.v);
+        a.z = array(in.k);
+        a.out = array(out.q);
+        a.w = array(in.q);
+        a.dc = d.d_value;
+        a.dout = d.d_key;
+        a.transposed = true;
+        a.scale_pair = a.scale_state = 1.f;
+        a.scale_out = d.scale;
+        a.first = in.state;
+        a.edges = const_cast<float*>(saved);
+        a.other_edges = edges;
+        a.other_last = d_last;
+        a.ends = ends;
+        a.dots = dots;
+        GSR_HIP(launch_kernel(d.dtype, kAttnGradQ, a, st));
+    }
+    if (out.k.p || out.gate) {
+        AttnArgs a = rev;
+        a.x = array(in.v);
+        a.y = array(dy);
+        a.z = array(in.q);
+        a.out = array(out.k);
+        a.w = array(in.k);
+        a.dc = d.d_value;
+        a.dout = d.d_key;
+        a.transposed = true;
+        a.dots = dots + 2 * plane;
+        GSR_HIP(launch_kernel(d.dtype, kAttnGradK, a, st));
+    }
+    if (out.gate) {
+        AttnArgs a = base;
+        a.ends = ends;
+        const AttnGateArgs g{dots, d.gate_per_row ? out.gate : nullptr, out.ld_gate, sums};
+        constexpr int64_t kWide = 1 << 22;
+        const int64_t x = std::min<int64_t>(a.slots, kWide);
+        k_attn_gate<<<dim3((unsigned)x, (unsigned)((a.slots + x - 1) / x), (unsigned)a.kv_heads), kThreads, 0, st>>>(a, g);
+        GSR_HIP(hipGetLastError());
+        if (sums) {
+            k_attn_gate_sum<<<d.kv_heads, kThreads, 0, st>>>(sums, a.slots, d.kv_heads, d.gate_dtype, out.gate);
+            GSR_HIP(hipGetLastError());
+        }
+    }
+    if (out.v.p || out.state) {
+        AttnArgs a = rev;
+        a.x = array(in.k);
+        a.y = array(in.q);
+        a.z = array(dy);
+        a.out = array(out.v);
+        a.dc = d.d_key;
+        a.dout = d.d_value;
+        a.last = out.state;
+        GSR_HIP(launch_kernel(d.dtype, kAttnGradV, a, st));
+    }
+    return hipSuccess;
+}
+
+}  // namespace gsr

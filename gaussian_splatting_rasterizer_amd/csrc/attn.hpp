@@ -1,0 +1,704 @@
+// attn.hpp -- the matrix-core kernel of linear attention with a decay for each head (device code and its launcher).
+//
+//   S_t = a_t S_{t-1} + k_t v_t^T,   y_t = scale S_t^T q_t,   a = sigma(gate)            per sequence and key head
+//
+// One kernel does every direction.  It takes destinations X, sources (Y, Z) and a state S [contracted x out]:
+//   out_i = sum over the sources j up to i of w_ij (x_i . y_j) z_j + w_i S^T x_i,   S' = w S + sum_j w'_j y_j z_j^T
+// forward: (q; k, v), gradient of q: (dy; v, k) with the transposed state; and against the rows' order, on the adjoint
+// D_t = scale sum_heads q_t dy_t^T + a_{t+1} D_{t+1} in the state's place: gradient of k: (v; dy, q) with D transposed,
+// gradient of v: (k; q, dy).
+//
+// Rows of a sequence are cut into spans, one workgroup's, and those into chunks of 32 rows, one matrix tile.  With
+// p_i the sum of log2 a over the chunk's rows up to i and P its total, w_ij = 2^(p_i - p_j), w_i = 2^p_i, w = 2^P and
+// w'_j = 2^(P - p_j) (against the order: 2^(p_j - p_i), 2^(P - p_i), 2^P, 2^p_j).  The sums p are float64 and kept in
+// pairs of float32, so that a difference keeps its precision behind a gate that forgets nearly everything.
+//
+// A wave holds 32 columns of the state (the whole contracted side) in the matrix instructions' result layout for as long
+// as the span lasts: S never goes through LDS.  That layout gives a lane, in two groups of four, half of the rows that a
+// following product's operand needs, in an order (0-3 8-11 | 4-7 12-15) that the other operand is stored in as well; the
+// same holds for the 32 x 32 scores, which every wave computes for itself instead of sharing them across a barrier.  Only
+// X, Y and Z go through LDS, row by row, and are read there either by rows or transposed.
+//
+// Operands are bfloat16 planes whose sum is the value: one for bfloat16 inputs, two for float16, three for float32 (24
+// bits); the state, the scores and the weighted z are split into ORDER + 1 planes where they are used, and products of
+// planes whose ranks add up to more than ORDER are left out (2^-8 per rank).  ORDER is 2, except for 16-bit results of the
+// forward pass, where 1 (2^-17) is far below their rounding; the state itself is always summed with 2.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gsr_internal.hpp"
+#include "values.hpp"
+
+namespace gsr {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 attn_bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 attn_bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t attn_u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t attn_u32x2 __attribute__((ext_vector_type(2)));
+typedef short attn_s16x4 __attribute__((ext_vector_type(4)));
+typedef float attn_f32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) attn_s16x4 attn_lds_s16x4;
+
+constexpr int kAttnChunk = 32;
+constexpr int kAttnMaxSpan = 1024;  // rows whose weights lie in LDS (16-bit)
+
+// Rows [rows, heads, d] of one array.
+struct AttnArray {
+    const void* p;
+    int64_t row, head;  // elements
+};
+
+struct AttnArgs {
+    AttnArray x, y, z, out, w;  // w: what the outputs are multiplied by for the gate's gradient
+    const void* gate;
+    int64_t ld_gate;            // 0: one value for each head
+    int gate_type;
+    const int64_t* offsets;
+    int64_t rows, n_seq, seq_len, slots;
+    int spans;                  // of every sequence (no offsets)
+    int span;                   // rows of a span
+    int kv_heads, group;        // query heads of a key head
+    int dc, dout;               // contracted and out widths
+    int dk, dv;                 // the state is [dk][dv]
+    bool transposed;            // contracted side is dv
+    float scale_pair, scale_state, scale_out;
+    const float* first;         // state (adjoint: gradient of the last one) that a sequence starts from; null: zero
+    const float* copies;        // the same for sequences of several spans (attn_copy); null: first
+    bool copies_by_sequence;
+    float* last;                // what a sequence ends with; null: not wanted
+    float* edges;               // [boundary][kv_heads][dk][dv]: the state at every boundary between two spans
+    const float* other_edges;   // the adjoint's, for the products at the spans' ends
+    const float* other_last;
+    float* ends;                // [slot][kv_heads] <adjoint behind the span, what its last chunk leaves of the state before>
+    float* totals;              // [slot][kv_heads] log a summed over the span
+    float* dots;                // [2][kv_heads][rows]: out . w, of what comes from before the chunk and from within it
+    bool against;               // aggregates: against the rows' order
+};
+
+// A span of a sequence.
+struct AttnSpan {
+    int64_t row0, seq, edge;    // edge: boundary in front of it (meant for a span that is not the first)
+    int n, index;
+    bool live, first, last, single;
+};
+
+__device__ __forceinline__ int64_t attn_offset(const AttnArgs& p, int64_t s) {
+    const int64_t o = p.offsets[s];
+    return o < 0 ? 0 : o > p.rows ? p.rows : o;
+}
+
+// Where the copy of a sequence's first state lies: by sequence, or by its first boundary where there are fewer of those.
+__device__ __forceinline__ int64_t attn_copy(const AttnArgs& p, int64_t seq, int64_t first_edge) {
+    return p.copies_by_sequence ? seq : first_edge;
+}
+
+// The span of a slot.  With offsets, sequence s has the slots from offsets[s] / span + s on, at least as many as it
+// needs, and the boundaries from offsets[s] / span on; spans that it does not need are not live.
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs& p, int64_t slot) {
+    AttnSpan r;
+    int64_t lo, hi;
+    if (!p.offsets) {
+        r.seq = slot / p.spans;
+        r.index = (int)(slot % p.spans);
+        lo = r.seq * p.seq_len;
+        hi = lo + p.seq_len;
+        r.edge = r.seq * (p.spans - 1) + r.index - 1;
+    } else {
+        // the last sequence whose slots start at or before this one: 64 probes at a time
+        const int lane = threadIdx.x & 63;
+        int64_t a = 0, b = p.n_seq;  // in [a, b)
+        while (b - a > 1) {
+            const int64_t step = (b - a + 63) / 64, at = a + lane * step;
+            const bool yes = at < b && attn_offset(p, at) / p.span + at <= slot;
+            const uint64_t votes = __ballot(yes) | 1;
+            const int k = 63 - __builtin_clzll(votes);
+            a += k * step;
+            b = min(b, a + step);
+        }
+        r.seq = a;
+        lo = attn_offset(p, a);
+        hi = max(lo, attn_offset(p, a + 1));
+        const int64_t index = slot - (lo / p.span + a);
+        r.index = (int)index;
+        r.edge = lo / p.span + index - 1;
+    }
+    const int64_t len = hi - lo;
+    r.row0 = lo + (int64_t)r.index * p.span;
+    r.live = r.index >= 0 && (r.row0 < hi || (r.index == 0 && len == 0));
+    r.n = (int)min((int64_t)p.span, hi - r.row0);
+    r.first = r.index == 0;
+    r.last = r.row0 + p.span >= hi;
+    r.single = len <= p.span;
+    return r;
+}
+
+template <class T>
+struct AttnType;
+template <>
+struct AttnType<__bf16> {
+    static constexpr int kPlanes = 1;
+};
+template <>
+struct AttnType<_Float16> {
+    static constexpr int kPlanes = 2;
+};
+template <>
+struct AttnType<float> {
+    static constexpr int kPlanes = 3;
+};
+
+// N planes of two values, a word each.
+template <int N>
+__device__ __forceinline__ void split_pair(float a, float b, uint32_t* out) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const attn_bf16x2 h = {(__bf16)a, (__bf16)b};
+        out[n] = __builtin_bit_cast(uint32_t, h);
+        if (n + 1 < N) {
+            a -= __builtin_bit_cast(float, out[n] << 16);
+            b -= __builtin_bit_cast(float, out[n] & 0xffff0000u);
+        }
+    }
+}
+// N operand fragments of eight values.
+template <int N>
+__device__ __forceinline__ void split_frag(const float* v, attn_u32x4* out) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t w[N];
+        split_pair<N>(v[2 * e], v[2 * e + 1], w);
+#pragma unroll
+        for (int n = 0; n < N; ++n) out[n][e] = w[n];
+    }
+}
+__device__ __forceinline__ f32x16 attn_mfma(attn_u32x4 a, attn_u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(attn_bf16x8, a), __builtin_bit_cast(attn_bf16x8, b), c,
+                                                   0, 0, 0);
+}
+
+// A tile of 32 rows x D in LDS, one plane: 16-byte slots, slot (k, half) of a row holding columns 16 k + 4 half + 0..3 and
+// 16 k + 8 + 4 half + 0..3, at position slot ^ row, so that the lanes of a read by rows spread over the banks.
+template <int D>
+struct AttnTile {
+    static constexpr int kRow = D * 2, kSlots = D / 8, kBytes = kAttnChunk * kRow;
+    // 8 bytes: columns 4 quad .. 4 quad + 3 of a row
+    static __device__ __forceinline__ int quad(int row, int q) {
+        const int slot = (q >> 2) * 2 + (q & 1);
+        return row * kRow + ((slot ^ (row & (kSlots - 1))) << 4) + ((q >> 1) & 1) * 8;
+    }
+    // by rows: the lane's row, columns of k-step kk
+    static __device__ __forceinline__ attn_u32x4 rows(const char* t, int kk, int lane) {
+        const int r = lane & 31, slot = kk * 2 + (lane >> 5);
+        return *(const attn_u32x4*)(t + r * kRow + ((slot ^ (r & (kSlots - 1))) << 4));
+    }
+    // transposed: column col0 + (lane & 31), rows 16 ks + 4 half + 0..3 and + 8
+    static __device__ __forceinline__ attn_u32x4 columns(const char* t, int col0, int ks, int lane) {
+        const int row = ks * 16 + (lane >> 5) * 4 + ((lane & 15) >> 2);
+        const int q = (col0 + ((lane >> 4) & 1) * 16) / 4 + (lane & 3);
+        const attn_s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s16x4*)(t + quad(row, q)));
+        const attn_s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s16x4*)(t + quad(row + 8, q)));
+        const attn_u32x2 x = __builtin_bit_cast(attn_u32x2, a), y = __builtin_bit_cast(attn_u32x2, b);
+        return attn_u32x4{x[0], x[1], y[0], y[1]};
+    }
+};
+
+// One tile on its way from memory to LDS: runs of eight values, spread over the workgroup.
+template <class T, int D, int NT>
+struct AttnFetch {
+    static constexpr int kRuns = kAttnChunk * (D / 8) / NT, kPlanes = AttnType<T>::kPlanes;
+    Run8<T> run[kRuns];
+    __device__ __forceinline__ void load(const AttnArray& a, int64_t row0, int n, int head, int d) {
+        const T* base = (const T*)a.p + row0 * a.row + head * a.head;
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) {
+            const int u = i * NT + threadIdx.x, r = u / (D / 8), c = (u % (D / 8)) * 8;
+            run[i].load(base + r * a.row + c, r < n ? d - c : 0);
+        }
+    }
+    __device__ __forceinline__ void store(char* tile) const {
+#pragma unroll
+        for (int i = 0; i < kRuns; ++i) {
+            const int u = i * NT + threadIdx.x, r = u / (D / 8), q = (u % (D / 8)) * 2;
+            uint32_t w[4][kPlanes];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (kPlanes == 1)
+                    __builtin_memcpy(w[e], &run[i].v[2 * e], 4);
+                else
+                    split_pair<kPlanes>(run[i].get(2 * e), run[i].get(2 * e + 1), w[e]);
+            }
+#pragma unroll
+            for (int n = 0; n < kPlanes; ++n) {
+                char* t = tile + n * AttnTile<D>::kBytes;
+                *(attn_u32x2*)(t + AttnTile<D>::quad(r, q)) = attn_u32x2{w[0][n], w[1][n]};
+                *(attn_u32x2*)(t + AttnTile<D>::quad(r, q + 1)) = attn_u32x2{w[2][n], w[3][n]};
+            }
+        }
+    }
+};
+
+// log2 sigma(z) to its own relative precision; a gate below about -177 counts as that: 2^-256 is zero in every use.
+__device__ __forceinline__ double log2_gate(float z) {
+    const float l = fminf(z, 0.f) - log1pf(expf(-__builtin_fabsf(z)));
+    const double g = (double)(z != z ? z : l) * 1.4426950408889634;
+    return g < -256.0 ? -256.0 : g;
+}
+
+__device__ __forceinline__ float attn_gate(const AttnArgs& p, int64_t row, int head) {
+    const int64_t at = p.ld_gate ? row * p.ld_gate + head : head;
+    if (p.gate_type == GS_F32) return ((const float*)p.gate)[at];
+    if (p.gate_type == GS_BF16) return (float)((const __bf16*)p.gate)[at];
+    return (float)((const _Float16*)p.gate)[at];
+}
+
+// Weights of a span's rows, in LDS.
+struct AttnWeights {
+    float *hi, *lo, *in, *out, *fade;  // fade: 1 - 2^P of a chunk
+};
+
+__device__ __forceinline__ void attn_weights(const AttnArgs& p, const AttnSpan& s, int head, bool against,
+                                             const AttnWeights& w, double* total) {
+    const int lane = threadIdx.x & 31;
+    const int rows = (s.n + kAttnChunk - 1) / kAttnChunk * kAttnChunk;
+    for (int r = threadIdx.x; r < (rows + 63) / 64 * 64; r += blockDim.x) {  // whole waves
+        double g = r < s.n ? log2_gate(attn_gate(p, s.row0 + r, head)) : 0.0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const double before = __shfl_up(g, d, 32);
+            if (lane >= d) g += before;
+        }
+        const double P = __shfl(g, 31, 32);
+        if (r < rows) {
+            const float hi = (float)g;
+            const float to = __builtin_amdgcn_exp2f(hi), rest = __builtin_amdgcn_exp2f((float)(P - g));
+            w.hi[r] = hi;
+            w.lo[r] = (float)(g - (double)hi);
+            w.in[r] = against ? rest : to;
+            w.out[r] = (against ? to : rest) * p.scale_state;
+            if (lane == 0) {
+                w.fade[r / kAttnChunk] = -expm1f((float)(P * 0.6931471805599453));
+                if (total) total[r / kAttnChunk] = P * 0.6931471805599453;
+            }
+        }
+    }
+}
+
+// 32 contracted rows of a wave's columns of a state (null: zero).
+__device__ __forceinline__ void attn_load_tile(f32x16& s, const float* from, const AttnArgs& p, int t, int col0, int lane) {
+    const int o = col0 + (lane & 31);
+    const int64_t sc = p.transposed ? 1 : p.dv, so = p.transposed ? p.dv : 1;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int c = t * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        s[r] = from && c < p.dc && o < p.dout ? from[c * sc + o * so] : 0.f;
+    }
+}
+template <int KT>
+__device__ __forceinline__ void attn_load_state(f32x16* s, const float* from, const AttnArgs& p, int col0, int lane) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t) attn_load_tile(s[t], from, p, t, col0, lane);
+}
+template <int KT>
+__device__ __forceinline__ void attn_store_state(const f32x16* s, float* to, const AttnArgs& p, int col0, int lane) {
+    const int o = col0 + (lane & 31);
+    const int64_t sc = p.transposed ? 1 : p.dv, so = p.transposed ? p.dv : 1;
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const int c = t * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+            if (c < p.dc && o < p.dout) to[c * sc + o * so] = s[t][r];
+        }
+}
+
+// Four consecutive columns of a row as they lie in memory.
+template <class T>
+__device__ __forceinline__ void attn_load4(const T* p, int n, float* out) {
+    T v[4];
+    if (n >= 4) {
+        __builtin_memcpy(v, p, sizeof(v));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = e < n ? p[e] : (T)0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[e] = (float)v[e];
+}
+template <class T>
+__device__ __forceinline__ void attn_store4(T* p, int n, const float* in) {
+    T v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (T)in[e];
+    if (n >= 4) {
+        __builtin_memcpy(p, v, sizeof(v));
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n) p[e] = v[e];
+    }
+}
+
+// LDS of a workgroup: tiles of X, Y, Z (twice where the type has one plane: the next ones are stored while these are
+// read), weights and a little for sums.
+template <class T, int KD, int OD, bool AGG>
+struct AttnLds {
+    static constexpr int kPlanes = AttnType<T>::kPlanes, kBuffers = kPlanes == 1 ? 2 : 1;
+    static constexpr int kX = AGG ? 0 : AttnTile<KD>::kBytes * kPlanes, kY = AttnTile<KD>::kBytes * kPlanes,
+                         kZ = AttnTile<OD>::kBytes * kPlanes;
+    static constexpr int kTiles = kBuffers * (kX + kY + kZ);
+    static constexpr int kSums = 2 * 2 * (OD / 32) * 32 * 4;
+    static constexpr int kFixed = kTiles + kSums;
+    static constexpr int bytes(int span) { return kFixed + span * 16 + span / kAttnChunk * 16; }
+};
+
+// REV: against the rows' order.  DOT: gradient of q (of k): also the products of the outputs with w and, at the span's end,
+// of the state and the adjoint.  AGG: what the span adds to the state alone.
+template <class T, int KD, int OD, int ORDER, bool REV, bool DOT, bool AGG>
+__global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
+    constexpr int NW = OD / 32, NT = NW * 64, KT = KD / 32, NP = AttnType<T>::kPlanes;
+    using Lds = AttnLds<T, KD, OD, AGG>;
+    extern __shared__ __attribute__((aligned(1024))) char smem[];
+    char* s_x = smem;
+    char* s_y = smem + Lds::kBuffers * Lds::kX;
+    char* s_z = s_y + Lds::kBuffers * Lds::kY;
+    float* s_sum = (float*)(smem + Lds::kTiles);  // [2][2][NW][32]
+    AttnWeights w;
+    w.hi = (float*)(smem + Lds::kFixed);
+    w.lo = w.hi + p.span;
+    w.in = w.lo + p.span;
+    w.out = w.in + p.span;
+    w.fade = w.out + p.span;
+    double* s_total = (double*)(w.fade + 2 * (p.span / kAttnChunk));
+
+    const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t slot = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int kv = blockIdx.z;
+    if (slot >= p.slots) return;
+    const AttnSpan sp = attn_span(p, slot);
+    const bool against = AGG ? p.against : REV;
+    if (!sp.live || (AGG && (against ? sp.first : sp.last))) return;
+    const int64_t state_size = (int64_t)p.dk * p.dv;
+    const int col0 = wave * 32;
+
+    f32x16 S[KT];
+    if constexpr (AGG) {
+        attn_load_state<KT>(S, nullptr, p, col0, lane);
+    } else {
+        const float* from;
+        if (REV ? sp.last : sp.first) {
+            from = p.copies && !sp.single
+                       ? p.copies + (attn_copy(p, sp.seq, sp.edge - sp.index + 1) * p.kv_heads + kv) * state_size
+                   : p.first ? p.first + (sp.seq * p.kv_heads + kv) * state_size
+                             : nullptr;
+        } else {
+            from = p.edges + ((sp.edge + (REV ? 1 : 0)) * p.kv_heads + kv) * state_size;
+        }
+        attn_load_state<KT>(S, from, p, col0, lane);
+    }
+    attn_weights(p, sp, kv, against, w, AGG ? s_total : nullptr);
+
+    const int chunks = (sp.n + kAttnChunk - 1) / kAttnChunk, G = AGG && !p.against ? 1 : p.group;
+    const bool rev_items = AGG ? p.against : REV;  // the group's heads are sources; otherwise destinations
+    const int items = chunks * G;
+    AttnFetch<T, KD, NT> fx, fy;
+    AttnFetch<T, OD, NT> fz;
+    auto chunk_of = [&](int it) { return against ? chunks - 1 - it / G : it / G; };
+    auto load = [&](int it) {
+        const int h = it % G, c = chunk_of(it), n = min(kAttnChunk, sp.n - c * kAttnChunk);
+        const int64_t row0 = sp.row0 + c * kAttnChunk;
+        if (!AGG && (!REV || h == 0)) fx.load(p.x, row0, n, REV ? kv : kv * G + h, p.dc);
+        if (rev_items || h == 0) {
+            fy.load(p.y, row0, n, rev_items ? kv * G + h : kv, p.dc);
+            fz.load(p.z, row0, n, rev_items ? kv * G + h : kv, p.dout);
+        }
+    };
+    auto x_tile = [&](int it) { return s_x + (Lds::kBuffers == 2 ? (REV ? it / G : it) & 1 : 0) * Lds::kX; };
+    auto yz_turn = [&](int it) { return Lds::kBuffers == 2 ? (rev_items ? it : it / G) & 1 : 0; };
+    auto store = [&](int it) {
+        const int h = it % G;
+        if (!AGG && (!REV || h == 0)) fx.store(x_tile(it));
+        if (rev_items || h == 0) {
+            fy.store(s_y + yz_turn(it) * Lds::kY);
+            fz.store(s_z + yz_turn(it) * Lds::kZ);
+        }
+    };
+    if (items > 0) {
+        load(0);
+        store(0);
+    }
+    __syncthreads();
+
+    f32x16 o;
+    float dot_in = 0.f, dot_own = 0.f, dot_end = 0.f;
+    for (int it = 0; it < items; ++it) {
+        const int h = it % G, c = chunk_of(it), n = min(kAttnChunk, sp.n - c * kAttnChunk);
+        const int64_t row0 = sp.row0 + c * kAttnChunk;
+        if (it + 1 < items) load(it + 1);
+        const char* tx = x_tile(it);
+        const char* ty = s_y + yz_turn(it) * Lds::kY;
+        const char* tz = s_z + yz_turn(it) * Lds::kZ;
+        const float *hi = w.hi + c * kAttnChunk, *lo = w.lo + c * kAttnChunk, *wout = w.out + c * kAttnChunk;
+
+        if constexpr (!AGG) {
+            const bool inter = !REV || h == 0;
+            float wv[16];
+            if constexpr (DOT) {
+                const T* wp = (const T*)p.w.p + (row0 + col) * p.w.row + (REV ? kv : kv * G + h) * p.w.head + col0 + 4 * half;
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    attn_load4<T>(wp + 8 * g, col < n ? p.dout - (col0 + 4 * half + 8 * g) : 0, wv + 4 * g);
+            }
+            if (inter) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[r] = 0.f;
+                dot_in = h == 0 ? 0.f : dot_in;
+            }
+            dot_own = h == 0 ? 0.f : dot_own;
+            f32x16 pt;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) pt[r] = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < KD / 16; ++kk) {
+                attn_u32x4 xf[NP], yf[NP];
+#pragma unroll
+                for (int n2 = 0; n2 < NP; ++n2) {
+                    xf[n2] = AttnTile<KD>::rows(tx + n2 * AttnTile<KD>::kBytes, kk, lane);
+                    yf[n2] = AttnTile<KD>::rows(ty + n2 * AttnTile<KD>::kBytes, kk, lane);
+                }
+#pragma unroll
+                for (int i = 0; i < NP; ++i)
+#pragma unroll
+                    for (int j = 0; j < NP; ++j)
+                        if (i + j <= ORDER) pt = attn_mfma(yf[i], xf[j], pt);
+                if (inter) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = S[kk >> 1][(kk & 1) * 8 + e];
+                    attn_u32x4 sf[ORDER + 1];
+                    split_frag<ORDER + 1>(v, sf);
+#pragma unroll
+                    for (int i = 0; i <= ORDER; ++i)
+#pragma unroll
+                        for (int j = 0; j < NP; ++j)
+                            if (i + j <= ORDER) o = attn_mfma(sf[i], xf[j], o);
+                }
+            }
+            if (inter) {
+                const float wi = w.in[c * kAttnChunk + col];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[r] *= wi;
+                if constexpr (DOT) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) dot_in = __builtin_fmaf(o[r], wv[r], dot_in);
+                }
+            }
+            // scores: row r of the tile is source 8 (r / 4) + 4 half + r % 4, the lane's column its destination
+            const float hi_i = hi[col], lo_i = lo[col];
+            f32x16 diag;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const attn_f32x4 hs = *(const attn_f32x4*)(hi + 8 * g + 4 * half), ls = *(const attn_f32x4*)(lo + 8 * g + 4 * half);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int s = 8 * g + 4 * half + e, r = 4 * g + e;
+                    const float d = (hi_i - hs[e]) + (lo_i - ls[e]);
+                    const float v = pt[r] * (__builtin_amdgcn_exp2f(REV ? -d : d) * p.scale_pair);
+                    if constexpr (DOT) {
+                        diag[r] = s == col ? v : 0.f;
+                        pt[r] = (REV ? s > col : s < col) ? v : 0.f;
+                    } else {
+                        pt[r] = (REV ? s >= col : s <= col) ? v : 0.f;
+                    }
+                }
+            }
+            auto add = [&](const f32x16& q, f32x16 acc) {
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = q[ks * 8 + e];
+                    attn_u32x4 pf[ORDER + 1];
+                    split_frag<ORDER + 1>(v, pf);
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) {
+                        const attn_u32x4 zf = AttnTile<OD>::columns(tz + j * AttnTile<OD>::kBytes, col0, ks, lane);
+#pragma unroll
+                        for (int i = 0; i <= ORDER; ++i)
+                            if (i + j <= ORDER) acc = attn_mfma(zf, pf[i], acc);
+                    }
+                }
+                return acc;
+            };
+            if constexpr (DOT) {
+                f32x16 t;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) t[r] = 0.f;
+                t = add(pt, t);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) dot_own = __builtin_fmaf(t[r], wv[r], dot_own);
+                t = add(diag, t);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) o[r] += t[r];
+            } else {
+                o = add(pt, o);
+            }
+            if (!REV || h == G - 1) {
+                T* op = (T*)const_cast<void*>(p.out.p) + (row0 + col) * p.out.row + (REV ? kv : kv * G + h) * p.out.head +
+                        col0 + 4 * half;
+                if (col < n && p.out.p) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float v[4] = {o[4 * g] * p.scale_out, o[4 * g + 1] * p.scale_out, o[4 * g + 2] * p.scale_out,
+                                            o[4 * g + 3] * p.scale_out};
+                        attn_store4<T>(op + 8 * g, p.dout - (col0 + 4 * half + 8 * g), v);
+                    }
+                }
+            }
+        }
+        // the state
+        if (rev_items || h == G - 1) {
+            if (!rev_items || h == 0) {
+                const float fade = w.fade[c];
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) S[t][r] = __builtin_fmaf(-fade, S[t][r], S[t][r]);
+            }
+            if constexpr (DOT && !REV) {
+                // what passes through the last chunk: <adjoint behind the span, faded state>
+                if (it + 1 == items) {
+                    const float* from = sp.last ? (p.other_last ? p.other_last + (sp.seq * p.kv_heads + kv) * state_size : nullptr)
+                                                : p.other_edges + ((sp.edge + 1) * p.kv_heads + kv) * state_size;
+#pragma unroll
+                    for (int t = 0; t < KT; ++t) {
+                        f32x16 D;
+                        attn_load_tile(D, from, p, t, col0, lane);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) dot_end = __builtin_fmaf(D[r], S[t][r], dot_end);
+                    }
+                }
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = 0.f;
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    const attn_u32x4 zf = AttnTile<OD>::columns(tz + j * AttnTile<OD>::kBytes, col0, ks, lane);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[2 * e] += __builtin_bit_cast(float, zf[e] << 16);
+                        v[2 * e + 1] += __builtin_bit_cast(float, zf[e] & 0xffff0000u);
+                    }
+                }
+                const attn_f32x4 w0 = *(const attn_f32x4*)(wout + 16 * ks + 4 * half),
+                                 w1 = *(const attn_f32x4*)(wout + 16 * ks + 8 + 4 * half);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[e] *= w0[e];
+                    v[4 + e] *= w1[e];
+                }
+                attn_u32x4 vf[3];
+                split_frag<3>(v, vf);
+#pragma unroll
+                for (int t = 0; t < KT; ++t)
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) {
+                        const attn_u32x4 yf = AttnTile<KD>::columns(ty + j * AttnTile<KD>::kBytes, t * 32, ks, lane);
+#pragma unroll
+                        for (int i = 0; i <= 2; ++i)
+                            if (i + j <= 2) S[t] = attn_mfma(yf, vf[i], S[t]);
+                    }
+            }
+        }
+        if constexpr (DOT) {
+            if (h == G - 1) {
+                float* to = s_sum + (it / G & 1) * 2 * NW * 32;
+                const float a = dot_in + __shfl_xor(dot_in, 32), b = dot_own + __shfl_xor(dot_own, 32);
+                if (half == 0) {
+                    to[wave * 32 + col] = a;
+                    to[(NW + wave) * 32 + col] = b;
+                }
+            }
+        }
+        if constexpr (Lds::kBuffers == 1) __syncthreads();
+        if (it + 1 < items) store(it + 1);
+        __syncthreads();
+        if constexpr (DOT) {
+            if (h == G - 1 && wave == 0 && col < n) {
+                const float* from = s_sum + ((it / G & 1) * 2 + half) * NW * 32 + col;
+                float v = from[0];
+#pragma unroll
+                for (int k = 1; k < NW; ++k) v += from[k * 32];
+                p.dots[((int64_t)half * p.kv_heads + kv) * p.rows + row0 + col] = v * p.scale_out;
+            }
+        }
+    }
+
+    if constexpr (AGG) {
+        const int64_t edge = sp.edge + (against ? 0 : 1);
+        attn_store_state<KT>(S, p.edges + (edge * p.kv_heads + kv) * state_size, p, col0, lane);
+        if (threadIdx.x == 0) {
+            double t = 0.0;
+            for (int k = 0; k < chunks; ++k) t += s_total[k];
+            p.totals[slot * p.kv_heads + kv] = (float)t;
+        }
+    } else if constexpr (DOT && !REV) {
+        for (int m = 32; m > 0; m >>= 1) dot_end += __shfl_xor(dot_end, m);
+        __syncthreads();  // the last chunk's sums are read
+        if (lane == 0) s_sum[wave] = dot_end;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int k = 1; k < NW; ++k) dot_end += s_sum[k];
+            p.ends[slot * p.kv_heads + kv] = dot_end;
+        }
+    } else if (p.last && (REV ? sp.first : sp.last)) {
+        if (sp.single) __syncthreads();  // state and last may be one array
+        attn_store_state<KT>(S, p.last + (sp.seq * p.kv_heads + kv) * state_size, p, col0, lane);
+    }
+}
+
+enum AttnKind { kAttnForward, kAttnAggregate, kAttnGradQ, kAttnGradK, kAttnGradV };
+template <class T>
+hipError_t launch_attn_kernel(AttnKind kind, const AttnArgs& a, hipStream_t st);
+
+template <class T, int KD, int OD, int ORDER, bool REV, bool DOT, bool AGG>
+hipError_t launch_attn_as(const AttnArgs& a, hipStream_t st) {
+    auto* k = k_attn<T, KD, OD, ORDER, REV, DOT, AGG>;
+    const int bytes = AttnLds<T, KD, OD, AGG>::bytes(a.span);
+    const hipError_t e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != hipSuccess) return e;
+    constexpr int64_t kWide = 1 << 22;  // a launch's threads along one side stay below 2^32
+    const int64_t x = a.slots < kWide ? a.slots : kWide;
+    k<<<dim3((unsigned)x, (unsigned)((a.slots + x - 1) / x), (unsigned)a.kv_heads), OD / 32 * 64, bytes, st>>>(a);
+    return hipGetLastError();
+}
+
+template <class T, int KD, int OD>
+hipError_t launch_attn_sized(AttnKind kind, const AttnArgs& a, hipStream_t st) {
+    constexpr int kForward = AttnType<T>::kPlanes == 3 ? 2 : 1;
+    switch (kind) {
+        case kAttnForward: return launch_attn_as<T, KD, OD, kForward, false, false, false>(a, st);
+        case kAttnAggregate: return launch_attn_as<T, KD, OD, 2, false, false, true>(a, st);
+        case kAttnGradQ: return launch_attn_as<T, KD, OD, 2, false, true, false>(a, st);
+        case kAttnGradK: return launch_attn_as<T, KD, OD, 2, true, true, false>(a, st);
+        case kAttnGradV: return launch_attn_as<T, KD, OD, 2, true, false, false>(a, st);
+    }
+    return hipErrorInvalidValue;
+}
+
+// Widths are padded to 64 or 128.
+#define GSR_ATTN_KERNELS(T)                                                                                    \
+    template <>                                                                                                \
+    hipError_t launch_attn_kernel<T>(AttnKind kind, const AttnArgs& a, hipStream_t st) {                       \
+        if (a.dc <= 64)                                                                                        \
+            return a.dout <= 64 ? launch_attn_sized<T, 64, 64>(kind, a, st) : launch_attn_sized<T, 64, 128>(kind, a, st); \
+        return a.dout <= 64 ? launch_attn_sized<T, 128, 64>(kind, a, st) : launch_attn_sized<T, 128, 128>(kind, a, st);   \
+    }
+
+}  // namespace gsr

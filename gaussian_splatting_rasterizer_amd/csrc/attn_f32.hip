@@ -1,0 +1,6 @@
+// attn_f32.hip -- the kernels of attn.hpp for one type of input.
+#include "attn.hpp"
+
+namespace gsr {
+GSR_ATTN_KERNELS(float)
+}  // namespace gsr

@@ -237,6 +237,15 @@ hipError_t launch_norm_backward(const gs_norm_dims& d, const void* h, int64_t ld
 hipError_t launch_adamw(const gs_adamw_dims& d, const gs_adamw_tensor* tensors, int64_t* steps, const float* grad_scale,
                         const float* rate_scale, hipStream_t st);
 
+// attn.hip
+constexpr int kAttnWidth = 128;  // of keys and values
+void attn_sizes(const gs_attn_dims& d, size_t* saved, size_t* fwd, size_t* bwd);
+hipError_t launch_attn_forward(const gs_attn_dims& d, const int64_t* offsets, const gs_attn_inputs& in, const gs_heads& y,
+                               float* last, float* saved, void* ws, hipStream_t st);
+hipError_t launch_attn_backward(const gs_attn_dims& d, const int64_t* offsets, const gs_attn_inputs& in,
+                                const float* saved, const gs_heads& dy, const float* d_last, const gs_attn_grads& out,
+                                void* ws, hipStream_t st);
+
 // the calling thread's last error message (gs_last_error) and the status to return with it
 gs_status fail(gs_status s, const char* fmt, ...);
 

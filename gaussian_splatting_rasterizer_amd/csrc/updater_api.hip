@@ -138,6 +138,65 @@ gs_status check_ortho(const char* call, const gs_ortho_dims* d) {
     return GS_OK;
 }
 
+gs_status check_attn(const char* call, const gs_attn_dims* d) {
+    if (!d) return fail(GS_ERR_INVALID_ARGUMENT, "%s: dims is null", call);
+    GSR_CHECK(check_dtype(call, d->dtype));
+    if (d->gate_dtype != d->dtype && d->gate_dtype != GS_F32)
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: the gate is of dtype or float32, got %d", call, d->gate_dtype);
+    if (d->gate_per_row != 0 && d->gate_per_row != 1)
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: gate_per_row %d is not 0 or 1", call, d->gate_per_row);
+    if (d->rows < 0 || d->n_seq < 0 || d->heads < 1 || d->kv_heads < 1 || d->d_key < 1 || d->d_value < 1 ||
+        d->heads % d->kv_heads != 0)
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: rows %lld, n_seq %lld, heads %d of %d, d_key %d, d_value %d", call,
+                    (long long)d->rows, (long long)d->n_seq, d->heads, d->kv_heads, d->d_key, d->d_value);
+    if (!std::isfinite(d->scale)) return fail(GS_ERR_INVALID_ARGUMENT, "%s: scale is not finite", call);
+    if (d->rows > kMaxRows || d->n_seq > kMaxRows || d->heads > 65535 || d->d_key > kAttnWidth || d->d_value > kAttnWidth)
+        return fail(GS_ERR_UNSUPPORTED, "%s: rows %lld, n_seq %lld, heads %d, d_key %d, d_value %d exceed the limits", call,
+                    (long long)d->rows, (long long)d->n_seq, d->heads, d->d_key, d->d_value);
+    return GS_OK;
+}
+
+gs_status check_heads(const char* call, const char* name, const gs_heads& h, int64_t rows, int heads, int width, size_t e,
+                      bool output) {
+    if (rows == 0) return GS_OK;
+    if (!h.p) return fail(GS_ERR_INVALID_ARGUMENT, "%s: %s is null", call, name);
+    if (!aligned(h.p, e)) return fail(GS_ERR_INVALID_ARGUMENT, "%s: %s is not %zu-byte aligned", call, name, e);
+    constexpr int64_t kMost = 1ll << 40;
+    if (h.ld_row < 0 || h.ld_head < 0)
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: strides of %s are negative", call, name);
+    if (h.ld_row > kMaxStride * 32 || h.ld_head > kMost)
+        return fail(GS_ERR_UNSUPPORTED, "%s: strides %lld, %lld of %s exceed the limits", call, (long long)h.ld_row,
+                    (long long)h.ld_head, name);
+    if (output) {
+        const bool by_rows = (heads == 1 || h.ld_head >= width) && (rows == 1 || h.ld_row >= (heads - 1) * h.ld_head + width);
+        const bool by_heads = (rows == 1 || h.ld_row >= width) && (heads == 1 || h.ld_head >= (rows - 1) * h.ld_row + width);
+        if (!by_rows && !by_heads)
+            return fail(GS_ERR_INVALID_ARGUMENT, "%s: rows and heads of %s overlap (strides %lld, %lld)", call, name,
+                        (long long)h.ld_row, (long long)h.ld_head);
+    }
+    return GS_OK;
+}
+
+gs_status check_attn_inputs(const char* call, const gs_attn_dims* d, const int64_t* offsets, const gs_attn_inputs* in) {
+    if (!in) return fail(GS_ERR_INVALID_ARGUMENT, "%s: inputs is null", call);
+    if (!aligned(offsets, 8)) return fail(GS_ERR_INVALID_ARGUMENT, "%s: offsets is not 8-byte aligned", call);
+    if (d->rows > 0 && d->n_seq == 0)
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: %lld rows but no sequence", call, (long long)d->rows);
+    if (!offsets && d->n_seq > 0 && d->rows % d->n_seq != 0)
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: %lld rows are not %lld sequences of equal length", call,
+                    (long long)d->rows, (long long)d->n_seq);
+    const size_t e = elem(d->dtype);
+    GSR_CHECK(check_heads(call, "q", in->q, d->rows, d->heads, d->d_key, e, false));
+    GSR_CHECK(check_heads(call, "k", in->k, d->rows, d->kv_heads, d->d_key, e, false));
+    GSR_CHECK(check_heads(call, "v", in->v, d->rows, d->kv_heads, d->d_value, e, false));
+    if (d->gate_per_row)
+        GSR_CHECK(check_array(call, "gate", in->gate, d->rows, d->kv_heads, in->ld_gate, elem(d->gate_dtype)));
+    else
+        GSR_CHECK(check_array(call, "gate", in->gate, d->rows, 0, 0, elem(d->gate_dtype)));
+    if (!aligned(in->state, 4)) return fail(GS_ERR_INVALID_ARGUMENT, "%s: state is not 4-byte aligned", call);
+    return GS_OK;
+}
+
 // Rows of an array in memory, as an interval.
 struct Extent {
     uintptr_t lo, hi;
@@ -150,6 +209,14 @@ struct Extent {
         return {a, a + (uintptr_t)(((rows - 1) * ld + width) * (int64_t)e), p, ld, name};
     }
 };
+
+gs_status check_output(const char* call, const Extent& out, const Extent& other, bool same);
+
+gs_status check_attn_states(const char* call, const gs_attn_dims* d, const char* in_name, const float* in,
+                            const char* out_name, const float* out) {
+    const int64_t n = (int64_t)d->kv_heads * d->d_key * d->d_value;
+    return check_output(call, Extent::of(out_name, out, d->n_seq, n, n, 4), Extent::of(in_name, in, d->n_seq, n, n, 4), true);
+}
 
 // An output may be an input that `same` allows it to replace element by element, and nothing else.
 gs_status check_output(const char* call, const Extent& out, const Extent& other, bool same) {
@@ -424,6 +491,58 @@ gs_status gs_norm_backward(const gs_norm_dims* dims, const void* h, int64_t ld_h
     const size_t need = grads->weight ? norm_workspace(*d) : 0;
     GSR_CHECK(check_workspace(call, workspace, workspace_bytes, need));
     return launched(launch_norm_backward(*d, h, ld_h, weight, dy, ld_dy, dh, ld_dh, *grads, workspace, stream), call);
+}
+
+gs_status gs_attn_sizes(const gs_attn_dims* dims, size_t* saved_bytes, size_t* forward_bytes, size_t* backward_bytes) {
+    GSR_CHECK(check_attn("gs_attn_sizes", dims));
+    size_t s, f, b;
+    attn_sizes(*dims, &s, &f, &b);
+    if (saved_bytes) *saved_bytes = s;
+    if (forward_bytes) *forward_bytes = f;
+    if (backward_bytes) *backward_bytes = b;
+    return GS_OK;
+}
+
+gs_status gs_attn_forward(const gs_attn_dims* dims, const int64_t* offsets, const gs_attn_inputs* in, const gs_heads* y,
+                          float* last, void* saved, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    const char* call = "gs_attn_forward";
+    GSR_CHECK(check_attn(call, dims));
+    GSR_CHECK(check_attn_inputs(call, dims, offsets, in));
+    if (!y) return fail(GS_ERR_INVALID_ARGUMENT, "%s: y is null", call);
+    GSR_CHECK(check_heads(call, "y", *y, dims->rows, dims->heads, dims->d_value, elem(dims->dtype), true));
+    if (!aligned(last, 4) || !aligned(saved, 256))
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: last or saved is misaligned", call);
+    GSR_CHECK(check_attn_states(call, dims, "state", in->state, "last", last));
+    size_t s, f, b;
+    attn_sizes(*dims, &s, &f, &b);
+    GSR_CHECK(check_workspace(call, workspace, workspace_bytes, f));
+    return launched(launch_attn_forward(*dims, offsets, *in, *y, last, (float*)saved, workspace, stream), call);
+}
+
+gs_status gs_attn_backward(const gs_attn_dims* dims, const int64_t* offsets, const gs_attn_inputs* in, const void* saved,
+                           const gs_heads* dy, const float* d_last, const gs_attn_grads* grads, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
+    const char* call = "gs_attn_backward";
+    GSR_CHECK(check_attn(call, dims));
+    GSR_CHECK(check_attn_inputs(call, dims, offsets, in));
+    if (!dy || !grads) return fail(GS_ERR_INVALID_ARGUMENT, "%s: dy or grads is null", call);
+    const gs_attn_dims& d = *dims;
+    const size_t e = elem(d.dtype);
+    GSR_CHECK(check_heads(call, "dy", *dy, d.rows, d.heads, d.d_value, e, false));
+    size_t s, f, b;
+    attn_sizes(d, &s, &f, &b);
+    if (s > 0) GSR_CHECK(check_array(call, "saved", saved, 1, 0, 0, 256));
+    if (grads->q.p) GSR_CHECK(check_heads(call, "grads.q", grads->q, d.rows, d.heads, d.d_key, e, true));
+    if (grads->k.p) GSR_CHECK(check_heads(call, "grads.k", grads->k, d.rows, d.kv_heads, d.d_key, e, true));
+    if (grads->v.p) GSR_CHECK(check_heads(call, "grads.v", grads->v, d.rows, d.kv_heads, d.d_value, e, true));
+    if (grads->gate && d.gate_per_row)
+        GSR_CHECK(check_array(call, "grads.gate", grads->gate, d.rows, d.kv_heads, grads->ld_gate, elem(d.gate_dtype)));
+    if (!aligned(grads->gate, elem(d.gate_dtype)) || !aligned(d_last, 4) || !aligned(grads->state, 4))
+        return fail(GS_ERR_INVALID_ARGUMENT, "%s: grads.gate, d_last or grads.state is misaligned", call);
+    GSR_CHECK(check_attn_states(call, dims, "d_last", d_last, "grads.state", grads->state));
+    GSR_CHECK(check_attn_states(call, dims, "state", in->state, "grads.state", grads->state));
+    GSR_CHECK(check_workspace(call, workspace, workspace_bytes, b));
+    return launched(launch_attn_backward(d, offsets, *in, (const float*)saved, *dy, d_last, *grads, workspace, stream), call);
 }
 
 gs_status gs_adamw_step(const gs_adamw_dims* dims, const gs_adamw_tensor* tensors, int64_t* steps,

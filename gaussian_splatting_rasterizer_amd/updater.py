@@ -323,6 +323,131 @@ class Orthogonalizer(_Op):
         return out
 
 
+class LinearAttention(_Op):
+    """S_t = sigma(gate_t) S_{t-1} + k_t v_t^T, y_t = scale S_t^T q_t for each head, over sequences that lie one after
+    another (scale: 1 / sqrt(d_key) unless given).
+
+    q [rows, heads, d_key], k [rows, kv_heads, d_key], v [rows, kv_heads, d_value], y [rows, heads, d_value] in dtype
+    (float32, bfloat16 or float16), each head's values contiguous, rows and heads in any order of strides; d_key and d_value
+    up to 128.  kv_heads divides heads; query head h reads the state of key head h // (heads // kv_heads).  gate
+    [rows, kv_heads] or [kv_heads], in dtype or float32.  States float32 [n_seq, kv_heads, d_key, d_value].  offsets: int64
+    [n_seq + 1] on the GPU (first row of each sequence, then the end of the last; rows behind it are left as they are), or
+    None for sequences of equal length, as many as state has (one without state).
+    """
+
+    def __init__(self, heads, d_key, d_value, dtype, kv_heads=None, scale=None, device="cuda"):
+        super().__init__(device)
+        self.heads, self.d_key, self.d_value = int(heads), int(d_key), int(d_value)
+        self.kv_heads = int(kv_heads) if kv_heads is not None else self.heads
+        self.dtype = dtype
+        self.code = _dtype_code(dtype)
+        self.scale = float(scale) if scale is not None else self.d_key ** -0.5
+        if self.heads < 1 or self.kv_heads < 1 or self.heads % self.kv_heads:
+            raise ValueError(f"{self.heads} heads are no multiple of {self.kv_heads} key heads")
+        self._sizes = {}
+
+    def _heads(self, t, name, rows, heads, width):
+        """Checks a [rows, heads, width] tensor."""
+        if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != heads or t.shape[2] != width:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{rows}, {heads}, {width}]")
+        if t.dtype != self.dtype or t.device != self.device:
+            raise ValueError(f"{name} is {t.dtype} on {t.device}, expected {self.dtype} on {self.device}")
+        row, head, one = t.stride()
+        if one != 1 and width > 1:
+            raise ValueError(f"{name} needs contiguous heads (strides {t.stride()})")
+        return b.gs_heads(t.data_ptr(), row, head)
+
+    def _setup(self, q, k, v, gate, state, offsets):
+        t, rows = self.torch, int(q.shape[0])
+        if offsets is not None:
+            if offsets.dim() != 1 or offsets.shape[0] < 1:
+                raise ValueError("offsets must have n_seq + 1 entries")
+            n_seq = int(offsets.shape[0]) - 1
+            _exact(offsets, "offsets", (n_seq + 1,), t.int64, self.device)
+        else:
+            n_seq = int(state.shape[0]) if state is not None else 1
+        if state is not None:
+            _exact(state, "state", (n_seq, self.kv_heads, self.d_key, self.d_value), t.float32, self.device)
+        if gate.dtype not in (self.dtype, t.float32):
+            raise ValueError(f"gate is {gate.dtype}, expected {self.dtype} or float32")
+        per_row = gate.dim() != 1
+        if per_row:
+            ld_gate = _matrix(gate, "gate", rows, self.kv_heads, gate.dtype, self.device)
+        else:
+            ld_gate = 0
+            _exact(gate, "gate", (self.kv_heads,), gate.dtype, self.device)
+        key = (rows, n_seq, gate.dtype, per_row)
+        if key not in self._sizes:
+            if len(self._sizes) > 64:
+                self._sizes.clear()
+            d = b.gs_attn_dims(rows, n_seq, self.heads, self.kv_heads, self.d_key, self.d_value, self.code,
+                               _dtype_code(gate.dtype), per_row, self.scale)
+            self._sizes[key] = (d, b.gs_attn_sizes(d))
+        dims, sizes = self._sizes[key]
+        inputs = b.gs_attn_inputs(self._heads(q, "q", rows, self.heads, self.d_key),
+                                  self._heads(k, "k", rows, self.kv_heads, self.d_key),
+                                  self._heads(v, "v", rows, self.kv_heads, self.d_value), gate.data_ptr(), ld_gate,
+                                  state.data_ptr() if state is not None else None)
+        return rows, n_seq, dims, sizes, inputs
+
+    def forward(self, q, k, v, gate, state=None, offsets=None, y=None, last=None, save=False, stream=None):
+        """-> (y, last); with save, (y, last, saved) for backward.  last may be state (updated in place; backward needs
+        the state from before)."""
+        return self._on(stream, self._forward, q, k, v, gate, state, offsets, y, last, save)
+
+    def _forward(self, stream, q, k, v, gate, state, offsets, y, last, save):
+        rows, n_seq, dims, (n_saved, n_ws, _), inputs = self._setup(q, k, v, gate, state, offsets)
+        t = self.torch
+        if y is None:
+            y = t.empty((rows, self.heads, self.d_value), dtype=self.dtype, device=self.device)
+        shape = (n_seq, self.kv_heads, self.d_key, self.d_value)
+        if last is None:
+            last = t.empty(shape, dtype=t.float32, device=self.device)
+        else:
+            _exact(last, "last", shape, t.float32, self.device)
+        saved = t.empty(max(n_saved, 256), dtype=t.uint8, device=self.device) if save else None
+        b.gs_attn_forward(dims, offsets, inputs, self._heads(y, "y", rows, self.heads, self.d_value), last, saved,
+                          self._scratch(n_ws, stream), stream)
+        return (y, last, saved) if save else (y, last)
+
+    def backward(self, q, k, v, gate, saved, dy, d_last=None, state=None, offsets=None, grads=None, stream=None):
+        """Gradients for dy [rows, heads, d_value] and d_last (like last): a dict of q, k, v, gate, state (written; with a
+        given dict, only the tensors it holds; its state may be d_last)."""
+        return self._on(stream, self._backward, q, k, v, gate, saved, dy, d_last, state, offsets, grads)
+
+    def _backward(self, stream, q, k, v, gate, saved, dy, d_last, state, offsets, grads):
+        rows, n_seq, dims, (n_saved, _, n_ws), inputs = self._setup(q, k, v, gate, state, offsets)
+        t = self.torch
+        if saved is None or saved.numel() < n_saved or saved.device != self.device:
+            raise ValueError("saved is not what forward(..., save=True) returned for these rows")
+        shape = (n_seq, self.kv_heads, self.d_key, self.d_value)
+        if d_last is not None:
+            _exact(d_last, "d_last", shape, t.float32, self.device)
+        if grads is None:
+            like = dict(dtype=self.dtype, device=self.device)
+            grads = {"q": t.empty((rows, self.heads, self.d_key), **like),
+                     "k": t.empty((rows, self.kv_heads, self.d_key), **like),
+                     "v": t.empty((rows, self.kv_heads, self.d_value), **like),
+                     "gate": t.empty(gate.shape, dtype=gate.dtype, device=self.device),
+                     "state": t.empty(shape, dtype=t.float32, device=self.device)}
+        out = b.gs_attn_grads()
+        for name, heads, width in (("q", self.heads, self.d_key), ("k", self.kv_heads, self.d_key),
+                                   ("v", self.kv_heads, self.d_value)):
+            if grads.get(name) is not None:
+                setattr(out, name, self._heads(grads[name], f"grads[{name!r}]", rows, heads, width))
+        if grads.get("gate") is not None:
+            if gate.dim() != 1:
+                out.ld_gate = _matrix(grads["gate"], "grads['gate']", rows, self.kv_heads, gate.dtype, self.device)
+            else:
+                _exact(grads["gate"], "grads['gate']", (self.kv_heads,), gate.dtype, self.device)
+            out.gate = grads["gate"].data_ptr()
+        if grads.get("state") is not None:
+            out.state = _exact(grads["state"], "grads['state']", shape, t.float32, self.device).data_ptr()
+        b.gs_attn_backward(dims, offsets, inputs, saved, self._heads(dy, "dy", rows, self.heads, self.d_value), d_last, out,
+                           self._scratch(n_ws, stream), stream)
+        return grads
+
+
 class ResidualNorm(_Op):
     """h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, over rows of the weight's length.
 

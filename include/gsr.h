@@ -507,6 +507,63 @@ typedef struct {
 GSR_API gs_status gs_adamw_step(const gs_adamw_dims* dims, const gs_adamw_tensor* tensors, int64_t* steps,
                                 const float* grad_scale, const float* rate_scale, hipStream_t stream);
 
+/* Linear attention with a decay for each key head, over sequences packed like those of gs_scan_forward:
+ *   S_t = sigma(gate_t) S_{t-1} + k_t v_t^T,   y_t = scale S_t^T q_t
+ * q [rows, heads, d_key], k [rows, kv_heads, d_key], v [rows, kv_heads, d_value], y [rows, heads, d_value] of type dtype;
+ * heads is a multiple of kv_heads, and query head h reads the state of key head h / (heads / kv_heads).  gate, of type
+ * gate_dtype (dtype or GS_F32): [rows, kv_heads] where gate_per_row is set, else [kv_heads].  States float32
+ * [n_seq, kv_heads, d_key, d_value], contiguous: state (before the first row, null: zero) and last (after the last row,
+ * null: not wanted; may be state, though a backward pass wants the one from before).
+ * offsets (device, [n_seq + 1], non-decreasing, first 0) gives the first row of each sequence and the end of the last;
+ * rows behind it are left as they are.  Null: n_seq sequences of equal length.  Offsets outside [0, rows] are taken as the
+ * nearer of the two; values that are not non-decreasing give unspecified results but no access out of range.
+ * Sequences may be empty; equal sequences of length 1 (single tokens) take a kernel of their own.
+ * Not a number and infinities stay in their sequence and reach no row before theirs; infinities may come out as NaN.
+ * d_key and d_value are 1 .. 128, rows and n_seq 0 .. 2^31 - 512, heads up to 65535. */
+typedef struct {
+    int64_t rows;
+    int64_t n_seq;
+    int32_t heads, kv_heads;
+    int32_t d_key, d_value;
+    int32_t dtype, gate_dtype; /* gs_dtype */
+    int32_t gate_per_row;      /* 0 or 1 */
+    float scale;
+} gs_attn_dims;
+/* [rows, heads, d] in any order of rows and heads: strides in elements, d contiguous.  Rows and heads of an output must not
+ * overlap. */
+typedef struct {
+    void* p;  /* inputs are not written */
+    int64_t ld_row, ld_head;
+} gs_heads;
+typedef struct {
+    gs_heads q, k, v;
+    const void* gate;
+    int64_t ld_gate;  /* row stride, where gate_per_row is set */
+    const float* state;
+} gs_attn_inputs;
+/* Gradients, written (not accumulated), of the inputs' types; null members are skipped.  A gate of one value for each
+ * head gets the sum over all rows. */
+typedef struct {
+    gs_heads q, k, v;
+    void* gate;
+    int64_t ld_gate;
+    float* state;
+} gs_attn_grads;
+/* Bytes of the saved states and of the two calls' workspaces (any pointer may be null). */
+GSR_API gs_status gs_attn_sizes(const gs_attn_dims* dims, size_t* saved_bytes, size_t* forward_bytes,
+                                size_t* backward_bytes);
+/* saved (may be null: inference) receives the float32 states that gs_attn_backward starts from.  saved and workspace are
+ * 256-byte aligned (null where their size is 0).  Outputs must not overlap inputs or each other, but for last. */
+GSR_API gs_status gs_attn_forward(const gs_attn_dims* dims, const int64_t* offsets, const gs_attn_inputs* in,
+                                  const gs_heads* y, float* last, void* saved, void* workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+/* Gradients for dy [rows, heads, d_value] (dtype) and d_last (float32, like last; null: zero); in and offsets as given to
+ * the forward pass.  grads.state may be d_last or state. */
+GSR_API gs_status gs_attn_backward(const gs_attn_dims* dims, const int64_t* offsets, const gs_attn_inputs* in,
+                                   const void* saved, const gs_heads* dy, const float* d_last,
+                                   const gs_attn_grads* grads, void* workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+
 GSR_API const char* gs_status_string(gs_status s);
 GSR_API const char* gs_last_error(void);
 
