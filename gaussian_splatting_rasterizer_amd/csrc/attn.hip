@@ -20,7 +20,7 @@ namespace gsr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kJoinValues = 4;  // of a state, each thread's
+constexpr int kJoinValues = 1;  // of a state, each thread's
 constexpr int kJoinParts = 32;  // shares of the sequences
 
 // The state at every boundary between two spans, in place of what the span beside it adds; one thread runs through a

@@ -21,8 +21,9 @@
 //
 // Operands are bfloat16 planes whose sum is the value: one for bfloat16 inputs, two for float16, three for float32 (24
 // bits); the state, the scores and the weighted z are split into ORDER + 1 planes where they are used, and products of
-// planes whose ranks add up to more than ORDER are left out (2^-8 per rank).  ORDER is 2, except for 16-bit results of the
-// forward pass, where 1 (2^-17) is far below their rounding; the state itself is always summed with 2.
+// planes whose ranks add up to more than ORDER are left out (2^-8 per rank).  ORDER is 2, except for 16-bit outputs and
+// gradients of v, where 1 (2^-17) is far below their rounding; the states themselves, and what the gate's gradient is a
+// difference of, are always summed with 2.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -150,6 +151,20 @@ struct AttnType<float> {
     static constexpr int kPlanes = 3;
 };
 
+// A value that is not known to be the same as last time: what depends on it is computed where it is used instead of being
+// kept in registers (lane masks: pairs of scalar ones) throughout a loop.
+__device__ __forceinline__ int afresh(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// All ones where bit s of x is set (the compiler would make three instructions of it).
+__device__ __forceinline__ int bit_mask(int x, int s) {
+    int m;
+    asm("v_bfe_i32 %0, %1, %2, 1" : "=v"(m) : "v"(x), "n"(s));
+    return m;
+}
+
 // N planes of two values, a word each.
 template <int N>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t* out) {
@@ -158,6 +173,7 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t* out) {
         const attn_bf16x2 h = {(__bf16)a, (__bf16)b};
         out[n] = __builtin_bit_cast(uint32_t, h);
         if (n + 1 < N) {
+            asm("" : "+v"(out[n]));  // keeps the compiler from rounding a once more by itself
             a -= __builtin_bit_cast(float, out[n] << 16);
             b -= __builtin_bit_cast(float, out[n] & 0xffff0000u);
         }
@@ -179,63 +195,75 @@ __device__ __forceinline__ f32x16 attn_mfma(attn_u32x4 a, attn_u32x4 b, f32x16 c
                                                    0, 0, 0);
 }
 
-// A tile of 32 rows x D in LDS, one plane: 16-byte slots, slot (k, half) of a row holding columns 16 k + 4 half + 0..3 and
-// 16 k + 8 + 4 half + 0..3, at position slot ^ row, so that the lanes of a read by rows spread over the banks.
+// Column (of 16) that row r of a state holds: the middle fours exchanged.
+__device__ __forceinline__ constexpr int attn_column(int r) { return (r & ~12) | (r & 4) << 1 | (r & 8) >> 1; }
+
+// A tile of 32 rows x D in LDS, one plane: slots of eight columns, at position slot ^ row, so that the lanes of a read by
+// rows spread over the banks.
 template <int D>
 struct AttnTile {
     static constexpr int kRow = D * 2, kSlots = D / 8, kBytes = kAttnChunk * kRow;
-    // 8 bytes: columns 4 quad .. 4 quad + 3 of a row
-    static __device__ __forceinline__ int quad(int row, int q) {
-        const int slot = (q >> 2) * 2 + (q & 1);
-        return row * kRow + ((slot ^ (row & (kSlots - 1))) << 4) + ((q >> 1) & 1) * 8;
+    static __device__ __forceinline__ int at(int row, int slot) {
+        return row * kRow + ((slot ^ (row & (kSlots - 1))) << 4);
     }
-    // by rows: the lane's row, columns of k-step kk
+    // by rows: the lane's row, columns 16 kk + 8 half + 0..7
     static __device__ __forceinline__ attn_u32x4 rows(const char* t, int kk, int lane) {
-        const int r = lane & 31, slot = kk * 2 + (lane >> 5);
-        return *(const attn_u32x4*)(t + r * kRow + ((slot ^ (r & (kSlots - 1))) << 4));
+        return *(const attn_u32x4*)(t + at(lane & 31, kk * 2 + (lane >> 5)));
     }
-    // transposed: column col0 + (lane & 31), rows 16 ks + 4 half + 0..3 and + 8
+    // transposed: one column of col0 + 0..31 (SWAP: of the state's order), rows 16 ks + 4 half + 0..3 and + 8
+    template <bool SWAP>
     static __device__ __forceinline__ attn_u32x4 columns(const char* t, int col0, int ks, int lane) {
         const int row = ks * 16 + (lane >> 5) * 4 + ((lane & 15) >> 2);
-        const int q = (col0 + ((lane >> 4) & 1) * 16) / 4 + (lane & 3);
-        const attn_s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s16x4*)(t + quad(row, q)));
-        const attn_s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s16x4*)(t + quad(row + 8, q)));
+        int four = lane & 3;  // of 16 columns
+        if (SWAP) four = (four & 1) << 1 | four >> 1;
+        const int slot = (col0 >> 3) + ((lane >> 4) & 1) * 2 + (four >> 1);
+        const char* p = t + (four & 1) * 8;
+        const attn_s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s16x4*)(p + at(row, slot)));
+        const attn_s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s16x4*)(p + at(row + 8, slot)));
         const attn_u32x2 x = __builtin_bit_cast(attn_u32x2, a), y = __builtin_bit_cast(attn_u32x2, b);
         return attn_u32x4{x[0], x[1], y[0], y[1]};
     }
 };
 
-// One tile on its way from memory to LDS: runs of eight values, spread over the workgroup.
+// One tile on its way from memory to LDS: runs of eight values, spread over the workgroup.  Rows past the last one repeat
+// it: as sources they have no weight, as destinations they are not written.
 template <class T, int D, int NT>
 struct AttnFetch {
     static constexpr int kRuns = kAttnChunk * (D / 8) / NT, kPlanes = AttnType<T>::kPlanes;
     Run8<T> run[kRuns];
-    __device__ __forceinline__ void load(const AttnArray& a, int64_t row0, int n, int head, int d) {
-        const T* base = (const T*)a.p + row0 * a.row + head * a.head;
+    // base: the chunk's first row of one head
+    __device__ __forceinline__ void load(const T* base, uint32_t ld, int n, int d) {
+        const int r = threadIdx.x / (D / 8), c = (threadIdx.x % (D / 8)) * 8;
+        if (n == kAttnChunk && d == D) {
+            const uint32_t off = (r * ld + c) * (uint32_t)sizeof(T);
 #pragma unroll
-        for (int i = 0; i < kRuns; ++i) {
-            const int u = i * NT + threadIdx.x, r = u / (D / 8), c = (u % (D / 8)) * 8;
-            run[i].load(base + r * a.row + c, r < n ? d - c : 0);
+            for (int i = 0; i < kRuns; ++i) {
+                const char* from = (const char*)base + (uint64_t)(i * (NT / (D / 8))) * ld * sizeof(T);
+                __builtin_memcpy(run[i].v, from + off, sizeof(run[i].v));
+            }
+        } else {
+            const int tid = afresh(threadIdx.x), r1 = tid / (D / 8), c1 = (tid % (D / 8)) * 8;
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i)
+                run[i].load(base + (uint32_t)min(r1 + i * (NT / (D / 8)), n - 1) * ld + c1, d - c1);
         }
     }
     __device__ __forceinline__ void store(char* tile) const {
+        const int r0 = threadIdx.x / (D / 8), slot = threadIdx.x % (D / 8);
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) {
-            const int u = i * NT + threadIdx.x, r = u / (D / 8), q = (u % (D / 8)) * 2;
-            uint32_t w[4][kPlanes];
+            attn_u32x4 w[kPlanes];
+            if constexpr (kPlanes == 1) {
+                __builtin_memcpy(&w[0], run[i].v, 16);
+            } else {
+                float v[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (kPlanes == 1)
-                    __builtin_memcpy(w[e], &run[i].v[2 * e], 4);
-                else
-                    split_pair<kPlanes>(run[i].get(2 * e), run[i].get(2 * e + 1), w[e]);
+                for (int e = 0; e < 8; ++e) v[e] = run[i].get(e);
+                split_frag<kPlanes>(v, w);
             }
+            char* t = tile + AttnTile<D>::at(r0 + i * (NT / (D / 8)), slot);
 #pragma unroll
-            for (int n = 0; n < kPlanes; ++n) {
-                char* t = tile + n * AttnTile<D>::kBytes;
-                *(attn_u32x2*)(t + AttnTile<D>::quad(r, q)) = attn_u32x2{w[0][n], w[1][n]};
-                *(attn_u32x2*)(t + AttnTile<D>::quad(r, q + 1)) = attn_u32x2{w[2][n], w[3][n]};
-            }
+            for (int n = 0; n < kPlanes; ++n) *(attn_u32x4*)(t + n * AttnTile<D>::kBytes) = w[n];
         }
     }
 };
@@ -277,7 +305,7 @@ __device__ __forceinline__ void attn_weights(const AttnArgs& p, const AttnSpan& 
             w.hi[r] = hi;
             w.lo[r] = (float)(g - (double)hi);
             w.in[r] = against ? rest : to;
-            w.out[r] = (against ? to : rest) * p.scale_state;
+            w.out[r] = r < s.n ? (against ? to : rest) * p.scale_state : 0.f;
             if (lane == 0) {
                 w.fade[r / kAttnChunk] = -expm1f((float)(P * 0.6931471805599453));
                 if (total) total[r / kAttnChunk] = P * 0.6931471805599453;
@@ -287,13 +315,17 @@ __device__ __forceinline__ void attn_weights(const AttnArgs& p, const AttnSpan& 
 }
 
 // 32 contracted rows of a wave's columns of a state (null: zero).
+__device__ __forceinline__ uint32_t attn_state_at(const AttnArgs& p, int t, int r, int o, int lane, bool& in) {
+    const int c = t * 32 + attn_column(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3));
+    in = c < p.dc && o < p.dout;
+    return p.transposed ? (uint32_t)(o * p.dv + c) : (uint32_t)(c * p.dv + o);
+}
 __device__ __forceinline__ void attn_load_tile(f32x16& s, const float* from, const AttnArgs& p, int t, int col0, int lane) {
-    const int o = col0 + (lane & 31);
-    const int64_t sc = p.transposed ? 1 : p.dv, so = p.transposed ? p.dv : 1;
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-        const int c = t * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        s[r] = from && c < p.dc && o < p.dout ? from[c * sc + o * so] : 0.f;
+        bool in;
+        const uint32_t at = attn_state_at(p, t, r, col0 + (lane & 31), lane, in);
+        s[r] = from && in ? from[at] : 0.f;
     }
 }
 template <int KT>
@@ -303,29 +335,36 @@ __device__ __forceinline__ void attn_load_state(f32x16* s, const float* from, co
 }
 template <int KT>
 __device__ __forceinline__ void attn_store_state(const f32x16* s, float* to, const AttnArgs& p, int col0, int lane) {
-    const int o = col0 + (lane & 31);
-    const int64_t sc = p.transposed ? 1 : p.dv, so = p.transposed ? p.dv : 1;
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            const int c = t * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-            if (c < p.dc && o < p.dout) to[c * sc + o * so] = s[t][r];
+            bool in;
+            const uint32_t at = attn_state_at(p, t, r, col0 + (lane & 31), lane, in);
+            if (in) to[at] = s[t][r];
         }
 }
 
 // Four consecutive columns of a row as they lie in memory.
 template <class T>
-__device__ __forceinline__ void attn_load4(const T* p, int n, float* out) {
+struct AttnFour {
     T v[4];
-    if (n >= 4) {
-        __builtin_memcpy(v, p, sizeof(v));
-    } else {
+    __device__ __forceinline__ void load(const T* p, int n) {
+        if (n >= 4) {
+            __builtin_memcpy(v, p, sizeof(v));
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = e < n ? p[e] : (T)0.f;
+            for (int e = 0; e < 4; ++e) v[e] = e < n ? p[e] : (T)0.f;
+        }
     }
+    __device__ __forceinline__ float get(int e) const { return (float)v[e]; }
+};
+template <class T>
+__device__ __forceinline__ void attn_load4(const T* p, int n, float* out) {
+    AttnFour<T> v;
+    v.load(p, n);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) out[e] = (float)v[e];
+    for (int e = 0; e < 4; ++e) out[e] = v.get(e);
 }
 template <class T>
 __device__ __forceinline__ void attn_store4(T* p, int n, const float* in) {
@@ -397,37 +436,41 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
         } else {
             from = p.edges + ((sp.edge + (REV ? 1 : 0)) * p.kv_heads + kv) * state_size;
         }
-        attn_load_state<KT>(S, from, p, col0, lane);
+        attn_load_state<KT>(S, from, p, col0, afresh(lane));
     }
     attn_weights(p, sp, kv, against, w, AGG ? s_total : nullptr);
 
     const int chunks = (sp.n + kAttnChunk - 1) / kAttnChunk, G = AGG && !p.against ? 1 : p.group;
-    const bool rev_items = AGG ? p.against : REV;  // the group's heads are sources; otherwise destinations
+    const bool many = AGG ? p.against : REV;  // the group's heads are sources; otherwise destinations
     const int items = chunks * G;
     AttnFetch<T, KD, NT> fx, fy;
     AttnFetch<T, OD, NT> fz;
-    auto chunk_of = [&](int it) { return against ? chunks - 1 - it / G : it / G; };
-    auto load = [&](int it) {
-        const int h = it % G, c = chunk_of(it), n = min(kAttnChunk, sp.n - c * kAttnChunk);
+    auto load = [&](int c, int h) {
+        const int n = min(kAttnChunk, sp.n - c * kAttnChunk);
         const int64_t row0 = sp.row0 + c * kAttnChunk;
-        if (!AGG && (!REV || h == 0)) fx.load(p.x, row0, n, REV ? kv : kv * G + h, p.dc);
-        if (rev_items || h == 0) {
-            fy.load(p.y, row0, n, rev_items ? kv * G + h : kv, p.dc);
-            fz.load(p.z, row0, n, rev_items ? kv * G + h : kv, p.dout);
+        if (!AGG && (!REV || h == 0))
+            fx.load((const T*)p.x.p + row0 * p.x.row + (REV ? kv : kv * G + h) * p.x.head, (uint32_t)p.x.row, n, p.dc);
+        if (many || h == 0) {
+            const int head = many ? kv * G + h : kv;
+            fy.load((const T*)p.y.p + row0 * p.y.row + head * p.y.head, (uint32_t)p.y.row, n, p.dc);
+            fz.load((const T*)p.z.p + row0 * p.z.row + head * p.z.head, (uint32_t)p.z.row, n, p.dout);
         }
     };
-    auto x_tile = [&](int it) { return s_x + (Lds::kBuffers == 2 ? (REV ? it / G : it) & 1 : 0) * Lds::kX; };
-    auto yz_turn = [&](int it) { return Lds::kBuffers == 2 ? (rev_items ? it : it / G) & 1 : 0; };
-    auto store = [&](int it) {
-        const int h = it % G;
-        if (!AGG && (!REV || h == 0)) fx.store(x_tile(it));
-        if (rev_items || h == 0) {
-            fy.store(s_y + yz_turn(it) * Lds::kY);
-            fz.store(s_z + yz_turn(it) * Lds::kZ);
+    int x_turn = 0, yz_turn = 0;  // buffer of the tiles in use
+    auto store = [&](int h) {     // into the next buffer, which is then in use
+        if (!AGG && (!REV || h == 0)) {
+            if (Lds::kBuffers == 2) x_turn ^= 1;
+            fx.store(s_x + x_turn * Lds::kX);
+        }
+        if (many || h == 0) {
+            if (Lds::kBuffers == 2) yz_turn ^= 1;
+            fy.store(s_y + yz_turn * Lds::kY);
+            fz.store(s_z + yz_turn * Lds::kZ);
         }
     };
+    int c = against ? chunks - 1 : 0, h = 0;
     if (items > 0) {
-        load(0);
+        load(c, 0);
         store(0);
     }
     __syncthreads();
@@ -435,22 +478,33 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
     f32x16 o;
     float dot_in = 0.f, dot_own = 0.f, dot_end = 0.f;
     for (int it = 0; it < items; ++it) {
-        const int h = it % G, c = chunk_of(it), n = min(kAttnChunk, sp.n - c * kAttnChunk);
+        const int n = min(kAttnChunk, sp.n - c * kAttnChunk);
         const int64_t row0 = sp.row0 + c * kAttnChunk;
-        if (it + 1 < items) load(it + 1);
-        const char* tx = x_tile(it);
-        const char* ty = s_y + yz_turn(it) * Lds::kY;
-        const char* tz = s_z + yz_turn(it) * Lds::kZ;
+        const char* tx = s_x + x_turn * Lds::kX;
+        const char* ty = s_y + yz_turn * Lds::kY;
+        const char* tz = s_z + yz_turn * Lds::kZ;
         const float *hi = w.hi + c * kAttnChunk, *lo = w.lo + c * kAttnChunk, *wout = w.out + c * kAttnChunk;
+        int next_c = c, next_h = h + 1;
+        if (next_h == G) {
+            next_h = 0;
+            next_c += against ? -1 : 1;
+        }
+        if (it + 1 < items) load(next_c, next_h);
 
         if constexpr (!AGG) {
             const bool inter = !REV || h == 0;
-            float wv[16];
+            AttnFour<T> wv[4];
             if constexpr (DOT) {
-                const T* wp = (const T*)p.w.p + (row0 + col) * p.w.row + (REV ? kv : kv * G + h) * p.w.head + col0 + 4 * half;
+                const T* wp = (const T*)p.w.p + row0 * p.w.row + (REV ? kv : kv * G + h) * p.w.head;
+                const uint32_t first = col0 + 4 * half, at = (uint32_t)min(col, n - 1) * (uint32_t)p.w.row + first;
+                if (p.dout == OD) {
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
-                    attn_load4<T>(wp + 8 * g, col < n ? p.dout - (col0 + 4 * half + 8 * g) : 0, wv + 4 * g);
+                    for (int g = 0; g < 4; ++g) wv[g].load(wp + (at + 8 * g), 4);
+                } else {
+                    const int left = afresh(p.dout - first);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) wv[g].load(wp + (at + 8 * g), left - 8 * g);
+                }
             }
             if (inter) {
 #pragma unroll
@@ -461,19 +515,23 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
             f32x16 pt;
 #pragma unroll
             for (int r = 0; r < 16; ++r) pt[r] = 0.f;
+            attn_u32x4 xf[2][NP], yf[2][NP];
+            auto read = [&](int kk) {
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    xf[kk & 1][j] = AttnTile<KD>::rows(tx + j * AttnTile<KD>::kBytes, kk, lane);
+                    yf[kk & 1][j] = AttnTile<KD>::rows(ty + j * AttnTile<KD>::kBytes, kk, lane);
+                }
+            };
+            read(0);
 #pragma unroll
             for (int kk = 0; kk < KD / 16; ++kk) {
-                attn_u32x4 xf[NP], yf[NP];
-#pragma unroll
-                for (int n2 = 0; n2 < NP; ++n2) {
-                    xf[n2] = AttnTile<KD>::rows(tx + n2 * AttnTile<KD>::kBytes, kk, lane);
-                    yf[n2] = AttnTile<KD>::rows(ty + n2 * AttnTile<KD>::kBytes, kk, lane);
-                }
+                if (kk + 1 < KD / 16) read(kk + 1);
 #pragma unroll
                 for (int i = 0; i < NP; ++i)
 #pragma unroll
                     for (int j = 0; j < NP; ++j)
-                        if (i + j <= ORDER) pt = attn_mfma(yf[i], xf[j], pt);
+                        if (i + j <= ORDER) pt = attn_mfma(yf[kk & 1][i], xf[kk & 1][j], pt);
                 if (inter) {
                     float v[8];
 #pragma unroll
@@ -484,8 +542,9 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                     for (int i = 0; i <= ORDER; ++i)
 #pragma unroll
                         for (int j = 0; j < NP; ++j)
-                            if (i + j <= ORDER) o = attn_mfma(sf[i], xf[j], o);
+                            if (i + j <= ORDER) o = attn_mfma(sf[i], xf[kk & 1][j], o);
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
             if (inter) {
                 const float wi = w.in[c * kAttnChunk + col];
@@ -493,43 +552,45 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                 for (int r = 0; r < 16; ++r) o[r] *= wi;
                 if constexpr (DOT) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) dot_in = __builtin_fmaf(o[r], wv[r], dot_in);
+                    for (int r = 0; r < 16; ++r) dot_in = __builtin_fmaf(o[r], wv[r >> 2].get(r & 3), dot_in);
                 }
             }
             // scores: row r of the tile is source 8 (r / 4) + 4 half + r % 4, the lane's column its destination
             const float hi_i = hi[col], lo_i = lo[col];
-            f32x16 diag;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const attn_f32x4 hs = *(const attn_f32x4*)(hi + 8 * g + 4 * half), ls = *(const attn_f32x4*)(lo + 8 * g + 4 * half);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int s = 8 * g + 4 * half + e, r = 4 * g + e;
                     const float d = (hi_i - hs[e]) + (lo_i - ls[e]);
-                    const float v = pt[r] * (__builtin_amdgcn_exp2f(REV ? -d : d) * p.scale_pair);
-                    if constexpr (DOT) {
-                        diag[r] = s == col ? v : 0.f;
-                        pt[r] = (REV ? s > col : s < col) ? v : 0.f;
-                    } else {
-                        pt[r] = (REV ? s >= col : s <= col) ? v : 0.f;
-                    }
+                    pt[4 * g + e] *= __builtin_amdgcn_exp2f(REV ? -d : d);
+                    if (REV) pt[4 * g + e] *= p.scale_pair;
                 }
             }
-            auto add = [&](const f32x16& q, f32x16 acc) {
+            // acc += z scores
+            const uint32_t own = 1u << col, real = n == kAttnChunk ? ~0u : (1u << n) - 1;
+            const uint32_t parted = REV ? -own & ~own & real : own - 1;
+            auto add = [&](f32x16 acc, uint32_t keep) {  // bits of the sources
+                const int bits = afresh((int)(keep >> (4 * half)));
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
                     float v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = q[ks * 8 + e];
+                    for (int e = 0; e < 8; ++e) {
+                        const int s = 16 * ks + 8 * (e >> 2) + (e & 3);
+                        const float score = pt[ks * 8 + e];
+                        v[e] = __builtin_bit_cast(float, __builtin_bit_cast(int, score) & bit_mask(bits, s));
+                    }
                     attn_u32x4 pf[ORDER + 1];
                     split_frag<ORDER + 1>(v, pf);
 #pragma unroll
                     for (int j = 0; j < NP; ++j) {
-                        const attn_u32x4 zf = AttnTile<OD>::columns(tz + j * AttnTile<OD>::kBytes, col0, ks, lane);
+                        const attn_u32x4 zf = AttnTile<OD>::template columns<false>(tz + j * AttnTile<OD>::kBytes, col0, ks, lane);
 #pragma unroll
                         for (int i = 0; i <= ORDER; ++i)
                             if (i + j <= ORDER) acc = attn_mfma(zf, pf[i], acc);
                     }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 return acc;
             };
@@ -537,31 +598,34 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                 f32x16 t;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) t[r] = 0.f;
-                t = add(pt, t);
+                t = add(t, parted);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) dot_own = __builtin_fmaf(t[r], wv[r], dot_own);
-                t = add(diag, t);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[r] += t[r];
+                for (int r = 0; r < 16; ++r) {
+                    dot_own = __builtin_fmaf(t[r], wv[r >> 2].get(r & 3), dot_own);
+                    o[r] += t[r];
+                }
+                o = add(o, own & real);
             } else {
-                o = add(pt, o);
+                o = add(o, parted | (own & real));
             }
             if (!REV || h == G - 1) {
-                T* op = (T*)const_cast<void*>(p.out.p) + (row0 + col) * p.out.row + (REV ? kv : kv * G + h) * p.out.head +
-                        col0 + 4 * half;
+                T* op = (T*)const_cast<void*>(p.out.p) + row0 * p.out.row + (REV ? kv : kv * G + h) * p.out.head;
+                const uint32_t first = col0 + 4 * half, at = (uint32_t)col * (uint32_t)p.out.row + first;
                 if (col < n && p.out.p) {
+                    const int left = p.dout == OD ? 32 : afresh(p.dout - first);
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const float v[4] = {o[4 * g] * p.scale_out, o[4 * g + 1] * p.scale_out, o[4 * g + 2] * p.scale_out,
-                                            o[4 * g + 3] * p.scale_out};
-                        attn_store4<T>(op + 8 * g, p.dout - (col0 + 4 * half + 8 * g), v);
+                        float v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = REV ? o[4 * g + e] : o[4 * g + e] * p.scale_out;
+                        attn_store4<T>(op + (at + 8 * g), left - 8 * g, v);
                     }
                 }
             }
         }
         // the state
-        if (rev_items || h == G - 1) {
-            if (!rev_items || h == 0) {
+        if (many || h == G - 1) {
+            if (!many || h == 0) {
                 const float fade = w.fade[c];
 #pragma unroll
                 for (int t = 0; t < KT; ++t)
@@ -576,9 +640,10 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
 #pragma unroll
                     for (int t = 0; t < KT; ++t) {
                         f32x16 D;
-                        attn_load_tile(D, from, p, t, col0, lane);
+                        attn_load_tile(D, from, p, t, col0, afresh(lane));
 #pragma unroll
                         for (int r = 0; r < 16; ++r) dot_end = __builtin_fmaf(D[r], S[t][r], dot_end);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             }
@@ -589,7 +654,7 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                 for (int e = 0; e < 8; ++e) v[e] = 0.f;
 #pragma unroll
                 for (int j = 0; j < NP; ++j) {
-                    const attn_u32x4 zf = AttnTile<OD>::columns(tz + j * AttnTile<OD>::kBytes, col0, ks, lane);
+                    const attn_u32x4 zf = AttnTile<OD>::template columns<false>(tz + j * AttnTile<OD>::kBytes, col0, ks, lane);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         v[2 * e] += __builtin_bit_cast(float, zf[e] << 16);
@@ -606,19 +671,21 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                 attn_u32x4 vf[3];
                 split_frag<3>(v, vf);
 #pragma unroll
-                for (int t = 0; t < KT; ++t)
+                for (int t = 0; t < KT; ++t) {
 #pragma unroll
                     for (int j = 0; j < NP; ++j) {
-                        const attn_u32x4 yf = AttnTile<KD>::columns(ty + j * AttnTile<KD>::kBytes, t * 32, ks, lane);
+                        const attn_u32x4 yf = AttnTile<KD>::template columns<true>(ty + j * AttnTile<KD>::kBytes, t * 32, ks, lane);
 #pragma unroll
                         for (int i = 0; i <= 2; ++i)
                             if (i + j <= 2) S[t] = attn_mfma(yf, vf[i], S[t]);
                     }
+                    if (t & 1) __builtin_amdgcn_sched_barrier(0);
+                }
             }
         }
         if constexpr (DOT) {
             if (h == G - 1) {
-                float* to = s_sum + (it / G & 1) * 2 * NW * 32;
+                float* to = s_sum + (c & 1) * 2 * NW * 32;
                 const float a = dot_in + __shfl_xor(dot_in, 32), b = dot_own + __shfl_xor(dot_own, 32);
                 if (half == 0) {
                     to[wave * 32 + col] = a;
@@ -627,22 +694,24 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
             }
         }
         if constexpr (Lds::kBuffers == 1) __syncthreads();
-        if (it + 1 < items) store(it + 1);
+        if (it + 1 < items) store(next_h);
         __syncthreads();
         if constexpr (DOT) {
             if (h == G - 1 && wave == 0 && col < n) {
-                const float* from = s_sum + ((it / G & 1) * 2 + half) * NW * 32 + col;
+                const float* from = s_sum + ((c & 1) * 2 + half) * NW * 32 + col;
                 float v = from[0];
 #pragma unroll
                 for (int k = 1; k < NW; ++k) v += from[k * 32];
                 p.dots[((int64_t)half * p.kv_heads + kv) * p.rows + row0 + col] = v * p.scale_out;
             }
         }
+        c = next_c;
+        h = next_h;
     }
 
     if constexpr (AGG) {
         const int64_t edge = sp.edge + (against ? 0 : 1);
-        attn_store_state<KT>(S, p.edges + (edge * p.kv_heads + kv) * state_size, p, col0, lane);
+        attn_store_state<KT>(S, p.edges + (edge * p.kv_heads + kv) * state_size, p, col0, afresh(lane));
         if (threadIdx.x == 0) {
             double t = 0.0;
             for (int k = 0; k < chunks; ++k) t += s_total[k];
@@ -659,7 +728,7 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
         }
     } else if (p.last && (REV ? sp.first : sp.last)) {
         if (sp.single) __syncthreads();  // state and last may be one array
-        attn_store_state<KT>(S, p.last + (sp.seq * p.kv_heads + kv) * state_size, p, col0, lane);
+        attn_store_state<KT>(S, p.last + (sp.seq * p.kv_heads + kv) * state_size, p, col0, afresh(lane));
     }
 }
 
@@ -681,13 +750,13 @@ hipError_t launch_attn_as(const AttnArgs& a, hipStream_t st) {
 
 template <class T, int KD, int OD>
 hipError_t launch_attn_sized(AttnKind kind, const AttnArgs& a, hipStream_t st) {
-    constexpr int kForward = AttnType<T>::kPlanes == 3 ? 2 : 1;
+    constexpr int kForward = AttnType<T>::kPlanes == 3 ? 2 : 1;  // results in the inputs' type alone
     switch (kind) {
         case kAttnForward: return launch_attn_as<T, KD, OD, kForward, false, false, false>(a, st);
         case kAttnAggregate: return launch_attn_as<T, KD, OD, 2, false, false, true>(a, st);
         case kAttnGradQ: return launch_attn_as<T, KD, OD, 2, false, true, false>(a, st);
         case kAttnGradK: return launch_attn_as<T, KD, OD, 2, true, true, false>(a, st);
-        case kAttnGradV: return launch_attn_as<T, KD, OD, 2, true, false, false>(a, st);
+        case kAttnGradV: return launch_attn_as<T, KD, OD, kForward, true, false, false>(a, st);
     }
     return hipErrorInvalidValue;
 }
