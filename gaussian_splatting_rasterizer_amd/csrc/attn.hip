@@ -21,10 +21,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kJoinValues = 1;  // of a state, each thread's
+constexpr int kJoinSteps = 16; // of the chain whose loads are asked for at a time
 constexpr int kJoinParts = 32;  // shares of the sequences
 
 // The state at every boundary between two spans, in place of what the span beside it adds; one thread runs through a
-// sequence's boundaries for its values.  The loads do not depend on the chain and are asked for eight at a time.
+// sequence's boundaries for its values.  The loads do not depend on the chain and are asked for ahead of it.
 __global__ __launch_bounds__(kThreads) void k_attn_join(const AttnArgs p, float* copies) {
     const int64_t size = (int64_t)p.dk * p.dv;
     const int kv = blockIdx.y, lane = threadIdx.x & 63;
@@ -56,28 +57,37 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(const AttnArgs p, float*
                 cur[i] = p.first && e < size ? p.first[(s * p.kv_heads + kv) * size + e] : 0.f;
                 if (copies && e < size) copies[(attn_copy(p, s, edge0) * p.kv_heads + kv) * size + e] = cur[i];
             }
-            for (int b0 = 0; b0 < spans - 1; b0 += 8) {
-                float u[8][kJoinValues], t[8];
+            // boundary of the chain's b-th step: what the span beside it adds (and then the state) and its log a
+            auto edge_of = [&](int b) { return edge0 + (p.against ? spans - 2 - b : b); };
+            float u[2][kJoinSteps][kJoinValues], t[2][kJoinSteps];
+            auto fetch = [&](int b0, int k) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int b = min(b0 + j, spans - 2), at = p.against ? spans - 2 - b : b;  // boundary at, at + 1
-                    t[j] = p.totals[(slot0 + at + (p.against ? 1 : 0)) * p.kv_heads + kv];
+                for (int j = 0; j < kJoinSteps; ++j) {
+                    const int b = min(b0 + j, spans - 2);
+                    t[k][j] = p.totals[(slot0 + (p.against ? spans - 1 - b : b)) * p.kv_heads + kv];
 #pragma unroll
                     for (int i = 0; i < kJoinValues; ++i) {
                         const int64_t e = e0 + i * kThreads;
-                        u[j][i] = e < size ? p.edges[((edge0 + at) * p.kv_heads + kv) * size + e] : 0.f;
+                        u[k][j][i] = e < size ? p.edges[(edge_of(b) * p.kv_heads + kv) * size + e] : 0.f;
                     }
                 }
+            };
+            fetch(0, 0);
+            for (int b0 = 0; b0 < spans - 1; b0 += 2 * kJoinSteps) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (b0 + j >= spans - 1) break;
-                    const int at = p.against ? spans - 2 - (b0 + j) : b0 + j;
-                    const float fade = -expm1f(t[j]);
+                for (int k = 0; k < 2; ++k) {
+                    const int first = b0 + k * kJoinSteps;
+                    fetch(first + kJoinSteps, k ^ 1);
 #pragma unroll
-                    for (int i = 0; i < kJoinValues; ++i) {
-                        const int64_t e = e0 + i * kThreads;
-                        cur[i] = __builtin_fmaf(-fade, cur[i], cur[i]) + u[j][i];
-                        if (e < size) p.edges[((edge0 + at) * p.kv_heads + kv) * size + e] = cur[i];
+                    for (int j = 0; j < kJoinSteps; ++j) {
+                        if (first + j >= spans - 1) break;
+                        const float fade = -expm1f(t[k][j]);
+#pragma unroll
+                        for (int i = 0; i < kJoinValues; ++i) {
+                            const int64_t e = e0 + i * kThreads;
+                            cur[i] = __builtin_fmaf(-fade, cur[i], cur[i]) + u[k][j][i];
+                            if (e < size) p.edges[(edge_of(first + j) * p.kv_heads + kv) * size + e] = cur[i];
+                        }
                     }
                 }
             }
@@ -370,7 +380,7 @@ hipError_t launch_attn_forward(const gs_attn_dims& d, const int64_t* offsets, co
     a.out = array(y);
     a.dc = d.d_key;
     a.dout = d.d_value;
-    a.scale_pair = a.scale_state = 1.f;
+    a.scale_state = 1.f;
     a.scale_out = d.scale;
     if (!offsets && a.seq_len == 1) {
         if (d.dtype == GS_BF16) return attn_step<__bf16>(a, st);
@@ -422,7 +432,7 @@ hipError_t launch_attn_backward(const gs_attn_dims& d, const int64_t* offsets, c
     rev.edges = edges;
     rev.totals = totals;
     rev.against = true;
-    rev.scale_pair = rev.scale_state = d.scale;
+    rev.scale_state = d.scale;
     rev.scale_out = 1.f;
     const bool split = attn_splits(base);
     if (split) {
@@ -445,7 +455,7 @@ hipError_t launch_attn_backward(const gs_attn_dims& d, const int64_t* offsets, c
         a.dc = d.d_value;
         a.dout = d.d_key;
         a.transposed = true;
-        a.scale_pair = a.scale_state = 1.f;
+        a.scale_state = 1.f;
         a.scale_out = d.scale;
         a.first = in.state;
         a.edges = const_cast<float*>(saved);

@@ -65,7 +65,7 @@ struct AttnArgs {
     int dc, dout;               // contracted and out widths
     int dk, dv;                 // the state is [dk][dv]
     bool transposed;            // contracted side is dv
-    float scale_pair, scale_state, scale_out;
+    float scale_state, scale_out;  // of what sources add, of the outputs
     const float* first;         // state (adjoint: gradient of the last one) that a sequence starts from; null: zero
     const float* copies;        // the same for sequences of several spans (attn_copy); null: first
     bool copies_by_sequence;
@@ -165,17 +165,24 @@ __device__ __forceinline__ int bit_mask(int x, int s) {
     return m;
 }
 
-// N planes of two values, a word each.
+// N planes of two values, a word each.  What a plane leaves over is exact, and a two-term product of the plane's pair with
+// (-1, 0) or (0, -1) takes it in one instruction; as asm it need not overwrite its operand, and brings its own wait
+// states (three to another instruction).  a and b may be results of matrix instructions: the rounding in front, which the
+// compiler places, has read them by then.
 template <int N>
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t* out) {
+    const uint32_t first = 0x0000bf80u, second = 0xbf800000u;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const attn_bf16x2 h = {(__bf16)a, (__bf16)b};
         out[n] = __builtin_bit_cast(uint32_t, h);
         if (n + 1 < N) {
-            asm("" : "+v"(out[n]));  // keeps the compiler from rounding a once more by itself
-            a -= __builtin_bit_cast(float, out[n] << 16);
-            b -= __builtin_bit_cast(float, out[n] & 0xffff0000u);
+            float x, y;
+            asm("v_dot2_f32_bf16 %0, %2, %3, %5\n\tv_dot2_f32_bf16 %1, %2, %4, %6\n\ts_nop 2"
+                : "=&v"(x), "=&v"(y)
+                : "v"(out[n]), "s"(first), "s"(second), "v"(a), "v"(b));
+            a = x;
+            b = y;
         }
     }
 }
@@ -225,31 +232,57 @@ struct AttnTile {
     }
 };
 
-// One tile on its way from memory to LDS: runs of eight values, spread over the workgroup.  Rows past the last one repeat
-// it: as sources they have no weight, as destinations they are not written.
+// Moves a run's values down by k places (from 8 on: none is left) and fills with zeros.
+template <class T>
+__device__ __forceinline__ void attn_shift(Run8<T>& run, int k) {
+    constexpr int W = sizeof(T) * 2;  // words
+    uint32_t w[W];
+    __builtin_memcpy(w, run.v, sizeof(run.v));
+#pragma unroll
+    for (int places = 4; places > 0; places >>= 1) {
+        const bool move = k & places;
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            const int words = places * (int)sizeof(T) / 4;
+            const uint32_t next = i + 1 < W ? w[i + 1] : 0u;
+            const uint32_t from = words == 0 ? w[i] >> 16 | next << 16 : i + words < W ? w[i + words] : 0u;
+            w[i] = move ? from : w[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = k < 8 ? w[i] : 0u;
+    __builtin_memcpy(run.v, w, sizeof(run.v));
+}
+
+// One tile on its way from memory to LDS: runs of eight values, spread over the workgroup.  A run that would leave its row
+// is read from where it ends with the row and put right when it is stored, so that nothing waits for the loads before
+// that.  Rows past the last one repeat it: as sources they have no weight, as destinations they are not written.
 template <class T, int D, int NT>
 struct AttnFetch {
-    static constexpr int kRuns = kAttnChunk * (D / 8) / NT, kPlanes = AttnType<T>::kPlanes;
+    static constexpr int kRuns = kAttnChunk * (D / 8) / NT, kPlanes = AttnType<T>::kPlanes, kStep = NT / (D / 8);
     Run8<T> run[kRuns];
     // base: the chunk's first row of one head
     __device__ __forceinline__ void load(const T* base, uint32_t ld, int n, int d) {
-        const int r = threadIdx.x / (D / 8), c = (threadIdx.x % (D / 8)) * 8;
-        if (n == kAttnChunk && d == D) {
-            const uint32_t off = (r * ld + c) * (uint32_t)sizeof(T);
+        if (d >= 8) {
+            const int r = threadIdx.x / (D / 8), c = min((int)(threadIdx.x % (D / 8)) * 8, d - 8);
 #pragma unroll
             for (int i = 0; i < kRuns; ++i) {
-                const char* from = (const char*)base + (uint64_t)(i * (NT / (D / 8))) * ld * sizeof(T);
-                __builtin_memcpy(run[i].v, from + off, sizeof(run[i].v));
+                const uint32_t at = __umul24((uint32_t)min(r + i * kStep, n - 1), ld) + c;
+                __builtin_memcpy(run[i].v, (const char*)base + at * (uint32_t)sizeof(T), sizeof(run[i].v));
             }
         } else {
-            const int tid = afresh(threadIdx.x), r1 = tid / (D / 8), c1 = (tid % (D / 8)) * 8;
+            const int tid = afresh(threadIdx.x), r = tid / (D / 8), c = (tid % (D / 8)) * 8;
 #pragma unroll
-            for (int i = 0; i < kRuns; ++i)
-                run[i].load(base + (uint32_t)min(r1 + i * (NT / (D / 8)), n - 1) * ld + c1, d - c1);
+            for (int i = 0; i < kRuns; ++i) run[i].load(base + __umul24((uint32_t)min(r + i * kStep, n - 1), ld) + c, d - c);
         }
     }
-    __device__ __forceinline__ void store(char* tile) const {
+    __device__ __forceinline__ void store(char* tile, int d) {
         const int r0 = threadIdx.x / (D / 8), slot = threadIdx.x % (D / 8);
+        if (d != D && d >= 8) {
+            const int k = afresh(slot * 8 - min(slot * 8, d - 8));
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i) attn_shift(run[i], k);
+        }
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) {
             attn_u32x4 w[kPlanes];
@@ -261,7 +294,7 @@ struct AttnFetch {
                 for (int e = 0; e < 8; ++e) v[e] = run[i].get(e);
                 split_frag<kPlanes>(v, w);
             }
-            char* t = tile + AttnTile<D>::at(r0 + i * (NT / (D / 8)), slot);
+            char* t = tile + AttnTile<D>::at(r0 + i * kStep, slot);
 #pragma unroll
             for (int n = 0; n < kPlanes; ++n) *(attn_u32x4*)(t + n * AttnTile<D>::kBytes) = w[n];
         }
@@ -282,35 +315,87 @@ __device__ __forceinline__ float attn_gate(const AttnArgs& p, int64_t row, int h
     return (float)((const _Float16*)p.gate)[at];
 }
 
-// Weights of a span's rows, in LDS.
+// 2^x for a long sum x.
+__device__ __forceinline__ float exp2_wide(double x) {
+    const double n = __builtin_rint(x);
+    return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(x - n)), (int)fmax(n, -300.0));
+}
+
+// Weights of a span's rows, in LDS.  The state is held as S 2^-e with an exponent e that starts at 0 and takes in each
+// chunk's total P, so that it is not multiplied chunk after chunk: a destination's weight is then 2^(p_i + e), a source's
+// 2^(-p_j - e) (against the order: 2^(P - p_i + e), 2^(p_j - P - e)), their product a pair's.  Below 2^-kAttnLow the state is
+// multiplied out instead, e starts again, and a source's weight is that of the header (lift makes the product a pair's). A
+// chunk that forgets more than that by itself keeps its rows' sums, from which every weight is taken.
+constexpr double kAttnLow = -60.0;
 struct AttnWeights {
-    float *hi, *lo, *in, *out, *fade;  // fade: 1 - 2^P of a chunk
+    float *in, *out;         // of rows; or the sum as a pair
+    float *lift, *through;   // of chunks: 1, 2^-(P + e) or 0 (the rows' sums); 2^(P + e)
+    double *total, *before;  // P, e
+    float* end;              // 2^e behind the last chunk
+    static constexpr int bytes(int span) { return span * 8 + span / kAttnChunk * 24 + 16; }
+    __device__ __forceinline__ void place(char* at, int span) {
+        const int chunks = span / kAttnChunk;
+        total = (double*)at;
+        before = total + chunks;
+        in = (float*)(before + chunks);
+        out = in + span;
+        lift = out + span;
+        through = lift + chunks;
+        end = through + chunks;
+    }
+    static __device__ __forceinline__ double arriving(bool against, double p, double P, double e) {
+        return (against ? P - p : p) + e;
+    }
+    static __device__ __forceinline__ double leaving(bool against, double p, double P) { return against ? p : P - p; }
 };
 
 __device__ __forceinline__ void attn_weights(const AttnArgs& p, const AttnSpan& s, int head, bool against,
-                                             const AttnWeights& w, double* total) {
-    const int lane = threadIdx.x & 31;
-    const int rows = (s.n + kAttnChunk - 1) / kAttnChunk * kAttnChunk;
-    for (int r = threadIdx.x; r < (rows + 63) / 64 * 64; r += blockDim.x) {  // whole waves
+                                             const AttnWeights& w) {
+    const int lane = threadIdx.x & 31, chunks = (s.n + kAttnChunk - 1) / kAttnChunk, rows = chunks * kAttnChunk;
+    const int whole = (rows + 63) / 64 * 64;  // waves
+    for (int r = threadIdx.x; r < whole; r += blockDim.x) {
         double g = r < s.n ? log2_gate(attn_gate(p, s.row0 + r, head)) : 0.0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const double before = __shfl_up(g, d, 32);
             if (lane >= d) g += before;
         }
-        const double P = __shfl(g, 31, 32);
         if (r < rows) {
             const float hi = (float)g;
-            const float to = __builtin_amdgcn_exp2f(hi), rest = __builtin_amdgcn_exp2f((float)(P - g));
-            w.hi[r] = hi;
-            w.lo[r] = (float)(g - (double)hi);
-            w.in[r] = against ? rest : to;
-            w.out[r] = r < s.n ? (against ? to : rest) * p.scale_state : 0.f;
-            if (lane == 0) {
-                w.fade[r / kAttnChunk] = -expm1f((float)(P * 0.6931471805599453));
-                if (total) total[r / kAttnChunk] = P * 0.6931471805599453;
-            }
+            w.in[r] = hi;
+            w.out[r] = (float)(g - (double)hi);
+            if (lane == 31) w.total[r / kAttnChunk] = g;
         }
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        const int k = threadIdx.x;  // the k-th chunk on the way (a span has at most 32)
+        const double P = k < chunks ? w.total[against ? chunks - 1 - k : k] : 0.0;
+        double e = 0.0, mine = 0.0;
+        for (int i = 0; i < chunks; ++i) {
+            if (i == k) mine = e;
+            e += __shfl(P, i);
+            if (!(e > kAttnLow)) e = e != e ? e : 0.0;
+        }
+        if (k < chunks) {
+            const int c = against ? chunks - 1 - k : k;
+            const double x = P + mine;
+            w.before[c] = mine;
+            w.lift[c] = x > kAttnLow || x != x ? 1.f : P > kAttnLow ? exp2_wide(-x) : 0.f;
+            w.through[c] = exp2_wide(x);
+        }
+        if (k == 0) *w.end = exp2_wide(e);
+    }
+    __syncthreads();
+    for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+        const int c = r / kAttnChunk;
+        const float lift = w.lift[c];
+        if (lift == 0.f) continue;
+        const double sum = (double)w.in[r] + (double)w.out[r], P = w.total[c], e = w.before[c];
+        w.in[r] = exp2_wide(AttnWeights::arriving(against, sum, P, e));
+        // not by way of P where that falls out: it may be no number while a row before is
+        const double out = lift == 1.f ? (against ? sum - P : -sum) - e : AttnWeights::leaving(against, sum, P);
+        w.out[r] = r < s.n ? exp2_wide(out) * p.scale_state : 0.f;
     }
 }
 
@@ -345,19 +430,40 @@ __device__ __forceinline__ void attn_store_state(const f32x16* s, float* to, con
         }
 }
 
-// Four consecutive columns of a row as they lie in memory.
+// Four consecutive columns of a row, in the words that they lie in.
 template <class T>
 struct AttnFour {
-    T v[4];
+    static constexpr int W = sizeof(T);
+    uint32_t w[W];
     __device__ __forceinline__ void load(const T* p, int n) {
         if (n >= 4) {
-            __builtin_memcpy(v, p, sizeof(v));
+            __builtin_memcpy(w, p, sizeof(w));
         } else {
+            T v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = e < n ? p[e] : (T)0.f;
+            __builtin_memcpy(w, v, sizeof(w));
         }
     }
-    __device__ __forceinline__ float get(int e) const { return (float)v[e]; }
+    __device__ __forceinline__ float get(int e) const {
+        if constexpr (W == 4)
+            return __builtin_bit_cast(float, w[e & 3]);
+        else
+            return (float)__builtin_bit_cast(T, (uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+    }
+    // down by k places
+    __device__ __forceinline__ void shift(int k) {
+#pragma unroll
+        for (int places = 2; places > 0; places >>= 1) {
+            const int words = places * (int)sizeof(T) / 4;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const uint32_t next = i + 1 < W ? w[i + 1] : 0u;
+                const uint32_t from = words == 0 ? w[i] >> 16 | next << 16 : i + words < W ? w[i + words] : 0u;
+                w[i] = k & places ? from : w[i];
+            }
+        }
+    }
 };
 template <class T>
 __device__ __forceinline__ void attn_load4(const T* p, int n, float* out) {
@@ -390,7 +496,7 @@ struct AttnLds {
     static constexpr int kTiles = kBuffers * (kX + kY + kZ);
     static constexpr int kSums = 2 * 2 * (OD / 32) * 32 * 4;
     static constexpr int kFixed = kTiles + kSums;
-    static constexpr int bytes(int span) { return kFixed + span * 16 + span / kAttnChunk * 16; }
+    static constexpr int bytes(int span) { return kFixed + AttnWeights::bytes(span); }
 };
 
 // REV: against the rows' order.  DOT: gradient of q (of k): also the products of the outputs with w and, at the span's end,
@@ -405,12 +511,7 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
     char* s_z = s_y + Lds::kBuffers * Lds::kY;
     float* s_sum = (float*)(smem + Lds::kTiles);  // [2][2][NW][32]
     AttnWeights w;
-    w.hi = (float*)(smem + Lds::kFixed);
-    w.lo = w.hi + p.span;
-    w.in = w.lo + p.span;
-    w.out = w.in + p.span;
-    w.fade = w.out + p.span;
-    double* s_total = (double*)(w.fade + 2 * (p.span / kAttnChunk));
+    w.place(smem + Lds::kFixed, p.span);
 
     const int lane = threadIdx.x & 63, half = lane >> 5, col = lane & 31;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -438,13 +539,17 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
         }
         attn_load_state<KT>(S, from, p, col0, afresh(lane));
     }
-    attn_weights(p, sp, kv, against, w, AGG ? s_total : nullptr);
+    attn_weights(p, sp, kv, against, w);
+    // the state is there before the loop, which would otherwise wait for every load that is under way
+#pragma unroll
+    for (int t = 0; t < KT; ++t) asm volatile("" : "+v"(S[t]));
 
     const int chunks = (sp.n + kAttnChunk - 1) / kAttnChunk, G = AGG && !p.against ? 1 : p.group;
     const bool many = AGG ? p.against : REV;  // the group's heads are sources; otherwise destinations
     const int items = chunks * G;
     AttnFetch<T, KD, NT> fx, fy;
     AttnFetch<T, OD, NT> fz;
+    AttnFour<T> wv[4], next_wv[4];  // w of the lane's row, columns col0 + 4 half + 8 g
     auto load = [&](int c, int h) {
         const int n = min(kAttnChunk, sp.n - c * kAttnChunk);
         const int64_t row0 = sp.row0 + c * kAttnChunk;
@@ -455,17 +560,40 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
             fy.load((const T*)p.y.p + row0 * p.y.row + head * p.y.head, (uint32_t)p.y.row, n, p.dc);
             fz.load((const T*)p.z.p + row0 * p.z.row + head * p.z.head, (uint32_t)p.z.row, n, p.dout);
         }
+        if constexpr (DOT) {
+            const T* base = (const T*)p.w.p + row0 * p.w.row + (REV ? kv : kv * G + h) * p.w.head;
+            const uint32_t at = __umul24((uint32_t)min(col, n - 1), (uint32_t)p.w.row);
+            if (p.dout >= 4) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) next_wv[g].load(base + (at + min(col0 + 4 * half + 8 * g, p.dout - 4)), 4);
+            } else {
+                const int left = afresh(p.dout - col0 - 4 * half);
+#pragma unroll
+                for (int g = 0; g < 4; ++g) next_wv[g].load(base + (at + col0 + 4 * half + 8 * g), left - 8 * g);
+            }
+        }
     };
     int x_turn = 0, yz_turn = 0;  // buffer of the tiles in use
     auto store = [&](int h) {     // into the next buffer, which is then in use
         if (!AGG && (!REV || h == 0)) {
             if (Lds::kBuffers == 2) x_turn ^= 1;
-            fx.store(s_x + x_turn * Lds::kX);
+            fx.store(s_x + x_turn * Lds::kX, p.dc);
         }
         if (many || h == 0) {
             if (Lds::kBuffers == 2) yz_turn ^= 1;
-            fy.store(s_y + yz_turn * Lds::kY);
-            fz.store(s_z + yz_turn * Lds::kZ);
+            fy.store(s_y + yz_turn * Lds::kY, p.dc);
+            fz.store(s_z + yz_turn * Lds::kZ, p.dout);
+        }
+        if constexpr (DOT) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) wv[g] = next_wv[g];
+            if (p.dout != OD && p.dout >= 4) {  // columns past the last meet zeros; a four that holds the last is put right
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int first = col0 + 4 * half + 8 * g;
+                    wv[g].shift(afresh(first - min(first, p.dout - 4)));
+                }
+            }
         }
     };
     int c = against ? chunks - 1 : 0, h = 0;
@@ -483,7 +611,36 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
         const char* tx = s_x + x_turn * Lds::kX;
         const char* ty = s_y + yz_turn * Lds::kY;
         const char* tz = s_z + yz_turn * Lds::kZ;
-        const float *hi = w.hi + c * kAttnChunk, *lo = w.lo + c * kAttnChunk, *wout = w.out + c * kAttnChunk;
+        const float lift = w.lift[c];
+        const bool sums = lift == 0.f;
+        auto sum_of = [&](int row) { return (double)w.in[c * kAttnChunk + row] + (double)w.out[c * kAttnChunk + row]; };
+        // weights of the sources 8 g + 4 half + 0..3
+        auto source = [&](int g) {
+            if (!sums) return *(const attn_f32x4*)(w.out + c * kAttnChunk + 8 * g + 4 * half);
+            attn_f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int s = 8 * g + 4 * half + e;
+                v[e] = s < n ? exp2_wide(AttnWeights::leaving(against, sum_of(s), w.total[c])) * p.scale_state : 0.f;
+            }
+            return v;
+        };
+        if constexpr (DOT && !REV) {
+            // what passes through the span's last chunk: <adjoint behind the span, faded state>
+            if (it + 1 == items) {
+                const float* from = sp.last ? (p.other_last ? p.other_last + (sp.seq * p.kv_heads + kv) * state_size : nullptr)
+                                            : p.other_edges + ((sp.edge + 1) * p.kv_heads + kv) * state_size;
+#pragma unroll
+                for (int t = 0; t < KT; ++t) {
+                    f32x16 D;
+                    attn_load_tile(D, from, p, t, col0, afresh(lane));
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) dot_end = __builtin_fmaf(D[r], S[t][r], dot_end);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                dot_end *= w.through[c];
+            }
+        }
         int next_c = c, next_h = h + 1;
         if (next_h == G) {
             next_h = 0;
@@ -493,19 +650,10 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
 
         if constexpr (!AGG) {
             const bool inter = !REV || h == 0;
-            AttnFour<T> wv[4];
-            if constexpr (DOT) {
-                const T* wp = (const T*)p.w.p + row0 * p.w.row + (REV ? kv : kv * G + h) * p.w.head;
-                const uint32_t first = col0 + 4 * half, at = (uint32_t)min(col, n - 1) * (uint32_t)p.w.row + first;
-                if (p.dout == OD) {
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) wv[g].load(wp + (at + 8 * g), 4);
-                } else {
-                    const int left = afresh(p.dout - first);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) wv[g].load(wp + (at + 8 * g), left - 8 * g);
-                }
-            }
+            auto arriving = [&] {
+                if (!sums) return w.in[c * kAttnChunk + col];
+                return exp2_wide(AttnWeights::arriving(against, sum_of(col), w.total[c], w.before[c]));
+            };
             if (inter) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[r] = 0.f;
@@ -547,7 +695,7 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                 __builtin_amdgcn_sched_barrier(0);
             }
             if (inter) {
-                const float wi = w.in[c * kAttnChunk + col];
+                const float wi = arriving();
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[r] *= wi;
                 if constexpr (DOT) {
@@ -556,15 +704,20 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                 }
             }
             // scores: row r of the tile is source 8 (r / 4) + 4 half + r % 4, the lane's column its destination
-            const float hi_i = hi[col], lo_i = lo[col];
+            if (!sums) {
+                const float a = w.in[c * kAttnChunk + col] * lift;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const attn_f32x4 hs = *(const attn_f32x4*)(hi + 8 * g + 4 * half), ls = *(const attn_f32x4*)(lo + 8 * g + 4 * half);
+                for (int g = 0; g < 4; ++g) {
+                    const attn_f32x4 ws = source(g);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float d = (hi_i - hs[e]) + (lo_i - ls[e]);
-                    pt[4 * g + e] *= __builtin_amdgcn_exp2f(REV ? -d : d);
-                    if (REV) pt[4 * g + e] *= p.scale_pair;
+                    for (int e = 0; e < 4; ++e) pt[4 * g + e] *= ws[e] * a;
+                }
+            } else {
+                const double own = sum_of(col);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const double d = own - sum_of(8 * (r >> 2) + 4 * half + (r & 3));
+                    pt[r] *= __builtin_amdgcn_exp2f((float)(REV ? -d : d)) * p.scale_state;
                 }
             }
             // acc += z scores
@@ -600,52 +753,45 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                 for (int r = 0; r < 16; ++r) t[r] = 0.f;
                 t = add(t, parted);
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    dot_own = __builtin_fmaf(t[r], wv[r >> 2].get(r & 3), dot_own);
-                    o[r] += t[r];
+                for (int r = 0; r < 16; ++r) dot_own = __builtin_fmaf(t[r], wv[r >> 2].get(r & 3), dot_own);
+                // the row's own pair: its score is in register 4 (col / 8) + col % 4 of one half wave
+                float v[16];
+#pragma unroll
+                for (int r = 0; r < 16; ++r) v[r] = pt[r];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const bool odd = col & (k < 2 ? 1 << k : 2 << k);  // bits 0, 1, 3, 4 of col
+#pragma unroll
+                    for (int i = 0; i < 8 >> k; ++i) v[i] = odd ? v[2 * i + 1] : v[2 * i];
                 }
-                o = add(o, own & real);
+                const float other = __shfl_xor(v[0], 32);
+                const float score = ((col >> 2) & 1) == half ? v[0] : other;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int j = 0; j < NP; ++j) {
+                        const attn_u32x2 w2 =
+                            *(const attn_u32x2*)(tz + j * AttnTile<OD>::kBytes + AttnTile<OD>::at(col, (col0 >> 3) + g) + 8 * half);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            z[e] += __builtin_bit_cast(float, e & 1 ? w2[e >> 1] & 0xffff0000u : w2[e >> 1] << 16);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[4 * g + e] += __builtin_fmaf(score, z[e], t[4 * g + e]);
+                }
             } else {
                 o = add(o, parted | (own & real));
-            }
-            if (!REV || h == G - 1) {
-                T* op = (T*)const_cast<void*>(p.out.p) + row0 * p.out.row + (REV ? kv : kv * G + h) * p.out.head;
-                const uint32_t first = col0 + 4 * half, at = (uint32_t)col * (uint32_t)p.out.row + first;
-                if (col < n && p.out.p) {
-                    const int left = p.dout == OD ? 32 : afresh(p.dout - first);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        float v[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] = REV ? o[4 * g + e] : o[4 * g + e] * p.scale_out;
-                        attn_store4<T>(op + (at + 8 * g), left - 8 * g, v);
-                    }
-                }
             }
         }
         // the state
         if (many || h == G - 1) {
-            if (!many || h == 0) {
-                const float fade = w.fade[c];
+            if ((!many || h == 0) && lift != 1.f) {
+                const float through = w.through[c];
 #pragma unroll
                 for (int t = 0; t < KT; ++t)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) S[t][r] = __builtin_fmaf(-fade, S[t][r], S[t][r]);
-            }
-            if constexpr (DOT && !REV) {
-                // what passes through the last chunk: <adjoint behind the span, faded state>
-                if (it + 1 == items) {
-                    const float* from = sp.last ? (p.other_last ? p.other_last + (sp.seq * p.kv_heads + kv) * state_size : nullptr)
-                                                : p.other_edges + ((sp.edge + 1) * p.kv_heads + kv) * state_size;
-#pragma unroll
-                    for (int t = 0; t < KT; ++t) {
-                        f32x16 D;
-                        attn_load_tile(D, from, p, t, col0, afresh(lane));
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) dot_end = __builtin_fmaf(D[r], S[t][r], dot_end);
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-                }
+                    for (int r = 0; r < 16; ++r) S[t][r] *= through;
             }
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
@@ -661,8 +807,7 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                         v[2 * e + 1] += __builtin_bit_cast(float, zf[e] & 0xffff0000u);
                     }
                 }
-                const attn_f32x4 w0 = *(const attn_f32x4*)(wout + 16 * ks + 4 * half),
-                                 w1 = *(const attn_f32x4*)(wout + 16 * ks + 8 + 4 * half);
+                const attn_f32x4 w0 = source(2 * ks), w1 = source(2 * ks + 1);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     v[e] *= w0[e];
@@ -695,6 +840,30 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
         }
         if constexpr (Lds::kBuffers == 1) __syncthreads();
         if (it + 1 < items) store(next_h);
+        if constexpr (!AGG) {  // behind the wait for the next tiles, which would be one for these as well
+            if (!REV || h == G - 1) {
+                T* op = (T*)const_cast<void*>(p.out.p) + row0 * p.out.row + (REV ? kv : kv * G + h) * p.out.head;
+                const uint32_t first = col0 + 4 * half, at = (uint32_t)col * (uint32_t)p.out.row + first;
+                if (!REV) {
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) o[r] *= p.scale_out;
+                }
+                auto put = [&](int g, int left) {
+                    const float v[4] = {o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]};
+                    attn_store4<T>(op + (at + 8 * g), left, v);
+                };
+                if (p.out.p && p.dout == OD) {
+                    if (col < n) {
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) put(g, 4);
+                    }
+                } else if (p.out.p) {
+                    const int left = afresh(col < n ? p.dout - (int)first : 0);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) put(g, left - 8 * g);
+                }
+            }
+        }
         __syncthreads();
         if constexpr (DOT) {
             if (h == G - 1 && wave == 0 && col < n) {
@@ -709,13 +878,21 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
         h = next_h;
     }
 
+    const bool keeps = AGG || (!DOT && p.last && (REV ? sp.first : sp.last));
+    if (keeps && items > 0) {
+        const float end = *w.end;
+#pragma unroll
+        for (int t = 0; t < KT; ++t)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) S[t][r] *= end;
+    }
     if constexpr (AGG) {
         const int64_t edge = sp.edge + (against ? 0 : 1);
         attn_store_state<KT>(S, p.edges + (edge * p.kv_heads + kv) * state_size, p, col0, afresh(lane));
         if (threadIdx.x == 0) {
             double t = 0.0;
-            for (int k = 0; k < chunks; ++k) t += s_total[k];
-            p.totals[slot * p.kv_heads + kv] = (float)t;
+            for (int k = 0; k < chunks; ++k) t += w.total[k];
+            p.totals[slot * p.kv_heads + kv] = (float)(t * 0.6931471805599453);
         }
     } else if constexpr (DOT && !REV) {
         for (int m = 32; m > 0; m >>= 1) dot_end += __shfl_xor(dot_end, m);
@@ -726,7 +903,7 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
             for (int k = 1; k < NW; ++k) dot_end += s_sum[k];
             p.ends[slot * p.kv_heads + kv] = dot_end;
         }
-    } else if (p.last && (REV ? sp.first : sp.last)) {
+    } else if (keeps) {
         if (sp.single) __syncthreads();  // state and last may be one array
         attn_store_state<KT>(S, p.last + (sp.seq * p.kv_heads + kv) * state_size, p, col0, afresh(lane));
     }
