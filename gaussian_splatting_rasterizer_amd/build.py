@@ -19,8 +19,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libgsr.so")
 SOURCES = ["api.hip", "project.hip", "binning.hip", "render.hip", "replay.hip", "backward.hip", "attributes.hip",
-           "ffn.hip", "attn_f32.hip", "attn_f16.hip", "attn_bf16.hip", "attn.hip", "scan.hip", "ortho.hip", "norm.hip",
-           "adamw.hip", "updater_api.hip"]
+           "ffn.hip", *[f"attn_{t}_{k}.hip" for t in ("f32", "f16", "bf16") for k in (128, 96, 64)], "attn.hip",
+           "scan.hip", "ortho.hip", "norm.hip", "adamw.hip", "updater_api.hip"]
 ARCH = os.environ.get("GSR_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = [

@@ -20,16 +20,20 @@ namespace gsr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kJoinValues = 1;  // of a state, each thread's
-constexpr int kJoinSteps = 16; // of the chain whose loads are asked for at a time
+constexpr int kJoinWaves = 16, kJoinSteps = 16;  // of k_attn_join; boundaries that a wave takes at a time
 constexpr int kJoinParts = 32;  // shares of the sequences
 
-// The state at every boundary between two spans, in place of what the span beside it adds; one thread runs through a
-// sequence's boundaries for its values.  The loads do not depend on the chain and are asked for ahead of it.
-__global__ __launch_bounds__(kThreads) void k_attn_join(const AttnArgs p, float* copies) {
+// The state at every boundary between two spans, in place of what the span beside it adds.  A workgroup runs through a
+// sequence's boundaries for 64 values of the state, its waves through consecutive runs of them at the same time: each from
+// zero, then with what the waves before it end with.  (One thread for a value's whole chain took 64 us for 256 boundaries
+// of 4 x 128 x 128, four times the data's time.)
+__global__ __launch_bounds__(kJoinWaves * 64) void k_attn_join(const AttnArgs p, float* copies) {
+    __shared__ float s_end[kJoinWaves][64], s_fade[kJoinWaves];
     const int64_t size = (int64_t)p.dk * p.dv;
     const int kv = blockIdx.y, lane = threadIdx.x & 63;
-    const int64_t e0 = (int64_t)blockIdx.x * kThreads * kJoinValues + threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t e = (int64_t)blockIdx.x * 64 + lane;
+    const bool in = e < size;
     const int64_t per = (p.n_seq + gridDim.z - 1) / gridDim.z;
     const int64_t end = min(p.n_seq, (blockIdx.z + 1) * per);
     for (int64_t s0 = blockIdx.z * per; s0 < end; s0 += 64) {
@@ -47,49 +51,47 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(const AttnArgs p, float*
         for (uint64_t todo = __ballot(len > p.span); todo; todo &= todo - 1) {
             const int k = __builtin_ctzll(todo);
             const int64_t s = s0 + k, slo = __shfl(lo, k);
-            const int spans = (int)((__shfl(len, k) + p.span - 1) / p.span);
+            const int spans = (int)((__shfl(len, k) + p.span - 1) / p.span), edges = spans - 1;
             const int64_t edge0 = p.offsets ? slo / p.span : s * (p.spans - 1);  // boundary between spans 0 and 1
             const int64_t slot0 = p.offsets ? slo / p.span + s : s * p.spans;
-            float cur[kJoinValues];
+            float carry = p.first && in ? p.first[(s * p.kv_heads + kv) * size + e] : 0.f;
+            if (copies && in && wave == 0) copies[(attn_copy(p, s, edge0) * p.kv_heads + kv) * size + e] = carry;
+            for (int b0 = 0; b0 < edges; b0 += kJoinWaves * kJoinSteps) {
+                // steps of this pass for each wave
+                const int steps = min(kJoinSteps, (edges - b0 + kJoinWaves - 1) / kJoinWaves), first = b0 + wave * steps;
+                const int mine = max(0, min(steps, edges - first));
+                auto at = [&](int b) { return ((edge0 + (p.against ? edges - 1 - b : b)) * p.kv_heads + kv) * size + e; };
+                float u[kJoinSteps];
 #pragma unroll
-            for (int i = 0; i < kJoinValues; ++i) {
-                const int64_t e = e0 + i * kThreads;
-                cur[i] = p.first && e < size ? p.first[(s * p.kv_heads + kv) * size + e] : 0.f;
-                if (copies && e < size) copies[(attn_copy(p, s, edge0) * p.kv_heads + kv) * size + e] = cur[i];
-            }
-            // boundary of the chain's b-th step: what the span beside it adds (and then the state) and its log a
-            auto edge_of = [&](int b) { return edge0 + (p.against ? spans - 2 - b : b); };
-            float u[2][kJoinSteps][kJoinValues], t[2][kJoinSteps];
-            auto fetch = [&](int b0, int k) {
+                for (int j = 0; j < kJoinSteps; ++j) u[j] = in && j < mine ? p.edges[at(first + j)] : 0.f;
+                // lane j: log a of step j, then of the steps up to it
+                float t = 0.f;
+                if (lane < mine) t = p.totals[(slot0 + (p.against ? spans - 1 - (first + lane) : first + lane)) * p.kv_heads + kv];
+                const float one = expm1f(t);
+#pragma unroll
+                for (int d = 1; d < kJoinSteps; d <<= 1) {
+                    const float before = __shfl_up(t, d);
+                    if (lane >= d) t += before;
+                }
+                const float all = expf(t);
+                float cur = 0.f;
 #pragma unroll
                 for (int j = 0; j < kJoinSteps; ++j) {
-                    const int b = min(b0 + j, spans - 2);
-                    t[k][j] = p.totals[(slot0 + (p.against ? spans - 1 - b : b)) * p.kv_heads + kv];
-#pragma unroll
-                    for (int i = 0; i < kJoinValues; ++i) {
-                        const int64_t e = e0 + i * kThreads;
-                        u[k][j][i] = e < size ? p.edges[(edge_of(b) * p.kv_heads + kv) * size + e] : 0.f;
-                    }
+                    cur = __builtin_fmaf(__shfl(one, j), cur, cur) + u[j];
+                    u[j] = cur;
                 }
-            };
-            fetch(0, 0);
-            for (int b0 = 0; b0 < spans - 1; b0 += 2 * kJoinSteps) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int first = b0 + k * kJoinSteps;
-                    fetch(first + kJoinSteps, k ^ 1);
-#pragma unroll
-                    for (int j = 0; j < kJoinSteps; ++j) {
-                        if (first + j >= spans - 1) break;
-                        const float fade = -expm1f(t[k][j]);
-#pragma unroll
-                        for (int i = 0; i < kJoinValues; ++i) {
-                            const int64_t e = e0 + i * kThreads;
-                            cur[i] = __builtin_fmaf(-fade, cur[i], cur[i]) + u[k][j][i];
-                            if (e < size) p.edges[(edge_of(first + j) * p.kv_heads + kv) * size + e] = cur[i];
-                        }
-                    }
+                s_end[wave][lane] = cur;
+                if (lane == kJoinSteps - 1) s_fade[wave] = all;
+                __syncthreads();
+                float in_front = carry;
+                for (int i = 0; i < kJoinWaves; ++i) {
+                    if (i == wave) in_front = carry;
+                    carry = __builtin_fmaf(s_fade[i], carry, s_end[i][lane]);
                 }
+#pragma unroll
+                for (int j = 0; j < kJoinSteps; ++j)
+                    if (in && j < mine) p.edges[at(first + j)] = __builtin_fmaf(__shfl(all, j), in_front, u[j]);
+                __syncthreads();
             }
         }
     }
@@ -285,10 +287,14 @@ hipError_t attn_step(const AttnArgs& a, hipStream_t st) {
     return hipGetLastError();
 }
 
-// Rows of a span: enough spans to fill the card, as long as they fit.
+// Rows of a span: as many spans as there are places for their workgroups at once -- two of four waves on each CU for widths
+// above 96, six of two up to 64 -- so that all end together (131072 x 4 x 128 training: 1295 us with 512, 1420 with 768, 1368
+// with 1024; 311296 x 4 x 64: 284 us with 1024, 268 with 1536, 276 with 2048).  At least 128 rows, so that reading a state
+// back costs less than the span.
 int attn_span_rows(const gs_attn_dims& d) {
-    constexpr int64_t kSpans = 1024;
-    const int64_t rows = (d.rows * d.kv_heads + kSpans - 1) / kSpans;
+    const int wide = d.d_key > d.d_value ? d.d_key : d.d_value;
+    const int64_t spans = wide <= 64 ? 1536 : wide <= 96 ? 768 : 512;
+    const int64_t rows = (d.rows * d.kv_heads + spans - 1) / spans;
     const int64_t most = d.dtype == GS_BF16 ? kAttnMaxSpan : kAttnMaxSpan / 2;
     return (int)std::min<int64_t>(most, std::max<int64_t>(128, (rows + kAttnChunk - 1) / kAttnChunk * kAttnChunk));
 }
@@ -345,10 +351,8 @@ hipError_t launch_kernel(int dtype, AttnKind kind, const AttnArgs& a, hipStream_
 bool attn_splits(const AttnArgs& a) { return a.offsets ? a.rows > a.span : a.spans > 1; }
 
 hipError_t join(const AttnArgs& a, float* copies, hipStream_t st) {
-    const int64_t size = (int64_t)a.dk * a.dv;
-    k_attn_join<<<dim3((unsigned)((size + kThreads * kJoinValues - 1) / (kThreads * kJoinValues)), a.kv_heads,
-                       (unsigned)std::min<int64_t>(a.n_seq, kJoinParts)),
-                  kThreads, 0, st>>>(a, copies);
+    k_attn_join<<<dim3((unsigned)(((int64_t)a.dk * a.dv + 63) / 64), a.kv_heads, (unsigned)std::min<int64_t>(a.n_seq, kJoinParts)),
+                  kJoinWaves * 64, 0, st>>>(a, copies);
     return hipGetLastError();
 }
 

@@ -205,28 +205,24 @@ __device__ __forceinline__ f32x16 attn_mfma(attn_u32x4 a, attn_u32x4 b, f32x16 c
 // Column (of 16) that row r of a state holds: the middle fours exchanged.
 __device__ __forceinline__ constexpr int attn_column(int r) { return (r & ~12) | (r & 4) << 1 | (r & 8) >> 1; }
 
-// A tile of 32 rows x D in LDS, one plane: slots of eight columns, at position slot ^ row, so that the lanes of a read by
-// rows spread over the banks.
+// A tile of 32 rows x D in LDS, one plane.  A row takes 16 bytes more than its columns, which spreads 16 rows' equal columns
+// over all 64 banks, and leaves every address a lane's own plus a constant.
 template <int D>
 struct AttnTile {
-    static constexpr int kRow = D * 2, kSlots = D / 8, kBytes = kAttnChunk * kRow;
-    static __device__ __forceinline__ int at(int row, int slot) {
-        return row * kRow + ((slot ^ (row & (kSlots - 1))) << 4);
-    }
+    static constexpr int kRow = D * 2 + 16, kBytes = kAttnChunk * kRow;
+    static __device__ __forceinline__ int at(int row, int slot) { return row * kRow + slot * 16; }
     // by rows: the lane's row, columns 16 kk + 8 half + 0..7
     static __device__ __forceinline__ attn_u32x4 rows(const char* t, int kk, int lane) {
-        return *(const attn_u32x4*)(t + at(lane & 31, kk * 2 + (lane >> 5)));
+        return *(const attn_u32x4*)(t + at(lane & 31, lane >> 5) + kk * 32);
     }
     // transposed: one column of col0 + 0..31 (SWAP: of the state's order), rows 16 ks + 4 half + 0..3 and + 8
     template <bool SWAP>
     static __device__ __forceinline__ attn_u32x4 columns(const char* t, int col0, int ks, int lane) {
-        const int row = ks * 16 + (lane >> 5) * 4 + ((lane & 15) >> 2);
         int four = lane & 3;  // of 16 columns
         if (SWAP) four = (four & 1) << 1 | four >> 1;
-        const int slot = (col0 >> 3) + ((lane >> 4) & 1) * 2 + (four >> 1);
-        const char* p = t + (four & 1) * 8;
-        const attn_s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s16x4*)(p + at(row, slot)));
-        const attn_s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s16x4*)(p + at(row + 8, slot)));
+        const char* p = t + at((lane >> 5) * 4 + ((lane & 15) >> 2), ((lane >> 4) & 1) * 2) + four * 8 + at(ks * 16, col0 >> 3);
+        const attn_s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s16x4*)p);
+        const attn_s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s16x4*)(p + at(8, 0)));
         const attn_u32x2 x = __builtin_bit_cast(attn_u32x2, a), y = __builtin_bit_cast(attn_u32x2, b);
         return attn_u32x4{x[0], x[1], y[0], y[1]};
     }
@@ -259,29 +255,49 @@ __device__ __forceinline__ void attn_shift(Run8<T>& run, int k) {
 // that.  Rows past the last one repeat it: as sources they have no weight, as destinations they are not written.
 template <class T, int D, int NT>
 struct AttnFetch {
-    static constexpr int kRuns = kAttnChunk * (D / 8) / NT, kPlanes = AttnType<T>::kPlanes, kStep = NT / (D / 8);
+    static constexpr int kSlots = D / 8, kAll = kAttnChunk * kSlots, kRuns = (kAll + NT - 1) / NT;
+    static constexpr int kPlanes = AttnType<T>::kPlanes;
     Run8<T> run[kRuns];
+    // row and first column of a thread's i-th run (beyond the tile: of its last row, and not stored)
+    static __device__ __forceinline__ void place(int i, int tid, int& row, int& col) {
+        if constexpr (NT % kSlots == 0) {
+            row = i * (NT / kSlots) + tid / kSlots;
+            col = tid % kSlots * 8;
+        } else {
+            const int u = i * NT + tid;
+            row = u / kSlots;
+            col = u % kSlots * 8;
+        }
+    }
     // base: the chunk's first row of one head
     __device__ __forceinline__ void load(const T* base, uint32_t ld, int n, int d) {
+        const int tid = d >= 8 ? (int)threadIdx.x : afresh(threadIdx.x);
         if (d >= 8) {
-            const int r = threadIdx.x / (D / 8), c = min((int)(threadIdx.x % (D / 8)) * 8, d - 8);
 #pragma unroll
             for (int i = 0; i < kRuns; ++i) {
-                const uint32_t at = __umul24((uint32_t)min(r + i * kStep, n - 1), ld) + c;
+                int r, c;
+                place(i, tid, r, c);
+                const uint32_t at = __umul24((uint32_t)min(r, n - 1), ld) + min(c, d - 8);
                 __builtin_memcpy(run[i].v, (const char*)base + at * (uint32_t)sizeof(T), sizeof(run[i].v));
             }
         } else {
-            const int tid = afresh(threadIdx.x), r = tid / (D / 8), c = (tid % (D / 8)) * 8;
 #pragma unroll
-            for (int i = 0; i < kRuns; ++i) run[i].load(base + __umul24((uint32_t)min(r + i * kStep, n - 1), ld) + c, d - c);
+            for (int i = 0; i < kRuns; ++i) {
+                int r, c;
+                place(i, tid, r, c);
+                run[i].load(base + __umul24((uint32_t)min(r, n - 1), ld) + c, d - c);
+            }
         }
     }
     __device__ __forceinline__ void store(char* tile, int d) {
-        const int r0 = threadIdx.x / (D / 8), slot = threadIdx.x % (D / 8);
         if (d != D && d >= 8) {
-            const int k = afresh(slot * 8 - min(slot * 8, d - 8));
+            const int tid = afresh(threadIdx.x);
 #pragma unroll
-            for (int i = 0; i < kRuns; ++i) attn_shift(run[i], k);
+            for (int i = 0; i < kRuns; ++i) {
+                int r, c;
+                place(i, tid, r, c);
+                attn_shift(run[i], c - min(c, d - 8));
+            }
         }
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) {
@@ -294,9 +310,13 @@ struct AttnFetch {
                 for (int e = 0; e < 8; ++e) v[e] = run[i].get(e);
                 split_frag<kPlanes>(v, w);
             }
-            char* t = tile + AttnTile<D>::at(r0 + i * kStep, slot);
+            int r, c;
+            place(i, threadIdx.x, r, c);
+            if (kAll % NT == 0 || i + 1 < kRuns || r < kAttnChunk) {
+                char* t = tile + AttnTile<D>::at(r, c / 8);
 #pragma unroll
-            for (int n = 0; n < kPlanes; ++n) *(attn_u32x4*)(t + n * AttnTile<D>::kBytes) = w[n];
+                for (int n = 0; n < kPlanes; ++n) *(attn_u32x4*)(t + n * AttnTile<D>::kBytes) = w[n];
+            }
         }
     }
 };
@@ -399,7 +419,9 @@ __device__ __forceinline__ void attn_weights(const AttnArgs& p, const AttnSpan& 
     }
 }
 
-// 32 contracted rows of a wave's columns of a state (null: zero).
+// 32 contracted rows of a wave's columns of a state (null: zero): one register after another, or four at once where the
+// contracted side is the inner one and ends with a four.
+__device__ __forceinline__ bool attn_fours(const AttnArgs& p) { return p.transposed && p.dv % 4 == 0; }
 __device__ __forceinline__ uint32_t attn_state_at(const AttnArgs& p, int t, int r, int o, int lane, bool& in) {
     const int c = t * 32 + attn_column(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3));
     in = c < p.dc && o < p.dout;
@@ -407,10 +429,25 @@ __device__ __forceinline__ uint32_t attn_state_at(const AttnArgs& p, int t, int 
 }
 __device__ __forceinline__ void attn_load_tile(f32x16& s, const float* from, const AttnArgs& p, int t, int col0, int lane) {
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-        bool in;
-        const uint32_t at = attn_state_at(p, t, r, col0 + (lane & 31), lane, in);
-        s[r] = from && in ? from[at] : 0.f;
+    for (int r = 0; r < 16; ++r) s[r] = 0.f;
+    if (!from) return;
+    const int o = col0 + (lane & 31);
+    bool in;
+    if (attn_fours(p)) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const uint32_t at = attn_state_at(p, t, 4 * g, o, lane, in);
+            attn_f32x4 v = {0.f, 0.f, 0.f, 0.f};
+            if (in) __builtin_memcpy(&v, from + at, 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[4 * g + e] = v[e];
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            const uint32_t at = attn_state_at(p, t, r, o, lane, in);
+            if (in) s[r] = from[at];
+        }
     }
 }
 template <int KT>
@@ -420,11 +457,11 @@ __device__ __forceinline__ void attn_load_state(f32x16* s, const float* from, co
 }
 template <int KT>
 __device__ __forceinline__ void attn_store_state(const f32x16* s, float* to, const AttnArgs& p, int col0, int lane) {
+    bool in;
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-            bool in;
             const uint32_t at = attn_state_at(p, t, r, col0 + (lane & 31), lane, in);
             if (in) to[at] = s[t][r];
         }
@@ -486,14 +523,15 @@ __device__ __forceinline__ void attn_store4(T* p, int n, const float* in) {
     }
 }
 
-// LDS of a workgroup: tiles of X, Y, Z (twice where the type has one plane: the next ones are stored while these are
-// read), weights and a little for sums.
+// LDS of a workgroup: tiles of X, Y, Z, weights and a little for sums.  One buffer a tile: the next tiles wait in registers,
+// and the second barrier costs less than a second buffer, which halves the workgroups on a CU (64 columns: 216 -> 174 us for
+// 311,296 rows of 4 heads; 128: no difference).
 template <class T, int KD, int OD, bool AGG>
 struct AttnLds {
-    static constexpr int kPlanes = AttnType<T>::kPlanes, kBuffers = kPlanes == 1 ? 2 : 1;
+    static constexpr int kPlanes = AttnType<T>::kPlanes;
     static constexpr int kX = AGG ? 0 : AttnTile<KD>::kBytes * kPlanes, kY = AttnTile<KD>::kBytes * kPlanes,
                          kZ = AttnTile<OD>::kBytes * kPlanes;
-    static constexpr int kTiles = kBuffers * (kX + kY + kZ);
+    static constexpr int kTiles = kX + kY + kZ;
     static constexpr int kSums = 2 * 2 * (OD / 32) * 32 * 4;
     static constexpr int kFixed = kTiles + kSums;
     static constexpr int bytes(int span) { return kFixed + AttnWeights::bytes(span); }
@@ -506,9 +544,9 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
     constexpr int NW = OD / 32, NT = NW * 64, KT = KD / 32, NP = AttnType<T>::kPlanes;
     using Lds = AttnLds<T, KD, OD, AGG>;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
-    char* s_x = smem;
-    char* s_y = smem + Lds::kBuffers * Lds::kX;
-    char* s_z = s_y + Lds::kBuffers * Lds::kY;
+    char* const tx = smem;
+    char* const ty = smem + Lds::kX;
+    char* const tz = ty + Lds::kY;
     float* s_sum = (float*)(smem + Lds::kTiles);  // [2][2][NW][32]
     AttnWeights w;
     w.place(smem + Lds::kFixed, p.span);
@@ -573,16 +611,11 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
             }
         }
     };
-    int x_turn = 0, yz_turn = 0;  // buffer of the tiles in use
-    auto store = [&](int h) {     // into the next buffer, which is then in use
-        if (!AGG && (!REV || h == 0)) {
-            if (Lds::kBuffers == 2) x_turn ^= 1;
-            fx.store(s_x + x_turn * Lds::kX, p.dc);
-        }
+    auto store = [&](int h) {
+        if (!AGG && (!REV || h == 0)) fx.store(tx, p.dc);
         if (many || h == 0) {
-            if (Lds::kBuffers == 2) yz_turn ^= 1;
-            fy.store(s_y + yz_turn * Lds::kY, p.dc);
-            fz.store(s_z + yz_turn * Lds::kZ, p.dout);
+            fy.store(ty, p.dc);
+            fz.store(tz, p.dout);
         }
         if constexpr (DOT) {
 #pragma unroll
@@ -608,9 +641,6 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
     for (int it = 0; it < items; ++it) {
         const int n = min(kAttnChunk, sp.n - c * kAttnChunk);
         const int64_t row0 = sp.row0 + c * kAttnChunk;
-        const char* tx = s_x + x_turn * Lds::kX;
-        const char* ty = s_y + yz_turn * Lds::kY;
-        const char* tz = s_z + yz_turn * Lds::kZ;
         const float lift = w.lift[c];
         const bool sums = lift == 0.f;
         auto sum_of = [&](int row) { return (double)w.in[c * kAttnChunk + row] + (double)w.out[c * kAttnChunk + row]; };
@@ -838,7 +868,7 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                 }
             }
         }
-        if constexpr (Lds::kBuffers == 1) __syncthreads();
+        __syncthreads();
         if (it + 1 < items) store(next_h);
         if constexpr (!AGG) {  // behind the wait for the next tiles, which would be one for these as well
             if (!REV || h == G - 1) {
@@ -910,8 +940,13 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
 }
 
 enum AttnKind { kAttnForward, kAttnAggregate, kAttnGradQ, kAttnGradK, kAttnGradV };
+template <class T, int KD>
+hipError_t launch_attn_wide(AttnKind kind, const AttnArgs& a, hipStream_t st);
 template <class T>
-hipError_t launch_attn_kernel(AttnKind kind, const AttnArgs& a, hipStream_t st);
+hipError_t launch_attn_kernel(AttnKind kind, const AttnArgs& a, hipStream_t st) {
+    if (a.dc <= 64) return launch_attn_wide<T, 64>(kind, a, st);
+    return a.dc <= 96 ? launch_attn_wide<T, 96>(kind, a, st) : launch_attn_wide<T, 128>(kind, a, st);
+}
 
 template <class T, int KD, int OD, int ORDER, bool REV, bool DOT, bool AGG>
 hipError_t launch_attn_as(const AttnArgs& a, hipStream_t st) {
@@ -938,13 +973,12 @@ hipError_t launch_attn_sized(AttnKind kind, const AttnArgs& a, hipStream_t st) {
     return hipErrorInvalidValue;
 }
 
-// Widths are padded to 64 or 128.
-#define GSR_ATTN_KERNELS(T)                                                                                    \
-    template <>                                                                                                \
-    hipError_t launch_attn_kernel<T>(AttnKind kind, const AttnArgs& a, hipStream_t st) {                       \
-        if (a.dc <= 64)                                                                                        \
-            return a.dout <= 64 ? launch_attn_sized<T, 64, 64>(kind, a, st) : launch_attn_sized<T, 64, 128>(kind, a, st); \
-        return a.dout <= 64 ? launch_attn_sized<T, 128, 64>(kind, a, st) : launch_attn_sized<T, 128, 128>(kind, a, st);   \
+// Widths are padded to 64, 96 or 128.
+#define GSR_ATTN_KERNELS(T, KD)                                                                       \
+    template <>                                                                                       \
+    hipError_t launch_attn_wide<T, KD>(AttnKind kind, const AttnArgs& a, hipStream_t st) {            \
+        if (a.dout <= 64) return launch_attn_sized<T, KD, 64>(kind, a, st);                           \
+        return a.dout <= 96 ? launch_attn_sized<T, KD, 96>(kind, a, st) : launch_attn_sized<T, KD, 128>(kind, a, st); \
     }
 
 }  // namespace gsr
