@@ -289,14 +289,16 @@ hipError_t attn_step(const AttnArgs& a, hipStream_t st) {
 
 // Rows of a span: as many spans as there are places for their workgroups at once -- two of four waves on each CU for widths
 // above 96, six of two up to 64 -- so that all end together (131072 x 4 x 128 training: 1295 us with 512, 1420 with 768, 1368
-// with 1024; 311296 x 4 x 64: 284 us with 1024, 268 with 1536, 276 with 2048).  At least 128 rows, so that reading a state
-// back costs less than the span.
+// with 1024; 311296 x 4 x 64: 284 us with 1024, 268 with 1536, 276 with 2048).  An odd number of chunks: the workgroups go
+// forward in step, and addresses a power of two apart would fall on the same memory channels (131072 rows in spans of 1024:
+// 2.49 ns a row forward, 126976 in spans of 992: 2.24).  At least 160 rows, so that reading a state back costs less than the
+// span.
 int attn_span_rows(const gs_attn_dims& d) {
     const int wide = d.d_key > d.d_value ? d.d_key : d.d_value;
     const int64_t spans = wide <= 64 ? 1536 : wide <= 96 ? 768 : 512;
     const int64_t rows = (d.rows * d.kv_heads + spans - 1) / spans;
-    const int64_t most = d.dtype == GS_BF16 ? kAttnMaxSpan : kAttnMaxSpan / 2;
-    return (int)std::min<int64_t>(most, std::max<int64_t>(128, (rows + kAttnChunk - 1) / kAttnChunk * kAttnChunk));
+    const int64_t chunks = (rows + kAttnChunk - 1) / kAttnChunk | 1;
+    return (int)std::min<int64_t>(kAttnMaxSpan - kAttnChunk, std::max<int64_t>(5 * kAttnChunk, chunks * kAttnChunk));
 }
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
@@ -449,6 +451,20 @@ hipError_t launch_attn_backward(const gs_attn_dims& d, const int64_t* offsets, c
         GSR_HIP(join(g, copies, st));
     }
     rev.copies = split ? copies : nullptr;
+    // in turn against the rows' order and along it: each finds the rows that the one before ended with in the cache
+    if (out.k.p || out.gate) {
+        AttnArgs a = rev;
+        a.x = array(in.v);
+        a.y = array(dy);
+        a.z = array(in.q);
+        a.out = array(out.k);
+        a.w = array(in.k);
+        a.dc = d.d_value;
+        a.dout = d.d_key;
+        a.transposed = true;
+        a.dots = dots + 2 * plane;
+        GSR_HIP(launch_kernel(d.dtype, kAttnGradK, a, st));
+    }
     if (out.q.p || out.gate) {
         AttnArgs a = base;
         a.x = array(dy);
@@ -468,19 +484,6 @@ hipError_t launch_attn_backward(const gs_attn_dims& d, const int64_t* offsets, c
         a.ends = ends;
         a.dots = dots;
         GSR_HIP(launch_kernel(d.dtype, kAttnGradQ, a, st));
-    }
-    if (out.k.p || out.gate) {
-        AttnArgs a = rev;
-        a.x = array(in.v);
-        a.y = array(dy);
-        a.z = array(in.q);
-        a.out = array(out.k);
-        a.w = array(in.k);
-        a.dc = d.d_value;
-        a.dout = d.d_key;
-        a.transposed = true;
-        a.dots = dots + 2 * plane;
-        GSR_HIP(launch_kernel(d.dtype, kAttnGradK, a, st));
     }
     if (out.gate) {
         AttnArgs a = base;

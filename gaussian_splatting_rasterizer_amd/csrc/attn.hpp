@@ -44,7 +44,7 @@ typedef float attn_f32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) attn_s16x4 attn_lds_s16x4;
 
 constexpr int kAttnChunk = 32;
-constexpr int kAttnMaxSpan = 1024;  // rows whose weights lie in LDS (16-bit)
+constexpr int kAttnMaxSpan = 2048;  // rows whose weights lie in LDS
 
 // Rows [rows, heads, d] of one array.
 struct AttnArray {
@@ -196,6 +196,27 @@ __device__ __forceinline__ void split_frag(const float* v, attn_u32x4* out) {
 #pragma unroll
         for (int n = 0; n < N; ++n) out[n][e] = w[n];
     }
+}
+// The same in instructions that the compiler can place between others; overwrites v.
+template <int N>
+__device__ __forceinline__ void split_frag_over(float* v, attn_u32x4* out) {
+    uint32_t first = 0x0000bf80u, second = 0xbf800000u;
+    asm("" : "+s"(first), "+s"(second));  // as inline constants they would be others
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const attn_bf16x2 h = {(__bf16)v[2 * e], (__bf16)v[2 * e + 1]};
+            uint32_t w = __builtin_bit_cast(uint32_t, h);
+            if (n + 1 < N) {
+                asm("" : "+v"(w));  // keeps the compiler from rounding the two by themselves
+                const attn_bf16x2 pair = __builtin_bit_cast(attn_bf16x2, w);
+                v[2 * e] = __builtin_amdgcn_fdot2_f32_bf16(pair, __builtin_bit_cast(attn_bf16x2, first), v[2 * e], false);
+                v[2 * e + 1] =
+                    __builtin_amdgcn_fdot2_f32_bf16(pair, __builtin_bit_cast(attn_bf16x2, second), v[2 * e + 1], false);
+            }
+            out[n][e] = w;
+        }
 }
 __device__ __forceinline__ f32x16 attn_mfma(attn_u32x4 a, attn_u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(attn_bf16x8, a), __builtin_bit_cast(attn_bf16x8, b), c,
@@ -369,7 +390,9 @@ struct AttnWeights {
     static __device__ __forceinline__ double leaving(bool against, double p, double P) { return against ? p : P - p; }
 };
 
-__device__ __forceinline__ void attn_weights(const AttnArgs& p, const AttnSpan& s, int head, bool against,
+// back: the chunks' order on the way; AGG: sources alone, weighted for the far end of the span, which the state is at.
+template <bool AGG>
+__device__ __forceinline__ void attn_weights(const AttnArgs& p, const AttnSpan& s, int head, bool against, bool back,
                                              const AttnWeights& w) {
     const int lane = threadIdx.x & 31, chunks = (s.n + kAttnChunk - 1) / kAttnChunk, rows = chunks * kAttnChunk;
     const int whole = (rows + 63) / 64 * 64;  // waves
@@ -389,22 +412,22 @@ __device__ __forceinline__ void attn_weights(const AttnArgs& p, const AttnSpan& 
     }
     __syncthreads();
     if (threadIdx.x < 64) {
-        const int k = threadIdx.x;  // the k-th chunk on the way (a span has at most 32)
-        const double P = k < chunks ? w.total[against ? chunks - 1 - k : k] : 0.0;
+        const int k = threadIdx.x;  // the k-th chunk on the way (a span has at most 64)
+        const double P = k < chunks ? w.total[back ? chunks - 1 - k : k] : 0.0;
         double e = 0.0, mine = 0.0;
         for (int i = 0; i < chunks; ++i) {
             if (i == k) mine = e;
             e += __shfl(P, i);
-            if (!(e > kAttnLow)) e = e != e ? e : 0.0;
+            if (!AGG && !(e > kAttnLow)) e = e != e ? e : 0.0;
         }
         if (k < chunks) {
-            const int c = against ? chunks - 1 - k : k;
+            const int c = back ? chunks - 1 - k : k;
             const double x = P + mine;
             w.before[c] = mine;
-            w.lift[c] = x > kAttnLow || x != x ? 1.f : P > kAttnLow ? exp2_wide(-x) : 0.f;
+            w.lift[c] = AGG || x > kAttnLow || x != x ? 1.f : P > kAttnLow ? exp2_wide(-x) : 0.f;
             w.through[c] = exp2_wide(x);
         }
-        if (k == 0) *w.end = exp2_wide(e);
+        if (k == 0) *w.end = AGG ? 1.f : exp2_wide(e);
     }
     __syncthreads();
     for (int r = threadIdx.x; r < rows; r += blockDim.x) {
@@ -412,9 +435,11 @@ __device__ __forceinline__ void attn_weights(const AttnArgs& p, const AttnSpan& 
         const float lift = w.lift[c];
         if (lift == 0.f) continue;
         const double sum = (double)w.in[r] + (double)w.out[r], P = w.total[c], e = w.before[c];
-        w.in[r] = exp2_wide(AttnWeights::arriving(against, sum, P, e));
+        if (!AGG) w.in[r] = exp2_wide(AttnWeights::arriving(against, sum, P, e));
         // not by way of P where that falls out: it may be no number while a row before is
-        const double out = lift == 1.f ? (against ? sum - P : -sum) - e : AttnWeights::leaving(against, sum, P);
+        const double out = AGG           ? AttnWeights::leaving(against, sum, P) + e
+                           : lift == 1.f ? (against ? sum - P : -sum) - e
+                                         : AttnWeights::leaving(against, sum, P);
         w.out[r] = r < s.n ? exp2_wide(out) * p.scale_state : 0.f;
     }
 }
@@ -540,7 +565,7 @@ struct AttnLds {
 // REV: against the rows' order.  DOT: gradient of q (of k): also the products of the outputs with w and, at the span's end,
 // of the state and the adjoint.  AGG: what the span adds to the state alone.
 template <class T, int KD, int OD, int ORDER, bool REV, bool DOT, bool AGG>
-__global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
+__global__ __launch_bounds__(OD / 32 * 64, KD == 64 && !DOT ? 3 : 2) void k_attn(const AttnArgs p) {
     constexpr int NW = OD / 32, NT = NW * 64, KT = KD / 32, NP = AttnType<T>::kPlanes;
     using Lds = AttnLds<T, KD, OD, AGG>;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -558,6 +583,9 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
     if (slot >= p.slots) return;
     const AttnSpan sp = attn_span(p, slot);
     const bool against = AGG ? p.against : REV;
+    // Aggregates begin at the end that the pass after them ends with, so that it finds what was read last in the
+    // last-level cache.
+    const bool back = AGG ? !p.against : REV;
     if (!sp.live || (AGG && (against ? sp.first : sp.last))) return;
     const int64_t state_size = (int64_t)p.dk * p.dv;
     const int col0 = wave * 32;
@@ -577,7 +605,7 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
         }
         attn_load_state<KT>(S, from, p, col0, afresh(lane));
     }
-    attn_weights(p, sp, kv, against, w);
+    attn_weights<AGG>(p, sp, kv, against, back, w);
     // the state is there before the loop, which would otherwise wait for every load that is under way
 #pragma unroll
     for (int t = 0; t < KT; ++t) asm volatile("" : "+v"(S[t]));
@@ -629,7 +657,7 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
             }
         }
     };
-    int c = against ? chunks - 1 : 0, h = 0;
+    int c = back ? chunks - 1 : 0, h = 0;
     if (items > 0) {
         load(c, 0);
         store(0);
@@ -645,8 +673,8 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
         const bool sums = lift == 0.f;
         auto sum_of = [&](int row) { return (double)w.in[c * kAttnChunk + row] + (double)w.out[c * kAttnChunk + row]; };
         // weights of the sources 8 g + 4 half + 0..3
-        auto source = [&](int g) {
-            if (!sums) return *(const attn_f32x4*)(w.out + c * kAttnChunk + 8 * g + 4 * half);
+        auto source = [&](int g) { return *(const attn_f32x4*)(w.out + c * kAttnChunk + 8 * g + 4 * half); };
+        auto slow_source = [&](int g) {
             attn_f32x4 v;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -655,6 +683,9 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
             }
             return v;
         };
+        attn_f32x4 ws[4];
+        f32x16 pt, t;
+        float own_score = 0.f;
         if constexpr (DOT && !REV) {
             // what passes through the span's last chunk: <adjoint behind the span, faded state>
             if (it + 1 == items) {
@@ -666,7 +697,6 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                     attn_load_tile(D, from, p, t, col0, afresh(lane));
 #pragma unroll
                     for (int r = 0; r < 16; ++r) dot_end = __builtin_fmaf(D[r], S[t][r], dot_end);
-                    __builtin_amdgcn_sched_barrier(0);
                 }
                 dot_end *= w.through[c];
             }
@@ -674,7 +704,7 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
         int next_c = c, next_h = h + 1;
         if (next_h == G) {
             next_h = 0;
-            next_c += against ? -1 : 1;
+            next_c += back ? -1 : 1;
         }
         if (it + 1 < items) load(next_c, next_h);
 
@@ -690,7 +720,6 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                 dot_in = h == 0 ? 0.f : dot_in;
             }
             dot_own = h == 0 ? 0.f : dot_own;
-            f32x16 pt;
 #pragma unroll
             for (int r = 0; r < 16; ++r) pt[r] = 0.f;
             attn_u32x4 xf[2][NP], yf[2][NP];
@@ -722,7 +751,6 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                         for (int j = 0; j < NP; ++j)
                             if (i + j <= ORDER) o = attn_mfma(sf[i], xf[kk & 1][j], o);
                 }
-                __builtin_amdgcn_sched_barrier(0);
             }
             if (inter) {
                 const float wi = arriving();
@@ -738,9 +766,9 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                 const float a = w.in[c * kAttnChunk + col] * lift;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const attn_f32x4 ws = source(g);
+                    ws[g] = source(g);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) pt[4 * g + e] *= ws[e] * a;
+                    for (int e = 0; e < 4; ++e) pt[4 * g + e] *= ws[g][e] * a;
                 }
             } else {
                 const double own = sum_of(col);
@@ -749,42 +777,14 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                     const double d = own - sum_of(8 * (r >> 2) + 4 * half + (r & 3));
                     pt[r] *= __builtin_amdgcn_exp2f((float)(REV ? -d : d)) * p.scale_state;
                 }
+#pragma unroll
+                for (int g = 0; g < 4; ++g) ws[g] = slow_source(g);
             }
-            // acc += z scores
-            const uint32_t own = 1u << col, real = n == kAttnChunk ? ~0u : (1u << n) - 1;
-            const uint32_t parted = REV ? -own & ~own & real : own - 1;
-            auto add = [&](f32x16 acc, uint32_t keep) {  // bits of the sources
-                const int bits = afresh((int)(keep >> (4 * half)));
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int s = 16 * ks + 8 * (e >> 2) + (e & 3);
-                        const float score = pt[ks * 8 + e];
-                        v[e] = __builtin_bit_cast(float, __builtin_bit_cast(int, score) & bit_mask(bits, s));
-                    }
-                    attn_u32x4 pf[ORDER + 1];
-                    split_frag<ORDER + 1>(v, pf);
-#pragma unroll
-                    for (int j = 0; j < NP; ++j) {
-                        const attn_u32x4 zf = AttnTile<OD>::template columns<false>(tz + j * AttnTile<OD>::kBytes, col0, ks, lane);
-#pragma unroll
-                        for (int i = 0; i <= ORDER; ++i)
-                            if (i + j <= ORDER) acc = attn_mfma(zf, pf[i], acc);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                return acc;
-            };
+            // only the pairs of a source before the destination (against the order: behind it) and, but for DOT, its own
+            const uint32_t self = 1u << col, real = n == kAttnChunk ? ~0u : (1u << n) - 1;
+            const uint32_t keep = (REV ? -self & ~self & real : self - 1) | (DOT ? 0u : self);
             if constexpr (DOT) {
-                f32x16 t;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) t[r] = 0.f;
-                t = add(t, parted);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) dot_own = __builtin_fmaf(t[r], wv[r >> 2].get(r & 3), dot_own);
-                // the row's own pair: its score is in register 4 (col / 8) + col % 4 of one half wave
+                // its own score is in register 4 (col / 8) + col % 4 of one half wave
                 float v[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) v[r] = pt[r];
@@ -795,34 +795,55 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                     for (int i = 0; i < 8 >> k; ++i) v[i] = odd ? v[2 * i + 1] : v[2 * i];
                 }
                 const float other = __shfl_xor(v[0], 32);
-                const float score = ((col >> 2) & 1) == half ? v[0] : other;
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float z[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int j = 0; j < NP; ++j) {
-                        const attn_u32x2 w2 =
-                            *(const attn_u32x2*)(tz + j * AttnTile<OD>::kBytes + AttnTile<OD>::at(col, (col0 >> 3) + g) + 8 * half);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            z[e] += __builtin_bit_cast(float, e & 1 ? w2[e >> 1] & 0xffff0000u : w2[e >> 1] << 16);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[4 * g + e] += __builtin_fmaf(score, z[e], t[4 * g + e]);
-                }
-            } else {
-                o = add(o, parted | (own & real));
+                own_score = ((col >> 2) & 1) == half ? v[0] : other;
             }
+            const int bits = afresh((int)(keep >> (4 * half)));
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float score = pt[r];
+                pt[r] = __builtin_bit_cast(float, __builtin_bit_cast(int, score) & bit_mask(bits, 8 * (r >> 2) + (r & 3)));
+            }
+            if constexpr (DOT) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) t[r] = 0.f;
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) ws[g] = source(g);
         }
-        // the state
-        if (many || h == G - 1) {
-            if ((!many || h == 0) && lift != 1.f) {
-                const float through = w.through[c];
+        const bool update = many || h == G - 1;
+        if (!AGG && update && (!many || h == 0) && lift != 1.f) {
+            const float through = w.through[c];
 #pragma unroll
-                for (int t = 0; t < KT; ++t)
+            for (int t2 = 0; t2 < KT; ++t2)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) S[t][r] *= through;
+                for (int r = 0; r < 16; ++r) S[t2][r] *= through;
+        }
+        // (DOT ? t : o) += z scores
+        auto add = [&] {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = pt[ks * 8 + e];
+                attn_u32x4 pf[ORDER + 1];
+                split_frag_over<ORDER + 1>(v, pf);
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    const attn_u32x4 zf = AttnTile<OD>::template columns<false>(tz + j * AttnTile<OD>::kBytes, col0, ks, lane);
+#pragma unroll
+                    for (int i = 0; i <= ORDER; ++i)
+                        if (i + j <= ORDER) {
+                            if constexpr (DOT)
+                                t = attn_mfma(zf, pf[i], t);
+                            else
+                                o = attn_mfma(zf, pf[i], o);
+                        }
+                }
             }
+        };
+        // S += y (w z)
+        auto grow = [&] {
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 float v[8];
@@ -837,25 +858,44 @@ __global__ __launch_bounds__(OD / 32 * 64, 2) void k_attn(const AttnArgs p) {
                         v[2 * e + 1] += __builtin_bit_cast(float, zf[e] & 0xffff0000u);
                     }
                 }
-                const attn_f32x4 w0 = source(2 * ks), w1 = source(2 * ks + 1);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[e] *= w0[e];
-                    v[4 + e] *= w1[e];
-                }
+                for (int e = 0; e < 8; ++e) v[e] *= ws[2 * ks + (e >> 2)][e & 3];
                 attn_u32x4 vf[3];
-                split_frag<3>(v, vf);
+                split_frag_over<3>(v, vf);
 #pragma unroll
-                for (int t = 0; t < KT; ++t) {
+                for (int t2 = 0; t2 < KT; ++t2)
 #pragma unroll
                     for (int j = 0; j < NP; ++j) {
-                        const attn_u32x4 yf = AttnTile<KD>::template columns<true>(ty + j * AttnTile<KD>::kBytes, t * 32, ks, lane);
+                        const attn_u32x4 yf =
+                            AttnTile<KD>::template columns<true>(ty + j * AttnTile<KD>::kBytes, t2 * 32, ks, lane);
 #pragma unroll
                         for (int i = 0; i <= 2; ++i)
-                            if (i + j <= 2) S[t] = attn_mfma(yf, vf[i], S[t]);
+                            if (i + j <= 2) S[t2] = attn_mfma(yf, vf[i], S[t2]);
                     }
-                    if (t & 1) __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        if (!update) {
+            if constexpr (!AGG) add();
+        } else {
+            grow();
+            if constexpr (!AGG) add();
+        }
+        if constexpr (DOT) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r) dot_own = __builtin_fmaf(t[r], wv[r >> 2].get(r & 3), dot_own);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float z[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    const attn_u32x2 w2 =
+                        *(const attn_u32x2*)(tz + j * AttnTile<OD>::kBytes + AttnTile<OD>::at(col, (col0 >> 3) + g) + 8 * half);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        z[e] += __builtin_bit_cast(float, e & 1 ? w2[e >> 1] & 0xffff0000u : w2[e >> 1] << 16);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[4 * g + e] += __builtin_fmaf(own_score, z[e], t[4 * g + e]);
             }
         }
         if constexpr (DOT) {
