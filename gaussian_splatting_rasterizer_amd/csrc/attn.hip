@@ -118,7 +118,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_gate(const AttnArgs p, const 
 #pragma unroll
     for (int k = 0; k < kTurns; ++k) {
         const int c = part + k * (kThreads / 32), row = c * kAttnChunk + lane;
-        const bool in = c < chunks && row < sp.n;
+        if (c >= chunks) continue;  // whole half waves
+        const bool in = row < sp.n;
         const int64_t at = (int64_t)kv * p.rows + sp.row0 + row;
         const double r = in ? (double)g.dots[at] : 0.0, own = in ? (double)g.dots[plane + at] : 0.0;
         const double cc = in ? (double)g.dots[2 * plane + at] : 0.0, cown = in ? (double)g.dots[3 * plane + at] : 0.0;
@@ -131,7 +132,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_gate(const AttnArgs p, const 
             sum_r += z;
         }
         known[k] = from + (before - cc);
-        if (lane == 31 && c < chunks) {
+        if (lane == 31) {
             s_r[c] = sum_r;
             s_c[c] = before;
         }

@@ -186,6 +186,21 @@ __device__ __forceinline__ void split_pair(float a, float b, uint32_t* out) {
         }
     }
 }
+// The same for two columns of a row, of which an infinite one must not reach the other (by way of 0 times it).
+template <int N>
+__device__ __forceinline__ void split_apart(float a, float b, uint32_t* out) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const attn_bf16x2 h = {(__bf16)a, (__bf16)b};
+        out[n] = __builtin_bit_cast(uint32_t, h);
+        if (n + 1 < N) {
+            asm("" : "+v"(out[n]));  // keeps the compiler from rounding the two by themselves
+            a -= __builtin_bit_cast(float, out[n] << 16);
+            b -= __builtin_bit_cast(float, out[n] & 0xffff0000u);
+        }
+    }
+}
+
 // N operand fragments of eight values.
 template <int N>
 __device__ __forceinline__ void split_frag(const float* v, attn_u32x4* out) {
@@ -271,6 +286,19 @@ __device__ __forceinline__ void attn_shift(Run8<T>& run, int k) {
     __builtin_memcpy(run.v, w, sizeof(run.v));
 }
 
+// Not zero where one of a run's values is not finite: its exponent, all ones, carries.
+template <class T>
+__device__ __forceinline__ uint32_t attn_not_finite(const Run8<T>& run) {
+    constexpr int W = sizeof(T) * 2;
+    constexpr uint32_t rest = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu, top = ~rest;
+    constexpr uint32_t one = sizeof(T) == 4 ? 0x00800000u : __is_same(T, _Float16) ? 0x04000400u : 0x00800080u;
+    uint32_t w[W], seen = 0;
+    __builtin_memcpy(w, run.v, sizeof(run.v));
+#pragma unroll
+    for (int i = 0; i < W; ++i) seen |= (w[i] & rest) + one;
+    return seen & top;
+}
+
 // One tile on its way from memory to LDS: runs of eight values, spread over the workgroup.  A run that would leave its row
 // is read from where it ends with the row and put right when it is stored, so that nothing waits for the loads before
 // that.  Rows past the last one repeat it: as sources they have no weight, as destinations they are not written.
@@ -310,7 +338,9 @@ struct AttnFetch {
             }
         }
     }
-    __device__ __forceinline__ void store(char* tile, int d) {
+    // Values that are not finite would meet the zero weights of earlier destinations: they become zero and bad[column] the
+    // first of their rows, *any set.  (null: they stay.)
+    __device__ __forceinline__ void store(char* tile, int d, int* bad = nullptr, int* any = nullptr) {
         if (d != D && d >= 8) {
             const int tid = afresh(threadIdx.x);
 #pragma unroll
@@ -320,16 +350,38 @@ struct AttnFetch {
                 attn_shift(run[i], c - min(c, d - 8));
             }
         }
+        if (bad) {
+            uint32_t seen = 0;
+#pragma unroll
+            for (int i = 0; i < kRuns; ++i) seen |= attn_not_finite(run[i]);
+            if (seen) {
+#pragma unroll
+                for (int i = 0; i < kRuns; ++i) {
+                    int r, c;
+                    place(i, threadIdx.x, r, c);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (r < kAttnChunk && !__builtin_isfinite(run[i].get(e))) {
+                            atomicMin(bad + c + e, r);
+                            run[i].set(e, 0.f);
+                        }
+                }
+                *any = 1;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < kRuns; ++i) {
             attn_u32x4 w[kPlanes];
             if constexpr (kPlanes == 1) {
                 __builtin_memcpy(&w[0], run[i].v, 16);
             } else {
-                float v[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = run[i].get(e);
-                split_frag<kPlanes>(v, w);
+                for (int e = 0; e < 4; ++e) {
+                    uint32_t part[kPlanes];
+                    split_apart<kPlanes>(run[i].get(2 * e), run[i].get(2 * e + 1), part);
+#pragma unroll
+                    for (int n = 0; n < kPlanes; ++n) w[n][e] = part[n];
+                }
             }
             int r, c;
             place(i, threadIdx.x, r, c);
@@ -557,7 +609,7 @@ struct AttnLds {
     static constexpr int kX = AGG ? 0 : AttnTile<KD>::kBytes * kPlanes, kY = AttnTile<KD>::kBytes * kPlanes,
                          kZ = AttnTile<OD>::kBytes * kPlanes;
     static constexpr int kTiles = kX + kY + kZ;
-    static constexpr int kSums = 2 * 2 * (OD / 32) * 32 * 4;
+    static constexpr int kSums = 2 * 2 * (OD / 32) * 32 * 4 + 16;  // sums of dots; or [2][OD] first rows, [2] whether any
     static constexpr int kFixed = kTiles + kSums;
     static constexpr int bytes(int span) { return kFixed + AttnWeights::bytes(span); }
 };
@@ -565,7 +617,7 @@ struct AttnLds {
 // REV: against the rows' order.  DOT: gradient of q (of k): also the products of the outputs with w and, at the span's end,
 // of the state and the adjoint.  AGG: what the span adds to the state alone.
 template <class T, int KD, int OD, int ORDER, bool REV, bool DOT, bool AGG>
-__global__ __launch_bounds__(OD / 32 * 64, KD == 64 && !DOT ? 3 : 2) void k_attn(const AttnArgs p) {
+__global__ __launch_bounds__(OD / 32 * 64, KD == 64 && !DOT && AttnType<T>::kPlanes == 1 ? 3 : 2) void k_attn(const AttnArgs p) {
     constexpr int NW = OD / 32, NT = NW * 64, KT = KD / 32, NP = AttnType<T>::kPlanes;
     using Lds = AttnLds<T, KD, OD, AGG>;
     extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -639,11 +691,19 @@ __global__ __launch_bounds__(OD / 32 * 64, KD == 64 && !DOT ? 3 : 2) void k_attn
             }
         }
     };
-    auto store = [&](int h) {
+    // The outputs of the forward pass alone: gradients may be no numbers throughout such a sequence.
+    constexpr bool CHECK = !REV && !DOT && !AGG;
+    int* const s_bad = (int*)s_sum;
+    int* const s_any = s_bad + 2 * OD;
+    if (CHECK) {
+        for (int i = threadIdx.x; i < 2 * OD + 2; i += NT) s_bad[i] = i < 2 * OD ? kAttnChunk : 0;
+        __syncthreads();
+    }
+    auto store = [&](int c, int h) {
         if (!AGG && (!REV || h == 0)) fx.store(tx, p.dc);
         if (many || h == 0) {
             fy.store(ty, p.dc);
-            fz.store(tz, p.dout);
+            fz.store(tz, p.dout, CHECK ? s_bad + (c & 1) * OD : nullptr, s_any + (c & 1));
         }
         if constexpr (DOT) {
 #pragma unroll
@@ -660,7 +720,7 @@ __global__ __launch_bounds__(OD / 32 * 64, KD == 64 && !DOT ? 3 : 2) void k_attn
     int c = back ? chunks - 1 : 0, h = 0;
     if (items > 0) {
         load(c, 0);
-        store(0);
+        store(c, 0);
     }
     __syncthreads();
 
@@ -880,6 +940,19 @@ __global__ __launch_bounds__(OD / 32 * 64, KD == 64 && !DOT ? 3 : 2) void k_attn
             grow();
             if constexpr (!AGG) add();
         }
+        const bool spoilt = CHECK && s_any[c & 1];
+        if (spoilt) {
+            const int* bad = s_bad + (c & 1) * OD + col0;
+            const float nan = __builtin_nanf("");
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (bad[8 * (r >> 2) + 4 * half + (r & 3)] <= col) o[r] = nan;
+            if (update && bad[col] < kAttnChunk)
+#pragma unroll
+                for (int t2 = 0; t2 < KT; ++t2)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) S[t2][r] = nan;
+        }
         if constexpr (DOT) {
 #pragma unroll
             for (int r = 0; r < 16; ++r) dot_own = __builtin_fmaf(t[r], wv[r >> 2].get(r & 3), dot_own);
@@ -909,7 +982,9 @@ __global__ __launch_bounds__(OD / 32 * 64, KD == 64 && !DOT ? 3 : 2) void k_attn
             }
         }
         __syncthreads();
-        if (it + 1 < items) store(next_h);
+        if (spoilt && h == G - 1)
+            for (int i = threadIdx.x; i <= OD; i += NT) (i < OD ? s_bad[(c & 1) * OD + i] : s_any[c & 1]) = i < OD ? kAttnChunk : 0;
+        if (it + 1 < items) store(next_c, next_h);
         if constexpr (!AGG) {  // behind the wait for the next tiles, which would be one for these as well
             if (!REV || h == G - 1) {
                 T* op = (T*)const_cast<void*>(p.out.p) + row0 * p.out.row + (REV ? kv : kv * G + h) * p.out.head;

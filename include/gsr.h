@@ -518,7 +518,8 @@ GSR_API gs_status gs_adamw_step(const gs_adamw_dims* dims, const gs_adamw_tensor
  * rows behind it are left as they are.  Null: n_seq sequences of equal length.  Offsets outside [0, rows] are taken as the
  * nearer of the two; values that are not non-decreasing give unspecified results but no access out of range.
  * Sequences may be empty; equal sequences of length 1 (single tokens) take a kernel of their own.
- * Not a number and infinities stay in their sequence and reach no row before theirs; infinities may come out as NaN.
+ * Not a number and infinities stay in their sequence, and in outputs reach no row before theirs (in gradients any row of
+ * the sequence); infinities may come out as NaN.
  * d_key and d_value are 1 .. 128, rows and n_seq 0 .. 2^31 - 512, heads up to 65535. */
 typedef struct {
     int64_t rows;

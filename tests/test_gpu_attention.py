@@ -403,3 +403,35 @@ def test_refusals():
     states = torch.zeros(4, 2, 16, 16, device="cuda")
     with pytest.raises(m.GsrError):
         att.forward(*args, state=states[:3], last=states[1:])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("name", ["q", "k", "v", "gate"])
+def test_earlier_rows_are_left_alone(name, dtype):
+    """What is not a number reaches no row before its own, whatever tile they share."""
+    x, _, _ = inputs(200, 1, 4, 2, 64, 72, dtype, seed=23)
+    att = gsr().LinearAttention(4, 64, 72, dtype, kv_heads=2)
+    run = lambda: att.forward(x["q"], x["k"], x["v"], x["gate"], state=x["state"])  # noqa: E731
+    want, _ = run()
+    at = 77
+    if name == "gate":
+        x[name][at, 1] = float("nan")
+    else:
+        x[name][at, -1, 5] = float("inf") if name == "v" else float("nan")
+        if name == "v":
+            x[name][at + 30, -1, 9] = float("nan")
+    got, last = run()
+    assert torch.equal(got[:at], want[:at])
+    heads = slice(3, 4) if name == "q" else slice(2, 4)  # of the second key head, or the one query head
+    other = slice(0, 3) if name == "q" else slice(0, 2)
+    assert torch.equal(got[:, other], want[:, other])
+    if name == "q":
+        assert torch.isnan(got[at, heads]).all() and torch.equal(got[at + 1:], want[at + 1:])
+    elif name == "v":
+        assert not torch.isfinite(got[at:, heads, 5]).any() and torch.isnan(got[at + 30:, heads, 9]).all()
+        rest = [c for c in range(72) if c not in (5, 9)]
+        assert torch.equal(got[:, heads][..., rest], want[:, heads][..., rest])
+        assert torch.equal(got[:at + 30, heads, 9], want[:at + 30, heads, 9])
+        assert not torch.isfinite(last[0, 1, :, 5]).any() and torch.isfinite(last[0, 0]).all()
+    else:
+        assert torch.isnan(got[at:, heads]).all()
