@@ -164,7 +164,7 @@ gs_status check_heads(const char* call, const char* name, const gs_heads& h, int
     constexpr int64_t kMost = 1ll << 40;
     if (h.ld_row < 0 || h.ld_head < 0)
         return fail(GS_ERR_INVALID_ARGUMENT, "%s: strides of %s are negative", call, name);
-    if (h.ld_row > kMaxStride * 8 || h.ld_head > kMost)
+    if (h.ld_row >= kMaxStride * 8 || h.ld_head > kMost)  // the kernels multiply row strides of 24 bits
         return fail(GS_ERR_UNSUPPORTED, "%s: strides %lld, %lld of %s exceed the limits", call, (long long)h.ld_row,
                     (long long)h.ld_head, name);
     if (output) {

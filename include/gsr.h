@@ -476,8 +476,9 @@ GSR_API gs_status gs_norm_backward(const gs_norm_dims* dims, const void* h, int6
 /* AdamW step over many tensors at once, for the updater's weights and the Gaussians' parameters:
  *   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2,
  *   p = p - lr weight_decay p - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
- * in float32 (the states in exactly these operations, each rounded by itself), t the number of this step.  A gradient is multiplied by *grad_scale and the rates by *rate_scale (device
- * scalars, null: 1), so that both can change under a captured graph; lr and weight_decay go by value.
+ * in float32 (the states in exactly these operations, each rounded by itself), t the number of this step.
+ * A gradient is multiplied by *grad_scale and the rates by *rate_scale (device scalars, null: 1), so that both can
+ * change under a captured graph; lr and weight_decay go by value.
  * state_bits 32: m and v are float32 arrays of n values.  state_bits 8: m and v are n 8-bit codes (the type of
  * gs_norm_forward8) of m and of sqrt(v), with one float32 scale for every 256 values in m_scale and v_scale
  * (ceil(n / 256)); a root above zero is at least the smallest code.  Not a number in a gradient reaches every value of
@@ -509,17 +510,17 @@ GSR_API gs_status gs_adamw_step(const gs_adamw_dims* dims, const gs_adamw_tensor
 
 /* Linear attention with a decay for each key head, over sequences packed like those of gs_scan_forward:
  *   S_t = sigma(gate_t) S_{t-1} + k_t v_t^T,   y_t = scale S_t^T q_t
- * q [rows, heads, d_key], k [rows, kv_heads, d_key], v [rows, kv_heads, d_value], y [rows, heads, d_value] of type dtype;
- * heads is a multiple of kv_heads, and query head h reads the state of key head h / (heads / kv_heads).  gate, of type
+ * q [rows, heads, d_key], k [rows, kv_heads, d_key], v [rows, kv_heads, d_value], y [rows, heads, d_value] of type
+ * dtype; heads is a multiple of kv_heads, and query head h reads the state of key head h / (heads / kv_heads).  gate, of type
  * gate_dtype (dtype or GS_F32): [rows, kv_heads] where gate_per_row is set, else [kv_heads].  States float32
  * [n_seq, kv_heads, d_key, d_value], contiguous: state (before the first row, null: zero) and last (after the last row,
  * null: not wanted; may be state, though a backward pass wants the one from before).
  * offsets (device, [n_seq + 1], non-decreasing, first 0) gives the first row of each sequence and the end of the last;
- * rows behind it are left as they are.  Null: n_seq sequences of equal length.  Offsets outside [0, rows] are taken as the
- * nearer of the two; values that are not non-decreasing give unspecified results but no access out of range.
+ * rows behind it are left as they are.  Null: n_seq sequences of equal length.  Offsets outside [0, rows] are taken as
+ * the nearer of the two; values that are not non-decreasing give unspecified results but no access out of range.
  * Sequences may be empty; equal sequences of length 1 (single tokens) take a kernel of their own.
- * Not a number and infinities stay in their sequence, and in outputs reach no row before theirs (in gradients any row of
- * the sequence); infinities may come out as NaN.
+ * Not a number and infinities stay in their sequence, and in outputs reach no row before theirs (in gradients any row
+ * of the sequence); infinities may come out as NaN.
  * d_key and d_value are 1 .. 128, rows and n_seq 0 .. 2^31 - 512, heads up to 65535. */
 typedef struct {
     int64_t rows;
@@ -530,8 +531,8 @@ typedef struct {
     int32_t gate_per_row;      /* 0 or 1 */
     float scale;
 } gs_attn_dims;
-/* [rows, heads, d] in any order of rows and heads: strides in elements, d contiguous.  Rows and heads of an output must not
- * overlap. */
+/* [rows, heads, d] in any order of rows and heads: strides in elements (ld_row below 2^24, ld_head up to 2^40),
+ * d contiguous.  Rows and heads of an output must not overlap. */
 typedef struct {
     void* p;  /* inputs are not written */
     int64_t ld_row, ld_head;
@@ -553,13 +554,13 @@ typedef struct {
 /* Bytes of the saved states and of the two calls' workspaces (any pointer may be null). */
 GSR_API gs_status gs_attn_sizes(const gs_attn_dims* dims, size_t* saved_bytes, size_t* forward_bytes,
                                 size_t* backward_bytes);
-/* saved (may be null: inference) receives the float32 states that gs_attn_backward starts from.  saved and workspace are
- * 256-byte aligned (null where their size is 0).  Outputs must not overlap inputs or each other, but for last. */
+/* saved (may be null: inference) receives the float32 states that gs_attn_backward starts from.  saved and workspace
+ * are 256-byte aligned (null where their size is 0).  Outputs must not overlap inputs or each other, but for last. */
 GSR_API gs_status gs_attn_forward(const gs_attn_dims* dims, const int64_t* offsets, const gs_attn_inputs* in,
                                   const gs_heads* y, float* last, void* saved, void* workspace, size_t workspace_bytes,
                                   hipStream_t stream);
-/* Gradients for dy [rows, heads, d_value] (dtype) and d_last (float32, like last; null: zero); in and offsets as given to
- * the forward pass.  grads.state may be d_last or state. */
+/* Gradients for dy [rows, heads, d_value] (dtype) and d_last (float32, like last; null: zero); in and offsets as given
+ * to the forward pass.  grads.state may be d_last or state. */
 GSR_API gs_status gs_attn_backward(const gs_attn_dims* dims, const int64_t* offsets, const gs_attn_inputs* in,
                                    const void* saved, const gs_heads* dy, const float* d_last,
                                    const gs_attn_grads* grads, void* workspace, size_t workspace_bytes,
