@@ -130,7 +130,9 @@ __device__ __forceinline__ uint32_t encode4(const float* x, bool root, float* sc
 #pragma unroll
     for (int e = 0; e < 4; ++e) top = max(top, magnitude(x[e]));
     for (int m = 32; m > 0; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
-    *scale = f8_scale(__builtin_bit_cast(float, top));
+    // not below the smallest normal number: m falls through the subnormal ones where gradients stop, and a scale rounded
+    // there could be zero, or so small that the largest code overflows
+    *scale = __builtin_fmaxf(f8_scale(__builtin_bit_cast(float, top)), 0x1p-126f);
     float c[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {

@@ -119,9 +119,10 @@ __device__ __forceinline__ void store_codes(const NormArgs& p, int64_t row, int 
         for (int m = share / 2; m > 0; m >>= 1) top = larger(top, __shfl_xor(top, m));
     }
     if (n <= 0) return;
-    // a row with an infinity or NaN (r is 0 or NaN), or without a value above zero: codes of y itself
-    const double inv = top > 0.0 && rstd > 0.f ? (double)kF8Max / top : (double)rstd;
-    const float scale = f8_scale((float)(top * (double)rstd));
+    // a row with an infinity or NaN (r is 0 or NaN), or without a value that float32 tells from zero: codes of y itself
+    const float y_top = (float)(top * (double)rstd);
+    const double inv = y_top > 0.f ? (double)kF8Max / top : (double)rstd;
+    const float scale = f8_scale(y_top);
     if (whole) {
         if (col == 0) p.scales[row] = scale;
     } else if (col % p.group == 0) {

@@ -234,3 +234,20 @@ def test_refusals():
         with pytest.raises(m.GsrError):
             bad()
     assert (p == 0).all()
+
+
+def test_states_that_fade():
+    """Without gradients m falls by b1 a step, through the subnormal numbers, where a scale could be rounded to nothing."""
+    p = torch.zeros(600, device="cuda")
+    opt = gsr().AdamW([p], lr=1.0, state_bits=8)
+    g = torch.full((600,), 1e-36, device="cuda") * torch.linspace(-1, 1, 600, device="cuda")
+    opt.step([g])
+    for _ in range(250):
+        m, v = held(opt, 0)
+        opt.step([torch.zeros_like(g)])
+        s = opt.m_scale[0].double().repeat_interleave(256)[:600]
+        assert (opt.m_scale[0] >= 2.0 ** -126).all() and torch.isfinite(p).all()
+        err = (held(opt, 0)[0] - 0.9 * m).abs()
+        assert (err <= (2.0 ** -4 + 64 * V) * 0.9 * m.abs() + (2.0 ** -10 + 64 * V) * s + 2.0 ** -149).all()
+    # the least scale's smallest codes round to themselves: 0.9 k is within half of k up to 5
+    assert (held(opt, 0)[0].abs() <= 5 * 2.0 ** -9 * 2.0 ** -126).all()

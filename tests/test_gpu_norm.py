@@ -307,3 +307,16 @@ def test_8bit_rows_with_infinities():
         assert torch.isnan(codes[0]).all() and torch.isnan(codes[1, 70])
         rest = torch.arange(300, device="cuda") != 70
         assert (codes[1, rest] == 0).all() and (scales[:2] == 1).all() and torch.isfinite(codes[2]).all()
+
+
+@pytest.mark.parametrize("group", [0, 32])
+def test_8bit_subnormal_values(group):
+    """Beside a code's half step: a scale rounded among the subnormal numbers, 2^-150 for each of up to 448 of them."""
+    x = torch.full((6, 96), 1e-36, device="cuda") * torch.linspace(-1, 1, 96, device="cuda")
+    w = torch.full((96,), 1.0, device="cuda")
+    for k, size in enumerate((1.0, 1e-4, 1e-6, 1e-8, 1e-9, 1e-12)):
+        codes, scales, _ = gsr().ResidualNorm(w * size, torch.float32, eps=EPS).forward8(x, group=group)
+        y = x.double() / math.sqrt(EPS) * (w * size).double()
+        s = scales.double().repeat_interleave(group or 96, 1)
+        err = (codes.double() * s - y).abs()
+        assert (err <= (2.0 ** -4 + 32 * V) * y.abs() + (2.0 ** -10 + 32 * V) * s + 448 * 2.0 ** -150).all(), k
