@@ -7,10 +7,15 @@
 // once.  The tensors' pointers and sizes travel in the kernel's arguments, so nothing is laid out on the device and
 // gradients may be other tensors at every call; kTensors of them fit, longer lists take several launches.
 //
+// Stores past the caches: 18.4 M float32 values (28 bytes each) 122 -> 113 us, 4.5 TB/s.  Loads past them serve what is
+// too large to find anything there from the step before: 348 M values with 8-bit states (16 bytes) 1265 -> 1220 us,
+// 4.6 TB/s, but the 18.4 M ones 113 -> 133 us.  Reading a block ahead brings nothing (123 and 1294 us).
+//
 // States in 8 bits hold m and sqrt(v) as 8-bit floats with one float32 scale for 256 values (one wave's four a lane): the
 // relative error of a code is at most 2^-4 over a range of 2^15 below the block's largest value, and the root takes v's
 // range down to it.  The update uses the new m and v before they are rounded.  A root above zero never rounds to zero: m
-// would be divided by eps alone where the next gradients are zero (a Gaussian that no view sees).
+// would be divided by eps alone where the next gradients are zero (a Gaussian that no view sees).  Codes are rounded to
+// nearest: next to its block's largest value, one moves only where a step changes it by more than half a code's step.
 //
 // The number of steps done is in device memory, so that a captured step goes on counting when it is replayed.  Every
 // workgroup reads it and then takes a ticket; the last one has to wait for nobody and writes the next number.
@@ -54,24 +59,30 @@ struct AdamArgs {
     int last;              // the launch that counts the step
 };
 
-// Four values of a type known at run time, from element i; n < 4: the others are zero (not written).
+// Four values of a type known at run time, from element i; n < 4: the others are zero (not written).  STREAM, and all
+// stores: not kept in the caches for longer than other data.
+template <bool STREAM>
 __device__ __forceinline__ void load4(const void* base, uint32_t type, int64_t i, int n, float* out) {
     if (type == GS_F32) {
         const float* p = (const float*)base + i;
-        if (n >= 4)
-            __builtin_memcpy(out, p, 16);
-        else
+        if (n >= 4) {
+            const Words4 w = STREAM ? __builtin_nontemporal_load((const Words4*)p) : *(const Words4*)p;
+            __builtin_memcpy(out, &w, 16);
+        } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e) out[e] = e < n ? p[e] : 0.f;
+        }
         return;
     }
     uint16_t h[4];
     const uint16_t* p = (const uint16_t*)base + i;
-    if (n >= 4)
-        __builtin_memcpy(h, p, 8);
-    else
+    if (n >= 4) {
+        const Words2 w = STREAM ? __builtin_nontemporal_load((const Words2*)p) : *(const Words2*)p;
+        __builtin_memcpy(h, &w, 8);
+    } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = e < n ? p[e] : 0;
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         out[e] = type == GS_BF16 ? (float)__builtin_bit_cast(__bf16, h[e]) : (float)__builtin_bit_cast(_Float16, h[e]);
@@ -79,12 +90,15 @@ __device__ __forceinline__ void load4(const void* base, uint32_t type, int64_t i
 __device__ __forceinline__ void store4(void* base, uint32_t type, int64_t i, int n, const float* v) {
     if (type == GS_F32) {
         float* p = (float*)base + i;
-        if (n >= 4)
-            __builtin_memcpy(p, v, 16);
-        else
+        if (n >= 4) {
+            Words4 w;
+            __builtin_memcpy(&w, v, 16);
+            __builtin_nontemporal_store(w, (Words4*)p);
+        } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (e < n) p[e] = v[e];
+        }
         return;
     }
     uint16_t h[4];
@@ -92,12 +106,15 @@ __device__ __forceinline__ void store4(void* base, uint32_t type, int64_t i, int
     for (int e = 0; e < 4; ++e)
         h[e] = type == GS_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)v[e]) : __builtin_bit_cast(uint16_t, (_Float16)v[e]);
     uint16_t* p = (uint16_t*)base + i;
-    if (n >= 4)
-        __builtin_memcpy(p, h, 8);
-    else
+    if (n >= 4) {
+        Words2 w;
+        __builtin_memcpy(&w, h, 8);
+        __builtin_nontemporal_store(w, (Words2*)p);
+    } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (e < n) p[e] = h[e];
+    }
 }
 
 __device__ __forceinline__ void store_codes4(void* base, int64_t i, int n, uint32_t w) {
@@ -176,16 +193,16 @@ __global__ __launch_bounds__(kThreads) void k_adamw(const AdamArgs a) {
             if (block * kBlock >= w.n) break;
             const int n = (int)min((int64_t)4, w.n - i);
             float p[4], g[4], m[4], v[4];
-            load4(w.p, tp, i, n, p);
-            load4(w.g, tg, i, n, g);
+            load4<BITS8>(w.p, tp, i, n, p);
+            load4<BITS8>(w.g, tg, i, n, g);
             if constexpr (BITS8) {
                 load_codes4(w.m, i, n, w.m_scale[block], m);
                 load_codes4(w.v, i, n, w.v_scale[block], v);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] *= v[e];
             } else {
-                load4(w.m, GS_F32, i, n, m);
-                load4(w.v, GS_F32, i, n, v);
+                load4<false>(w.m, GS_F32, i, n, m);
+                load4<false>(w.v, GS_F32, i, n, v);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {

@@ -9,6 +9,10 @@
 // again (from the caches) instead.  Sums are float32.  The forward pass normalises h before it is rounded to the
 // stream's type; the backward pass is given the rounded one and takes r from it again, which costs no reading.
 //
+// Rows of registers are read, and gradients written, past the caches (nothing reads them again here): 131072 x 512, bf16
+// with a float32 stream, 385 -> 368 us for both passes, 8-bit outputs 101 -> 92 us.  Reading the next row ahead brings
+// nothing (382 us), nor do other numbers of workgroups (386, 387).
+//
 // The weight's gradient: every workgroup sums its rows in registers and leaves one row of partial sums, which
 // k_norm_weight adds up in a fixed order, so results are the same from run to run.
 #include <algorithm>
@@ -165,11 +169,11 @@ __global__ __launch_bounds__(kThreads) void k_norm(const NormArgs p) {
         Run8<T> x[NV];
         Run8<R> r[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) x[i].load((const T*)p.x + row * p.ldx + column<WG>(i, lane, lanes), n[i]);
+        for (int i = 0; i < NV; ++i) x[i].template load<true>((const T*)p.x + row * p.ldx + column<WG>(i, lane, lanes), n[i]);
         if (p.residual) {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                r[i].load((const R*)p.residual + row * p.ldr + column<WG>(i, lane, lanes), n[i]);
+                r[i].template load<true>((const R*)p.residual + row * p.ldr + column<WG>(i, lane, lanes), n[i]);
         }
         float h[NV][8], s = 0.f;
 #pragma unroll
@@ -299,13 +303,13 @@ __device__ __forceinline__ void store_grads(const NormBackArgs& p, int64_t row, 
         Run8<T> o;
 #pragma unroll
         for (int e = 0; e < 8; ++e) o.set(e, d[e]);
-        o.store((T*)p.dx + row * p.lddx + col, n);
+        o.template store<true>((T*)p.dx + row * p.lddx + col, n);
     }
     if (p.dr) {
         Run8<R> o;
 #pragma unroll
         for (int e = 0; e < 8; ++e) o.set(e, d[e]);
-        o.store((R*)p.dr + row * p.lddr + col, n);
+        o.template store<true>((R*)p.dr + row * p.lddr + col, n);
     }
 }
 
@@ -333,12 +337,12 @@ __global__ __launch_bounds__(kThreads) void k_norm_backward(const NormBackArgs p
         Run8<R> h[NV], g[NV];
         Run8<T> dy[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) h[i].load((const R*)p.h + row * p.ldh + column<WG>(i, lane, lanes), n[i]);
+        for (int i = 0; i < NV; ++i) h[i].template load<true>((const R*)p.h + row * p.ldh + column<WG>(i, lane, lanes), n[i]);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) dy[i].load((const T*)p.dy + row * p.lddy + column<WG>(i, lane, lanes), n[i]);
+        for (int i = 0; i < NV; ++i) dy[i].template load<true>((const T*)p.dy + row * p.lddy + column<WG>(i, lane, lanes), n[i]);
         if (p.dh) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) g[i].load((const R*)p.dh + row * p.lddh + column<WG>(i, lane, lanes), n[i]);
+            for (int i = 0; i < NV; ++i) g[i].template load<true>((const R*)p.dh + row * p.lddh + column<WG>(i, lane, lanes), n[i]);
         }
         float s = 0.f, t = 0.f;  // of h^2 and of u h
 #pragma unroll

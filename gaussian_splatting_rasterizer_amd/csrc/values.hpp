@@ -6,24 +6,47 @@
 
 namespace gsr {
 
+// 16 and 8 bytes at any element's address.
+typedef uint32_t Words4 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t Words2 __attribute__((ext_vector_type(2), aligned(2)));
+
 // Eight values as they lie in memory.  Rows of odd length and views start anywhere, and the memory system takes 16-byte
 // accesses at any element's address, so a whole run is always one (float32: two) of them; only the last run of a row
 // goes element by element.
 template <class T>
 struct Run8 {
     T v[8];
-    // n values from p; the rest zero
+    // n values from p; the rest zero.  STREAM, here and in store: not kept in the caches for longer than other data
+    template <bool STREAM = false>
     __device__ __forceinline__ void load(const T* p, int n) {
         if (n >= 8) {
-            __builtin_memcpy(v, p, sizeof(v));
+            if constexpr (STREAM) {
+#pragma unroll
+                for (int i = 0; i < (int)sizeof(v) / 16; ++i) {
+                    const Words4 w = __builtin_nontemporal_load((const Words4*)p + i);
+                    __builtin_memcpy((char*)v + 16 * i, &w, 16);
+                }
+            } else {
+                __builtin_memcpy(v, p, sizeof(v));
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : (T)0.f;
         }
     }
+    template <bool STREAM = false>
     __device__ __forceinline__ void store(T* p, int n) const {
         if (n >= 8) {
-            __builtin_memcpy(p, v, sizeof(v));
+            if constexpr (STREAM) {
+#pragma unroll
+                for (int i = 0; i < (int)sizeof(v) / 16; ++i) {
+                    Words4 w;
+                    __builtin_memcpy(&w, (const char*)v + 16 * i, 16);
+                    __builtin_nontemporal_store(w, (Words4*)p + i);
+                }
+            } else {
+                __builtin_memcpy(p, v, sizeof(v));
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
