@@ -1,6 +1,9 @@
-"""Building blocks of the learned updater that consumes the score tokens: a gated
+"""Building blocks of the learned updater that consumes the score tokens: the
+residual stream's norm, linear attention with a decay (a matrix of memory for
+each head, along the Gaussians of a scene or from update to update), a gated
 feed-forward block, a gated linear recurrence (the hidden state carried from
-update to update) and the orthogonalisation of a weight's update.
+update to update), the orthogonalisation of a weight's update, and AdamW for the
+other weights and for the Gaussians themselves.
 
 Each class checks its tensors, owns the workspace its calls need (grown when a
 call needs more) and runs on the current stream or the one given; like a
@@ -11,11 +14,14 @@ backward passes are explicit calls, as in Rasterizer.backward.
 """
 from __future__ import annotations
 
+import functools
+
 from . import binding as b
 
 _ACTIVATIONS = {"silu": b.GS_ACT_SILU, "gelu": b.GS_ACT_GELU}
 
 
+@functools.lru_cache(maxsize=None)
 def _dtype_code(dtype, allowed=("float32", "bfloat16", "float16")):
     name = str(dtype).replace("torch.", "")
     if name not in allowed:
