@@ -72,8 +72,9 @@ struct AttnArgs {
     float* last;                // what a sequence ends with; null: not wanted
     float* edges;               // [boundary][kv_heads][dk][dv]: the state at every boundary between two spans
     const float* other_edges;   // the adjoint's, for the products at the spans' ends
-    const float* other_last;
-    float* ends;                // [slot][kv_heads] <adjoint behind the span, what its last chunk leaves of the state before>
+    const float* other_last;    // the adjoint behind a sequence (gradient of k: the state before it); null: zero
+    float* ends;                // [slot][kv_heads] <adjoint behind the span, what its last chunk leaves of the state before>;
+                                // gradient of k, first spans of several chunks: <state before the sequence, its adjoint>
     float* totals;              // [slot][kv_heads] log a summed over the span
     float* dots;                // [2][kv_heads][rows]: out . w, of what comes from before the chunk and from within it
     bool against;               // aggregates: against the rows' order
@@ -1039,7 +1040,19 @@ __global__ __launch_bounds__(OD / 32 * 64, KD == 64 && !DOT && AttnType<T>::kPla
             for (int k = 0; k < chunks; ++k) t += w.total[k];
             p.totals[slot * p.kv_heads + kv] = (float)(t * 0.6931471805599453);
         }
-    } else if constexpr (DOT && !REV) {
+    } else if constexpr (DOT) {
+        if constexpr (REV) {
+            if (!sp.first || !p.other_last || chunks <= 1) return;  // of one chunk nothing is summed from chunk to chunk
+            const float* from = p.other_last + (sp.seq * p.kv_heads + kv) * state_size;
+            const float end = *w.end;
+#pragma unroll
+            for (int t = 0; t < KT; ++t) {
+                f32x16 D;
+                attn_load_tile(D, from, p, t, col0, afresh(lane));
+#pragma unroll
+                for (int r = 0; r < 16; ++r) dot_end = __builtin_fmaf(D[r], S[t][r] * end, dot_end);
+            }
+        }
         for (int m = 32; m > 0; m >>= 1) dot_end += __shfl_xor(dot_end, m);
         __syncthreads();  // the last chunk's sums are read
         if (lane == 0) s_sum[wave] = dot_end;
