@@ -24,15 +24,16 @@ namespace gsr {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kJoinWaves = 16, kJoinSteps = 16;  // of k_attn_join; boundaries that a wave takes at a time
+constexpr int kJoinSteps = 16;  // boundaries that a wave of k_attn_join takes at a time
 constexpr int kJoinParts = 32;  // shares of the sequences
 
 // The state at every boundary between two spans, in place of what the span beside it adds.  A workgroup runs through a
 // sequence's boundaries for 64 values of the state, its waves through consecutive runs of them at the same time: each from
 // zero, then with what the waves before it end with.  (One thread for a value's whole chain took 64 us for 256 boundaries
 // of 4 x 128 x 128, four times the data's time.)
-__global__ __launch_bounds__(kJoinWaves * 64) void k_attn_join(const AttnArgs p, float* copies) {
-    __shared__ float s_end[kJoinWaves][64], s_fade[kJoinWaves];
+template <int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void k_attn_join(const AttnArgs p, float* copies) {
+    __shared__ float s_end[WAVES][64], s_fade[WAVES];
     const int64_t size = (int64_t)p.dk * p.dv;
     const int kv = blockIdx.y, lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -60,9 +61,9 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_attn_join(const AttnArgs p,
             const int64_t slot0 = p.offsets ? slo / p.span + s : s * p.spans;
             float carry = p.first && in ? p.first[(s * p.kv_heads + kv) * size + e] : 0.f;
             if (copies && in && wave == 0) copies[(attn_copy(p, s, edge0) * p.kv_heads + kv) * size + e] = carry;
-            for (int b0 = 0; b0 < edges; b0 += kJoinWaves * kJoinSteps) {
+            for (int b0 = 0; b0 < edges; b0 += WAVES * kJoinSteps) {
                 // steps of this pass for each wave
-                const int steps = min(kJoinSteps, (edges - b0 + kJoinWaves - 1) / kJoinWaves), first = b0 + wave * steps;
+                const int steps = min(kJoinSteps, (edges - b0 + WAVES - 1) / WAVES), first = b0 + wave * steps;
                 const int mine = max(0, min(steps, edges - first));
                 auto at = [&](int b) { return ((edge0 + (p.against ? edges - 1 - b : b)) * p.kv_heads + kv) * size + e; };
                 float u[kJoinSteps];
@@ -88,7 +89,7 @@ __global__ __launch_bounds__(kJoinWaves * 64) void k_attn_join(const AttnArgs p,
                 if (lane == kJoinSteps - 1) s_fade[wave] = all;
                 __syncthreads();
                 float in_front = carry;
-                for (int i = 0; i < kJoinWaves; ++i) {
+                for (int i = 0; i < WAVES; ++i) {
                     if (i == wave) in_front = carry;
                     carry = __builtin_fmaf(s_fade[i], carry, s_end[i][lane]);
                 }
@@ -399,8 +400,13 @@ hipError_t launch_kernel(int dtype, AttnKind kind, const AttnArgs& a, hipStream_
 bool attn_splits(const AttnArgs& a) { return a.offsets ? a.rows > a.span : a.spans > 1; }
 
 hipError_t join(const AttnArgs& a, float* copies, hipStream_t st) {
-    k_attn_join<<<dim3((unsigned)(((int64_t)a.dk * a.dv + 63) / 64), a.kv_heads, (unsigned)std::min<int64_t>(a.n_seq, kJoinParts)),
-                  kJoinWaves * 64, 0, st>>>(a, copies);
+    const dim3 grid((unsigned)(((int64_t)a.dk * a.dv + 63) / 64), a.kv_heads, (unsigned)std::min<int64_t>(a.n_seq, kJoinParts));
+    // Few boundaries a sequence leave most of 16 waves without one: 37 sequences of 1350 rows 71 -> 20 us with 4 waves; one
+    // sequence of 294 boundaries 15 us, with 4 waves 21.
+    if (a.rows / a.span <= 16 * a.n_seq)
+        k_attn_join<4><<<grid, 4 * 64, 0, st>>>(a, copies);
+    else
+        k_attn_join<16><<<grid, 16 * 64, 0, st>>>(a, copies);
     return hipGetLastError();
 }
 
