@@ -382,7 +382,7 @@ class LinearAttention(_Op):
         else:
             ld_gate = 0
             _exact(gate, "gate", (self.kv_heads,), gate.dtype, self.device)
-        key = (rows, n_seq, gate.dtype, per_row)
+        key = (rows, n_seq, gate.dtype, per_row, self.scale)
         if key not in self._sizes:
             if len(self._sizes) > 64:
                 self._sizes.clear()
