@@ -481,8 +481,10 @@ GSR_API gs_status gs_norm_backward(const gs_norm_dims* dims, const void* h, int6
  * change under a captured graph; lr and weight_decay go by value.
  * state_bits 32: m and v are float32 arrays of n values.  state_bits 8: m and v are n 8-bit codes (the type of
  * gs_norm_forward8) of m and of sqrt(v), with one float32 scale for every 256 values in m_scale and v_scale
- * (ceil(n / 256)); a root above zero is at least the smallest code.  Not a number in a gradient reaches every value of
- * its 256 at the next step.  All states start as zeros (scales too).
+ * (ceil(n / 256)); a root above zero is at least the smallest code, and scales are at least 2^-126.  Codes are rounded to
+ * nearest: one moves only where a step changes it by more than half of its own step next to the block's largest.  An
+ * infinity or not a number in a gradient reaches every value of its 256 at the next step.  All states start as zeros
+ * (scales too).
  * steps: two int64 on the device, zeros at the start; the first is the number of steps done and may be set, the second
  * belongs to the call.  Two calls with the same steps or tensors must not overlap in time. */
 typedef struct {
